@@ -48,6 +48,11 @@ class SwigluError(RuntimeError):
         super().__init__("%s: %s (%s)" % (where, STATUS.get(code, code), status_string(code)))
 
 
+class W4Format(ctypes.Structure):
+    """swiglu_mlp_w4_format: group size and zero-point flag of packed 4-bit experts."""
+    _fields_ = [("group", ctypes.c_int), ("zeros", ctypes.c_int)]
+
+
 class Options(ctypes.Structure):
     """swiglu_mlp_options: gate/down multipliers and weight-gradient accumulation."""
     _fields_ = [("gate_multiplier", ctypes.c_float), ("down_multiplier", ctypes.c_float),
@@ -159,6 +164,34 @@ def _load(path: str) -> ctypes.CDLL:
     L.swiglu_mlp_profile_read.argtypes = [ci, vp, vp]
     L.swiglu_mlp_kernel_name.restype = ctypes.c_char_p
     L.swiglu_mlp_kernel_name.argtypes = [ci]
+    L.swiglu_mlp_w4_packed_bytes.restype = sz
+    L.swiglu_mlp_w4_packed_bytes.argtypes = [i64, i64, i64, ci, ci, ci]
+    L.swiglu_mlp_w4_quantize.restype = ci
+    L.swiglu_mlp_w4_quantize.argtypes = [vp, vp, vp, vp, i64, i64, ci, ci, vp]
+    L.swiglu_mlp_w4_pack.restype = ci
+    L.swiglu_mlp_w4_pack.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp]
+    L.swiglu_mlp_w4_unpack.restype = ci
+    L.swiglu_mlp_w4_unpack.argtypes = [vp, vp, i64, i64, i64, ci, ci, ci, ci, vp]
+    L.swiglu_mlp_w4_workspace_bytes.restype = sz
+    L.swiglu_mlp_w4_workspace_bytes.argtypes = [i64, i64, i64]
+    L.swiglu_mlp_fwd_nograd_w4_workspace_bytes.restype = sz
+    L.swiglu_mlp_fwd_nograd_w4_workspace_bytes.argtypes = [i64, i64, i64]
+    L.swiglu_mlp_w4_linear.restype = ci
+    L.swiglu_mlp_w4_linear.argtypes = [vp, vp, vp, i64, i64, i64, ci, ci, ci, vp, sz, vp]
+    L.swiglu_mlp_fwd_nograd_w4.restype = ci
+    L.swiglu_mlp_fwd_nograd_w4.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, op, vp,
+                                           sz, vp]
+    cf = ctypes.c_float
+    L.swiglu_mlp_moe_workspace_bytes.restype = sz
+    L.swiglu_mlp_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, ci]
+    L.swiglu_mlp_moe_route.restype = ci
+    L.swiglu_mlp_moe_route.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, cf, ci, vp]
+    L.swiglu_mlp_moe_experts.restype = ci
+    L.swiglu_mlp_moe_experts.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, vp, ci,
+                                         op, vp, sz, vp]
+    L.swiglu_mlp_moe_fwd_nograd.restype = ci
+    L.swiglu_mlp_moe_fwd_nograd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, ci,
+                                            cf, vp, ci, op, vp, sz, vp]
     L.swiglu_mlp_debug_build.restype = ci
     L.swiglu_mlp_debug_build.argtypes = []
     L.swiglu_mlp_debug_narrow_once.restype = None
@@ -407,6 +440,256 @@ def swiglu_mlp_bwd(dY, X, Wgu, Wd, saved, out: dict | None = None, ws=None,
            "swiglu_mlp_bwd")
     _device_check(ws, "swiglu_mlp_bwd")
     return dX, dWgu, dWd
+
+
+def _serving_checks(X, *others):
+    """Contiguous CUDA tensors of X's device; returns X's stream."""
+    for t in (X, *others):
+        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.device != X.device):
+            raise ValueError("inputs and outputs must be contiguous CUDA tensors of one device")
+    return ctypes.c_void_p(_stream(X.device))
+
+
+def _out(out, name, shape, dtype, device):
+    """The caller's output tensor, checked, or a new one."""
+    t = out.get(name) if out else None
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError("out[%r] must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), device))
+    return t
+
+
+def _ws(ws, size, device):
+    """The caller's workspace (its size is checked by the call) or a new one."""
+    return torch.zeros(int(size()), dtype=torch.uint8, device=device) if ws is None else ws
+
+
+class W4Weights:
+    """One 4-bit matrix [N, K], or ``experts`` of them, in the layout the
+    few-token products stream (swiglu_mlp_w4_pack).  ``gate_up``: the rows are
+    a [Wg; Wu] pair."""
+
+    def __init__(self, packed, N, K, group, zeros, gate_up, dtype, experts=None):
+        self.packed, self.N, self.K, self.group = packed, int(N), int(K), int(group)
+        self.zeros, self.gate_up, self.dtype = bool(zeros), bool(gate_up), dtype
+        self.experts = experts
+
+    @property
+    def device(self):
+        return self.packed.device
+
+    @property
+    def shape(self):
+        return (self.N, self.K) if self.experts is None else (self.experts, self.N, self.K)
+
+    def __repr__(self):
+        return "W4Weights(%s, group=%d, zeros=%s, gate_up=%s, dtype=%s)" % (
+            tuple(self.shape), self.group, self.zeros, self.gate_up, self.dtype)
+
+
+def swiglu_mlp_w4_quantize(W, group: int = 128, zeros: bool = False):
+    """Rounds W [N, K] or [E, N, K] to 4 bits: (codes uint8 [.., N, K/2],
+    scales [.., N, ceil(K/group)] in W's type, zero points uint8 or None)."""
+    st = _serving_checks(W)
+    if W.dim() not in (2, 3):
+        raise ValueError("expected W [N, K] or [E, N, K], got %s" % (tuple(W.shape),))
+    *lead, N, K = W.shape
+    rows = W.numel() // K if K else 0
+    if group not in (32, 64, 128):
+        raise SwigluError(1, "swiglu_mlp_w4_quantize")
+    ng = -(-K // group)
+    codes = torch.empty(*lead, N, K // 2, dtype=torch.uint8, device=W.device)
+    scales = torch.empty(*lead, N, ng, dtype=W.dtype, device=W.device)
+    zp = torch.empty(*lead, N, ng, dtype=torch.uint8, device=W.device) if zeros else None
+    _check(lib().swiglu_mlp_w4_quantize(_ptr(W), _ptr(codes), _ptr(scales), _ptr(zp), rows, K,
+                                        group, dtype_code(W.dtype), st),
+           "swiglu_mlp_w4_quantize")
+    return codes, scales, zp
+
+
+def swiglu_mlp_w4_pack(codes, scales, zeros=None, group: int = 128,
+                       gate_up: bool = False) -> W4Weights:
+    """The packed copy of 4-bit weights (codes uint8 [.., N, K/2], scales
+    [.., N, ceil(K/group)] in the activations' type, optional zero points) that
+    the few-token products stream."""
+    st = _serving_checks(codes, scales, zeros)
+    if codes.dim() not in (2, 3) or codes.dtype != torch.uint8:
+        raise ValueError("expected uint8 codes [N, K/2] or [E, N, K/2]")
+    *lead, N, half = codes.shape
+    E, K = (lead[0] if lead else 1), 2 * half
+    want = (*lead, N, -(-K // group))
+    if tuple(scales.shape) != want:
+        raise ValueError("expected scales of shape %s, got %s" % (want, tuple(scales.shape)))
+    if zeros is not None and (tuple(zeros.shape) != want or zeros.dtype != torch.uint8):
+        raise ValueError("expected uint8 zero points of shape %s" % (want,))
+    zp = zeros is not None
+    n = int(lib().swiglu_mlp_w4_packed_bytes(E, N, K, group, int(zp), int(gate_up)))
+    packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    _check(lib().swiglu_mlp_w4_pack(_ptr(codes), _ptr(scales), _ptr(zeros), _ptr(packed), E, N, K,
+                                    group, int(gate_up), dtype_code(scales.dtype), st),
+           "swiglu_mlp_w4_pack")
+    return W4Weights(packed, N, K, group, zp, gate_up, scales.dtype, lead[0] if lead else None)
+
+
+def swiglu_mlp_w4_unpack(W: W4Weights) -> torch.Tensor:
+    """The 16-bit weights a packed copy stands for ([N, K] or [E, N, K])."""
+    out = torch.empty(W.shape, dtype=W.dtype, device=W.device)
+    _check(lib().swiglu_mlp_w4_unpack(_ptr(W.packed), _ptr(out), W.experts or 1, W.N, W.K, W.group,
+                                      int(W.zeros), int(W.gate_up), dtype_code(W.dtype),
+                                      ctypes.c_void_p(_stream(W.device))),
+           "swiglu_mlp_w4_unpack")
+    return out
+
+
+def w4_linear_workspace(M: int, N: int, K: int, device) -> torch.Tensor:
+    """A zero-filled workspace for swiglu_mlp_w4_linear."""
+    return _ws(None, lambda: lib().swiglu_mlp_w4_workspace_bytes(M, N, K), device)
+
+
+def w4_workspace(M: int, D: int, H: int, device) -> torch.Tensor:
+    """A zero-filled workspace for swiglu_mlp_fwd_nograd_w4."""
+    return _ws(None, lambda: lib().swiglu_mlp_fwd_nograd_w4_workspace_bytes(M, D, H), device)
+
+
+def moe_workspace(T: int, D: int, H: int, E: int, top_k: int, device) -> torch.Tensor:
+    """A zero-filled workspace for swiglu_mlp_moe_experts / _moe_fwd_nograd."""
+    return _ws(None, lambda: lib().swiglu_mlp_moe_workspace_bytes(T, D, H, E, top_k), device)
+
+
+def _w4_match(X, K, *weights):
+    for W in weights:
+        if W.dtype != X.dtype or W.device != X.device:
+            raise ValueError("4-bit weights for %s on %s, activations %s on %s"
+                             % (W.dtype, W.device, X.dtype, X.device))
+    if X.dim() != 2 or X.shape[1] != K:
+        raise ValueError("expected X [M, %d], got %s" % (K, tuple(X.shape)))
+
+
+def swiglu_mlp_w4_linear(X, W: W4Weights, out: dict | None = None, ws=None):
+    """Y [M, N] = X [M, K] W^T for up to 64 tokens and 4-bit weights."""
+    if W.gate_up or W.experts is not None:
+        raise ValueError("expected one matrix packed without gate_up")
+    _w4_match(X, W.K, W)
+    M, dev = X.shape[0], X.device
+    Y = _out(out, "Y", (M, W.N), X.dtype, dev)
+    L = lib()
+    ws = _ws(ws, lambda: L.swiglu_mlp_w4_workspace_bytes(M, W.N, W.K), dev)
+    _check(L.swiglu_mlp_w4_linear(_ptr(X), _ptr(W.packed), _ptr(Y), M, W.N, W.K, W.group,
+                                  int(W.zeros), dtype_code(X.dtype), _ptr(ws), ws.numel(),
+                                  _serving_checks(X, W.packed, ws)),
+           "swiglu_mlp_w4_linear")
+    _device_check(ws, "swiglu_mlp_w4_linear")
+    return Y
+
+
+def swiglu_mlp_fwd_nograd_w4(X, Wgu: W4Weights, Wd: W4Weights, out: dict | None = None, ws=None,
+                             gate_mul: float = 1.0, down_mul: float = 1.0):
+    """The no-grad MLP on 4-bit weights for up to 64 tokens: (Y [M,D], A [M,H])."""
+    if not Wgu.gate_up or Wd.gate_up or Wgu.experts is not None or Wd.experts is not None:
+        raise ValueError("expected Wgu packed with gate_up and Wd without")
+    H, D = Wd.K, Wd.N
+    if Wgu.shape != (2 * H, D) or (Wgu.group, Wgu.zeros) != (Wd.group, Wd.zeros):
+        raise ValueError("mismatch: Wgu %r, Wd %r" % (Wgu, Wd))
+    _w4_match(X, D, Wgu, Wd)
+    M, dev = X.shape[0], X.device
+    Y = _out(out, "Y", (M, D), X.dtype, dev)
+    A = _out(out, "A", (M, H), X.dtype, dev)
+    L = lib()
+    ws = _ws(ws, lambda: L.swiglu_mlp_fwd_nograd_w4_workspace_bytes(M, D, H), dev)
+    _check(L.swiglu_mlp_fwd_nograd_w4(_ptr(X), _ptr(Wgu.packed), _ptr(Wd.packed), _ptr(Y), _ptr(A),
+                                      M, D, H, Wd.group, int(Wd.zeros), dtype_code(X.dtype),
+                                      _opts(gate_mul, down_mul, False), _ptr(ws), ws.numel(),
+                                      _serving_checks(X, Wgu.packed, Wd.packed, ws)),
+           "swiglu_mlp_fwd_nograd_w4")
+    _device_check(ws, "swiglu_mlp_fwd_nograd_w4")
+    return Y, A
+
+
+def swiglu_mlp_moe_route(X, Wr, top_k: int, norm_topk: bool = True, route_scale: float = 1.0,
+                         out: dict | None = None):
+    """The router: (idx int32 [T, top_k], weights fp32 [T, top_k])."""
+    st = _serving_checks(X, Wr)
+    T, D = X.shape
+    E = Wr.shape[0]
+    if Wr.shape != (E, D) or Wr.dtype != X.dtype:
+        raise ValueError("expected Wr [E, %d] of %s, got %s %s" % (D, X.dtype, tuple(Wr.shape),
+                                                                   Wr.dtype))
+    idx = _out(out, "idx", (T, top_k), torch.int32, X.device)
+    w = _out(out, "weights", (T, top_k), torch.float32, X.device)
+    _check(lib().swiglu_mlp_moe_route(_ptr(X), _ptr(Wr), _ptr(idx), _ptr(w), T, D, E, top_k,
+                                      int(norm_topk), float(route_scale), dtype_code(X.dtype), st),
+           "swiglu_mlp_moe_route")
+    return idx, w
+
+
+def _experts(X, Wgu, Wd):
+    """(T, D, H, E, the format struct or None, the two buffers) of a layer."""
+    if X.dim() != 2:
+        raise ValueError("expected X [T, D], got %s" % (tuple(X.shape),))
+    T, D = X.shape
+    w4 = isinstance(Wgu, W4Weights)
+    if w4 != isinstance(Wd, W4Weights):
+        raise ValueError("Wgu and Wd must both be 16-bit tensors or both W4Weights")
+    E, H = Wd.shape[0], Wd.shape[-1]
+    if tuple(Wgu.shape) != (E, 2 * H, D) or tuple(Wd.shape) != (E, D, H):
+        raise ValueError("expected Wgu [E, 2H, %d] and Wd [E, %d, H], got %s and %s"
+                         % (D, D, tuple(Wgu.shape), tuple(Wd.shape)))
+    if Wgu.dtype != X.dtype or Wd.dtype != X.dtype:
+        raise ValueError("activations and experts must have one dtype")
+    if not w4:
+        return T, D, H, E, None, Wgu, Wd
+    if not Wgu.gate_up or Wd.gate_up or (Wgu.group, Wgu.zeros) != (Wd.group, Wd.zeros):
+        raise ValueError("mismatch: Wgu %r, Wd %r" % (Wgu, Wd))
+    return T, D, H, E, ctypes.byref(W4Format(Wd.group, int(Wd.zeros))), Wgu.packed, Wd.packed
+
+
+def swiglu_mlp_moe_experts(X, idx, weights, Wgu, Wd, out: dict | None = None, ws=None,
+                           gate_mul: float = 1.0, down_mul: float = 1.0):
+    """Y[t] = sum_j weights[t, j] MLP_{idx[t, j]}(X[t]) for up to 64 tokens:
+    Y [T, D].  Wgu [E, 2H, D] and Wd [E, D, H], or their W4Weights.  An idx
+    outside 0..E-1 is no expert."""
+    T, D, H, E, fmt, gu, down = _experts(X, Wgu, Wd)
+    if idx.dim() != 2 or idx.shape[0] != T or idx.dtype != torch.int32 \
+            or weights.shape != idx.shape or weights.dtype != torch.float32:
+        raise ValueError("expected idx int32 [T, top_k] and weights fp32 of its shape")
+    k = idx.shape[1]
+    Y = _out(out, "Y", (T, D), X.dtype, X.device)
+    L = lib()
+    ws = _ws(ws, lambda: L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, k), X.device)
+    _check(L.swiglu_mlp_moe_experts(_ptr(X), _ptr(idx), _ptr(weights), _ptr(gu), _ptr(down),
+                                    _ptr(Y), T, D, H, E, k, fmt, dtype_code(X.dtype),
+                                    _opts(gate_mul, down_mul, False), _ptr(ws), ws.numel(),
+                                    _serving_checks(X, idx, weights, gu, down, ws)),
+           "swiglu_mlp_moe_experts")
+    _device_check(ws, "swiglu_mlp_moe_experts")
+    return Y
+
+
+def swiglu_mlp_moe_fwd_nograd(X, Wr, Wgu, Wd, top_k: int, norm_topk: bool = True,
+                              route_scale: float = 1.0, out: dict | None = None, ws=None,
+                              gate_mul: float = 1.0, down_mul: float = 1.0):
+    """A mixture-of-experts layer for up to 64 tokens, without gradients:
+    (Y [T, D], idx int32 [T, top_k], weights fp32 [T, top_k])."""
+    T, D, H, E, fmt, gu, down = _experts(X, Wgu, Wd)
+    if tuple(Wr.shape) != (E, D) or Wr.dtype != X.dtype:
+        raise ValueError("expected Wr [%d, %d] of %s, got %s %s" % (E, D, X.dtype, tuple(Wr.shape),
+                                                                    Wr.dtype))
+    Y = _out(out, "Y", (T, D), X.dtype, X.device)
+    idx = _out(out, "idx", (T, top_k), torch.int32, X.device)
+    w = _out(out, "weights", (T, top_k), torch.float32, X.device)
+    L = lib()
+    ws = _ws(ws, lambda: L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, top_k), X.device)
+    _check(L.swiglu_mlp_moe_fwd_nograd(_ptr(X), _ptr(Wr), _ptr(gu), _ptr(down), _ptr(Y), _ptr(idx),
+                                       _ptr(w), T, D, H, E, top_k, int(norm_topk),
+                                       float(route_scale), fmt, dtype_code(X.dtype),
+                                       _opts(gate_mul, down_mul, False), _ptr(ws), ws.numel(),
+                                       _serving_checks(X, Wr, gu, down, ws)),
+           "swiglu_mlp_moe_fwd_nograd")
+    _device_check(ws, "swiglu_mlp_moe_fwd_nograd")
+    return Y, idx, w
 
 
 def swiglu_mlp_query_error(ws) -> int:

@@ -26,7 +26,7 @@ struct DbgWin {
 };
 
 #ifdef SWIGLU_DEBUG
-__device__ __noinline__ bool dbg_fail(int* err) {
+static __device__ __noinline__ bool dbg_fail(int* err) {
   atomicCAS(err, DEV_ERR_NONE, DEV_ERR_BOUNDS);
   return false;
 }

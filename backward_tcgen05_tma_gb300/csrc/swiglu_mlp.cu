@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "../../include/swiglu_mlp.h"
+#include "../csrc_serving/host_shared.h"
 #include "ng_fused.cuh"
 #include "ng_gemm.cuh"
 #include "simt_gemm.cuh"
@@ -115,12 +116,14 @@ constexpr int TC2_STAGES = 6;
 enum KernelId : int {
   K_GATE_UP = 0, K_DOWN, K_DGU, K_DWD, K_DWGU, K_DX, K_GATE_UP_NOGRAD, K_DOWN_NOGRAD,
   K_SIMT_GATE_UP, K_SIMT_DOWN, K_SIMT_DGU, K_SIMT_DWD, K_SIMT_DWGU, K_SIMT_DX, K_NG_GATE_UP,
-  K_NG_DOWN, K_NG_FUSED, K_COUNT
+  K_NG_DOWN, K_NG_FUSED, K_SERVING, K_COUNT = K_SERVING + swiglu::host::SK_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {
     "gate_up_swiglu", "down_proj", "dgu_inplace", "dwd", "dwgu", "dx", "gate_up_nograd",
     "down_proj_nograd", "simt_gate_up_swiglu", "simt_down_proj", "simt_dgu_inplace", "simt_dwd",
-    "simt_dwgu", "simt_dx", "nograd_small_gate_up", "nograd_small_down", "nograd_small_fused"};
+    "simt_dwgu", "simt_dx", "nograd_small_gate_up", "nograd_small_down", "nograd_small_fused",
+    "w4_linear", "w4_gate_up", "w4_down", "moe_route", "moe_gate_up", "moe_down",
+    "moe_w4_gate_up", "moe_w4_down"};
 
 struct ProfRec {
   int id;
@@ -1179,6 +1182,41 @@ __global__ void elementwise_test_kernel(int64_t chunks, const float* acc_g, cons
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------------------
+// the host state shared with the other translation units
+// ---------------------------------------------------------------------------
+namespace swiglu {
+namespace host {
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+bool take_stall() { return take_inject(); }
+void reset_launches() { g_last_launches.store(0); }
+void count_launch() { g_last_launches.fetch_add(1); }
+int sms() { return sm_count(); }
+bool profiling() { return g_prof_on.load() != 0; }
+
+Prof::Prof(ServingKernel id, cudaStream_t st) : st_(st) {
+  if (!g_prof_on.load()) return;
+  std::lock_guard<std::mutex> g(g_prof_mu);
+  cudaEvent_t a = prof_event();
+  end_ = prof_event();
+  cudaEventRecord(a, st);
+  g_prof_pending.push_back(ProfRec{K_SERVING + (int)id, a, end_});
+}
+
+Prof::~Prof() {
+  if (end_ != nullptr) cudaEventRecord(end_, st_);
+}
+
+#ifdef SWIGLU_DEBUG
+DbgWin windows(std::initializer_list<std::pair<const void*, size_t>> wins) {
+  return make_windows(wins);
+}
+#endif
+
+}  // namespace host
+}  // namespace swiglu
 
 // ===========================================================================
 // C ABI

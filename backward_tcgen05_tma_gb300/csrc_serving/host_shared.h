@@ -1,0 +1,49 @@
+// host_shared.h -- the process-wide host state of the library (wait limit,
+// stall injection, launch count, per-kernel timing, debug windows), defined in
+// csrc/swiglu_mlp.cu and used by every translation unit that launches kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <initializer_list>
+#include <utility>
+
+#include "../csrc/sm103_ptx.cuh"
+
+namespace swiglu {
+namespace host {
+
+// Kernel ids of the per-kernel timing (swiglu_mlp_profile_read), after those
+// of the training and dense no-grad kernels.
+enum ServingKernel : int {
+  SK_W4_LINEAR = 0, SK_W4_GATE_UP, SK_W4_DOWN, SK_MOE_ROUTE, SK_MOE_GATE_UP, SK_MOE_DOWN,
+  SK_MOE_W4_GATE_UP, SK_MOE_W4_DOWN, SK_COUNT
+};
+
+uint64_t wait_limit_ns();
+bool take_stall();       // true for the launch that swiglu_mlp_inject_stall_once chose
+void reset_launches();   // at the start of an entry point
+void count_launch();
+int sms();               // SMs of the current device
+bool profiling();
+
+// Brackets one launch with events while per-kernel timing is enabled.
+class Prof {
+ public:
+  Prof(ServingKernel id, cudaStream_t st);
+  ~Prof();
+  Prof(const Prof&) = delete;
+  Prof& operator=(const Prof&) = delete;
+
+ private:
+  cudaStream_t st_;
+  cudaEvent_t end_ = nullptr;
+};
+
+#ifdef SWIGLU_DEBUG
+DbgWin windows(std::initializer_list<std::pair<const void*, size_t>> wins);
+#endif
+
+}  // namespace host
+}  // namespace swiglu

@@ -1,0 +1,510 @@
+// serving.cu -- C ABI of the few-token serving operators
+// (include/swiglu_mlp.h): 4-bit weights and mixture-of-experts layers.
+// Argument checks, shared-memory plans and launches.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/swiglu_mlp.h"
+#include "fewtok.cuh"
+#include "host_shared.h"
+#include "moe_route.cuh"
+#include "w4_layout.cuh"
+
+using namespace swiglu;
+
+namespace {
+
+constexpr int64_t LIMIT = 0x7fffffffLL;
+constexpr size_t HEADER = 256;  // workspace header: the error word
+
+swiglu_status status_of(cudaError_t e) { return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA; }
+
+bool sixteen_bit(swiglu_dtype dt) { return dt == SWIGLU_BF16 || dt == SWIGLU_F16; }
+
+swiglu_status check_ptrs(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p == nullptr) return SWIGLU_ERR_INVALID_ARG;
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return SWIGLU_ERR_ALIGNMENT;
+  return SWIGLU_OK;
+}
+
+int log2_group(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
+
+// One 4-bit matrix [N, K]: sizes, group and zero-point flag.
+swiglu_status check_w4(int64_t E, int64_t N, int64_t K, int group, int zeros) {
+  if (E <= 0 || N <= 0 || K <= 0) return SWIGLU_ERR_INVALID_ARG;
+  if (log2_group(group) < 0 || (zeros != 0 && zeros != 1)) return SWIGLU_ERR_INVALID_ARG;
+  if (K % 8 != 0) return SWIGLU_ERR_ALIGNMENT;
+  if (E > LIMIT || N > LIMIT || K > LIMIT) return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+
+swiglu_status check_ws(const void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr || bytes < need) return SWIGLU_ERR_WORKSPACE;
+  return (reinterpret_cast<uintptr_t>(ws) & 15u) ? SWIGLU_ERR_ALIGNMENT : SWIGLU_OK;
+}
+
+struct Muls {
+  float gate = 1.0f, down = 1.0f;
+};
+swiglu_status read_muls(const swiglu_mlp_options* o, Muls* m) {
+  if (o == nullptr) return SWIGLU_OK;
+  if (!std::isfinite(o->gate_multiplier) || !std::isfinite(o->down_multiplier) || o->accumulate != 0)
+    return SWIGLU_ERR_INVALID_ARG;
+  m->gate = o->gate_multiplier;
+  m->down = o->down_multiplier;
+  return SWIGLU_OK;
+}
+
+// The dynamic shared memory of a kernel, raised once per device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+
+constexpr int SMEM_ONE = 226 * 1024;  // one block per SM
+constexpr int SMEM_TWO = 112 * 1024;  // two
+
+template <bool BF16, bool W4, int NT, bool MOE>
+cudaError_t launch_ft(host::ServingKernel id, FtArgs a, cudaStream_t st) {
+  using S = FtShape<W4, NT>;
+  constexpr auto kern = ft_kernel<BF16, W4, NT, MOE>;
+  cudaError_t e = allow_smem<kern>(SMEM_ONE);
+  if (e != cudaSuccess) return e;
+  auto up = [](int v) { return (v + 127) & ~127; };
+  a.xrows = a.M < S::TOKENS ? a.M : S::TOKENS;
+  a.list_off = up(16 * FT_MAX_STAGES + 16) + (MOE ? FT_MAX_TOKENS * 16 * 4 : 0);
+  a.red_off = a.list_off + (MOE ? ft_lists_bytes(a.M, a.topk, a.E, S::TOKENS) : 0);
+  a.ring_off = a.red_off + S::RED_BYTES;
+  int b = W4 ? S::KC / 64 * 512 : 16 * S::ROW;
+  a.sc_off = b;
+  if (W4) b += (S::KC >> a.group_log2) * 32;
+  a.z_off = b;
+  if (W4 && a.zeros) b += (S::KC >> a.group_log2) * 16;
+  a.x_off = up(b);
+  a.stage_bytes = up(a.x_off + a.xrows * S::ROW);
+  int per_sm = 2;
+  int stages = (SMEM_TWO - a.ring_off) / a.stage_bytes;
+  if (stages < 2) {
+    per_sm = 1;
+    stages = (SMEM_ONE - a.ring_off) / a.stage_bytes;
+  }
+  if (stages < 1) return cudaErrorInvalidConfiguration;
+  a.stages = stages < FT_MAX_STAGES ? stages : FT_MAX_STAGES;
+  const int smem = a.ring_off + a.stages * a.stage_bytes;
+  int64_t items = a.tiles;
+  if (!(MOE && a.mode == FT_COMBINE))
+    items *= MOE ? ft_max_entries(a.M, a.topk, a.E, S::TOKENS) : (a.M + S::TOKENS - 1) / S::TOKENS;
+  const int nsm = host::sms();
+  const int64_t most = (int64_t)(nsm > 0 ? nsm : 1) * per_sm;
+  a.wait_limit_ns = host::wait_limit_ns();
+  a.inject = host::take_stall() ? 1 : 0;
+  host::Prof prof(id, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+  cfg.blockDim = dim3(FT_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // per-kernel event timing would serialise the launches, so no overlap then
+  if (host::profiling()) a.dependent = 0;
+  cfg.attrs = a.dependent ? attr : nullptr;
+  cfg.numAttrs = a.dependent ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  host::count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Tokens per pass over a tile: 8, 16 or 32 columns (more take several passes).
+template <bool BF16, bool W4, bool MOE>
+cudaError_t launch_nt(host::ServingKernel id, const FtArgs& a, int tokens, cudaStream_t st) {
+  if (tokens <= 8) return launch_ft<BF16, W4, 1, MOE>(id, a, st);
+  if (tokens <= 16) return launch_ft<BF16, W4, 2, MOE>(id, a, st);
+  return launch_ft<BF16, W4, 4, MOE>(id, a, st);
+}
+
+template <bool W4, bool MOE>
+cudaError_t launch_dt(host::ServingKernel id, const FtArgs& a, int tokens, swiglu_dtype dt,
+                      cudaStream_t st) {
+  return dt == SWIGLU_BF16 ? launch_nt<true, W4, MOE>(id, a, tokens, st)
+                           : launch_nt<false, W4, MOE>(id, a, tokens, st);
+}
+
+void set_w4(FtArgs& a, const W4Geom& w) {
+  a.tiles = w.tiles;
+  a.expert_bytes = w.bytes;
+  a.group_log2 = w.group_log2;
+  a.groups = w.groups;
+  a.zeros = w.zeros;
+  a.scales_off = w.scales_off;
+  a.zeros_off = w.zeros_off;
+}
+
+#ifdef SWIGLU_DEBUG
+#define SET_WINDOWS(args, ...) (args).dbg = host::windows(__VA_ARGS__)
+#else
+#define SET_WINDOWS(args, ...) (void)0
+#endif
+
+int grid_for(int64_t threads) {
+  const int64_t want = (threads + 255) / 256, most = (int64_t)(host::sms() > 0 ? host::sms() : 1) * 8;
+  return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+size_t moe_inner_bytes(int64_t T, int64_t H, int topk) {
+  return ((size_t)T * (size_t)topk * (size_t)H * 2 + 255) & ~(size_t)255;
+}
+
+// Sizes, types and formats of a mixture-of-experts layer.
+swiglu_status check_moe(int64_t T, int64_t D, int64_t H, int64_t E, int64_t topk,
+                        const swiglu_mlp_w4_format* f, swiglu_dtype dt) {
+  if (dt != SWIGLU_F32_IEEE && !sixteen_bit(dt)) return SWIGLU_ERR_INVALID_ARG;
+  if (!sixteen_bit(dt)) return SWIGLU_ERR_UNSUPPORTED;
+  if (T < 0 || D <= 0 || H <= 0 || E <= 0 || topk <= 0 || topk > E) return SWIGLU_ERR_INVALID_ARG;
+  if (f != nullptr && (log2_group(f->group) < 0 || (f->zeros != 0 && f->zeros != 1)))
+    return SWIGLU_ERR_INVALID_ARG;
+  if (D % 8 != 0 || H % 8 != 0) return SWIGLU_ERR_ALIGNMENT;
+  if (T > FT_MAX_TOKENS || E > FT_MAX_EXPERTS || topk > FT_MAX_TOPK || D > LIMIT / 2 || H > LIMIT / 2)
+    return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+
+// Token columns per pass for a mixture of experts: an expert meets T topk / E
+// tokens on average; one with more takes several passes over its weights.
+int moe_tokens(int64_t T, int64_t E, int64_t topk) {
+  if (T <= 8) return 8;
+  return 2 * T * topk <= 16 * E ? 8 : T <= 16 || 3 * T * topk <= 32 * E ? 16 : 32;
+}
+
+// The experts of a layer: gate/up over the active experts' rows into the
+// assignments' hidden values (workspace), then down and the weighted sums.
+swiglu_status run_experts(const void* X, const int* idx, const float* wts, const void* Wgu,
+                          const void* Wd, void* Y, int T, int D, int H, int E, int topk,
+                          const swiglu_mlp_w4_format* f, swiglu_dtype dt, const Muls& mu, char* ws,
+                          size_t ws_bytes, bool after_router, cudaStream_t st) {
+  (void)ws_bytes;
+  void* A = ws + HEADER;
+  FtArgs a = {};
+  a.mode = FT_GATE_UP;
+  a.M = T;
+  a.K = D;
+  a.rows = H;
+  a.tiles = (H + 7) / 8;
+  a.W = static_cast<const uint8_t*>(Wgu);
+  a.expert_bytes = (int64_t)2 * H * D * 2;
+  a.X = X;
+  a.out = A;
+  a.scale = mu.gate;
+  a.E = E;
+  a.topk = topk;
+  a.idx = idx;
+  a.wts = wts;
+  a.dependent = after_router ? 1 : 0;
+  a.clear_err = after_router ? 0 : 1;
+  a.err = reinterpret_cast<int*>(ws);
+  if (f != nullptr) set_w4(a, w4_geom(2 * (int64_t)H, D, log2_group(f->group), f->zeros, 1));
+  SET_WINDOWS(a, {{A, (size_t)T * topk * H * 2},
+                  {idx, (size_t)T * topk * 4},
+                  {wts, (size_t)T * topk * 4},
+                  {ws, ws_bytes}});
+  const int tokens = moe_tokens(T, E, topk);
+  cudaError_t e = f != nullptr ? launch_dt<true, true>(host::SK_MOE_W4_GATE_UP, a, tokens, dt, st)
+                               : launch_dt<false, true>(host::SK_MOE_GATE_UP, a, tokens, dt, st);
+  if (e != cudaSuccess) return SWIGLU_ERR_CUDA;
+  a.mode = FT_COMBINE;
+  a.K = H;
+  a.rows = D;
+  a.tiles = (D + 15) / 16;
+  a.W = static_cast<const uint8_t*>(Wd);
+  a.expert_bytes = (int64_t)D * H * 2;
+  a.X = A;
+  a.out = Y;
+  a.scale = mu.down;
+  a.dependent = 1;
+  a.idx_ready = 1;
+  a.clear_err = 0;
+  if (f != nullptr) set_w4(a, w4_geom(D, H, log2_group(f->group), f->zeros, 0));
+  SET_WINDOWS(a, {{Y, (size_t)T * D * 2},
+                  {idx, (size_t)T * topk * 4},
+                  {wts, (size_t)T * topk * 4},
+                  {ws, ws_bytes}});
+  e = f != nullptr ? launch_dt<true, true>(host::SK_MOE_W4_DOWN, a, tokens, dt, st)
+                   : launch_dt<false, true>(host::SK_MOE_DOWN, a, tokens, dt, st);
+  return status_of(e);
+}
+
+swiglu_status run_route(const void* X, const void* Wr, int* idx, float* wts, int T, int D, int E,
+                        int topk, int norm, float scale, swiglu_dtype dt, int* err,
+                        cudaStream_t st) {
+  RtArgs a = {};
+  a.X = static_cast<const uint8_t*>(X);
+  a.Wr = static_cast<const uint8_t*>(Wr);
+  a.idx = idx;
+  a.wts = wts;
+  a.M = T;
+  a.D = D;
+  a.E = E;
+  a.topk = topk;
+  a.norm = norm;
+  a.scale = scale;
+  a.err = err;
+  SET_WINDOWS(a, {{idx, (size_t)T * topk * 4},
+                  {wts, (size_t)T * topk * 4},
+                  {X, (size_t)T * D * 2},
+                  {Wr, (size_t)E * D * 2}});
+  const int blocks = (E + 7) / 8 < RT_CLUSTER ? (E + 7) / 8 : RT_CLUSTER;
+  a.per_block = (E + blocks - 1) / blocks;
+  host::Prof prof(host::SK_MOE_ROUTE, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((T + RT_TOKENS - 1) / RT_TOKENS * blocks));
+  cfg.blockDim = dim3(RT_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)blocks, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = dt == SWIGLU_BF16 ? cudaLaunchKernelEx(&cfg, route_kernel<true>, a)
+                                    : cudaLaunchKernelEx(&cfg, route_kernel<false>, a);
+  host::count_launch();
+  return status_of(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t swiglu_mlp_w4_packed_bytes(int64_t E, int64_t N, int64_t K, int group, int zeros,
+                                  int gate_up) {
+  if (check_w4(E, N, K, group, zeros) != SWIGLU_OK || (gate_up && N % 2 != 0)) return 0;
+  return (size_t)(w4_geom(N, K, log2_group(group), zeros, gate_up ? 1 : 0).bytes) * (size_t)E;
+}
+
+swiglu_status swiglu_mlp_w4_quantize(const void* W, void* codes, void* scales, void* zeros,
+                                     int64_t N, int64_t K, int group, swiglu_dtype dtype,
+                                     void* stream) {
+  host::reset_launches();
+  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  swiglu_status st = check_w4(1, N, K, group, zeros != nullptr);
+  if (st != SWIGLU_OK) return st;
+  if ((st = check_ptrs({W, codes, scales})) != SWIGLU_OK) return st;
+  if (reinterpret_cast<uintptr_t>(zeros) & 15u) return SWIGLU_ERR_ALIGNMENT;
+  const int lg = log2_group(group), groups = (int)((K + group - 1) / group);
+  const int grid = grid_for(N * ((int64_t)groups << (lg - 3)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto k = dtype == SWIGLU_BF16 ? w4_quantize_kernel<true> : w4_quantize_kernel<false>;
+  k<<<grid, 256, 0, s>>>(N, (int)K, lg, groups, static_cast<const uint16_t*>(W),
+                         static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales),
+                         static_cast<uint8_t*>(zeros));
+  host::count_launch();
+  return status_of(cudaGetLastError());
+}
+
+swiglu_status swiglu_mlp_w4_pack(const void* codes, const void* scales, const void* zeros,
+                                 void* packed, int64_t E, int64_t N, int64_t K, int group,
+                                 int gate_up, swiglu_dtype dtype, void* stream) {
+  host::reset_launches();
+  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  swiglu_status st = check_w4(E, N, K, group, zeros != nullptr);
+  if (st != SWIGLU_OK) return st;
+  if (gate_up && N % 16 != 0) return SWIGLU_ERR_ALIGNMENT;
+  if ((st = check_ptrs({codes, scales, packed})) != SWIGLU_OK) return st;
+  if (reinterpret_cast<uintptr_t>(zeros) & 15u) return SWIGLU_ERR_ALIGNMENT;
+  const W4Geom w = w4_geom(N, K, log2_group(group), zeros != nullptr, gate_up ? 1 : 0);
+  const int grid = grid_for(((int64_t)w.tiles * w.blocks * 32 + (int64_t)w.tiles * w.groups * 16) * E);
+  w4_pack_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      w, E, static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
+      static_cast<const uint8_t*>(zeros), static_cast<uint8_t*>(packed));
+  host::count_launch();
+  return status_of(cudaGetLastError());
+}
+
+swiglu_status swiglu_mlp_w4_unpack(const void* packed, void* W, int64_t E, int64_t N, int64_t K,
+                                   int group, int zeros, int gate_up, swiglu_dtype dtype,
+                                   void* stream) {
+  host::reset_launches();
+  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  swiglu_status st = check_w4(E, N, K, group, zeros);
+  if (st != SWIGLU_OK) return st;
+  if (gate_up && N % 16 != 0) return SWIGLU_ERR_ALIGNMENT;
+  if ((st = check_ptrs({packed, W})) != SWIGLU_OK) return st;
+  const W4Geom w = w4_geom(N, K, log2_group(group), zeros, gate_up ? 1 : 0);
+  const int grid = grid_for((int64_t)w.tiles * w.blocks * 32 * E);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto k = dtype == SWIGLU_BF16 ? w4_unpack_kernel<true> : w4_unpack_kernel<false>;
+  k<<<grid, 256, 0, s>>>(w, E, static_cast<const uint8_t*>(packed), static_cast<uint16_t*>(W));
+  host::count_launch();
+  return status_of(cudaGetLastError());
+}
+
+size_t swiglu_mlp_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  (void)M;
+  (void)N;
+  (void)K;
+  return HEADER;
+}
+
+size_t swiglu_mlp_fwd_nograd_w4_workspace_bytes(int64_t M, int64_t D, int64_t H) {
+  const size_t a = swiglu_mlp_w4_workspace_bytes(M, 2 * H, D), b = swiglu_mlp_w4_workspace_bytes(M, D, H);
+  return a > b ? a : b;
+}
+
+swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, int64_t M, int64_t N,
+                                   int64_t K, int group, int zeros, swiglu_dtype dtype, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  host::reset_launches();
+  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  if (M < 0) return SWIGLU_ERR_INVALID_ARG;
+  swiglu_status st = check_w4(1, N, K, group, zeros);
+  if (st != SWIGLU_OK) return st;
+  if (M > FT_MAX_TOKENS) return SWIGLU_ERR_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, swiglu_mlp_w4_workspace_bytes(M, N, K))) != SWIGLU_OK) return st;
+  if (M == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, packed, Y})) != SWIGLU_OK) return st;
+  FtArgs a = {};
+  a.mode = FT_LINEAR;
+  a.M = (int)M;
+  a.K = (int)K;
+  a.rows = (int)N;
+  a.W = static_cast<const uint8_t*>(packed);
+  a.X = X;
+  a.out = Y;
+  a.scale = 1.0f;
+  a.clear_err = 1;
+  a.err = static_cast<int*>(ws);
+  set_w4(a, w4_geom(N, K, log2_group(group), zeros, 0));
+  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {ws, ws_bytes}});
+  return status_of(launch_dt<true, false>(host::SK_W4_LINEAR, a, (int)M, dtype,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const void* Wd, void* Y,
+                                       void* A, int64_t M, int64_t D, int64_t H, int group,
+                                       int zeros, swiglu_dtype dtype,
+                                       const swiglu_mlp_options* options, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  host::reset_launches();
+  Muls mu;
+  swiglu_status st = read_muls(options, &mu);
+  if (st != SWIGLU_OK) return st;
+  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  if (M < 0) return SWIGLU_ERR_INVALID_ARG;
+  if ((st = check_w4(1, D, H, group, zeros)) != SWIGLU_OK) return st;
+  if (D % 8 != 0) return SWIGLU_ERR_ALIGNMENT;
+  if (M > FT_MAX_TOKENS || H > LIMIT / 2) return SWIGLU_ERR_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, swiglu_mlp_fwd_nograd_w4_workspace_bytes(M, D, H))) != SWIGLU_OK)
+    return st;
+  if (M == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, Wgu, Wd, Y, A})) != SWIGLU_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  FtArgs a = {};
+  a.mode = FT_GATE_UP;
+  a.M = (int)M;
+  a.K = (int)D;
+  a.rows = (int)H;
+  a.W = static_cast<const uint8_t*>(Wgu);
+  a.X = X;
+  a.out = A;
+  a.scale = mu.gate;
+  a.clear_err = 1;
+  a.err = static_cast<int*>(ws);
+  set_w4(a, w4_geom(2 * H, D, log2_group(group), zeros, 1));
+  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {ws, ws_bytes}});
+  if (launch_dt<true, false>(host::SK_W4_GATE_UP, a, (int)M, dtype, s) != cudaSuccess)
+    return SWIGLU_ERR_CUDA;
+  a.mode = FT_LINEAR;
+  a.K = (int)H;
+  a.rows = (int)D;
+  a.W = static_cast<const uint8_t*>(Wd);
+  a.X = A;
+  a.out = Y;
+  a.scale = mu.down;
+  a.dependent = 1;
+  a.clear_err = 0;
+  set_w4(a, w4_geom(D, H, log2_group(group), zeros, 0));
+  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {ws, ws_bytes}});
+  return status_of(launch_dt<true, false>(host::SK_W4_DOWN, a, (int)M, dtype, s));
+}
+
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int topk) {
+  (void)D;
+  (void)E;
+  if (T < 0 || H <= 0 || topk <= 0) return 0;
+  return HEADER + moe_inner_bytes(T, H, topk);
+}
+
+swiglu_status swiglu_mlp_moe_route(const void* X, const void* Wr, int32_t* idx, float* weights,
+                                   int64_t T, int64_t D, int64_t E, int topk, int norm_topk,
+                                   float route_scale, swiglu_dtype dtype, void* stream) {
+  host::reset_launches();
+  swiglu_status st = check_moe(T, D, 8, E, topk, nullptr, dtype);
+  if (st != SWIGLU_OK) return st;
+  if ((norm_topk != 0 && norm_topk != 1) || !std::isfinite(route_scale))
+    return SWIGLU_ERR_INVALID_ARG;
+  if (T == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, Wr, idx, weights})) != SWIGLU_OK) return st;
+  return run_route(X, Wr, idx, weights, (int)T, (int)D, (int)E, topk, norm_topk, route_scale, dtype,
+                   nullptr, static_cast<cudaStream_t>(stream));
+}
+
+swiglu_status swiglu_mlp_moe_experts(const void* X, const int32_t* idx, const float* weights,
+                                     const void* Wgu, const void* Wd, void* Y, int64_t T, int64_t D,
+                                     int64_t H, int64_t E, int topk,
+                                     const swiglu_mlp_w4_format* format, swiglu_dtype dtype,
+                                     const swiglu_mlp_options* options, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  host::reset_launches();
+  Muls mu;
+  swiglu_status st = read_muls(options, &mu);
+  if (st != SWIGLU_OK) return st;
+  if ((st = check_moe(T, D, H, E, topk, format, dtype)) != SWIGLU_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, swiglu_mlp_moe_workspace_bytes(T, D, H, E, topk))) != SWIGLU_OK)
+    return st;
+  if (T == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, idx, weights, Wgu, Wd, Y})) != SWIGLU_OK) return st;
+  return run_experts(X, idx, weights, Wgu, Wd, Y, (int)T, (int)D, (int)H, (int)E, topk, format, dtype,
+                     mu, static_cast<char*>(ws), ws_bytes, false, static_cast<cudaStream_t>(stream));
+}
+
+swiglu_status swiglu_mlp_moe_fwd_nograd(const void* X, const void* Wr, const void* Wgu,
+                                        const void* Wd, void* Y, int32_t* idx, float* weights,
+                                        int64_t T, int64_t D, int64_t H, int64_t E, int topk,
+                                        int norm_topk, float route_scale,
+                                        const swiglu_mlp_w4_format* format, swiglu_dtype dtype,
+                                        const swiglu_mlp_options* options, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  host::reset_launches();
+  Muls mu;
+  swiglu_status st = read_muls(options, &mu);
+  if (st != SWIGLU_OK) return st;
+  if ((st = check_moe(T, D, H, E, topk, format, dtype)) != SWIGLU_OK) return st;
+  if ((norm_topk != 0 && norm_topk != 1) || !std::isfinite(route_scale))
+    return SWIGLU_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, swiglu_mlp_moe_workspace_bytes(T, D, H, E, topk))) != SWIGLU_OK)
+    return st;
+  if (T == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, Wr, Wgu, Wd, Y, idx, weights})) != SWIGLU_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = run_route(X, Wr, idx, weights, (int)T, (int)D, (int)E, topk, norm_topk, route_scale, dtype,
+                 static_cast<int*>(ws), s);
+  if (st != SWIGLU_OK) return st;
+  return run_experts(X, idx, weights, Wgu, Wd, Y, (int)T, (int)D, (int)H, (int)E, topk, format, dtype,
+                     mu, static_cast<char*>(ws), ws_bytes, true, s);
+}
+
+}  // extern "C"

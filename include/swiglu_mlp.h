@@ -291,6 +291,126 @@ swiglu_status swiglu_mlp_bwd_ex(const void* dY, const void* X, const void* Wgu, 
                                 const swiglu_mlp_options* options, void* ws, size_t ws_bytes,
                                 void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Few-token serving: 4-bit weights and mixture-of-experts layers (T, M <= 64
+ * tokens, bf16 or fp16, no gradients).  The pages have no counterpart: these
+ * are this library's forms of the no-grad path for weights that are kept in 4
+ * bits and for layers whose MLP is a choice of experts.  Both are bound by the
+ * bytes of the weights.
+ *
+ * 4-bit weights.  A matrix [N, K] (K a multiple of 8) is
+ *     W[n, k] = s[n, k / group] * (q[n, k] - z[n, k / group]),
+ * codes q in 0..15, `group` 32, 64 or 128 consecutive k per scale (the last
+ * group of a row may be a part of one), and zero points z in 0..15, or 8
+ * everywhere when there are none.  In their plain form
+ *     codes   uint8 [N, K/2]   byte b of a row: q[2b] low, q[2b + 1] high
+ *     scales  16-bit [N, ceil(K/group)], in the activations' type
+ *     zeros   uint8 [N, ceil(K/group)], or NULL
+ * The products read a packed copy (swiglu_mlp_w4_pack; the layout is described
+ * in csrc_serving/w4_layout.cuh).  They multiply the whole numbers q - z by
+ * the tokens on the tensor cores and apply the scales to fp32 partial sums, so
+ * no weight is rounded; sums are fp32, outputs rounded once.
+ *
+ * Every call below obeys the rules above: device pointers, 16-byte aligned,
+ * argument errors before any launch, asynchronous on `stream`, deterministic;
+ * 0 tokens launch nothing; more than 64 tokens and SWIGLU_F32_IEEE return
+ * SWIGLU_ERR_UNSUPPORTED (expand the weights with swiglu_mlp_w4_unpack and
+ * use the training or no-grad calls).  Workspaces follow the workspace rules
+ * (zero-filled before first use, error word for swiglu_mlp_query_error). */
+
+/* Bytes of E packed matrices; gate_up: each is a pair [Wg; Wu], N = 2H.  0 for
+ * invalid arguments. */
+size_t swiglu_mlp_w4_packed_bytes(int64_t E, int64_t N, int64_t K, int group, int zeros,
+                                  int gate_up);
+
+/* Rounds W [N, K] (bf16 or fp16, finite) to codes and scales, and with a
+ * non-NULL `zeros` to zero points too, by each group's values:
+ *   zeros == NULL:  s = rnd(max |w| / 7),  q = clamp(rint(w / s) + 8, 0, 15)
+ *   else, with lo = min(w, 0), hi = max(w, 0) over the group:
+ *                   s = rnd((hi - lo) / 15),  z = clamp(rint(-lo / s), 0, 15),
+ *                   q = clamp(rint(w / s) + z, 0, 15)
+ * (rnd: to the 16-bit type; rint: to even; a group whose s is 0 gets q = z =
+ * 8). */
+swiglu_status swiglu_mlp_w4_quantize(const void* W, void* codes, void* scales, void* zeros,
+                                     int64_t N, int64_t K, int group, swiglu_dtype dtype,
+                                     void* stream);
+
+/* Writes the packed copy of E matrices (codes [E, N, K/2], scales, zeros or
+ * NULL) that the calls below stream.  gate_up: the rows are [Wg; Wu] pairs (N
+ * = 2H, H a multiple of 8), laid out so that a hidden unit's two rows meet. */
+swiglu_status swiglu_mlp_w4_pack(const void* codes, const void* scales, const void* zeros,
+                                 void* packed, int64_t E, int64_t N, int64_t K, int group,
+                                 int gate_up, swiglu_dtype dtype, void* stream);
+
+/* The inverse: W [E, N, K] in 16 bits, each weight s * (q - z) rounded once. */
+swiglu_status swiglu_mlp_w4_unpack(const void* packed, void* W, int64_t E, int64_t N, int64_t K,
+                                   int group, int zeros, int gate_up, swiglu_dtype dtype,
+                                   void* stream);
+
+/* Workspace bytes of swiglu_mlp_w4_linear and swiglu_mlp_fwd_nograd_w4. */
+size_t swiglu_mlp_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t swiglu_mlp_fwd_nograd_w4_workspace_bytes(int64_t M, int64_t D, int64_t H);
+
+/* Y [M, N] = X [M, K] W^T for 0 <= M <= 64 tokens, W packed without gate_up;
+ * `zeros` is 1 when the packed copy has zero points.  N >= 1 need not be a
+ * multiple of anything. */
+swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, int64_t M, int64_t N,
+                                   int64_t K, int group, int zeros, swiglu_dtype dtype, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* The no-grad MLP on 4-bit weights for 0 <= M <= 64 tokens: A [M, H] =
+ * SiLU(mg X Wg^T) * (X Wu^T) rounded once, Y [M, D] = md (A Wd^T).  Wgu is
+ * packed with gate_up, Wd without; both have the same group and zero-point
+ * flag.  options: the gate/down multipliers, or NULL. */
+swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const void* Wd, void* Y,
+                                       void* A, int64_t M, int64_t D, int64_t H, int group,
+                                       int zeros, swiglu_dtype dtype,
+                                       const swiglu_mlp_options* options, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* Mixture of experts: E <= 512 experts, each a SwiGLU MLP (Wgu [E, 2H, D], Wd
+ * [E, D, H]), of which a router picks topk <= 16 for each of T <= 64 tokens:
+ *     l = X Wr^T (Wr [E, D]; fp32),  p = softmax(l),
+ *     the topk largest l, a tie going to the lower index (idx [T, topk], in
+ *     descending order),  weights = route_scale p, or with norm_topk
+ *     route_scale p / (sum of the chosen p)   (fp32 [T, topk]),
+ *     Y[t] = md sum_j weights[t, j] MLP_{idx[t, j]}(X[t])   (fp32 sum, one
+ *     rounding; the hidden values are rounded once, as A above).
+ * A NaN logit counts as the largest; the weights of its token are NaN. */
+typedef struct {
+  int group;  /* 32, 64 or 128 */
+  int zeros;  /* the packed copies have zero points */
+} swiglu_mlp_w4_format;
+
+/* Workspace bytes of the two calls that run experts. */
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int topk);
+
+/* The router alone: writes idx and weights.  No workspace. */
+swiglu_status swiglu_mlp_moe_route(const void* X, const void* Wr, int32_t* idx, float* weights,
+                                   int64_t T, int64_t D, int64_t E, int topk, int norm_topk,
+                                   float route_scale, swiglu_dtype dtype, void* stream);
+
+/* The experts alone, on idx [T, topk] and weights [T, topk] given by the
+ * caller.  An idx outside 0..E-1 is no expert (a token without any gets a row
+ * of zeros); an expert named twice by one token counts with the sum of its
+ * weights.  format NULL: Wgu and Wd are 16-bit row-major; else packed 4-bit
+ * copies of the E matrices (Wgu with gate_up). */
+swiglu_status swiglu_mlp_moe_experts(const void* X, const int32_t* idx, const float* weights,
+                                     const void* Wgu, const void* Wd, void* Y, int64_t T, int64_t D,
+                                     int64_t H, int64_t E, int topk,
+                                     const swiglu_mlp_w4_format* format, swiglu_dtype dtype,
+                                     const swiglu_mlp_options* options, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* The whole layer: router, experts, weighted sum. */
+swiglu_status swiglu_mlp_moe_fwd_nograd(const void* X, const void* Wr, const void* Wgu,
+                                        const void* Wd, void* Y, int32_t* idx, float* weights,
+                                        int64_t T, int64_t D, int64_t H, int64_t E, int topk,
+                                        int norm_topk, float route_scale,
+                                        const swiglu_mlp_w4_format* format, swiglu_dtype dtype,
+                                        const swiglu_mlp_options* options, void* ws,
+                                        size_t ws_bytes, void* stream);
+
 /* Synchronises ``stream`` and reads the device error word in ``ws``:
  * SWIGLU_OK, SWIGLU_ERR_DEVICE_TIMEOUT, SWIGLU_ERR_DEVICE_BOUNDS (debug
  * builds), or SWIGLU_ERR_CUDA if the stream reported an error. */
