@@ -4,23 +4,33 @@
 //
 //   Y[m, r] = sum_k X[m, k] W[r, k],   W[r, k] = s[r, k/G] (q[r, k] - z[r, k/G])
 //
-// Work: a tile of 16 weight rows (for gate/up 8 rows of Wg and the 8 rows of
-// Wu of the same hidden units) over the whole contraction is one block's; its
-// 8 warps split each chunk of KC elements of k, and their partial tiles meet
-// in shared memory at the tile's end, in warp order, so results are
-// deterministic and no block waits for another.  A ninth warp keeps a ring of
-// chunks filled by bulk copies (cp.async.bulk): the tile's weights, its group
-// scales, and the same chunk of the token rows.
+// Work: a tile of 16 RT weight rows (for gate/up, each 16 are 8 rows of Wg and
+// the 8 rows of Wu of the same hidden units) over the whole contraction, cut
+// into units of 64 k.  A block takes a run of tiles, lays their units end to
+// end and gives each of its 16 warps an equal share; a share that ends inside
+// a tile leaves a partial tile in shared memory, and at the end of the run the
+// block adds each tile's partials in order, applies the epilogue and writes.
+// So warps never wait for one another while they stream, shares are even for
+// any size, and results are deterministic.  The combining (down) kernel of a
+// mixture of experts lays the units of ALL experts' tiles of the same output
+// rows end to end, and each warp adds its weighted partials per token.
+//
+// Loads: every lane copies exactly the 16-byte pieces of the weights that it
+// will multiply (cp.async, zero-filled past the end of a row) into a ring of
+// its own in shared memory, several units ahead: a queue per lane, with no
+// barriers, no swizzle (neighbouring lanes are neighbours there) and no
+// registers held.  The token rows, which every tile reads again, come through
+// the L1 cache, one unit ahead in registers.
 //
 // Products: mma.sync m16n8k16 with the weights as the 16-row operand and 8
 // tokens as the columns.  The contraction's order is free, so lane t of a
-// quad takes 8 consecutive k of every 32: token rows and 16-bit weights are
-// read from shared memory by 16-byte loads, and a 4-bit tile is stored so that
-// one 16-byte load brings a lane all its codes of 64 k.  A code becomes a
-// 16-bit number by OR-ing it into the mantissa of 128 (bf16) or 1024 (fp16)
-// and subtracting 128 + z (1024 + z): both steps are exact, so the tensor core
-// multiplies whole numbers by the tokens and each 32-k partial sum is scaled
-// by its group's scale in fp32.  No weight is ever rounded.
+// quad takes 8 consecutive k of every 32: token rows and 16-bit weights come
+// in 16-byte pieces, and a 4-bit tile is stored so that one 16-byte piece
+// holds all of a lane's codes of 64 k.  A code becomes a 16-bit number by
+// OR-ing it into the mantissa of 128 (bf16) or 1024 (fp16) and subtracting
+// 128 + z (1024 + z): both steps are exact, so the tensor core multiplies
+// whole numbers by the tokens and each group's partial sum is scaled in fp32.
+// No weight is ever rounded.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,10 +40,8 @@
 
 namespace swiglu {
 
-constexpr int FT_WARPS = 8;  // consumer warps; one more warp issues the copies
-constexpr int FT_CONSUMERS = FT_WARPS * 32;
-constexpr int FT_THREADS = FT_CONSUMERS + 32;
-constexpr int FT_MAX_STAGES = 16;
+constexpr int FT_WARPS = 16;
+constexpr int FT_THREADS = FT_WARPS * 32;
 constexpr int FT_MAX_TOKENS = 64;
 constexpr int FT_MAX_EXPERTS = 512;
 constexpr int FT_MAX_TOPK = 16;
@@ -46,7 +54,8 @@ struct FtArgs {
   int M;             // tokens
   int K;             // contraction, a multiple of 8
   int rows;          // rows of out: output features, or hidden units (gate/up)
-  int tiles;         // 16-row tiles of one expert's matrix
+  int tiles;         // 16 RT-row tiles of one expert's matrix
+  int tiles16;       // ... and its 16-row tiles
   const uint8_t* W;  // weights: row-major 16-bit [E][R][K], or packed 4-bit matrices
   int64_t expert_bytes;
   const void* X;     // [*, K]: token rows, or (FT_COMBINE) one row per assignment
@@ -63,11 +72,10 @@ struct FtArgs {
   int dependent;     // launched as a programmatic dependent of the kernel before it
   int idx_ready;     // idx was complete before that kernel began
   int clear_err;     // block 0 clears the error word (first kernel of a call)
-  int inject;        // test hook: the first stage is never filled
   // shared-memory plan
-  int xrows;         // token rows of a stage
-  int stages, stage_bytes, sc_off, z_off, x_off, list_off, red_off, ring_off;
-  uint64_t wait_limit_ns;
+  int depth;         // units a warp's ring holds
+  int run;           // tiles of one run
+  int list_off, red_off, ring_off;
   int* err;
 #ifdef SWIGLU_DEBUG
   DbgWin dbg;        // out, X, idx / wts, workspace
@@ -159,21 +167,47 @@ __device__ __forceinline__ void ft_codes(uint32_t w, uint32_t zlo, uint32_t zhi,
 
 __device__ __forceinline__ float ft_silu(float g) { return g / (1.0f + __expf(-g)); }
 
-// k per ring stage: 1024 for 4-bit weights (8 KB of codes), 512 for 16-bit
-// weights (16 KB) and where the token rows would make a stage too large.
-template <bool W4, int NT>
-struct FtShape {
-  static constexpr int KC = W4 && NT <= 2 ? 1024 : 512;
-  static constexpr int UNITS = KC / 64 / FT_WARPS;  // 64-k units of a warp per stage
-  // row stride in shared memory: 64 bytes past a multiple of 128, so that the
-  // 16-byte loads of two neighbouring rows fall into different banks
-  static constexpr int ROW = KC * 2 + 64;
-  static constexpr int TOKENS = 8 * NT;             // tokens of one pass over a tile
-  static constexpr int RED_BYTES = 2 * FT_WARPS * NT * 512;
+// One unit's place in a warp's ring.
+template <bool W4, int RT, int NT, bool G32, bool ZP>
+struct FtUnit {
+  static constexpr int TOKENS = 8 * NT;                 // tokens of one pass over a tile
+  static constexpr int GROUPS = G32 ? 2 : 1;            // groups of 64 k
+  static constexpr int W = 0;                           // RT x (4-bit: 512, 16-bit: 2048) bytes
+  static constexpr int S = RT * (W4 ? 512 : 2048);      // RT x GROUPS x 128: two scales per lane
+  static constexpr int Z = S + (W4 ? RT * GROUPS * 128 : 0);  // and two zero points (in 4 bytes)
+  static constexpr int BYTES = Z + (ZP ? RT * GROUPS * 128 : 0);
+  static constexpr int PART = RT * NT * 512;            // a partial tile
 };
 
-__device__ __forceinline__ void ft_bar_consumers() {
-  asm volatile("bar.sync 1, %0;" ::"n"(FT_CONSUMERS) : "memory");
+__device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+// 16 bytes through the L1 cache.  Not the read-only path: the rows may be
+// written while this kernel's prologue runs (before griddepcontrol.wait).
+__device__ __forceinline__ uint4 ft_load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void cp_async_ca4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most n of this thread's committed groups are incomplete.
+__device__ __forceinline__ void cp_async_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
 }
 
 // The experts' token lists of a call, built by every block for itself in
@@ -270,26 +304,22 @@ __device__ __forceinline__ void ft_build_lists(const FtArgs& a, const FtLists& l
   __syncthreads();
 }
 
-template <bool BF16, bool W4, int NT, bool MOE>
-__global__ void __launch_bounds__(FT_THREADS, 2) ft_kernel(const FtArgs a) {
-  using S = FtShape<W4, NT>;
+// A warp's way through its block's work: runs of tiles, in each run the warp's
+// share [v, v_end) of the units laid end to end, unit v = piece v / nk, k-unit
+// v % nk.  A piece is a tile of the run (linear, gate/up) or one entry's tile
+// (combining).
+struct FtWalk {
+  int run, v, v_end, piece, u;
+};
+
+template <bool BF16, bool W4, int RT, int NT, bool G32, bool ZP, bool MOE>
+__global__ void __launch_bounds__(FT_THREADS, 1) ft_kernel(const FtArgs a) {
+  using U = FtUnit<W4, RT, NT, G32, ZP>;
   using P = Ft16<BF16>;
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t sbase = smem_u32(smem);
-  auto full_bar = [&](int i) { return sbase + 8u * i; };
-  auto empty_bar = [&](int i) { return sbase + 8u * (FT_MAX_STAGES + i); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 16 * FT_MAX_STAGES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   if (blockIdx.x == 0 && a.clear_err && threadIdx.x == 0) *a.err = 0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(full_bar(i), 1);
-      mbar_init(empty_bar(i), FT_WARPS);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
   // A mixture of experts reads idx before anything else.  Where idx comes from
   // the kernel just before (gate/up after the router) that kernel is waited
   // for here, and only then may the next one start: so the combining kernel,
@@ -298,25 +328,40 @@ __global__ void __launch_bounds__(FT_THREADS, 2) ft_kernel(const FtArgs a) {
   if (wait_first) pdl_wait();
   if (a.mode != FT_COMBINE) pdl_launch_dependents();
 
+  const bool combine = MOE && a.mode == FT_COMBINE;
   FtLists l = {};
-  float* yacc = reinterpret_cast<float*>(smem + a.list_off - FT_MAX_TOKENS * 16 * 4);
+  float* red = reinterpret_cast<float*>(smem + a.red_off);
   if (MOE) {
-    l = ft_lists(smem + a.list_off, a, S::TOKENS);
-    if (a.mode == FT_COMBINE)
-      for (int i = threadIdx.x; i < a.M * 16; i += FT_THREADS) yacc[i] = 0.0f;
-    ft_build_lists(a, l, S::TOKENS);
-  } else {
-    __syncthreads();
+    l = ft_lists(smem + a.list_off, a, U::TOKENS);
+    if (combine)
+      for (int i = threadIdx.x; i < FT_WARPS * a.M * 16 * RT; i += FT_THREADS) red[i] = 0.0f;
+    ft_build_lists(a, l, U::TOKENS);
   }
 
-  // the block's work: items of one tile; a combining item goes through every
-  // entry, the others belong to one
-  const int entries = MOE ? *l.n : (a.M + S::TOKENS - 1) / S::TOKENS;
-  const bool combine = MOE && a.mode == FT_COMBINE;
-  const int items = combine ? a.tiles : entries * a.tiles;
-  const int segs = combine ? entries : 1;
-  auto segment = [&](int item, int s, int& tile, int& expert, int& first, int& count) {
-    const int en = combine ? s : item / a.tiles;
+  // the block's share of the items (tile, or entry and tile): a contiguous run
+  const int nk = (a.K + 63) >> 6;
+  const int entries = MOE ? *l.n : (a.M + U::TOKENS - 1) / U::TOKENS;
+  const int64_t items = combine ? a.tiles : (int64_t)entries * a.tiles;
+  const int item0 = (int)(items * blockIdx.x / gridDim.x);
+  const int item1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  const int run_len = combine ? 1 : a.run;
+  const int runs = (item1 - item0 + run_len - 1) / run_len;
+  auto pieces_of = [&](int r) { return combine ? entries : min(run_len, item1 - item0 - r * run_len); };
+  auto enter = [&](FtWalk& w) {  // this warp's share of run w.run, skipping runs without one
+    for (; w.run < runs; ++w.run) {
+      const int64_t total = (int64_t)pieces_of(w.run) * nk;
+      w.v = (int)(total * warp / FT_WARPS);
+      w.v_end = (int)(total * (warp + 1) / FT_WARPS);
+      if (w.v < w.v_end) {
+        w.piece = w.v / nk;
+        w.u = w.v - w.piece * nk;
+        return;
+      }
+    }
+  };
+  auto piece_at = [&](int run, int piece, int& tile, int& expert, int& first, int& count) {
+    const int item = item0 + (combine ? run : run * run_len + piece);
+    const int en = combine ? piece : item / a.tiles;
     tile = combine ? item : item - en * a.tiles;
     if (MOE) {
       const int2 v = l.entry[en];
@@ -325,273 +370,319 @@ __global__ void __launch_bounds__(FT_THREADS, 2) ft_kernel(const FtArgs a) {
       first = v.y;
     } else {
       expert = 0;
-      first = en * S::TOKENS;
-      count = min(S::TOKENS, a.M - first);
+      first = en * U::TOKENS;
+      count = min(U::TOKENS, a.M - first);
     }
   };
 
-  if (warp == FT_WARPS) {
-    // ---------------------------------------------------------------- producer
-    uint32_t issued = 0, parity = 0;
-    auto bytes_w = [&](int tile, int kn) -> uint32_t {
+  // ---------------------------------------------------------------- copies in
+  const uint32_t ring = smem_u32(smem) + a.ring_off + warp * a.depth * U::BYTES;
+  FtWalk in = {0, 0, 0, 0, 0};
+  const uint8_t *pw[RT], *pw8[RT], *ps[RT], *pz[RT];  // this lane's sources at u = 0
+  auto weights_of = [&](const FtWalk& w) {
+    int tile, expert, first, count;
+    piece_at(w.run, w.piece, tile, expert, first, count);
+    const uint8_t* m = a.W + (int64_t)expert * a.expert_bytes;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int t16 = min(tile * RT + i, a.tiles16 - 1);  // a tile past the end repeats the last
       if (W4) {
-        const uint32_t ng = (uint32_t)((kn + (1 << a.group_log2) - 1) >> a.group_log2);
-        return (uint32_t)((kn + 63) >> 6) * 512u + ng * (a.zeros ? 48u : 32u);
-      }
-      const int rows = a.mode == FT_GATE_UP ? 16 : min(16, a.rows - tile * 16);
-      return (uint32_t)(rows * kn * 2);
-    };
-    auto load_w = [&](int slot, int tile, int expert, int k0, int kn) {
-      const uint32_t dst = sbase + a.ring_off + slot * a.stage_bytes, bar = full_bar(slot);
-      const uint8_t* w = a.W + (int64_t)expert * a.expert_bytes;
-      if (W4) {
-        const int ng = (kn + (1 << a.group_log2) - 1) >> a.group_log2;
-        const int64_t g0 = (int64_t)tile * a.groups + (k0 >> a.group_log2);
-        if (lane == 0)
-          bulk_load(dst, w + ((int64_t)tile * ((a.K + 63) >> 6) + (k0 >> 6)) * 512,
-                    (uint32_t)((kn + 63) >> 6) * 512u, bar);
-        if (lane == 1) bulk_load(dst + a.sc_off, w + a.scales_off + g0 * 32, (uint32_t)ng * 32u, bar);
-        if (lane == 2 && a.zeros)
-          bulk_load(dst + a.z_off, w + a.zeros_off + g0 * 16, (uint32_t)ng * 16u, bar);
-      } else if (lane < 16) {
+        pw[i] = m + (int64_t)t16 * nk * 512 + lane * 16;
+        ps[i] = m + a.scales_off + (int64_t)t16 * a.groups * 32 + g * 4;
+        if (ZP) pz[i] = m + a.zeros_off + (int64_t)t16 * a.groups * 16 + (g >> 1) * 4;
+      } else {
+        // a row past the end repeats the last one (its results are not stored)
         const bool gu = a.mode == FT_GATE_UP;
-        const int r = gu ? tile * 8 + (lane & 7) : tile * 16 + lane;
-        if (r < a.rows)
-          bulk_load(dst + lane * S::ROW,
-                    w + ((int64_t)(r + (gu && lane >= 8 ? a.rows : 0)) * a.K + k0) * 2,
-                    (uint32_t)kn * 2u, bar);
+        const int64_t r0 = gu ? t16 * 8 + g : min(t16 * 16 + g, a.rows - 1);
+        const int64_t r1 = gu ? a.rows + t16 * 8 + g : min(t16 * 16 + 8 + g, a.rows - 1);
+        pw[i] = m + (r0 * a.K + t * 8) * 2;
+        pw8[i] = m + (r1 * a.K + t * 8) * 2;
       }
-    };
-    auto load_x = [&](int slot, int first, int count, int k0, int kn) {
-      const uint32_t dst = sbase + a.ring_off + slot * a.stage_bytes + a.x_off;
-      for (int i = lane; i < count; i += 32) {
-        int64_t r = first + i;
-        if (MOE && a.mode != FT_COMBINE) r = l.at[first + i] / a.topk;
-        bulk_load(dst + i * S::ROW, static_cast<const uint8_t*>(a.X) + (r * a.K + k0) * 2,
-                  (uint32_t)kn * 2u, full_bar(slot));
-      }
-    };
-    // A dependent launch first fills the ring with weights, which the kernel
-    // before it does not write, then waits for it and adds the token rows.
-    int pre = 0;
-    if (a.dependent && !wait_first) {
-      for (int item = blockIdx.x; item < items && pre < a.stages; item += gridDim.x)
-        for (int s = 0; s < segs && pre < a.stages; ++s) {
-          int tile, expert, first, count;
-          segment(item, s, tile, expert, first, count);
-          for (int k0 = 0; k0 < a.K && pre < a.stages; k0 += S::KC, ++pre) {
-            if (a.inject && pre == 0) continue;
-            const int kn = min(S::KC, a.K - k0);
-            if (lane == 0)
-              mbar_arrive_expect_tx(full_bar(pre), bytes_w(tile, kn) + (uint32_t)(count * kn * 2));
-            __syncwarp();
-            load_w(pre, tile, expert, k0, kn);
-            issued |= 1u << pre;
-          }
-        }
-      pdl_wait();
     }
-    int stage = 0, n = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += gridDim.x)
-      for (int s = 0; ok && s < segs; ++s) {
-        int tile, expert, first, count;
-        segment(item, s, tile, expert, first, count);
-        for (int k0 = 0; k0 < a.K; k0 += S::KC, ++n) {
-          const int kn = min(S::KC, a.K - k0);
-          const bool skip = a.inject && n == 0;
-          if (n >= pre && !skip) {
-            int w = 1;
-            if (lane == 0)
-              w = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, a.wait_limit_ns, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, w, 0) != 0;
-            if (!ok) break;
-            if (lane == 0)
-              mbar_arrive_expect_tx(full_bar(stage), bytes_w(tile, kn) + (uint32_t)(count * kn * 2));
-            __syncwarp();
-            load_w(stage, tile, expert, k0, kn);
-            issued |= 1u << stage;
-            parity = (parity & ~(1u << stage)) | (phase << stage);
-          }
-          if (!skip) load_x(stage, first, count, k0, kn);
-          if (++stage == a.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+  };
+  const uint8_t* px[NT];  // the token rows of this lane's columns
+  bool has_x[NT];
+  auto tokens_of = [&](const FtWalk& w) {
+    int tile, expert, first, count;
+    piece_at(w.run, w.piece, tile, expert, first, count);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int c = nt * 8 + g;
+      has_x[nt] = c < count;
+      int64_t r = first + (has_x[nt] ? c : 0);
+      if (MOE && !combine) r = l.at[r] / a.topk;
+      px[nt] = static_cast<const uint8_t*>(a.X) + (r * a.K + t * 8) * 2;
+    }
+  };
+  // bytes of the 16 at element k of a row that lie inside it (K % 8 == 0): 16 or 0
+  auto inside = [&](int k) { return k < a.K ? 16u : 0u; };
+  auto copy_w = [&](uint32_t slot, int u) {
+    const uint32_t d = slot + lane * 16;
+    if (W4) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        cp_async_cg16(d + U::W + i * 512, pw[i] + (int64_t)u * 512, 16u);
+        const int g0 = (u * 64) >> a.group_log2;
+        cp_async_ca4(slot + U::S + (i * U::GROUPS) * 128 + lane * 4, ps[i] + (int64_t)g0 * 32);
+        if (ZP)
+          cp_async_ca4(slot + U::Z + (i * U::GROUPS) * 128 + lane * 4, pz[i] + (int64_t)g0 * 16);
+        if (G32) {
+          const int g1 = min(g0 + 1, a.groups - 1);
+          cp_async_ca4(slot + U::S + (i * 2 + 1) * 128 + lane * 4, ps[i] + (int64_t)g1 * 32);
+          if (ZP) cp_async_ca4(slot + U::Z + (i * 2 + 1) * 128 + lane * 4, pz[i] + (int64_t)g1 * 16);
         }
       }
-    if (!ok)  // no copy may land after the block has gone
-      for (int i = 0; i < a.stages; ++i)
-        if (issued & (1u << i))
-          mbar_wait_bounded(full_bar(i), (parity >> i) & 1u, a.wait_limit_ns, nullptr, a.err);
-    return;
+    } else {
+      const uint32_t b0 = inside(u * 64 + t * 8), b1 = inside(u * 64 + 32 + t * 8);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int64_t o0 = b0 ? (int64_t)u * 128 : 0, o1 = b1 ? (int64_t)u * 128 + 64 : 0;
+        cp_async_cg16(d + U::W + i * 2048, pw[i] + o0, b0);
+        cp_async_cg16(d + U::W + i * 2048 + 512, pw[i] + o1, b1);
+        cp_async_cg16(d + U::W + i * 2048 + 1024, pw8[i] + o0, b0);
+        cp_async_cg16(d + U::W + i * 2048 + 1536, pw8[i] + o1, b1);
+      }
+    }
+  };
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  auto load_x = [&](uint4 (&x)[2], int nt, int u) {
+    const bool in0 = has_x[nt] && u * 64 + t * 8 < a.K, in1 = has_x[nt] && u * 64 + 32 + t * 8 < a.K;
+    const uint8_t* p = px[nt] + (int64_t)u * 128;
+    x[0] = in0 && SWIGLU_CHECK_PTR(a.dbg, p, 16, a.err) ? ft_load16(p) : none;
+    x[1] = in1 && SWIGLU_CHECK_PTR(a.dbg, p + 64, 16, a.err) ? ft_load16(p + 64) : none;
+  };
+  auto step = [&](FtWalk& w) {  // to the next unit; true where it belongs to another piece
+    if (++w.v == w.v_end) {
+      ++w.run;
+      enter(w);
+      return true;
+    }
+    if (++w.u == nk) {
+      w.u = 0;
+      ++w.piece;
+      return true;
+    }
+    return false;
+  };
+
+  // fill the ring; a dependent launch copies weights, which the kernel before
+  // it does not write, then waits for it before it reads token rows
+  enter(in);
+  const FtWalk begin = in;
+  const int ahead = a.depth - 1;
+  if (in.run < runs) weights_of(in);
+  for (int i = 0; i < ahead; ++i) {
+    if (in.run < runs) {
+      copy_w(ring + i * U::BYTES, in.u);
+      if (step(in) && in.run < runs) weights_of(in);
+    }
+    cp_async_commit();
   }
+  if (a.dependent && !wait_first) pdl_wait();
 
-  // ------------------------------------------------------------------ consumers
-  const int g = lane >> 2, t = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + a.red_off);
-  int stage = 0, buf = 0;
-  uint32_t phase = 0;
-  bool live = true;  // false after a wait ran out: go through the motions, read nothing
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    int tile = 0;
-    for (int s = 0; s < segs; ++s) {
-      int expert, first, count;
-      segment(item, s, tile, expert, first, count);
-      const int nts = (count + 7) >> 3;
-      float acc[NT][4];
+  // ---------------------------------------------------------------- products
+  FtWalk at = begin;
+  int slot_in = ahead, slot_at = 0;
+  constexpr bool XREG = NT <= 2;  // token rows held one unit ahead
+  uint4 x[NT][2];
+  if (at.run < runs) {
+    tokens_of(at);
+    if (XREG)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) load_x(x[nt], nt, at.u);
+  }
+  float acc[RT][NT][4];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[nt][c] = 0.0f;
-
-      for (int k0 = 0; k0 < a.K; k0 += S::KC) {
-        if (live)
-          live = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, a.wait_limit_ns,
-                                                           abort_flag, a.err));
-        if (live) {
-          const uint32_t sw = sbase + a.ring_off + stage * a.stage_bytes;
-          const int left = a.K - k0;
-          const bool tail = left < S::KC;
+        for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.0f;
+  };
+  clear();
+  // the partial tile of the piece just finished: its own place in shared
+  // memory, or added to the warp's weighted sums per token
+  auto flush = [&](int run, int piece) {
+    if (combine) {
+      int tile, expert, first, count;
+      piece_at(run, piece, tile, expert, first, count);
+      float* y = red + warp * a.M * 16 * RT;
+      __syncwarp();
 #pragma unroll
-          for (int i = 0; i < S::UNITS; ++i) {
-            const int u = warp + FT_WARPS * i;
-            if (tail && u * 64 >= left) continue;
-            // k of this lane past the end of the row: what lies there is stale
-            const bool z0 = tail && u * 64 + t * 8 >= left;
-            const bool z1 = tail && u * 64 + 32 + t * 8 >= left;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            uint32_t A[4][4];
-            float s0g = 0.0f, s0h = 0.0f, s1g = 0.0f, s1h = 0.0f;
-            if (W4) {
-              const uint4 c = lds128(sw + u * 512 + lane * 16);
-              const int g0 = (u * 64) >> a.group_log2;
-              int g1 = (u * 64 + 32) >> a.group_log2;
-              if (tail && u * 64 + 32 >= left) g1 = g0;
-              const uint32_t sc0 = lds32(sw + a.sc_off + g0 * 32 + g * 4);
-              const uint32_t sc1 = lds32(sw + a.sc_off + g1 * 32 + g * 4);
-              uint32_t q0 = 0x0808u, q1 = 0x0808u;
-              if (a.zeros) {
-                q0 = lds16(sw + a.z_off + g0 * 16 + g * 2);
-                q1 = lds16(sw + a.z_off + g1 * 16 + g * 2);
-              }
-              s0g = P::lo(sc0);
-              s0h = P::hi(sc0);
-              s1g = P::lo(sc1);
-              s1h = P::hi(sc1);
-              const uint32_t z0l = P::MAGIC + (q0 & 0xffu) * 0x10001u;
-              const uint32_t z0h = P::MAGIC + (q0 >> 8) * 0x10001u;
-              const uint32_t z1l = P::MAGIC + (q1 & 0xffu) * 0x10001u;
-              const uint32_t z1h = P::MAGIC + (q1 >> 8) * 0x10001u;
-              ft_codes<BF16>(c.x, z0l, z0h, A[0]);
-              ft_codes<BF16>(c.y, z0l, z0h, A[1]);
-              ft_codes<BF16>(c.z, z1l, z1h, A[2]);
-              ft_codes<BF16>(c.w, z1l, z1h, A[3]);
-            } else {
-              const uint32_t p = sw + g * S::ROW + u * 128 + t * 16;
-              uint4 g0 = lds128(p), g1 = lds128(p + 64);
-              uint4 h0 = lds128(p + 8 * S::ROW), h1 = lds128(p + 8 * S::ROW + 64);
-              if (z0) g0 = h0 = zero;
-              if (z1) g1 = h1 = zero;
-              A[0][0] = g0.x, A[0][1] = h0.x, A[0][2] = g0.y, A[0][3] = h0.y;
-              A[1][0] = g0.z, A[1][1] = h0.z, A[1][2] = g0.w, A[1][3] = h0.w;
-              A[2][0] = g1.x, A[2][1] = h1.x, A[2][2] = g1.y, A[2][3] = h1.y;
-              A[3][0] = g1.z, A[3][1] = h1.z, A[3][2] = g1.w, A[3][3] = h1.w;
-            }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (nt >= nts) continue;
-              const int r = min(nt * 8 + g, a.xrows - 1);
-              const uint32_t p = sw + a.x_off + r * S::ROW + u * 128 + t * 16;
-              uint4 x0 = lds128(p), x1 = lds128(p + 64);
-              if (z0) x0 = zero;
-              if (z1) x1 = zero;
-              if (W4) {
-                float p0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, p1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_16816<BF16>(p0, A[0][0], A[0][1], A[0][2], A[0][3], x0.x, x0.y);
-                mma_16816<BF16>(p1, A[2][0], A[2][1], A[2][2], A[2][3], x1.x, x1.y);
-                mma_16816<BF16>(p0, A[1][0], A[1][1], A[1][2], A[1][3], x0.z, x0.w);
-                mma_16816<BF16>(p1, A[3][0], A[3][1], A[3][2], A[3][3], x1.z, x1.w);
-                acc[nt][0] = fmaf(s0g, p0[0], fmaf(s1g, p1[0], acc[nt][0]));
-                acc[nt][1] = fmaf(s0g, p0[1], fmaf(s1g, p1[1], acc[nt][1]));
-                acc[nt][2] = fmaf(s0h, p0[2], fmaf(s1h, p1[2], acc[nt][2]));
-                acc[nt][3] = fmaf(s0h, p0[3], fmaf(s1h, p1[3], acc[nt][3]));
-              } else {
-                mma_16816<BF16>(acc[nt], A[0][0], A[0][1], A[0][2], A[0][3], x0.x, x0.y);
-                mma_16816<BF16>(acc[nt], A[1][0], A[1][1], A[1][2], A[1][3], x0.z, x0.w);
-                mma_16816<BF16>(acc[nt], A[2][0], A[2][1], A[2][2], A[2][3], x1.x, x1.y);
-                mma_16816<BF16>(acc[nt], A[3][0], A[3][1], A[3][2], A[3][3], x1.z, x1.w);
-              }
+        for (int c = 0; c < 2; ++c) {
+          const int m = nt * 8 + 2 * t + c;
+          if (m < count) {
+            const float w = l.w[first + m];
+            float* yt = y + (l.at[first + m] / a.topk) * 16 * RT + g;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              yt[16 * i] += w * acc[i][nt][c];
+              yt[16 * i + 8] += w * acc[i][nt][c + 2];
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty_bar(stage));
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
+    } else {
+      float4* p = reinterpret_cast<float4*>(red + (size_t)(piece + warp) * (U::PART / 4)) + lane;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          p[(i * NT + nt) * 32] =
+              make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+    }
+    clear();
+  };
+  auto multiply = [&](uint32_t slot, const uint4 (&x)[NT][2]) {
+    const uint32_t d = slot + lane * 16;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      uint32_t A[4][4];
+      if (W4) {
+        const uint4 c = lds128(d + U::W + i * 512);
+        const uint32_t sc0 = lds32(slot + U::S + i * U::GROUPS * 128 + lane * 4);
+        const uint32_t sc1 = G32 ? lds32(slot + U::S + (i * 2 + 1) * 128 + lane * 4) : sc0;
+        uint32_t z0l = P::MAGIC + 0x00080008u, z0h = z0l, z1l = z0l, z1h = z0l;
+        if (ZP) {
+          const int sh = (g & 1) * 16;
+          const uint32_t q0 = lds32(slot + U::Z + i * U::GROUPS * 128 + lane * 4) >> sh;
+          z0l = P::MAGIC + (q0 & 0xffu) * 0x10001u;
+          z0h = P::MAGIC + ((q0 >> 8) & 0xffu) * 0x10001u;
+          z1l = z0l;
+          z1h = z0h;
+          if (G32) {
+            const uint32_t q1 = lds32(slot + U::Z + (i * 2 + 1) * 128 + lane * 4) >> sh;
+            z1l = P::MAGIC + (q1 & 0xffu) * 0x10001u;
+            z1h = P::MAGIC + ((q1 >> 8) & 0xffu) * 0x10001u;
+          }
         }
-      }
-
-      // the warps' partial tiles meet, in warp order
-      float* mine = red + ((buf * FT_WARPS + warp) * NT * 32 + lane) * 4;
+        ft_codes<BF16>(c.x, z0l, z0h, A[0]);
+        ft_codes<BF16>(c.y, z0l, z0h, A[1]);
+        ft_codes<BF16>(c.z, z1l, z1h, A[2]);
+        ft_codes<BF16>(c.w, z1l, z1h, A[3]);
+        const float s0g = P::lo(sc0), s0h = P::hi(sc0);
+        const float s1g = G32 ? P::lo(sc1) : s0g, s1h = G32 ? P::hi(sc1) : s0h;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<float4*>(mine + nt * 128) =
-            make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-      ft_bar_consumers();
-      const float* part = red + buf * FT_WARPS * NT * 128;
-      buf ^= 1;
-      // element (row of the tile, token of the entry) of the summed tile
-      auto sum = [&](int row, int m) {
-        const float* p = part + (m >> 3) * 128 + ((row & 7) * 4 + ((m & 7) >> 1)) * 4 + (m & 1) +
-                         2 * (row >> 3);
-        float v = p[0];
-#pragma unroll
-        for (int w = 1; w < FT_WARPS; ++w) v += p[w * NT * 128];
-        return v;
-      };
-      uint16_t* out = static_cast<uint16_t*>(a.out);
-      if (a.mode == FT_GATE_UP) {
-        for (int i = threadIdx.x; i < count * 8; i += FT_CONSUMERS) {
-          const int m = i >> 3, u = tile * 8 + (i & 7);
-          if (u >= a.rows) continue;
-          const float v = ft_silu(a.scale * sum(i & 7, m)) * sum((i & 7) + 8, m);
-          uint16_t* o = out + (int64_t)(first + m) * a.rows + u;
-          if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(v);
+        for (int nt = 0; nt < NT; ++nt) {
+          float p0[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_16816<BF16>(p0, A[0][0], A[0][1], A[0][2], A[0][3], x[nt][0].x, x[nt][0].y);
+          mma_16816<BF16>(p0, A[1][0], A[1][1], A[1][2], A[1][3], x[nt][0].z, x[nt][0].w);
+          float(&o)[4] = acc[i][nt];
+          if (G32) {
+            o[0] = fmaf(s0g, p0[0], o[0]);
+            o[1] = fmaf(s0g, p0[1], o[1]);
+            o[2] = fmaf(s0h, p0[2], o[2]);
+            o[3] = fmaf(s0h, p0[3], o[3]);
+            p0[0] = p0[1] = p0[2] = p0[3] = 0.0f;
+          }
+          mma_16816<BF16>(p0, A[2][0], A[2][1], A[2][2], A[2][3], x[nt][1].x, x[nt][1].y);
+          mma_16816<BF16>(p0, A[3][0], A[3][1], A[3][2], A[3][3], x[nt][1].z, x[nt][1].w);
+          o[0] = fmaf(s1g, p0[0], o[0]);
+          o[1] = fmaf(s1g, p0[1], o[1]);
+          o[2] = fmaf(s1h, p0[2], o[2]);
+          o[3] = fmaf(s1h, p0[3], o[3]);
         }
       } else {
-        for (int i = threadIdx.x; i < count * 16; i += FT_CONSUMERS) {
-          const int m = i >> 4, r = tile * 16 + (i & 15);
-          if (r >= a.rows) continue;
-          const float v = sum(i & 15, m);
-          if (combine) {
-            // one thread per (token, row): an expert's entries name a token once
-            yacc[(l.at[first + m] / a.topk) * 16 + (i & 15)] += l.w[first + m] * v;
-          } else {
-            uint16_t* o = out + (int64_t)(first + m) * a.rows + r;
-            if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(a.scale * v);
-          }
+        const uint4 g0 = lds128(d + U::W + i * 2048), g1 = lds128(d + U::W + i * 2048 + 512);
+        const uint4 h0 = lds128(d + U::W + i * 2048 + 1024), h1 = lds128(d + U::W + i * 2048 + 1536);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816<BF16>(acc[i][nt], g0.x, h0.x, g0.y, h0.y, x[nt][0].x, x[nt][0].y);
+          mma_16816<BF16>(acc[i][nt], g0.z, h0.z, g0.w, h0.w, x[nt][0].z, x[nt][0].w);
+          mma_16816<BF16>(acc[i][nt], g1.x, h1.x, g1.y, h1.y, x[nt][1].x, x[nt][1].y);
+          mma_16816<BF16>(acc[i][nt], g1.z, h1.z, g1.w, h1.w, x[nt][1].z, x[nt][1].w);
         }
       }
     }
+  };
+
+  uint16_t* const out = static_cast<uint16_t*>(a.out);
+  for (int run = 0; run < runs; ++run) {
+    while (at.run == run) {
+      cp_async_wait(ahead - 1);
+      if (in.run < runs) {
+        copy_w(ring + slot_in * U::BYTES, in.u);
+        if (step(in) && in.run < runs) weights_of(in);
+      }
+      cp_async_commit();
+      if (++slot_in == a.depth) slot_in = 0;
+      const uint32_t slot = ring + slot_at * U::BYTES;
+      if (++slot_at == a.depth) slot_at = 0;
+      if (!XREG)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) load_x(x[nt], nt, at.u);
+      const int piece = at.piece;
+      const bool last = step(at);  // of this piece
+      if (last && at.run < runs) tokens_of(at);
+      if (XREG) {
+        uint4 xn[NT][2];
+        if (at.run < runs)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) load_x(xn[nt], nt, at.u);
+        multiply(slot, x);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          x[nt][0] = xn[nt][0];
+          x[nt][1] = xn[nt][1];
+        }
+      } else {
+        multiply(slot, x);
+      }
+      if (last) flush(run, piece);
+    }
+    __syncthreads();
     if (combine) {
-      if (segs == 0) tile = item;
-      ft_bar_consumers();
-      for (int i = threadIdx.x; i < a.M * 16; i += FT_CONSUMERS) {
-        const int r = tile * 16 + (i & 15);
-        if (r < a.rows) {
-          uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)(i >> 4) * a.rows + r;
-          if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(a.scale * yacc[i]);
+      // the warps' weighted sums, in warp order
+      const int tile = item0 + run;
+      for (int i = threadIdx.x; i < a.M * 16 * RT; i += FT_THREADS) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < FT_WARPS; ++w) {
+          v += red[w * a.M * 16 * RT + i];
+          red[w * a.M * 16 * RT + i] = 0.0f;
         }
-        yacc[i] = 0.0f;
+        const int m = i / (16 * RT), r = tile * 16 * RT + i % (16 * RT);
+        if (r < a.rows) {
+          uint16_t* o = out + (int64_t)m * a.rows + r;
+          if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(a.scale * v);
+        }
+      }
+    } else {
+      // a tile's partials, in warp order: the warps whose shares meet it
+      const int n = pieces_of(run);
+      const int64_t total = (int64_t)n * nk;
+      const bool gu = a.mode == FT_GATE_UP;
+      const int per = (gu ? 8 : 16) * RT;  // outputs of a tile and token
+      const int each = per * U::TOKENS;
+      for (int i = threadIdx.x; i < n * each; i += FT_THREADS) {
+        const int j = i / each, m = (i - j * each) / per, r = i % per;
+        int tile, expert, first, count;
+        piece_at(run, j, tile, expert, first, count);
+        if (m >= count) continue;
+        // row r of the tile: 16-row part r / 16 (gate/up: r / 8), row g or g + 8 of it
+        const int part = gu ? r >> 3 : r >> 4, rg = r & 7, half = gu ? 0 : (r >> 3) & 1;
+        const int at0 = (part * NT + (m >> 3)) * 128 + (rg * 4 + ((m & 7) >> 1)) * 4 + (m & 1) + 2 * half;
+        // shares: warp w has [total w / 16, total (w + 1) / 16)
+        int w = (int)(((int64_t)j * nk * FT_WARPS) / total);
+        while (w + 1 < FT_WARPS && total * (w + 1) / FT_WARPS <= (int64_t)j * nk) ++w;
+        float v = 0.0f, v2 = 0.0f;
+        for (; w < FT_WARPS && total * w / FT_WARPS < (int64_t)(j + 1) * nk; ++w) {
+          if (total * w / FT_WARPS == total * (w + 1) / FT_WARPS) continue;  // an empty share
+          const float* p = red + (size_t)(j + w) * (U::PART / 4) + at0;
+          v += p[0];
+          if (gu) v2 += p[2];
+        }
+        const int col = tile * per + r;
+        if (col >= a.rows) continue;
+        uint16_t* o = out + (int64_t)(first + m) * a.rows + col;
+        v = gu ? ft_silu(a.scale * v) * v2 : a.scale * v;
+        if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(v);
       }
     }
+    __syncthreads();
   }
-  // a dependent block without work still may not finish before the kernel it
-  // depends on has (the next call's first kernel waits for this one alone)
-  if (a.dependent && !wait_first) pdl_wait();
 }
 
 }  // namespace swiglu

@@ -75,46 +75,34 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-constexpr int SMEM_ONE = 226 * 1024;  // one block per SM
-constexpr int SMEM_TWO = 112 * 1024;  // two
+constexpr int SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
+constexpr int FT_MAX_DEPTH = 8;
 
-template <bool BF16, bool W4, int NT, bool MOE>
+template <bool BF16, bool W4, int RT, int NT, bool G32, bool ZP, bool MOE>
 cudaError_t launch_ft(host::ServingKernel id, FtArgs a, cudaStream_t st) {
-  using S = FtShape<W4, NT>;
-  constexpr auto kern = ft_kernel<BF16, W4, NT, MOE>;
-  cudaError_t e = allow_smem<kern>(SMEM_ONE);
+  using U = FtUnit<W4, RT, NT, G32, ZP>;
+  constexpr auto kern = ft_kernel<BF16, W4, RT, NT, G32, ZP, MOE>;
+  cudaError_t e = allow_smem<kern>(SMEM);
   if (e != cudaSuccess) return e;
-  auto up = [](int v) { return (v + 127) & ~127; };
-  a.xrows = a.M < S::TOKENS ? a.M : S::TOKENS;
-  a.list_off = up(16 * FT_MAX_STAGES + 16) + (MOE ? FT_MAX_TOKENS * 16 * 4 : 0);
-  a.red_off = a.list_off + (MOE ? ft_lists_bytes(a.M, a.topk, a.E, S::TOKENS) : 0);
-  a.ring_off = a.red_off + S::RED_BYTES;
-  int b = W4 ? S::KC / 64 * 512 : 16 * S::ROW;
-  a.sc_off = b;
-  if (W4) b += (S::KC >> a.group_log2) * 32;
-  a.z_off = b;
-  if (W4 && a.zeros) b += (S::KC >> a.group_log2) * 16;
-  a.x_off = up(b);
-  a.stage_bytes = up(a.x_off + a.xrows * S::ROW);
-  int per_sm = 2;
-  int stages = (SMEM_TWO - a.ring_off) / a.stage_bytes;
-  if (stages < 2) {
-    per_sm = 1;
-    stages = (SMEM_ONE - a.ring_off) / a.stage_bytes;
-  }
-  if (stages < 1) return cudaErrorInvalidConfiguration;
-  a.stages = stages < FT_MAX_STAGES ? stages : FT_MAX_STAGES;
-  const int smem = a.ring_off + a.stages * a.stage_bytes;
+  const bool combine = MOE && a.mode == FT_COMBINE;
+  const int nsm = host::sms() > 0 ? host::sms() : 1;
+  a.tiles = (a.tiles16 + RT - 1) / RT;
   int64_t items = a.tiles;
-  if (!(MOE && a.mode == FT_COMBINE))
-    items *= MOE ? ft_max_entries(a.M, a.topk, a.E, S::TOKENS) : (a.M + S::TOKENS - 1) / S::TOKENS;
-  const int nsm = host::sms();
-  const int64_t most = (int64_t)(nsm > 0 ? nsm : 1) * per_sm;
-  a.wait_limit_ns = host::wait_limit_ns();
-  a.inject = host::take_stall() ? 1 : 0;
+  if (!combine)
+    items *= MOE ? ft_max_entries(a.M, a.topk, a.E, U::TOKENS) : (a.M + U::TOKENS - 1) / U::TOKENS;
+  const int grid = (int)(items < nsm ? items : nsm);
+  const int64_t most = (items + grid - 1) / grid;  // tiles of a block
+  a.list_off = 0;
+  a.red_off = MOE ? ft_lists_bytes(a.M, a.topk, a.E, U::TOKENS) : 0;
+  a.run = (int)(most < 32 / NT ? most : 32 / NT);
+  a.ring_off = a.red_off + (combine ? FT_WARPS * a.M * 16 * RT * 4 : (a.run + FT_WARPS - 1) * U::PART);
+  a.depth = (SMEM - a.ring_off) / (FT_WARPS * U::BYTES);
+  if (a.depth < 2) return cudaErrorInvalidConfiguration;
+  if (a.depth > FT_MAX_DEPTH) a.depth = FT_MAX_DEPTH;
+  const int smem = a.ring_off + a.depth * FT_WARPS * U::BYTES;
   host::Prof prof(id, st);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(FT_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -131,22 +119,35 @@ cudaError_t launch_ft(host::ServingKernel id, FtArgs a, cudaStream_t st) {
 }
 
 // Tokens per pass over a tile: 8, 16 or 32 columns (more take several passes).
-template <bool BF16, bool W4, bool MOE>
+template <bool BF16, bool W4, bool G32, bool ZP, bool MOE>
 cudaError_t launch_nt(host::ServingKernel id, const FtArgs& a, int tokens, cudaStream_t st) {
-  if (tokens <= 8) return launch_ft<BF16, W4, 1, MOE>(id, a, st);
-  if (tokens <= 16) return launch_ft<BF16, W4, 2, MOE>(id, a, st);
-  return launch_ft<BF16, W4, 4, MOE>(id, a, st);
+  if (tokens <= 8) return launch_ft<BF16, W4, 1, 1, G32, ZP, MOE>(id, a, st);
+  if (tokens <= 16) return launch_ft<BF16, W4, MOE ? 1 : 2, 2, G32, ZP, MOE>(id, a, st);
+  return launch_ft<BF16, W4, 1, 4, G32, ZP, MOE>(id, a, st);
+}
+
+template <bool BF16, bool W4, bool MOE>
+cudaError_t launch_fmt(host::ServingKernel id, const FtArgs& a, int tokens, cudaStream_t st) {
+  if constexpr (!W4) {
+    return launch_nt<BF16, false, false, false, MOE>(id, a, tokens, st);
+  } else {
+    if (a.group_log2 == 5)
+      return a.zeros ? launch_nt<BF16, true, true, true, MOE>(id, a, tokens, st)
+                     : launch_nt<BF16, true, true, false, MOE>(id, a, tokens, st);
+    return a.zeros ? launch_nt<BF16, true, false, true, MOE>(id, a, tokens, st)
+                   : launch_nt<BF16, true, false, false, MOE>(id, a, tokens, st);
+  }
 }
 
 template <bool W4, bool MOE>
 cudaError_t launch_dt(host::ServingKernel id, const FtArgs& a, int tokens, swiglu_dtype dt,
                       cudaStream_t st) {
-  return dt == SWIGLU_BF16 ? launch_nt<true, W4, MOE>(id, a, tokens, st)
-                           : launch_nt<false, W4, MOE>(id, a, tokens, st);
+  return dt == SWIGLU_BF16 ? launch_fmt<true, W4, MOE>(id, a, tokens, st)
+                           : launch_fmt<false, W4, MOE>(id, a, tokens, st);
 }
 
 void set_w4(FtArgs& a, const W4Geom& w) {
-  a.tiles = w.tiles;
+  a.tiles16 = w.tiles;
   a.expert_bytes = w.bytes;
   a.group_log2 = w.group_log2;
   a.groups = w.groups;
@@ -204,7 +205,7 @@ swiglu_status run_experts(const void* X, const int* idx, const float* wts, const
   a.M = T;
   a.K = D;
   a.rows = H;
-  a.tiles = (H + 7) / 8;
+  a.tiles16 = (H + 7) / 8;
   a.W = static_cast<const uint8_t*>(Wgu);
   a.expert_bytes = (int64_t)2 * H * D * 2;
   a.X = X;
@@ -229,7 +230,7 @@ swiglu_status run_experts(const void* X, const int* idx, const float* wts, const
   a.mode = FT_COMBINE;
   a.K = H;
   a.rows = D;
-  a.tiles = (D + 15) / 16;
+  a.tiles16 = (D + 15) / 16;
   a.W = static_cast<const uint8_t*>(Wd);
   a.expert_bytes = (int64_t)D * H * 2;
   a.X = A;
