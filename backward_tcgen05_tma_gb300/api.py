@@ -442,12 +442,20 @@ def swiglu_mlp_bwd(dY, X, Wgu, Wd, saved, out: dict | None = None, ws=None,
     return dX, dWgu, dWd
 
 
-def _serving_checks(X, *others):
-    """Contiguous CUDA tensors of X's device; returns X's stream."""
-    for t in (X, *others):
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.device != X.device):
-            raise ValueError("inputs and outputs must be contiguous CUDA tensors of one device")
-    return ctypes.c_void_p(_stream(X.device))
+# The few-token calls below last a few microseconds, so their Python part is
+# kept short: plain integers for pointers and streams, no temporaries.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _serving_checks(X, *others) -> int:
+    """Contiguous CUDA tensors of X's device; returns X's current stream."""
+    dev = X.get_device()
+    ok = dev >= 0 and X.is_contiguous()
+    for t in others:
+        ok = ok and t.get_device() == dev and t.is_contiguous()
+    if not ok:
+        raise ValueError("inputs and outputs must be contiguous CUDA tensors of one device")
+    return _raw_stream(dev)
 
 
 def _out(out, name, shape, dtype, device):
@@ -455,8 +463,7 @@ def _out(out, name, shape, dtype, device):
     t = out.get(name) if out else None
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
-            or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError("out[%r] must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device))
     return t
@@ -476,14 +483,12 @@ class W4Weights:
         self.packed, self.N, self.K, self.group = packed, int(N), int(K), int(group)
         self.zeros, self.gate_up, self.dtype = bool(zeros), bool(gate_up), dtype
         self.experts = experts
+        self.shape = (self.N, self.K) if experts is None else (experts, self.N, self.K)
+        self.format = W4Format(self.group, int(self.zeros))
 
     @property
     def device(self):
         return self.packed.device
-
-    @property
-    def shape(self):
-        return (self.N, self.K) if self.experts is None else (self.experts, self.N, self.K)
 
     def __repr__(self):
         return "W4Weights(%s, group=%d, zeros=%s, gate_up=%s, dtype=%s)" % (
@@ -515,7 +520,7 @@ def swiglu_mlp_w4_pack(codes, scales, zeros=None, group: int = 128,
     """The packed copy of 4-bit weights (codes uint8 [.., N, K/2], scales
     [.., N, ceil(K/group)] in the activations' type, optional zero points) that
     the few-token products stream."""
-    st = _serving_checks(codes, scales, zeros)
+    st = _serving_checks(codes, scales, *(() if zeros is None else (zeros,)))
     if codes.dim() not in (2, 3) or codes.dtype != torch.uint8:
         raise ValueError("expected uint8 codes [N, K/2] or [E, N, K/2]")
     *lead, N, half = codes.shape
@@ -561,9 +566,8 @@ def moe_workspace(T: int, D: int, H: int, E: int, top_k: int, device) -> torch.T
 
 def _w4_match(X, K, *weights):
     for W in weights:
-        if W.dtype != X.dtype or W.device != X.device:
-            raise ValueError("4-bit weights for %s on %s, activations %s on %s"
-                             % (W.dtype, W.device, X.dtype, X.device))
+        if W.dtype != X.dtype:
+            raise ValueError("4-bit weights for %s, activations %s" % (W.dtype, X.dtype))
     if X.dim() != 2 or X.shape[1] != K:
         raise ValueError("expected X [M, %d], got %s" % (K, tuple(X.shape)))
 
@@ -573,13 +577,14 @@ def swiglu_mlp_w4_linear(X, W: W4Weights, out: dict | None = None, ws=None):
     if W.gate_up or W.experts is not None:
         raise ValueError("expected one matrix packed without gate_up")
     _w4_match(X, W.K, W)
-    M, dev = X.shape[0], X.device
-    Y = _out(out, "Y", (M, W.N), X.dtype, dev)
-    L = lib()
-    ws = _ws(ws, lambda: L.swiglu_mlp_w4_workspace_bytes(M, W.N, W.K), dev)
-    _check(L.swiglu_mlp_w4_linear(_ptr(X), _ptr(W.packed), _ptr(Y), M, W.N, W.K, W.group,
-                                  int(W.zeros), dtype_code(X.dtype), _ptr(ws), ws.numel(),
-                                  _serving_checks(X, W.packed, ws)),
+    M = X.shape[0]
+    Y = _out(out, "Y", (M, W.N), X.dtype, X.device)
+    L = _lib or lib()
+    ws = _ws(ws, lambda: L.swiglu_mlp_w4_workspace_bytes(M, W.N, W.K), X.device)
+    st = _serving_checks(X, W.packed, ws)
+    _check(L.swiglu_mlp_w4_linear(X.data_ptr(), W.packed.data_ptr(), Y.data_ptr(), M, W.N, W.K,
+                                  W.group, W.zeros, dtype_code(X.dtype), ws.data_ptr(), ws.numel(),
+                                  st),
            "swiglu_mlp_w4_linear")
     _device_check(ws, "swiglu_mlp_w4_linear")
     return Y
@@ -591,18 +596,19 @@ def swiglu_mlp_fwd_nograd_w4(X, Wgu: W4Weights, Wd: W4Weights, out: dict | None 
     if not Wgu.gate_up or Wd.gate_up or Wgu.experts is not None or Wd.experts is not None:
         raise ValueError("expected Wgu packed with gate_up and Wd without")
     H, D = Wd.K, Wd.N
-    if Wgu.shape != (2 * H, D) or (Wgu.group, Wgu.zeros) != (Wd.group, Wd.zeros):
+    if Wgu.shape != (2 * H, D) or Wgu.group != Wd.group or Wgu.zeros != Wd.zeros:
         raise ValueError("mismatch: Wgu %r, Wd %r" % (Wgu, Wd))
     _w4_match(X, D, Wgu, Wd)
-    M, dev = X.shape[0], X.device
-    Y = _out(out, "Y", (M, D), X.dtype, dev)
-    A = _out(out, "A", (M, H), X.dtype, dev)
-    L = lib()
-    ws = _ws(ws, lambda: L.swiglu_mlp_fwd_nograd_w4_workspace_bytes(M, D, H), dev)
-    _check(L.swiglu_mlp_fwd_nograd_w4(_ptr(X), _ptr(Wgu.packed), _ptr(Wd.packed), _ptr(Y), _ptr(A),
-                                      M, D, H, Wd.group, int(Wd.zeros), dtype_code(X.dtype),
-                                      _opts(gate_mul, down_mul, False), _ptr(ws), ws.numel(),
-                                      _serving_checks(X, Wgu.packed, Wd.packed, ws)),
+    M = X.shape[0]
+    Y = _out(out, "Y", (M, D), X.dtype, X.device)
+    A = _out(out, "A", (M, H), X.dtype, X.device)
+    L = _lib or lib()
+    ws = _ws(ws, lambda: L.swiglu_mlp_fwd_nograd_w4_workspace_bytes(M, D, H), X.device)
+    st = _serving_checks(X, Wgu.packed, Wd.packed, ws)
+    _check(L.swiglu_mlp_fwd_nograd_w4(X.data_ptr(), Wgu.packed.data_ptr(), Wd.packed.data_ptr(),
+                                      Y.data_ptr(), A.data_ptr(), M, D, H, Wd.group, Wd.zeros,
+                                      dtype_code(X.dtype), _opts(gate_mul, down_mul, False),
+                                      ws.data_ptr(), ws.numel(), st),
            "swiglu_mlp_fwd_nograd_w4")
     _device_check(ws, "swiglu_mlp_fwd_nograd_w4")
     return Y, A
@@ -611,7 +617,6 @@ def swiglu_mlp_fwd_nograd_w4(X, Wgu: W4Weights, Wd: W4Weights, out: dict | None 
 def swiglu_mlp_moe_route(X, Wr, top_k: int, norm_topk: bool = True, route_scale: float = 1.0,
                          out: dict | None = None):
     """The router: (idx int32 [T, top_k], weights fp32 [T, top_k])."""
-    st = _serving_checks(X, Wr)
     T, D = X.shape
     E = Wr.shape[0]
     if Wr.shape != (E, D) or Wr.dtype != X.dtype:
@@ -619,31 +624,32 @@ def swiglu_mlp_moe_route(X, Wr, top_k: int, norm_topk: bool = True, route_scale:
                                                                    Wr.dtype))
     idx = _out(out, "idx", (T, top_k), torch.int32, X.device)
     w = _out(out, "weights", (T, top_k), torch.float32, X.device)
-    _check(lib().swiglu_mlp_moe_route(_ptr(X), _ptr(Wr), _ptr(idx), _ptr(w), T, D, E, top_k,
-                                      int(norm_topk), float(route_scale), dtype_code(X.dtype), st),
+    st = _serving_checks(X, Wr)
+    _check(lib().swiglu_mlp_moe_route(X.data_ptr(), Wr.data_ptr(), idx.data_ptr(), w.data_ptr(), T,
+                                      D, E, top_k, int(norm_topk), float(route_scale),
+                                      dtype_code(X.dtype), st),
            "swiglu_mlp_moe_route")
     return idx, w
 
 
 def _experts(X, Wgu, Wd):
     """(T, D, H, E, the format struct or None, the two buffers) of a layer."""
-    if X.dim() != 2:
-        raise ValueError("expected X [T, D], got %s" % (tuple(X.shape),))
-    T, D = X.shape
     w4 = isinstance(Wgu, W4Weights)
-    if w4 != isinstance(Wd, W4Weights):
-        raise ValueError("Wgu and Wd must both be 16-bit tensors or both W4Weights")
-    E, H = Wd.shape[0], Wd.shape[-1]
-    if tuple(Wgu.shape) != (E, 2 * H, D) or tuple(Wd.shape) != (E, D, H):
+    if X.dim() != 2 or w4 != isinstance(Wd, W4Weights) or len(Wd.shape) != 3:
+        raise ValueError("expected X [T, D], and Wgu [E, 2H, D] and Wd [E, D, H] either as 16-bit "
+                         "tensors or as W4Weights")
+    T, D = X.shape
+    E, H = Wd.shape[0], Wd.shape[2]
+    if Wgu.shape != (E, 2 * H, D) or Wd.shape != (E, D, H):
         raise ValueError("expected Wgu [E, 2H, %d] and Wd [E, %d, H], got %s and %s"
                          % (D, D, tuple(Wgu.shape), tuple(Wd.shape)))
     if Wgu.dtype != X.dtype or Wd.dtype != X.dtype:
         raise ValueError("activations and experts must have one dtype")
     if not w4:
         return T, D, H, E, None, Wgu, Wd
-    if not Wgu.gate_up or Wd.gate_up or (Wgu.group, Wgu.zeros) != (Wd.group, Wd.zeros):
+    if not Wgu.gate_up or Wd.gate_up or Wgu.group != Wd.group or Wgu.zeros != Wd.zeros:
         raise ValueError("mismatch: Wgu %r, Wd %r" % (Wgu, Wd))
-    return T, D, H, E, ctypes.byref(W4Format(Wd.group, int(Wd.zeros))), Wgu.packed, Wd.packed
+    return T, D, H, E, ctypes.byref(Wd.format), Wgu.packed, Wd.packed
 
 
 def swiglu_mlp_moe_experts(X, idx, weights, Wgu, Wd, out: dict | None = None, ws=None,
@@ -657,12 +663,13 @@ def swiglu_mlp_moe_experts(X, idx, weights, Wgu, Wd, out: dict | None = None, ws
         raise ValueError("expected idx int32 [T, top_k] and weights fp32 of its shape")
     k = idx.shape[1]
     Y = _out(out, "Y", (T, D), X.dtype, X.device)
-    L = lib()
+    L = _lib or lib()
     ws = _ws(ws, lambda: L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, k), X.device)
-    _check(L.swiglu_mlp_moe_experts(_ptr(X), _ptr(idx), _ptr(weights), _ptr(gu), _ptr(down),
-                                    _ptr(Y), T, D, H, E, k, fmt, dtype_code(X.dtype),
-                                    _opts(gate_mul, down_mul, False), _ptr(ws), ws.numel(),
-                                    _serving_checks(X, idx, weights, gu, down, ws)),
+    st = _serving_checks(X, idx, weights, gu, down, ws)
+    _check(L.swiglu_mlp_moe_experts(X.data_ptr(), idx.data_ptr(), weights.data_ptr(), gu.data_ptr(),
+                                    down.data_ptr(), Y.data_ptr(), T, D, H, E, k, fmt,
+                                    dtype_code(X.dtype), _opts(gate_mul, down_mul, False),
+                                    ws.data_ptr(), ws.numel(), st),
            "swiglu_mlp_moe_experts")
     _device_check(ws, "swiglu_mlp_moe_experts")
     return Y
@@ -674,19 +681,20 @@ def swiglu_mlp_moe_fwd_nograd(X, Wr, Wgu, Wd, top_k: int, norm_topk: bool = True
     """A mixture-of-experts layer for up to 64 tokens, without gradients:
     (Y [T, D], idx int32 [T, top_k], weights fp32 [T, top_k])."""
     T, D, H, E, fmt, gu, down = _experts(X, Wgu, Wd)
-    if tuple(Wr.shape) != (E, D) or Wr.dtype != X.dtype:
+    if Wr.shape != (E, D) or Wr.dtype != X.dtype:
         raise ValueError("expected Wr [%d, %d] of %s, got %s %s" % (E, D, X.dtype, tuple(Wr.shape),
                                                                     Wr.dtype))
     Y = _out(out, "Y", (T, D), X.dtype, X.device)
     idx = _out(out, "idx", (T, top_k), torch.int32, X.device)
     w = _out(out, "weights", (T, top_k), torch.float32, X.device)
-    L = lib()
+    L = _lib or lib()
     ws = _ws(ws, lambda: L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, top_k), X.device)
-    _check(L.swiglu_mlp_moe_fwd_nograd(_ptr(X), _ptr(Wr), _ptr(gu), _ptr(down), _ptr(Y), _ptr(idx),
-                                       _ptr(w), T, D, H, E, top_k, int(norm_topk),
-                                       float(route_scale), fmt, dtype_code(X.dtype),
-                                       _opts(gate_mul, down_mul, False), _ptr(ws), ws.numel(),
-                                       _serving_checks(X, Wr, gu, down, ws)),
+    st = _serving_checks(X, Wr, gu, down, ws)
+    _check(L.swiglu_mlp_moe_fwd_nograd(X.data_ptr(), Wr.data_ptr(), gu.data_ptr(), down.data_ptr(),
+                                       Y.data_ptr(), idx.data_ptr(), w.data_ptr(), T, D, H, E,
+                                       top_k, int(norm_topk), float(route_scale), fmt,
+                                       dtype_code(X.dtype), _opts(gate_mul, down_mul, False),
+                                       ws.data_ptr(), ws.numel(), st),
            "swiglu_mlp_moe_fwd_nograd")
     _device_check(ws, "swiglu_mlp_moe_fwd_nograd")
     return Y, idx, w

@@ -61,10 +61,7 @@ struct FtArgs {
   const void* X;     // [*, K]: token rows, or (FT_COMBINE) one row per assignment
   void* out;
   float scale;
-  // 4-bit weights: group = 1 << group_log2, groups per row, offsets of the
-  // scales and the zero points in a packed matrix
-  int group_log2, groups, zeros;
-  int64_t scales_off, zeros_off;
+  int group_log2, zeros;  // 4-bit weights: group = 1 << group_log2, zero points
   // mixture of experts
   int E, topk;
   const int* idx;    // [M, topk] experts (values outside 0..E-1: none)
@@ -153,16 +150,17 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   return v;
 }
 
-// Four 16-bit pairs of whole numbers q - z from the 8 codes of a word: nibble
-// i (i < 4) and nibble i + 4 are the halves of pair i; pairs 0 and 2 belong to
-// row g (zlo = 128 + z or 1024 + z, twice), 1 and 3 to row g + 8 (zhi).
+// The four operand registers of one 16-k product from the codes of rows g (lo)
+// and g + 8 (hi), as whole numbers q - z: bits 0..7 and 16..23 of each word
+// are used (zlo, zhi = 128 + z or 1024 + z of the two rows, twice).
 template <bool BF16>
-__device__ __forceinline__ void ft_codes(uint32_t w, uint32_t zlo, uint32_t zhi, uint32_t (&a)[4]) {
+__device__ __forceinline__ void ft_codes(uint32_t lo, uint32_t hi, uint32_t zlo, uint32_t zhi,
+                                         uint32_t (&a)[4]) {
   constexpr uint32_t M = Ft16<BF16>::MAGIC;
-  a[0] = Ft16<BF16>::sub2((w & 0x000f000fu) | M, zlo);
-  a[1] = Ft16<BF16>::sub2(((w >> 4) & 0x000f000fu) | M, zhi);
-  a[2] = Ft16<BF16>::sub2(((w >> 8) & 0x000f000fu) | M, zlo);
-  a[3] = Ft16<BF16>::sub2(((w >> 12) & 0x000f000fu) | M, zhi);
+  a[0] = Ft16<BF16>::sub2((lo & 0x000f000fu) | M, zlo);
+  a[1] = Ft16<BF16>::sub2((hi & 0x000f000fu) | M, zhi);
+  a[2] = Ft16<BF16>::sub2(((lo >> 4) & 0x000f000fu) | M, zlo);
+  a[3] = Ft16<BF16>::sub2(((hi >> 4) & 0x000f000fu) | M, zhi);
 }
 
 __device__ __forceinline__ float ft_silu(float g) { return g / (1.0f + __expf(-g)); }
@@ -173,6 +171,7 @@ struct FtUnit {
   static constexpr int TOKENS = 8 * NT;                 // tokens of one pass over a tile
   static constexpr int GROUPS = G32 ? 2 : 1;            // groups of 64 k
   static constexpr int W = 0;                           // RT x (4-bit: 512, 16-bit: 2048) bytes
+  static constexpr int RECORD = 512 + GROUPS * (ZP ? 48 : 32);  // a packed unit in memory
   static constexpr int S = RT * (W4 ? 512 : 2048);      // RT x GROUPS x 128: two scales per lane
   static constexpr int Z = S + (W4 ? RT * GROUPS * 128 : 0);  // and two zero points (in 4 bytes)
   static constexpr int BYTES = Z + (ZP ? RT * GROUPS * 128 : 0);
@@ -378,7 +377,7 @@ __global__ void __launch_bounds__(FT_THREADS, 1) ft_kernel(const FtArgs a) {
   // ---------------------------------------------------------------- copies in
   const uint32_t ring = smem_u32(smem) + a.ring_off + warp * a.depth * U::BYTES;
   FtWalk in = {0, 0, 0, 0, 0};
-  const uint8_t *pw[RT], *pw8[RT], *ps[RT], *pz[RT];  // this lane's sources at u = 0
+  const uint8_t *pw[RT], *pw8[RT];  // this lane's sources at u = 0
   auto weights_of = [&](const FtWalk& w) {
     int tile, expert, first, count;
     piece_at(w.run, w.piece, tile, expert, first, count);
@@ -387,9 +386,7 @@ __global__ void __launch_bounds__(FT_THREADS, 1) ft_kernel(const FtArgs a) {
     for (int i = 0; i < RT; ++i) {
       const int t16 = min(tile * RT + i, a.tiles16 - 1);  // a tile past the end repeats the last
       if (W4) {
-        pw[i] = m + (int64_t)t16 * nk * 512 + lane * 16;
-        ps[i] = m + a.scales_off + (int64_t)t16 * a.groups * 32 + g * 4;
-        if (ZP) pz[i] = m + a.zeros_off + (int64_t)t16 * a.groups * 16 + (g >> 1) * 4;
+        pw[i] = m + (int64_t)t16 * nk * U::RECORD;
       } else {
         // a row past the end repeats the last one (its results are not stored)
         const bool gu = a.mode == FT_GATE_UP;
@@ -421,15 +418,13 @@ __global__ void __launch_bounds__(FT_THREADS, 1) ft_kernel(const FtArgs a) {
     if (W4) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        cp_async_cg16(d + U::W + i * 512, pw[i] + (int64_t)u * 512, 16u);
-        const int g0 = (u * 64) >> a.group_log2;
-        cp_async_ca4(slot + U::S + (i * U::GROUPS) * 128 + lane * 4, ps[i] + (int64_t)g0 * 32);
-        if (ZP)
-          cp_async_ca4(slot + U::Z + (i * U::GROUPS) * 128 + lane * 4, pz[i] + (int64_t)g0 * 16);
-        if (G32) {
-          const int g1 = min(g0 + 1, a.groups - 1);
-          cp_async_ca4(slot + U::S + (i * 2 + 1) * 128 + lane * 4, ps[i] + (int64_t)g1 * 32);
-          if (ZP) cp_async_ca4(slot + U::Z + (i * 2 + 1) * 128 + lane * 4, pz[i] + (int64_t)g1 * 16);
+        const uint8_t* rec = pw[i] + (int64_t)u * U::RECORD;
+        cp_async_cg16(d + U::W + i * 512, rec + lane * 16, 16u);
+#pragma unroll
+        for (int h = 0; h < U::GROUPS; ++h) {
+          const uint32_t at = (i * U::GROUPS + h) * 128 + lane * 4;
+          cp_async_ca4(slot + U::S + at, rec + 512 + h * 32 + g * 4);
+          if (ZP) cp_async_ca4(slot + U::Z + at, rec + 512 + U::GROUPS * 32 + h * 16 + (g >> 1) * 4);
         }
       }
     } else {
@@ -558,10 +553,10 @@ __global__ void __launch_bounds__(FT_THREADS, 1) ft_kernel(const FtArgs a) {
             z1h = P::MAGIC + ((q1 >> 8) & 0xffu) * 0x10001u;
           }
         }
-        ft_codes<BF16>(c.x, z0l, z0h, A[0]);
-        ft_codes<BF16>(c.y, z0l, z0h, A[1]);
-        ft_codes<BF16>(c.z, z1l, z1h, A[2]);
-        ft_codes<BF16>(c.w, z1l, z1h, A[3]);
+        ft_codes<BF16>(c.x, c.y, z0l, z0h, A[0]);
+        ft_codes<BF16>(c.x >> 8, c.y >> 8, z0l, z0h, A[1]);
+        ft_codes<BF16>(c.z, c.w, z1l, z1h, A[2]);
+        ft_codes<BF16>(c.z >> 8, c.w >> 8, z1l, z1h, A[3]);
         const float s0g = P::lo(sc0), s0h = P::hi(sc0);
         const float s1g = G32 ? P::lo(sc1) : s0g, s1h = G32 ? P::hi(sc1) : s0h;
 #pragma unroll

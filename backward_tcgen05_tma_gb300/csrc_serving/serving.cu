@@ -13,6 +13,7 @@
 #include "host_shared.h"
 #include "moe_route.cuh"
 #include "w4_layout.cuh"
+#include "w4_stream.cuh"
 
 using namespace swiglu;
 
@@ -77,6 +78,7 @@ cudaError_t allow_smem(int bytes) {
 
 constexpr int SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
 constexpr int FT_MAX_DEPTH = 8;
+constexpr int WS_SMEM = 224 * 1024;
 
 template <bool BF16, bool W4, int RT, int NT, bool G32, bool ZP, bool MOE>
 cudaError_t launch_ft(host::ServingKernel id, FtArgs a, cudaStream_t st) {
@@ -150,10 +152,79 @@ void set_w4(FtArgs& a, const W4Geom& w) {
   a.tiles16 = w.tiles;
   a.expert_bytes = w.bytes;
   a.group_log2 = w.group_log2;
-  a.groups = w.groups;
   a.zeros = w.zeros;
-  a.scales_off = w.scales_off;
-  a.zeros_off = w.zeros_off;
+}
+
+// One product with packed 4-bit weights: the shared-memory plan (as few phases
+// of the contraction as leave the ring two stages) and the launch.
+template <bool BF16, int RT, int NT, bool G32, bool ZP>
+cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_t st) {
+  using S = WsShape<RT, NT, G32, ZP>;
+  constexpr auto kern = w4_stream_kernel<BF16, RT, NT, G32, ZP>;
+  cudaError_t e = allow_smem<kern>(WS_SMEM);
+  if (e != cudaSuccess) return e;
+  auto up = [](int v) { return (v + 127) & ~127; };
+  const int nsm = host::sms() > 0 ? host::sms() : 1;
+  const int tiles = (tiles16 + RT - 1) / RT, grid = tiles < nsm ? tiles : nsm;
+  a.tiles16 = tiles16;
+  a.tile_quot = tiles / grid;
+  a.tile_rem = tiles % grid;
+  const int per_block = a.tile_quot + (a.tile_rem != 0), most = 24 / (RT * NT);
+  a.run = per_block < most ? per_block : most;
+  const int nk = (a.K + 63) / 64, rows = a.M < S::TOKENS ? a.M : S::TOKENS;
+  const int ring = WS_WARPS * S::STAGE, part = (a.run + WS_WARPS - 1) * S::PART;
+  for (int phases = 1;; ++phases) {
+    a.phase_units = (nk + phases - 1) / phases;
+    if (phases > 1) a.phase_units = (a.phase_units + S::UNITS - 1) / S::UNITS * S::UNITS;
+    a.phases = (nk + a.phase_units - 1) / a.phase_units;
+    a.sum_off = up(rows * S::xrow(a.phase_units));
+    a.part_off = up(a.sum_off + a.phase_units * S::SUMS);
+    a.tile_off = up(a.part_off + part);
+    a.ring_off = up(a.tile_off + (a.phases > 1 ? a.run * S::PART : 0));
+    a.stages = a.ring_off < WS_SMEM ? (WS_SMEM - a.ring_off) / ring : 0;
+    if (a.stages >= 2) break;
+    if (a.phase_units <= S::UNITS) return cudaErrorInvalidConfiguration;
+  }
+  if (a.stages > WS_MAX_STAGES) a.stages = WS_MAX_STAGES;
+  a.wait_limit_ns = host::wait_limit_ns();
+  a.inject = host::take_stall() ? 1 : 0;
+  host::Prof prof(id, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(WS_THREADS);
+  cfg.dynamicSmemBytes = a.ring_off + a.stages * ring;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // per-kernel event timing would serialise the launches, so no overlap then
+  cfg.attrs = attr;
+  cfg.numAttrs = host::profiling() ? 0 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  host::count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, cudaStream_t st) {
+  const bool zeros = w.zeros != 0, g32 = w.sets == 2;
+  if (a.M <= 8) {
+    if (g32)
+      return zeros ? launch_ws<BF16, 1, 1, true, true>(id, a, w.tiles, st)
+                   : launch_ws<BF16, 1, 1, true, false>(id, a, w.tiles, st);
+    return zeros ? launch_ws<BF16, 1, 1, false, true>(id, a, w.tiles, st)
+                 : launch_ws<BF16, 1, 1, false, false>(id, a, w.tiles, st);
+  }
+  if (g32)
+    return zeros ? launch_ws<BF16, 2, 2, true, true>(id, a, w.tiles, st)
+                 : launch_ws<BF16, 2, 2, true, false>(id, a, w.tiles, st);
+  return zeros ? launch_ws<BF16, 2, 2, false, true>(id, a, w.tiles, st)
+               : launch_ws<BF16, 2, 2, false, false>(id, a, w.tiles, st);
+}
+
+cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, swiglu_dtype dt,
+                      cudaStream_t st) {
+  return dt == SWIGLU_BF16 ? launch_ws<true>(id, a, w, st) : launch_ws<false>(id, a, w, st);
 }
 
 #ifdef SWIGLU_DEBUG
@@ -327,7 +398,7 @@ swiglu_status swiglu_mlp_w4_pack(const void* codes, const void* scales, const vo
   if ((st = check_ptrs({codes, scales, packed})) != SWIGLU_OK) return st;
   if (reinterpret_cast<uintptr_t>(zeros) & 15u) return SWIGLU_ERR_ALIGNMENT;
   const W4Geom w = w4_geom(N, K, log2_group(group), zeros != nullptr, gate_up ? 1 : 0);
-  const int grid = grid_for(((int64_t)w.tiles * w.blocks * 32 + (int64_t)w.tiles * w.groups * 16) * E);
+  const int grid = grid_for((int64_t)w.tiles * w.blocks * 32 * E);
   w4_pack_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
       w, E, static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
       static_cast<const uint8_t*>(zeros), static_cast<uint8_t*>(packed));
@@ -377,8 +448,8 @@ swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, i
   if ((st = check_ws(ws, ws_bytes, swiglu_mlp_w4_workspace_bytes(M, N, K))) != SWIGLU_OK) return st;
   if (M == 0) return SWIGLU_OK;
   if ((st = check_ptrs({X, packed, Y})) != SWIGLU_OK) return st;
-  FtArgs a = {};
-  a.mode = FT_LINEAR;
+  const W4Geom w = w4_geom(N, K, log2_group(group), zeros, 0);
+  WsArgs a = {};
   a.M = (int)M;
   a.K = (int)K;
   a.rows = (int)N;
@@ -386,12 +457,11 @@ swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, i
   a.X = X;
   a.out = Y;
   a.scale = 1.0f;
-  a.clear_err = 1;
+  a.first = 1;
   a.err = static_cast<int*>(ws);
-  set_w4(a, w4_geom(N, K, log2_group(group), zeros, 0));
-  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {ws, ws_bytes}});
-  return status_of(launch_dt<true, false>(host::SK_W4_LINEAR, a, (int)M, dtype,
-                                          static_cast<cudaStream_t>(stream)));
+  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {X, (size_t)(M * K * 2)}, {packed, (size_t)w.bytes}});
+  return status_of(launch_ws(host::SK_W4_LINEAR, a, w, dtype,
+                             static_cast<cudaStream_t>(stream)));
 }
 
 swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const void* Wd, void* Y,
@@ -413,8 +483,9 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   if (M == 0) return SWIGLU_OK;
   if ((st = check_ptrs({X, Wgu, Wd, Y, A})) != SWIGLU_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  FtArgs a = {};
-  a.mode = FT_GATE_UP;
+  const W4Geom gu = w4_geom(2 * H, D, log2_group(group), zeros, 1);
+  WsArgs a = {};
+  a.gate_up = 1;
   a.M = (int)M;
   a.K = (int)D;
   a.rows = (int)H;
@@ -422,24 +493,22 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   a.X = X;
   a.out = A;
   a.scale = mu.gate;
-  a.clear_err = 1;
+  a.first = 1;
   a.err = static_cast<int*>(ws);
-  set_w4(a, w4_geom(2 * H, D, log2_group(group), zeros, 1));
-  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {ws, ws_bytes}});
-  if (launch_dt<true, false>(host::SK_W4_GATE_UP, a, (int)M, dtype, s) != cudaSuccess)
+  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {X, (size_t)(M * D * 2)}, {Wgu, (size_t)gu.bytes}});
+  if (launch_ws(host::SK_W4_GATE_UP, a, gu, dtype, s) != cudaSuccess)
     return SWIGLU_ERR_CUDA;
-  a.mode = FT_LINEAR;
+  const W4Geom dn = w4_geom(D, H, log2_group(group), zeros, 0);
+  a.gate_up = 0;
   a.K = (int)H;
   a.rows = (int)D;
   a.W = static_cast<const uint8_t*>(Wd);
   a.X = A;
   a.out = Y;
   a.scale = mu.down;
-  a.dependent = 1;
-  a.clear_err = 0;
-  set_w4(a, w4_geom(D, H, log2_group(group), zeros, 0));
-  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {ws, ws_bytes}});
-  return status_of(launch_dt<true, false>(host::SK_W4_DOWN, a, (int)M, dtype, s));
+  a.first = 0;
+  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {A, (size_t)(M * H * 2)}, {Wd, (size_t)dn.bytes}});
+  return status_of(launch_ws(host::SK_W4_DOWN, a, dn, dtype, s));
 }
 
 size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int topk) {

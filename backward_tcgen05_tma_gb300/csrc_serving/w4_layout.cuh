@@ -2,14 +2,18 @@
 // scales, laying codes out for the few-token kernels, and expanding them.
 //
 // A packed matrix [R, K] is a run of 16-row tiles (a gate/up pair: 8 rows of
-// Wg and the 8 rows of Wu of the same hidden units), in three parts:
-//   codes   tile x ceil(K/64) blocks of 512 bytes; lane l = 4 g + t of a warp
-//           has 16 bytes at 16 l: word 2 c + h holds, of rows g and g + 8, the
-//           k = 32 c + 8 t + 4 h + {0..3} of the block's 64: nibbles 0, 4, 2, 6
-//           are row g's, 1, 5, 3, 7 row g + 8's;
-//   scales  tile x groups x 16, 16-bit, rows in the order 0, 8, 1, 9, ...;
-//   zeros   (with zero points) tile x groups x 16 bytes in the same order.
-// Rows past R have scale 0 and code = zero point; k past K has code 8.
+// Wg and the 8 rows of Wu of the same hidden units), each a run of records of
+// 64 k, each
+//   codes   512 bytes; lane l = 4 g + t of a warp has 16 bytes at 16 l: word
+//           2 c + r holds the k = 32 c + 8 t + {0..7} of row g + 8 r: k + 0, 2,
+//           4, 6 in nibbles 0..3, k + 1, 3, 5, 7 in nibbles 4..7;
+//   scales  one set of 16 (groups of 32: two, one per half), 16-bit, rows in
+//           the order 0, 8, 1, 9, ...; a scale of a group of 128 is in both of
+//           the group's records, so that a record is all a unit needs (3% more
+//           bytes, one address);
+//   zeros   (with zero points) as many sets of 16 bytes, in the same order.
+// Rows past R have scale 0; k past K have code 8, and scale 0 in a half of its
+// own.
 #pragma once
 
 #include "fewtok.cuh"
@@ -19,9 +23,11 @@ namespace swiglu {
 struct W4Geom {
   int64_t N;      // rows of the matrix (gate/up: 2H)
   int K, group_log2, groups, zeros, gate_up;
-  int blocks;     // 64-k blocks of a row
+  int blocks;     // records of a tile
   int tiles;      // 16-row tiles
-  int64_t scales_off, zeros_off, bytes;  // of one packed matrix
+  int sets;       // scale sets of a record
+  int record;     // bytes
+  int64_t bytes;  // of one packed matrix
 };
 
 __host__ __device__ inline W4Geom w4_geom(int64_t N, int64_t K, int group_log2, int zeros,
@@ -35,9 +41,9 @@ __host__ __device__ inline W4Geom w4_geom(int64_t N, int64_t K, int group_log2, 
   w.gate_up = gate_up;
   w.blocks = (int)((K + 63) >> 6);
   w.tiles = (int)(gate_up ? (N / 2 + 7) / 8 : (N + 15) / 16);
-  w.scales_off = (int64_t)w.tiles * w.blocks * 512;
-  w.zeros_off = w.scales_off + (int64_t)w.tiles * w.groups * 32;
-  w.bytes = w.zeros_off + (zeros ? (int64_t)w.tiles * w.groups * 16 : 0);
+  w.sets = group_log2 == 5 ? 2 : 1;
+  w.record = 512 + w.sets * (zeros ? 48 : 32);
+  w.bytes = (int64_t)w.tiles * w.blocks * w.record;
   return w;
 }
 
@@ -51,88 +57,76 @@ __device__ __forceinline__ int64_t w4_row(const W4Geom& w, int tile, int r) {
   return n < w.N ? n : -1;
 }
 
-// One thread per 16 bytes of a matrix's packed codes, then per scale.
+// One warp per record of the packed copy.
 __global__ void w4_pack_kernel(W4Geom w, int64_t experts, const uint8_t* codes,
                                const uint16_t* scales, const uint8_t* zeros, uint8_t* packed) {
-  const int64_t nc = (int64_t)w.tiles * w.blocks * 32, ns = (int64_t)w.tiles * w.groups * 16;
-  const int64_t total = (nc + ns) * experts;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t e = i / (nc + ns), j = i - e * (nc + ns);
-    uint8_t* out = packed + e * w.bytes;
-    if (j < nc) {
-      const int lane = (int)(j & 31), g = lane >> 2, t = lane & 3;
-      const int b = (int)((j >> 5) % w.blocks), tile = (int)((j >> 5) / w.blocks);
-      const int64_t r0 = w4_row(w, tile, g), r1 = w4_row(w, tile, g + 8);
-      uint32_t o[4];
+  const int64_t per = (int64_t)w.tiles * w.blocks, total = per * experts;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < total; i += warps) {
+    const int64_t e = i / per, j = i - e * per;
+    const int tile = (int)(j / w.blocks), b = (int)(j - (int64_t)tile * w.blocks);
+    uint8_t* out = packed + e * w.bytes + j * w.record;
+    uint32_t o[4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t row = w4_row(w, tile, g + 8 * r);
         const int k = b * 64 + c * 32 + t * 8;
-        uint32_t v0 = 0x88888888u, v1 = 0x88888888u;  // 8 codes of each row, nibble n = k + n
-        if (k < w.K) {
-          const int64_t half = w.K / 2;
-          if (r0 >= 0) v0 = *reinterpret_cast<const uint32_t*>(codes + (e * w.N + r0) * half + k / 2);
-          if (r1 >= 0) v1 = *reinterpret_cast<const uint32_t*>(codes + (e * w.N + r1) * half + k / 2);
-        }
+        uint32_t v = 0x88888888u;  // nibble n: element k + n
+        if (k < w.K && row >= 0)
+          v = *reinterpret_cast<const uint32_t*>(codes + ((e * w.N + row) * w.K + k) / 2);
+        uint32_t x = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = v0 >> (16 * h), q = v1 >> (16 * h);
-          o[2 * c + h] = (a & 15u) | (q & 15u) << 4 | ((a >> 8) & 15u) << 8 | ((q >> 8) & 15u) << 12 |
-                         ((a >> 4) & 15u) << 16 | ((q >> 4) & 15u) << 20 |
-                         ((a >> 12) & 15u) << 24 | ((q >> 12) & 15u) << 28;
-        }
+        for (int n = 0; n < 4; ++n)
+          x |= ((v >> (8 * n)) & 15u) << (4 * n) | ((v >> (8 * n + 4)) & 15u) << (16 + 4 * n);
+        o[2 * c + r] = x;
       }
-      reinterpret_cast<uint4*>(out)[j] = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      const int64_t q = j - nc;
-      const int slot = (int)(q & 15), gr = (int)((q >> 4) % w.groups),
-                tile = (int)((q >> 4) / w.groups);
-      const int64_t r = w4_row(w, tile, (slot >> 1) + 8 * (slot & 1));
-      const int64_t src = (e * w.N + r) * w.groups + gr;
-      reinterpret_cast<uint16_t*>(out + w.scales_off)[q] = r >= 0 ? scales[src] : 0;
-      if (w.zeros) out[w.zeros_off + q] = r >= 0 ? zeros[src] & 15u : 8u;
+    reinterpret_cast<uint4*>(out)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
+    if (lane < 16 * w.sets) {
+      const int slot = lane & 15, h = lane >> 4;
+      const int64_t row = w4_row(w, tile, (slot >> 1) + 8 * (slot & 1));
+      const int gr = (b * 64 + h * 32) >> w.group_log2;
+      const bool in = row >= 0 && gr < w.groups;
+      const int64_t src = (e * w.N + row) * w.groups + gr;
+      reinterpret_cast<uint16_t*>(out + 512)[lane] = in ? scales[src] : 0;
+      if (w.zeros) out[512 + 32 * w.sets + lane] = in ? zeros[src] & 15u : 8u;
     }
   }
 }
 
-// W[n, k] = rnd(s (q - z)), one thread per 16 bytes of packed codes; s (q - z)
-// is exact in fp32 (12 + 4 bits), so each weight is rounded once.
+// W[n, k] = rnd(s (q - z)), one warp per record; s (q - z) is exact in fp32
+// (12 + 4 bits), so each weight is rounded once.
 template <bool BF16>
 __global__ void w4_unpack_kernel(W4Geom w, int64_t experts, const uint8_t* packed, uint16_t* W) {
-  const int64_t nc = (int64_t)w.tiles * w.blocks * 32, total = nc * experts;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t e = i / nc, j = i - e * nc;
-    const uint8_t* in = packed + e * w.bytes;
-    const int lane = (int)(j & 31), g = lane >> 2, t = lane & 3;
-    const int b = (int)((j >> 5) % w.blocks), tile = (int)((j >> 5) / w.blocks);
-    const uint4 v = reinterpret_cast<const uint4*>(in)[j];
+  const int64_t per = (int64_t)w.tiles * w.blocks, total = per * experts;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < total; i += warps) {
+    const int64_t e = i / per, j = i - e * per;
+    const int tile = (int)(j / w.blocks), b = (int)(j - (int64_t)tile * w.blocks);
+    const uint8_t* in = packed + e * w.bytes + j * w.record;
+    const uint4 v = reinterpret_cast<const uint4*>(in)[lane];
     const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int k = b * 64 + c * 32 + t * 8;
-      if (k >= w.K) continue;
-      const int64_t gi = (int64_t)tile * w.groups + (k >> w.group_log2);
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const int64_t r = w4_row(w, tile, g + 8 * hi);
-        if (r < 0) continue;
-        const uint16_t sb = reinterpret_cast<const uint16_t*>(in + w.scales_off)[gi * 16 + g * 2 + hi];
-        const float s = Ft16<BF16>::lo(sb);
-        const int z = w.zeros ? in[w.zeros_off + gi * 16 + g * 2 + hi] : 8;
+      for (int r = 0; r < 2; ++r) {
+        const int64_t row = w4_row(w, tile, g + 8 * r);
+        const int k = b * 64 + c * 32 + t * 8, set = w.sets == 2 ? c : 0;
+        if (k >= w.K || row < 0) continue;
+        const float s = Ft16<BF16>::lo(reinterpret_cast<const uint16_t*>(in + 512)[set * 16 + g * 2 + r]);
+        const int z = w.zeros ? in[512 + 32 * w.sets + set * 16 + g * 2 + r] : 8;
         uint32_t o[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = word[2 * c + h] >> (4 * hi);
-          // nibbles 0, 4 are k + {0, 1}; 2, 6 are k + {2, 3}
-          o[2 * h] = Ft16<BF16>::rnd(s * (float)((int)(x & 15u) - z)) |
-                     (uint32_t)Ft16<BF16>::rnd(s * (float)((int)((x >> 16) & 15u) - z)) << 16;
-          o[2 * h + 1] = Ft16<BF16>::rnd(s * (float)((int)((x >> 8) & 15u) - z)) |
-                         (uint32_t)Ft16<BF16>::rnd(s * (float)((int)((x >> 24) & 15u) - z)) << 16;
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t x = word[2 * c + r] >> (4 * n);
+          o[n] = Ft16<BF16>::rnd(s * (float)((int)(x & 15u) - z)) |
+                 (uint32_t)Ft16<BF16>::rnd(s * (float)((int)((x >> 16) & 15u) - z)) << 16;
         }
-        *reinterpret_cast<uint4*>(W + (e * w.N + r) * w.K + k) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(W + (e * w.N + row) * w.K + k) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-    }
   }
 }
 

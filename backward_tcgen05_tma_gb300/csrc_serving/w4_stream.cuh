@@ -1,0 +1,552 @@
+// w4_stream.cuh -- products of a few tokens (1..64) with 4-bit weights:
+//   Y[m, r] = sum_k X[m, k] W[r, k],   W[r, k] = s[r, k/G] (q[r, k] - z[r, k/G])
+// and the SwiGLU of such products (gate/up).
+//
+// What bounds it: half a byte per weight, so at the HBM rate an SM meets 46
+// weights per cycle, and unpacking them takes most of its issue slots.  The
+// design spends as few instructions per weight as it can:
+//   * A code becomes a 16-bit number by OR-ing it into the mantissa of 128
+//     (bf16) or 1024 (fp16).  In fp16 bits 4..7 can stay where they are, as
+//     1024 + 16 q: one shift serves two nibbles, and the products of the two
+//     forms are added up apart, the second sum scaled by 1/16.
+//   * Nothing is subtracted from the codes.  The accumulator of a unit (64 k,
+//     or with groups of 32 half of one) starts at
+//         -(m1 + z) S1 - (m2 + z) S2
+//     with S1, S2 the sums of the token elements that meet the two forms (m1 =
+//     m2 = 128 in bf16; 1024 and 64 in fp16), which are computed once per token
+//     (on the tensor core, as products with constant rows) and shared by all
+//     weight rows.  What the products then add leaves sum (q - z) x up to fp32
+//     rounding, 2^-24 of some 30 (bf16) or 200 (fp16) times the mean term: far
+//     below the output's own rounding.
+//   * A warp's weights are runs of unit records (codes, then scales, then zero
+//     points) that bulk copies bring into a ring of its own, 8 records a copy.
+// Each group's sum is scaled in fp32; no weight is rounded.  (A token with an
+// infinity gives NaN where exact arithmetic might give an infinity.)
+//
+// Work: a block takes a contiguous run of tiles of 16 RT weight rows (gate/up:
+// each 16 are 8 rows of Wg and the 8 rows of Wu of the same hidden units), cuts
+// each into chunks of units, lays the chunks end to end and gives each of its
+// 16 warps an equal share.  A share that ends inside a tile leaves a partial
+// tile in shared memory; at the end of the run the block adds each tile's
+// partials in order, applies the epilogue and writes, so results are
+// deterministic.  Where the tokens' rows do not fit shared memory the
+// contraction is taken in phases; more than 16 tokens take several passes over
+// the weights, which the L2 cache then holds.  From 9 tokens on a tile has 32
+// rows (RT = 2): shared memory, which delivers 128 bytes a cycle, would
+// otherwise give most of them to the token rows.
+#pragma once
+
+#include "fewtok.cuh"
+
+namespace swiglu {
+
+constexpr int WS_WARPS = 16;
+constexpr int WS_THREADS = WS_WARPS * 32;
+constexpr int WS_MAX_STAGES = 8;
+
+struct WsArgs {
+  int gate_up;       // out = rnd(SiLU(scale g) u), else rnd(scale v)
+  int M, K;          // tokens; contraction, a multiple of 8
+  int rows;          // rows of out: output features, or hidden units (gate/up)
+  int tiles16;       // 16-row tiles
+  int tile_quot, tile_rem;  // tiles of 16 RT rows: quot a block, one more in the first rem
+  const uint8_t* W;  // packed
+  const void* X;     // [M, K]
+  void* out;         // [M, rows]
+  float scale;
+  int first;         // first kernel of a call: waits for the work before it at once, and
+                     //   block 0 clears the error word; else the weights are read before
+                     //   the kernel before it, which writes X, is waited for
+  int inject;        // test hook: warp 0's first stage is never filled
+  // plan: k-units of a phase, tiles of a run, ring stages, shared-memory offsets
+  int phases, phase_units, run, stages;
+  int sum_off, part_off, tile_off, ring_off;
+  uint64_t wait_limit_ns;
+  int* err;
+#ifdef SWIGLU_DEBUG
+  DbgWin dbg;        // out, X, packed weights, workspace
+#endif
+};
+
+template <int RT, int NT, bool G32, bool ZP>
+struct WsShape {
+  static constexpr int TOKENS = 8 * NT;
+  static constexpr int UNITS = 8 / RT;                             // units of a chunk
+  static constexpr int GROUPS = G32 ? 2 : 1;                       // scales of a unit and row
+  static constexpr int RECORD = 512 + GROUPS * (ZP ? 48 : 32);     // bytes of a unit
+  static constexpr int PIECE = UNITS * RECORD;                     // one 16-row tile's chunk
+  static constexpr int STAGE = RT * PIECE;
+  static constexpr int SUMS = GROUPS * NT * 64;                    // bytes of a unit's sums
+  static constexpr int PART = RT * NT * 512;                       // a partial tile
+  static __host__ __device__ constexpr int xrow(int units) { return units * 128 + 64; }
+};
+
+// Shared-memory loads at a compile-time distance from a lane's base address.
+template <int OFF>
+__device__ __forceinline__ uint4 lds128_at(uint32_t base) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(base), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds32_at(uint32_t base) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(base), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds16_at(uint32_t base) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1+%2];" : "=h"(v) : "r"(base), "n"(OFF));
+  return v;
+}
+template <int N>
+struct WsInt {
+  static constexpr int value = N;
+};
+
+// (v & mask) | bits in one instruction
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "r"(bits));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float4 mma_ws(float4 c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  float4 d;
+  if (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z),
+          "f"(c.w));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z),
+          "f"(c.w));
+  return d;
+}
+
+// 16-bit pairs of the constants that the token sums are products with: the
+// magic numbers of the first and the second form (negative; with -8 where there
+// are no zero points), and 1.
+template <bool BF16, bool ZP>
+struct WsConst {
+  static constexpr uint32_t C1 = BF16 ? (ZP ? 0xc300c300u : 0xc308c308u)   // -128, -136
+                                      : (ZP ? 0xe400e400u : 0xe408e408u);  // -1024, -1032
+  static constexpr uint32_t C2 = BF16 ? C1 : (ZP ? 0xd400d400u : 0xd480d480u);  // -64, -72
+  static constexpr uint32_t ONE = BF16 ? 0x3f803f80u : 0x3c003c00u;
+};
+
+// One warp's place in the block's work: token pass, run of tiles, phase of the
+// contraction, and the chunks [v, v_end) of the run and phase laid end to end;
+// chunk v is chunk c of the run's tile j.
+struct WsWalk {
+  int pass, run, phase, v, v_end, j, c;
+};
+
+template <bool BF16, int RT, int NT, bool G32, bool ZP>
+__global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a) {
+  using S = WsShape<RT, NT, G32, ZP>;
+  using P = Ft16<BF16>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[WS_WARPS * WS_MAX_STAGES + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = smem_u32(bars) + warp * WS_MAX_STAGES * 8;
+  const uint32_t xbar = smem_u32(bars + WS_WARPS * WS_MAX_STAGES);
+
+  // Every launch is a programmatic dependent of the one before it, so that its
+  // blocks are in place when that one ends; the first kernel of a call touches
+  // nothing before then.
+  if (a.first) {
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  }
+  pdl_launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < a.stages; ++i) mbar_init(bar0 + 8 * i, 1);
+    if (warp == 0) mbar_init(xbar, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  const int nk = (a.K + 63) >> 6;
+  const int b = blockIdx.x;
+  const int tile0 = b * a.tile_quot + min(b, a.tile_rem);
+  const int tiles = a.tile_quot + (b < a.tile_rem ? 1 : 0);
+  const int passes = (a.M + S::TOKENS - 1) / S::TOKENS;
+  const int runs = tiles <= a.run ? 1 : (tiles + a.run - 1) / a.run;
+  const int phases = a.phases;
+  auto run_tiles = [&](int r) { return min(a.run, tiles - r * a.run); };
+  auto phase_len = [&](int p) { return min(a.phase_units, nk - p * a.phase_units); };  // units
+  auto chunks_of = [&](int len) { return (len + S::UNITS - 1) / S::UNITS; };
+  auto enter = [&](WsWalk& w) {  // this warp's share from here on, skipping empty ones
+    for (; w.pass < passes; ++w.pass, w.run = 0) {
+      for (; w.run < runs; ++w.run, w.phase = 0) {
+        for (; w.phase < phases; ++w.phase) {
+          const int per = chunks_of(phase_len(w.phase)), total = run_tiles(w.run) * per;
+          w.v = total * warp / WS_WARPS;
+          w.v_end = total * (warp + 1) / WS_WARPS;
+          w.j = w.v / per;
+          w.c = w.v - w.j * per;
+          if (w.v < w.v_end) return;
+        }
+      }
+    }
+  };
+
+  // ---------------------------------------------------------------- weights in
+  WsWalk in = {0, 0, 0, 0, 0, 0, 0};
+  const uint8_t* src = nullptr;       // the next chunk
+  int in_per = 0, in_last = 0;        // chunks of a tile; bytes of its last chunk (16 rows)
+  auto locate = [&]() {
+    if (in.pass >= passes) return;
+    const int len = phase_len(in.phase);
+    in_per = chunks_of(len);
+    in_last = (len - (in_per - 1) * S::UNITS) * S::RECORD;
+    src = a.W + ((int64_t)(tile0 + in.run * a.run + in.j) * RT * nk + in.phase * a.phase_units +
+                 in.c * S::UNITS) * S::RECORD;
+  };
+  enter(in);
+  locate();
+  uint32_t slot_in = 0;               // byte offset of the next stage to fill, in its ring
+  uint32_t bar_in = bar0;             // and its barrier
+  int filled = 0;                     // stages filled and not yet consumed
+  const uint32_t ring = sbase + a.ring_off + warp * a.stages * S::STAGE;
+  const uint32_t ring_bytes = a.stages * S::STAGE, bar_end = bar0 + 8 * a.stages;
+  bool skip = a.inject && warp == 0;  // test hook
+  auto fill = [&]() {  // the next stage: the units of one chunk
+    if (in.pass >= passes) return;
+    const uint32_t bytes = in.c == in_per - 1 ? in_last : S::PIECE;
+    if (lane == 0 && !skip) {
+      // the second half of the last tile may lie past the matrix
+      const int parts = RT == 1 ? 1 : min(RT, a.tiles16 - (tile0 + in.run * a.run + in.j) * RT);
+      mbar_arrive_expect_tx(bar_in, parts * bytes);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        if (i < parts) {
+          const uint8_t* p = src + (int64_t)i * nk * S::RECORD;
+          if (SWIGLU_CHECK_PTR(a.dbg, p, bytes, a.err))
+            bulk_load(ring + slot_in + i * S::PIECE, p, bytes, bar_in);
+        }
+    }
+    skip = false;
+    src += bytes;
+    slot_in += S::STAGE;
+    bar_in += 8;
+    if (slot_in == ring_bytes) {
+      slot_in = 0;
+      bar_in = bar0;
+    }
+    ++filled;
+    if (++in.c == in_per) {
+      in.c = 0;
+      src += (int64_t)(RT * nk - phase_len(in.phase)) * S::RECORD;  // the next tile
+    }
+    if (++in.v == in.v_end) {
+      ++in.phase;
+      enter(in);
+      locate();
+    }
+  };
+  for (int i = 0; i < a.stages; ++i) fill();
+  if (!a.first) pdl_wait();  // before the first read of a token row
+
+  // ---------------------------------------------------------------- token rows
+  // Units [u0, u0 + len) of the rows [m0, m0 + count): bulk copies bring them,
+  // and the warps add up each unit's elements per token.
+  uint32_t xparity = 0;
+  bool xlive = true;
+  auto stage_rows = [&](int m0, int count, int u0, int len) {
+    const int xrow = S::xrow(a.phase_units);
+    const int inside = min(len * 64, a.K - u0 * 64);  // elements of a row
+    if (warp == 0) {
+      // what was read or written here before is ordered with the copies
+      fence_proxy_async_shared();
+      if (lane == 0) mbar_arrive_expect_tx(xbar, count * inside * 2);
+      __syncwarp();
+      if (lane < count) {
+        const uint8_t* p = static_cast<const uint8_t*>(a.X) + ((int64_t)(m0 + lane) * a.K + u0 * 64) * 2;
+        if (SWIGLU_CHECK_PTR(a.dbg, p, inside * 2, a.err))
+          bulk_load(sbase + lane * xrow, p, inside * 2, xbar);
+      }
+    }
+    // zeros from the end of a row to the end of its last unit
+    const int gap = (len * 64 - inside) / 8;  // 16-byte pieces, 0..7
+    if ((int)threadIdx.x < count * gap) {
+      const int m = threadIdx.x / gap, c = threadIdx.x - m * gap;
+      *reinterpret_cast<uint4*>(smem + m * xrow + inside * 2 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    if (xlive) xlive = mbar_wait_bounded(xbar, xparity, a.wait_limit_ns, nullptr, a.err);
+    xparity ^= 1u;
+    __syncthreads();
+    using C = WsConst<BF16, ZP>;
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = warp; i < len * NT; i += WS_WARPS) {
+      const int u = i / NT, nt = i - u * NT;
+      const uint32_t p = sbase + min(nt * 8 + g, count - 1) * xrow + u * 128 + t * 16;
+      const uint4 x0 = lds128_at<0>(p), x1 = lds128_at<64>(p);
+      auto half = [&](float4 c, uint4 x, uint32_t k1, uint32_t k2) {
+        c = mma_ws<BF16>(c, k1, k1, k1, k1, x.x, x.z);
+        return mma_ws<BF16>(c, k2, k2, k2, k2, x.y, x.w);
+      };
+      float* o = reinterpret_cast<float*>(smem + a.sum_off + u * S::SUMS + nt * 64 + t * 16);
+      float4 c = half(zero, x0, C::C1, C::C2), z = ZP ? half(zero, x0, C::ONE, C::ONE) : c;
+      if (G32) {
+        if (g == 0) *reinterpret_cast<float4*>(o) = make_float4(c.x, c.y, z.x, z.y);
+        o += NT * 16;
+        c = z = zero;
+      }
+      c = half(c, x1, C::C1, C::C2);
+      z = ZP ? half(z, x1, C::ONE, C::ONE) : c;
+      if (g == 0) *reinterpret_cast<float4*>(o) = make_float4(c.x, c.y, z.x, z.y);
+    }
+    __syncthreads();
+  };
+
+  // ---------------------------------------------------------------- products
+  float4 acc[RT][NT];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[i][nt] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  clear();
+  float* const part = reinterpret_cast<float*>(smem + a.part_off);
+  float* const tsum = reinterpret_cast<float*>(smem + a.tile_off);
+  auto flush = [&](int j) {  // the partial of the run's tile j
+    float4* p = reinterpret_cast<float4*>(part + (j + warp) * (S::PART / 4)) + lane;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) p[(i * NT + nt) * 32] = acc[i][nt];
+    clear();
+  };
+  // Unit Q of a chunk: base addresses of the chunk's records (rc, the lane's
+  // codes; rs, its scales), of its token rows and of its sums.
+  auto multiply = [&](auto q, uint32_t rc, uint32_t rs, const uint32_t (&xu)[NT], uint32_t su) {
+    constexpr int Q = decltype(q)::value, R = Q * S::RECORD;
+    uint4 x0[NT], x1[NT], s0[NT], s1[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      x0[nt] = lds128_at<Q * 128>(xu[nt]);
+      x1[nt] = lds128_at<Q * 128 + 64>(xu[nt]);
+      s0[nt] = nt == 0 ? lds128_at<Q * S::SUMS>(su) : lds128_at<Q * S::SUMS + (NT > 1) * 64>(su);
+      if (G32)
+        s1[nt] = nt == 0 ? lds128_at<Q * S::SUMS + NT * 64>(su)
+                         : lds128_at<Q * S::SUMS + NT * 64 + (NT > 1) * 64>(su);
+    }
+    auto tile = [&](auto which) {
+      constexpr int I = decltype(which)::value, RI = R + I * S::PIECE, Z = RI + S::GROUPS * 32;
+      const uint4 cw = lds128_at<RI>(rc);
+      const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};  // rows g, g + 8 of k 0..31, then of 32..63
+      const uint32_t sc0 = lds32_at<RI>(rs), sc1 = G32 ? lds32_at<RI + 32>(rs) : sc0;
+      uint32_t z0 = 0, z1 = 0;
+      if (ZP) {
+        z0 = lds16_at<Z>(rs - g * 2);
+        z1 = G32 ? lds16_at<Z + 16>(rs - g * 2) : z0;
+      }
+      // A[h][f]: half h, elements k + {0, 1}, {4, 5} (f = 0) and k + {2, 3}, {6, 7}
+      uint32_t A[2][2][4];
+      constexpr uint32_t M = P::MAGIC, LO = 0x000f000fu, HI = 0x00f000f0u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t v = w[2 * h + r];
+          A[h][0][r] = and_or<LO>(v, M);
+          A[h][0][2 + r] = and_or<LO>(v >> 8, M);
+          A[h][1][r] = BF16 ? and_or<LO>(v >> 4, M) : and_or<HI>(v, M);
+          A[h][1][2 + r] = BF16 ? and_or<LO>(v >> 12, M) : and_or<HI>(v >> 8, M);
+        }
+      auto sum_of = [&](uint4 v, uint32_t z) {  // what a unit's (half's) products start from
+        float4 c = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                               __uint_as_float(v.w));
+        if (ZP) {
+          const float zg = -(float)(z & 0xffu), zh = -(float)(z >> 8);
+          c = make_float4(fmaf(zg, c.z, c.x), fmaf(zg, c.w, c.y), fmaf(zh, c.z, c.x),
+                          fmaf(zh, c.w, c.y));
+        }
+        return c;
+      };
+      auto scale_in = [&](float4& o, float4 p, uint32_t sc, float by) {
+        const float sg = P::lo(sc) * by, sh = P::hi(sc) * by;
+        o.x = fmaf(sg, p.x, o.x);
+        o.y = fmaf(sg, p.y, o.y);
+        o.z = fmaf(sh, p.z, o.z);
+        o.w = fmaf(sh, p.w, o.w);
+      };
+      const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        auto first = [&](float4 c, int h) {
+          return mma_ws<BF16>(c, A[h][0][0], A[h][0][1], A[h][0][2], A[h][0][3],
+                              h ? x1[nt].x : x0[nt].x, h ? x1[nt].z : x0[nt].z);
+        };
+        auto second = [&](float4 c, int h) {
+          return mma_ws<BF16>(c, A[h][1][0], A[h][1][1], A[h][1][2], A[h][1][3],
+                              h ? x1[nt].y : x0[nt].y, h ? x1[nt].w : x0[nt].w);
+        };
+        // fp16: the second form's sums are 16 times too large
+        float4& o = acc[I][nt];
+        float4 p = first(sum_of(s0[nt], z0), 0), r = zero;
+        if (BF16)
+          p = second(p, 0);
+        else
+          r = second(r, 0);
+        if (G32) {
+          scale_in(o, p, sc0, 1.0f);
+          if (!BF16) scale_in(o, r, sc0, 0.0625f);
+          p = sum_of(s1[nt], z1);
+          r = zero;
+        }
+        p = first(p, 1);
+        if (BF16)
+          p = second(p, 1);
+        else
+          r = second(r, 1);
+        scale_in(o, p, sc1, 1.0f);
+        if (!BF16) scale_in(o, r, sc1, 0.0625f);
+      }
+    };
+    tile(WsInt<0>{});
+    if constexpr (RT > 1) tile(WsInt<1>{});
+  };
+
+  uint32_t slot_at = 0, bar_at = bar0, parity = 0;  // the next stage to consume
+  bool live = true;  // false after a wait ran out: go through the motions, read nothing
+  uint16_t* const out = static_cast<uint16_t*>(a.out);
+  for (int pass = 0; pass < passes; ++pass) {
+    const int m0 = pass * S::TOKENS, count = min(S::TOKENS, a.M - m0);
+    uint32_t xa[NT];  // this lane's token rows; columns past the last repeat it, unread
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      xa[nt] = sbase + min(nt * 8 + g, count - 1) * S::xrow(a.phase_units) + t * 16;
+    for (int run = 0; run < runs; ++run) {
+      const int n = run_tiles(run);
+      for (int phase = 0; phase < phases; ++phase) {
+        const int len = phase_len(phase);
+        if (phases > 1 || run == 0) {
+          stage_rows(m0, count, phase * a.phase_units, len);
+        }
+        const int per = chunks_of(len), total = n * per;  // chunks of a tile, of the run
+        const int v0 = total * warp / WS_WARPS, v1 = total * (warp + 1) / WS_WARPS;
+        int j = v0 / per, c = v0 - j * per;
+        const int tail = len - (per - 1) * S::UNITS;  // units of a tile's last chunk
+        uint32_t xu[NT], su = sbase + a.sum_off + t * 16 + c * (S::UNITS * S::SUMS);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt] + c * (S::UNITS * 128);
+        for (int v = v0; v < v1; ++v) {
+          if (live && !mbar_try_wait(bar_at, parity))
+            live = mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);
+          live = __all_sync(0xffffffffu, live);
+          const bool last = ++c == per;
+          if (live) {
+            uint32_t rc = ring + slot_at + lane * 16, rs = ring + slot_at + 512 + g * 4;
+            int left = last ? tail : S::UNITS;
+            for (; left >= 4; left -= 4) {
+              multiply(WsInt<0>{}, rc, rs, xu, su);
+              multiply(WsInt<1>{}, rc, rs, xu, su);
+              multiply(WsInt<2>{}, rc, rs, xu, su);
+              multiply(WsInt<3>{}, rc, rs, xu, su);
+              rc += 4 * S::RECORD;
+              rs += 4 * S::RECORD;
+              su += 4 * S::SUMS;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) xu[nt] += 4 * 128;
+            }
+            for (; left > 0; --left) {
+              multiply(WsInt<0>{}, rc, rs, xu, su);
+              rc += S::RECORD;
+              rs += S::RECORD;
+              su += S::SUMS;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) xu[nt] += 128;
+            }
+            __syncwarp();
+            --filled;
+            slot_at += S::STAGE;
+            bar_at += 8;
+            if (slot_at == ring_bytes) {
+              slot_at = 0;
+              bar_at = bar0;
+              parity ^= 1u;
+            }
+            fill();
+          }
+          if (last) {
+            c = 0;
+            flush(j++);
+            su = sbase + a.sum_off + t * 16;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt];
+          }
+        }
+        if (c != 0) flush(j);
+        __syncthreads();
+        // a tile's partials, in warp order: the warps whose shares meet it
+        const bool gu = a.gate_up != 0;
+        const int lg = gu ? 3 : 4;  // outputs of a 16-row tile and token: 8 or 16
+        for (int i = threadIdx.x; i < (n * RT * count) << lg; i += WS_THREADS) {
+          const int r = i & ((1 << lg) - 1), q = i >> lg;
+          const int t16 = (int)((unsigned)q / (unsigned)count), m = q - t16 * count;
+          const int jt = t16 / RT;
+          const int at0 = ((t16 % RT) * NT + (m >> 3)) * 128 + ((r & 7) * 4 + ((m & 7) >> 1)) * 4 +
+                          (m & 1) + (r >> 3) * 2;
+          const int x0 = jt * per, x1 = x0 + per;
+          int w = (int)((unsigned)(x0 * WS_WARPS) / (unsigned)total);
+          while (total * (w + 1) / WS_WARPS <= x0) ++w;
+          float v = 0.0f, v2 = 0.0f;
+          for (int s0 = total * w / WS_WARPS; w < WS_WARPS && s0 < x1; ++w) {
+            const int s1 = total * (w + 1) / WS_WARPS;
+            if (s0 < s1) {
+              const float* p = part + (jt + w) * (S::PART / 4) + at0;
+              v += p[0];
+              if (gu) v2 += p[2];
+            }
+            s0 = s1;
+          }
+          if (phases > 1) {
+            float* ts = tsum + jt * (S::PART / 4) + at0;
+            if (phase > 0) {
+              v += ts[0];
+              if (gu) v2 += ts[2];
+            }
+            if (phase + 1 < phases) {
+              ts[0] = v;
+              if (gu) ts[2] = v2;
+              continue;
+            }
+          }
+          const int col = (((tile0 + run * a.run) * RT + t16) << lg) + r;
+          if (col >= a.rows) continue;
+          v = gu ? ft_silu(a.scale * v) * v2 : a.scale * v;
+          uint16_t* o = out + (int64_t)(m0 + m) * a.rows + col;
+          if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(v);
+        }
+        __syncthreads();
+      }
+    }
+  }
+  // after a wait ran out: no copy may land after the block has gone
+  if (!live)
+    for (; filled > 0; --filled) {
+      mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);
+      bar_at += 8;
+      if (bar_at == bar_end) {
+        bar_at = bar0;
+        parity ^= 1u;
+      }
+    }
+}
+
+}  // namespace swiglu
