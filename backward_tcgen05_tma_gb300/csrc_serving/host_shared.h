@@ -28,6 +28,11 @@ void count_launch();
 int sms();               // SMs of the current device
 bool profiling();
 
+// Tensor map of a 16-bit array [n2][n1][n0] (n0 contiguous) with boxes of
+// b2 x b1 x b0 elements, 128-byte swizzle; elements outside read as 0.
+bool encode_3d(CUtensorMap* tm, bool bf16, const void* base, int64_t n0, int64_t n1, int64_t n2,
+               int b0, int b1, int b2);
+
 // Brackets one launch with events while per-kernel timing is enabled.
 class Prof {
  public:

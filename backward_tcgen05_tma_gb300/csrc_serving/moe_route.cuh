@@ -61,15 +61,17 @@ __device__ __forceinline__ uint32_t rt_key(float v) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-template <bool BF16>
+// V: 32 V >= E
+template <bool BF16, int V>
 __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RtArgs a) {
   __shared__ float4 part[RT_THREADS];                          // [warp][lane]
-  __shared__ float logits[RT_TOKENS][FT_MAX_EXPERTS];          // the first block's are used
+  __shared__ float logits[RT_TOKENS][32 * V];          // the first block's are used
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_rank();
   uint32_t nblocks;
   asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(nblocks));
   const int t0 = (int)(blockIdx.x / nblocks) * RT_TOKENS;
+  pdl_wait();  // launched early: nothing is touched before the kernel before has ended
   cluster_arrive();  // waited for before the first store to another block
   pdl_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.err != nullptr) *a.err = 0;
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RtArgs a) {
     const uint8_t* pl = a.Wr + ((int64_t)(e0 + g) * a.D + t * 8) * 2;
     const uint8_t* ph = pl + (int64_t)a.D * 16;
     const int steps = (a.D + 31) >> 5;
-    constexpr int U = 4;
+    constexpr int U = 8;  // all the loads of d = 2048 at once: they are all latency
     for (int s0 = warp; s0 < steps; s0 += 8 * U) {
       uint4 x[U], wl[U], wh[U];
 #pragma unroll
@@ -127,7 +129,6 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RtArgs a) {
   const int token = t0 + warp;
   if (rank != 0 || token >= a.M) return;
 
-  constexpr int V = FT_MAX_EXPERTS / 32;
   const float* l = logits[warp];
   uint32_t key[V];
 #pragma unroll

@@ -9,6 +9,7 @@
 #include <initializer_list>
 
 #include "../../include/swiglu_mlp.h"
+#include "experts.cuh"
 #include "fewtok.cuh"
 #include "host_shared.h"
 #include "moe_route.cuh"
@@ -76,83 +77,66 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-constexpr int SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
-constexpr int FT_MAX_DEPTH = 8;
 constexpr int WS_SMEM = 224 * 1024;
+constexpr int WX_SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
 
-template <bool BF16, bool W4, int RT, int NT, bool G32, bool ZP, bool MOE>
-cudaError_t launch_ft(host::ServingKernel id, FtArgs a, cudaStream_t st) {
-  using U = FtUnit<W4, RT, NT, G32, ZP>;
-  constexpr auto kern = ft_kernel<BF16, W4, RT, NT, G32, ZP, MOE>;
-  cudaError_t e = allow_smem<kern>(SMEM);
+template <bool BF16, bool W4, int NT, bool G32, bool ZP>
+cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, FtArgs a,
+                           cudaStream_t st) {
+  using S = WxShape<W4, NT, G32, ZP>;
+  constexpr int ring = WX_WARPS * S::STAGE;
+  constexpr auto kern = experts_kernel<BF16, W4, NT, G32, ZP>;
+  cudaError_t e = allow_smem<kern>(WX_SMEM + 1024);  // the ring's alignment
   if (e != cudaSuccess) return e;
-  const bool combine = MOE && a.mode == FT_COMBINE;
+  const bool combine = a.mode == FT_COMBINE;
   const int nsm = host::sms() > 0 ? host::sms() : 1;
-  a.tiles = (a.tiles16 + RT - 1) / RT;
-  int64_t items = a.tiles;
-  if (!combine)
-    items *= MOE ? ft_max_entries(a.M, a.topk, a.E, U::TOKENS) : (a.M + U::TOKENS - 1) / U::TOKENS;
+  const int64_t items =
+      combine ? a.tiles : (int64_t)a.tiles * ft_max_entries(a.M, a.topk, a.E, S::TOKENS);
   const int grid = (int)(items < nsm ? items : nsm);
-  const int64_t most = (items + grid - 1) / grid;  // tiles of a block
+  const int64_t most = (items + grid - 1) / grid;  // items of a block
+  a.run = (int)(most < 64 / NT ? most : 64 / NT);
   a.list_off = 0;
-  a.red_off = MOE ? ft_lists_bytes(a.M, a.topk, a.E, U::TOKENS) : 0;
-  a.run = (int)(most < 32 / NT ? most : 32 / NT);
-  a.ring_off = a.red_off + (combine ? FT_WARPS * a.M * 16 * RT * 4 : (a.run + FT_WARPS - 1) * U::PART);
-  a.depth = (SMEM - a.ring_off) / (FT_WARPS * U::BYTES);
-  if (a.depth < 2) return cudaErrorInvalidConfiguration;
-  if (a.depth > FT_MAX_DEPTH) a.depth = FT_MAX_DEPTH;
-  const int smem = a.ring_off + a.depth * FT_WARPS * U::BYTES;
+  a.red_off = ft_lists_bytes(a.M, a.topk, a.E, S::TOKENS);
+  a.ring_off = a.red_off + (combine ? WX_WARPS * a.M * 64 : (a.run + WX_WARPS - 1) * NT * 512);
+  a.stages = (WX_SMEM - a.ring_off) / ring;
+  if (a.stages > WX_MAX_STAGES) a.stages = WX_MAX_STAGES;
+  if (a.stages < 1) return cudaErrorInvalidConfiguration;
+  a.wait_limit_ns = host::wait_limit_ns();
+  a.inject = host::take_stall() ? 1 : 0;
   host::Prof prof(id, st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(FT_THREADS);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(WX_THREADS);
+  cfg.dynamicSmemBytes = a.ring_off + a.stages * ring + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   // per-kernel event timing would serialise the launches, so no overlap then
-  if (host::profiling()) a.dependent = 0;
-  cfg.attrs = a.dependent ? attr : nullptr;
-  cfg.numAttrs = a.dependent ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
+  cfg.attrs = attr;
+  cfg.numAttrs = host::profiling() ? 0 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tm, a);
   host::count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tokens per pass over a tile: 8, 16 or 32 columns (more take several passes).
-template <bool BF16, bool W4, bool G32, bool ZP, bool MOE>
-cudaError_t launch_nt(host::ServingKernel id, const FtArgs& a, int tokens, cudaStream_t st) {
-  if (tokens <= 8) return launch_ft<BF16, W4, 1, 1, G32, ZP, MOE>(id, a, st);
-  if (tokens <= 16) return launch_ft<BF16, W4, MOE ? 1 : 2, 2, G32, ZP, MOE>(id, a, st);
-  return launch_ft<BF16, W4, 1, 4, G32, ZP, MOE>(id, a, st);
+// nt: 8-token columns of a pass over an expert's weights
+template <bool BF16, int NT>
+cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, const FtArgs& a,
+                           const swiglu_mlp_w4_format* f, cudaStream_t st) {
+  if (f == nullptr) return launch_experts<BF16, false, NT, false, false>(id, tm, a, st);
+  if (f->group == 32)
+    return f->zeros ? launch_experts<BF16, true, NT, true, true>(id, tm, a, st)
+                    : launch_experts<BF16, true, NT, true, false>(id, tm, a, st);
+  return f->zeros ? launch_experts<BF16, true, NT, false, true>(id, tm, a, st)
+                  : launch_experts<BF16, true, NT, false, false>(id, tm, a, st);
 }
 
-template <bool BF16, bool W4, bool MOE>
-cudaError_t launch_fmt(host::ServingKernel id, const FtArgs& a, int tokens, cudaStream_t st) {
-  if constexpr (!W4) {
-    return launch_nt<BF16, false, false, false, MOE>(id, a, tokens, st);
-  } else {
-    if (a.group_log2 == 5)
-      return a.zeros ? launch_nt<BF16, true, true, true, MOE>(id, a, tokens, st)
-                     : launch_nt<BF16, true, true, false, MOE>(id, a, tokens, st);
-    return a.zeros ? launch_nt<BF16, true, false, true, MOE>(id, a, tokens, st)
-                   : launch_nt<BF16, true, false, false, MOE>(id, a, tokens, st);
-  }
-}
-
-template <bool W4, bool MOE>
-cudaError_t launch_dt(host::ServingKernel id, const FtArgs& a, int tokens, swiglu_dtype dt,
-                      cudaStream_t st) {
-  return dt == SWIGLU_BF16 ? launch_fmt<true, W4, MOE>(id, a, tokens, st)
-                           : launch_fmt<false, W4, MOE>(id, a, tokens, st);
-}
-
-void set_w4(FtArgs& a, const W4Geom& w) {
-  a.tiles16 = w.tiles;
-  a.expert_bytes = w.bytes;
-  a.group_log2 = w.group_log2;
-  a.zeros = w.zeros;
+cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, const FtArgs& a, int nt,
+                           const swiglu_mlp_w4_format* f, swiglu_dtype dt, cudaStream_t st) {
+  if (dt == SWIGLU_BF16)
+    return nt == 1 ? launch_experts<true, 1>(id, tm, a, f, st) : launch_experts<true, 2>(id, tm, a, f, st);
+  return nt == 1 ? launch_experts<false, 1>(id, tm, a, f, st) : launch_experts<false, 2>(id, tm, a, f, st);
 }
 
 // One product with packed 4-bit weights: the shared-memory plan (as few phases
@@ -256,11 +240,10 @@ swiglu_status check_moe(int64_t T, int64_t D, int64_t H, int64_t E, int64_t topk
   return SWIGLU_OK;
 }
 
-// Token columns per pass for a mixture of experts: an expert meets T topk / E
-// tokens on average; one with more takes several passes over its weights.
-int moe_tokens(int64_t T, int64_t E, int64_t topk) {
-  if (T <= 8) return 8;
-  return 2 * T * topk <= 16 * E ? 8 : T <= 16 || 3 * T * topk <= 32 * E ? 16 : 32;
+// 8-token columns per pass over an expert's weights: an expert meets T topk / E
+// tokens on average, and one with more takes several passes.
+int moe_columns(int64_t T, int64_t E, int64_t topk) {
+  return T <= 8 || 3 * T * topk <= 8 * E ? 1 : 2;
 }
 
 // The experts of a layer: gate/up over the active experts' rows into the
@@ -271,14 +254,23 @@ swiglu_status run_experts(const void* X, const int* idx, const float* wts, const
                           size_t ws_bytes, bool after_router, cudaStream_t st) {
   (void)ws_bytes;
   void* A = ws + HEADER;
+  const bool w4 = f != nullptr, bf = dt == SWIGLU_BF16;
+  const W4Geom gu = w4 ? w4_geom(2 * (int64_t)H, D, log2_group(f->group), f->zeros, 1) : W4Geom{};
+  const W4Geom dn = w4 ? w4_geom(D, H, log2_group(f->group), f->zeros, 0) : W4Geom{};
+  CUtensorMap tgu = {}, tdn = {};
+  // one box: 64 k of 8 rows of an expert's Wg and the same 8 of its Wu, or of
+  // 16 rows of its Wd
+  if (!w4 && (!host::encode_3d(&tgu, bf, Wgu, D, H, 2 * (int64_t)E, 64, 8, 2) ||
+              !host::encode_3d(&tdn, bf, Wd, H, D, E, 64, 16, 1)))
+    return SWIGLU_ERR_CUDA;
   FtArgs a = {};
   a.mode = FT_GATE_UP;
   a.M = T;
   a.K = D;
   a.rows = H;
-  a.tiles16 = (H + 7) / 8;
+  a.tiles = H / 8;
   a.W = static_cast<const uint8_t*>(Wgu);
-  a.expert_bytes = (int64_t)2 * H * D * 2;
+  a.expert_bytes = gu.bytes;
   a.X = X;
   a.out = A;
   a.scale = mu.gate;
@@ -286,38 +278,32 @@ swiglu_status run_experts(const void* X, const int* idx, const float* wts, const
   a.topk = topk;
   a.idx = idx;
   a.wts = wts;
-  a.dependent = after_router ? 1 : 0;
-  a.clear_err = after_router ? 0 : 1;
+  a.first = after_router ? 0 : 1;
   a.err = reinterpret_cast<int*>(ws);
-  if (f != nullptr) set_w4(a, w4_geom(2 * (int64_t)H, D, log2_group(f->group), f->zeros, 1));
-  SET_WINDOWS(a, {{A, (size_t)T * topk * H * 2},
+  const int nt = moe_columns(T, E, topk);
+  SET_WINDOWS(a, {{ws, ws_bytes},
                   {idx, (size_t)T * topk * 4},
                   {wts, (size_t)T * topk * 4},
-                  {ws, ws_bytes}});
-  const int tokens = moe_tokens(T, E, topk);
-  cudaError_t e = f != nullptr ? launch_dt<true, true>(host::SK_MOE_W4_GATE_UP, a, tokens, dt, st)
-                               : launch_dt<false, true>(host::SK_MOE_GATE_UP, a, tokens, dt, st);
-  if (e != cudaSuccess) return SWIGLU_ERR_CUDA;
+                  {X, (size_t)T * D * 2}});
+  if (launch_experts(w4 ? host::SK_MOE_W4_GATE_UP : host::SK_MOE_GATE_UP, tgu, a, nt, f, dt, st) !=
+      cudaSuccess)
+    return SWIGLU_ERR_CUDA;
   a.mode = FT_COMBINE;
   a.K = H;
   a.rows = D;
-  a.tiles16 = (D + 15) / 16;
+  a.tiles = (D + 15) / 16;
   a.W = static_cast<const uint8_t*>(Wd);
-  a.expert_bytes = (int64_t)D * H * 2;
+  a.expert_bytes = dn.bytes;
   a.X = A;
   a.out = Y;
   a.scale = mu.down;
-  a.dependent = 1;
+  a.first = 0;
   a.idx_ready = 1;
-  a.clear_err = 0;
-  if (f != nullptr) set_w4(a, w4_geom(D, H, log2_group(f->group), f->zeros, 0));
   SET_WINDOWS(a, {{Y, (size_t)T * D * 2},
                   {idx, (size_t)T * topk * 4},
                   {wts, (size_t)T * topk * 4},
                   {ws, ws_bytes}});
-  e = f != nullptr ? launch_dt<true, true>(host::SK_MOE_W4_DOWN, a, tokens, dt, st)
-                   : launch_dt<false, true>(host::SK_MOE_DOWN, a, tokens, dt, st);
-  return status_of(e);
+  return status_of(launch_experts(w4 ? host::SK_MOE_W4_DOWN : host::SK_MOE_DOWN, tdn, a, nt, f, dt, st));
 }
 
 swiglu_status run_route(const void* X, const void* Wr, int* idx, float* wts, int T, int D, int E,
@@ -346,13 +332,18 @@ swiglu_status run_route(const void* X, const void* Wr, int* idx, float* wts, int
   cfg.gridDim = dim3((unsigned)((T + RT_TOKENS - 1) / RT_TOKENS * blocks));
   cfg.blockDim = dim3(RT_THREADS);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)blocks, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = dt == SWIGLU_BF16 ? cudaLaunchKernelEx(&cfg, route_kernel<true>, a)
-                                    : cudaLaunchKernelEx(&cfg, route_kernel<false>, a);
+  cfg.numAttrs = host::profiling() ? 1 : 2;
+  const bool bf = dt == SWIGLU_BF16;
+  cudaError_t e =
+      E <= 64 ? cudaLaunchKernelEx(&cfg, bf ? route_kernel<true, 2> : route_kernel<false, 2>, a)
+      : E <= 128 ? cudaLaunchKernelEx(&cfg, bf ? route_kernel<true, 4> : route_kernel<false, 4>, a)
+                 : cudaLaunchKernelEx(&cfg, bf ? route_kernel<true, 16> : route_kernel<false, 16>, a);
   host::count_launch();
   return status_of(e != cudaSuccess ? e : cudaGetLastError());
 }

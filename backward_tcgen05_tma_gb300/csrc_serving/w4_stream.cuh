@@ -26,7 +26,7 @@
 // Work: a block takes a contiguous run of tiles of 16 RT weight rows (gate/up:
 // each 16 are 8 rows of Wg and the 8 rows of Wu of the same hidden units), cuts
 // each into chunks of units, lays the chunks end to end and gives each of its
-// 16 warps an equal share.  A share that ends inside a tile leaves a partial
+// 12 warps an equal share.  A share that ends inside a tile leaves a partial
 // tile in shared memory; at the end of the run the block adds each tile's
 // partials in order, applies the epilogue and writes, so results are
 // deterministic.  Where the tokens' rows do not fit shared memory the
@@ -40,7 +40,7 @@
 
 namespace swiglu {
 
-constexpr int WS_WARPS = 16;
+constexpr int WS_WARPS = 12;
 constexpr int WS_THREADS = WS_WARPS * 32;
 constexpr int WS_MAX_STAGES = 8;
 
@@ -71,7 +71,7 @@ struct WsArgs {
 template <int RT, int NT, bool G32, bool ZP>
 struct WsShape {
   static constexpr int TOKENS = 8 * NT;
-  static constexpr int UNITS = 8 / RT;                             // units of a chunk
+  static constexpr int UNITS = RT == 1 ? 8 : 2;                    // units of a chunk
   static constexpr int GROUPS = G32 ? 2 : 1;                       // scales of a unit and row
   static constexpr int RECORD = 512 + GROUPS * (ZP ? 48 : 32);     // bytes of a unit
   static constexpr int PIECE = UNITS * RECORD;                     // one 16-row tile's chunk
@@ -453,16 +453,19 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
           if (live) {
             uint32_t rc = ring + slot_at + lane * 16, rs = ring + slot_at + 512 + g * 4;
             int left = last ? tail : S::UNITS;
-            for (; left >= 4; left -= 4) {
+            constexpr int STEP = 4 / RT;  // independent chains in flight
+            for (; left >= STEP; left -= STEP) {
               multiply(WsInt<0>{}, rc, rs, xu, su);
               multiply(WsInt<1>{}, rc, rs, xu, su);
-              multiply(WsInt<2>{}, rc, rs, xu, su);
-              multiply(WsInt<3>{}, rc, rs, xu, su);
-              rc += 4 * S::RECORD;
-              rs += 4 * S::RECORD;
-              su += 4 * S::SUMS;
+              if constexpr (STEP == 4) {
+                multiply(WsInt<2>{}, rc, rs, xu, su);
+                multiply(WsInt<3>{}, rc, rs, xu, su);
+              }
+              rc += STEP * S::RECORD;
+              rs += STEP * S::RECORD;
+              su += STEP * S::SUMS;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) xu[nt] += 4 * 128;
+              for (int nt = 0; nt < NT; ++nt) xu[nt] += STEP * 128;
             }
             for (; left > 0; --left) {
               multiply(WsInt<0>{}, rc, rs, xu, su);
@@ -493,45 +496,46 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
         }
         if (c != 0) flush(j);
         __syncthreads();
-        // a tile's partials, in warp order: the warps whose shares meet it
-        const bool gu = a.gate_up != 0;
-        const int lg = gu ? 3 : 4;  // outputs of a 16-row tile and token: 8 or 16
-        for (int i = threadIdx.x; i < (n * RT * count) << lg; i += WS_THREADS) {
-          const int r = i & ((1 << lg) - 1), q = i >> lg;
-          const int t16 = (int)((unsigned)q / (unsigned)count), m = q - t16 * count;
-          const int jt = t16 / RT;
-          const int at0 = ((t16 % RT) * NT + (m >> 3)) * 128 + ((r & 7) * 4 + ((m & 7) >> 1)) * 4 +
-                          (m & 1) + (r >> 3) * 2;
-          const int x0 = jt * per, x1 = x0 + per;
-          int w = (int)((unsigned)(x0 * WS_WARPS) / (unsigned)total);
-          while (total * (w + 1) / WS_WARPS <= x0) ++w;
-          float v = 0.0f, v2 = 0.0f;
-          for (int s0 = total * w / WS_WARPS; w < WS_WARPS && s0 < x1; ++w) {
-            const int s1 = total * (w + 1) / WS_WARPS;
-            if (s0 < s1) {
-              const float* p = part + (jt + w) * (S::PART / 4) + at0;
-              v += p[0];
-              if (gu) v2 += p[2];
-            }
-            s0 = s1;
+        // a tile's partials, in warp order: those of the warps whose shares meet
+        // it.  A warp takes a 16-row tile and 8 tokens; lane (g, t) has rows g and
+        // g + 8 of tokens 2 t and 2 t + 1.
+        const int s0 = total * lane / WS_WARPS, s1 = total * (lane + 1) / WS_WARPS;  // lane's share
+        for (int i = warp; i < n * RT * NT; i += WS_WARPS) {
+          const int jt = i / (RT * NT), rest = i % (RT * NT), nt = rest % NT;
+          uint32_t meet = __ballot_sync(0xffffffffu, lane < WS_WARPS && s0 < s1 &&
+                                                         s0 < (jt + 1) * per && s1 > jt * per);
+          const float4* p = reinterpret_cast<const float4*>(part) + rest * 32 + lane;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (; meet != 0; meet &= meet - 1) {
+            const float4 q = p[(jt + __ffs(meet) - 1) * (S::PART / 16)];
+            v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
           }
           if (phases > 1) {
-            float* ts = tsum + jt * (S::PART / 4) + at0;
+            float4* ts = reinterpret_cast<float4*>(tsum) + jt * (S::PART / 16) + rest * 32 + lane;
             if (phase > 0) {
-              v += ts[0];
-              if (gu) v2 += ts[2];
+              const float4 q = *ts;
+              v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
             }
             if (phase + 1 < phases) {
-              ts[0] = v;
-              if (gu) ts[2] = v2;
+              *ts = v;
               continue;
             }
           }
-          const int col = (((tile0 + run * a.run) * RT + t16) << lg) + r;
-          if (col >= a.rows) continue;
-          v = gu ? ft_silu(a.scale * v) * v2 : a.scale * v;
-          uint16_t* o = out + (int64_t)(m0 + m) * a.rows + col;
-          if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(v);
+          const int t16 = (tile0 + run * a.run + jt) * RT + rest / NT, m = nt * 8 + 2 * t;
+          auto put = [&](int row, int token, float x) {
+            if (row >= a.rows || token >= count) return;
+            uint16_t* o = out + (int64_t)(m0 + token) * a.rows + row;
+            if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(x);
+          };
+          if (a.gate_up) {
+            put(t16 * 8 + g, m, ft_silu(a.scale * v.x) * v.z);
+            put(t16 * 8 + g, m + 1, ft_silu(a.scale * v.y) * v.w);
+          } else {
+            put(t16 * 16 + g, m, a.scale * v.x);
+            put(t16 * 16 + g, m + 1, a.scale * v.y);
+            put(t16 * 16 + g + 8, m, a.scale * v.z);
+            put(t16 * 16 + g + 8, m + 1, a.scale * v.w);
+          }
         }
         __syncthreads();
       }
