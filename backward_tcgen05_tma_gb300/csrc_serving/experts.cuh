@@ -29,38 +29,49 @@
 
 namespace swiglu {
 
-constexpr int WX_WARPS = 12;
-constexpr int WX_THREADS = WX_WARPS * 32;
 constexpr int WX_MAX_STAGES = 8;
 
 template <bool W4, int NT, bool G32, bool ZP>
 struct WxShape {
+  // 4-bit: 12 warps of 168 registers (16 of 128 spill); 16-bit weights need more
+  // warps to hide their latencies than registers (16 tokens, 64 experts: 125
+  // against 130 us)
+  static constexpr int WARPS = W4 ? 12 : 16;
   static constexpr int TOKENS = 8 * NT;                       // tokens of a pass
-  static constexpr int UNITS = W4 && NT == 1 ? 4 : 2;         // units of a chunk, a ring stage
+  static constexpr int UNITS = W4 && NT == 1 ? 8 : 4;         // units of a chunk
+  static constexpr int HALF = UNITS / 2;                      // units whose token rows are loaded at once
+  static constexpr int STAGE_UNITS = W4 ? UNITS : HALF;       // units of a ring stage
   static constexpr int GROUPS = G32 ? 2 : 1;
   static constexpr int RECORD = W4 ? 512 + GROUPS * (ZP ? 48 : 32) : 2048;
-  static constexpr int STAGE = UNITS * RECORD;
+  static constexpr int STAGE = STAGE_UNITS * RECORD;
 };
 
 // One warp's place: run, chunk v of its share [v, v_end), which is chunk c of
-// the run's piece j.
+// the run's piece j (gate/up: an item; down: an entry).
 struct WxWalk {
   int run, v, v_end, j, c;
 };
 
 template <bool BF16, bool W4, int NT, bool G32, bool ZP>
-__global__ void __launch_bounds__(WX_THREADS, 1)
+__global__ void __launch_bounds__(WxShape<W4, NT, G32, ZP>::WARPS * 32, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tm, const FtArgs a) {
   using S = WxShape<W4, NT, G32, ZP>;
   using P = Ft16<BF16>;
-  constexpr int GROUPS = S::GROUPS, RECORD = S::RECORD, STAGE = S::STAGE, UNITS = S::UNITS;
+  constexpr int GROUPS = S::GROUPS, RECORD = S::RECORD, STAGE = S::STAGE, UNITS = S::UNITS,
+                HALF = S::HALF, WX_WARPS = S::WARPS, WX_THREADS = WX_WARPS * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[WX_WARPS * WX_MAX_STAGES];
+  __shared__ uint4 constants[3];  // 0; minus the magic number plus 8, for each form of code
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t bar0 = smem_u32(bars) + warp * WX_MAX_STAGES * 8;
   const bool combine = a.mode == FT_COMBINE;
 
   ft_begin(a);
+  if (threadIdx.x < 12) {
+    const uint32_t c1 = P::MAGIC | 0x80088008u, c2 = BF16 ? c1 : P::MAGIC | 0x80808080u;
+    reinterpret_cast<uint32_t*>(constants)[threadIdx.x] =
+        threadIdx.x < 4 ? 0 : threadIdx.x < 8 ? c1 : c2;
+  }
   if (lane == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(bar0 + 8 * i, 1);
     fence_mbar_init();
@@ -104,7 +115,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
   };
   auto piece_at = [&](int run, int j, int& tile) -> int2 {  // its tile and entry
     const int item = item0 + (combine ? run : run * run_len + j);
-    const int en = combine ? j : item / a.tiles;
+    const int en = combine ? j : (int)((unsigned)item / (unsigned)a.tiles);
     tile = combine ? item : item - en * a.tiles;
     return l.entry[en];
   };
@@ -131,20 +142,21 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
   uint32_t slot_in = 0, bar_in = bar0;
   int filled = 0;
   bool skip = a.inject && warp == 0;  // test hook
+  int in_half = 0;  // 16-bit: a chunk's halves are stages of their own
   auto fill = [&]() {
     if (in.run >= runs) return;
-    const uint32_t bytes = min(UNITS, nk - in.c * UNITS) * RECORD;
+    const int u = in.c * UNITS + in_half * HALF, n = min(S::STAGE_UNITS, nk - u);
     if (lane == 0 && !skip) {
-      mbar_arrive_expect_tx(bar_in, bytes);
+      mbar_arrive_expect_tx(bar_in, n * RECORD);
       if (W4) {
-        bulk_load(ring + slot_in, src, bytes, bar_in);
+        bulk_load(ring + slot_in, src, n * RECORD, bar_in);
       } else {
-        for (int q = 0; q < UNITS && in.c * UNITS + q < nk; ++q)
-          tma_load_3d(ring + slot_in + q * RECORD, &tm, bar_in, (in.c * UNITS + q) * 64, in_row, in_z);
+        for (int q = 0; q < n; ++q)
+          tma_load_3d(ring + slot_in + q * RECORD, &tm, bar_in, (u + q) * 64, in_row, in_z);
       }
     }
     skip = false;
-    if (W4) src += bytes;
+    if (W4) src += n * RECORD;
     slot_in += STAGE;
     bar_in += 8;
     if (slot_in == ring_bytes) {
@@ -152,6 +164,11 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
       bar_in = bar0;
     }
     ++filled;
+    if (!W4 && in_half == 0 && u + HALF < nk) {
+      in_half = 1;
+      return;
+    }
+    in_half = 0;
     if (step(in)) locate();
   };
   enter(in);
@@ -161,35 +178,44 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
   if (!ft_waits_first(a)) pdl_wait();  // before the first read of a token row
 
   // ---------------------------------------------------------------- products
-  // token rows of a chunk: [8 tokens][unit][half]
-  uint4 x[NT][UNITS][2];
+  // token rows of the first and the second half of a chunk: [8 tokens][unit][half unit]
+  using Rows = uint4[NT][HALF][2];
+  Rows xa, xb;
   const uint8_t* px[NT];  // this lane's token rows, at its elements of unit 0
-  bool has[NT];
   auto tokens_of = [&](const WxWalk& w) {
     int tile;
     const int2 e = piece_at(w.run, w.j, tile);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      has[nt] = nt * 8 + g < e.x >> 16;
-      int r = e.y + (has[nt] ? nt * 8 + g : 0);
-      if (!combine) r = l.at[r] / a.topk;
+      // columns past the entry's last token repeat its first; no one reads them
+      int r = e.y + (nt * 8 + g < e.x >> 16 ? nt * 8 + g : 0);
+      if (!combine) r = (int)((unsigned)l.at[r] / (unsigned)a.topk);
       px[nt] = static_cast<const uint8_t*>(a.X) + ((int64_t)r * a.K + t * 8) * 2;
     }
   };
-  auto load_x = [&](uint4 (&v)[NT][UNITS][2], int c) {
+  auto load_x = [&](Rows& v, int u) {  // units u .. u + HALF - 1
+    const int left = a.K - u * 64;     // elements of the rows from there on
+    const bool whole = left >= HALF * 64;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint8_t* p = px[nt] + (int64_t)c * (UNITS * 128);
-      const int left = has[nt] ? a.K - c * (UNITS * 64) - t * 8 : 0;  // elements from p on
+      const uint8_t* p = px[nt] + (int64_t)u * 128;
+      if (whole && SWIGLU_CHECK_PTR(a.dbg, p, HALF * 128 - 48, a.err)) {
 #pragma unroll
-      for (int q = 0; q < UNITS; ++q)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* s = p + q * 128 + h * 64;
-          v[nt][q][h] = q * 64 + h * 32 < left && SWIGLU_CHECK_PTR(a.dbg, s, 16, a.err)
-                            ? ft_load16(s)
-                            : make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < HALF; ++q) {
+          v[nt][q][0] = ft_load16(p + q * 128);
+          v[nt][q][1] = ft_load16(p + q * 128 + 64);
         }
+      } else {
+#pragma unroll
+        for (int q = 0; q < HALF; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* s = p + q * 128 + h * 64;
+            v[nt][q][h] = q * 64 + h * 32 + t * 8 < left && SWIGLU_CHECK_PTR(a.dbg, s, 16, a.err)
+                              ? ft_load16(s)
+                              : make_uint4(0, 0, 0, 0);
+          }
+      }
     }
   };
   const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -207,7 +233,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
       auto put = [&](int m, float lo, float hi) {
         if (m >= e.x >> 16) return;
         const float w = l.w[e.y + m];
-        float* yt = y + (l.at[e.y + m] / a.topk) * 16;
+        float* yt = y + (unsigned)l.at[e.y + m] / (unsigned)a.topk * 16;
         yt[0] += w * lo;
         yt[8] += w * hi;
       };
@@ -226,8 +252,8 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
   };
   // 16-bit: this lane's 16 bytes of row g, k 0..31 and 32..63, in a swizzled box
   const uint32_t sw0 = g * 128 + (t ^ g) * 16, sw1 = g * 128 + ((4 + t) ^ g) * 16;
-  auto unit16 = [&](auto q, uint32_t box) {
-    constexpr int Q = decltype(q)::value, R = Q * RECORD;
+  auto unit16 = [&](auto q, const Rows& x, uint32_t box) {
+    constexpr int Q = decltype(q)::value % HALF, R = Q * RECORD;  // in a half's own stage
     const uint4 g0 = lds128_at<R>(box + sw0), g1 = lds128_at<R>(box + sw1);
     const uint4 h0 = lds128_at<R + 1024>(box + sw0), h1 = lds128_at<R + 1024>(box + sw1);
 #pragma unroll
@@ -239,52 +265,64 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
       acc[nt] = mma_ws<BF16>(p, g1.z, h1.z, g1.w, h1.w, x1.z, x1.w);
     }
   };
-  auto unit4 = [&](auto q, uint32_t rc, uint32_t rs) {
-    constexpr int Q = decltype(q)::value, R = Q * RECORD, Z = R + GROUPS * 32;
+  // Operands that never change, four registers each as the tensor core takes
+  // them, read from shared memory so that the compiler keeps them: constants
+  // that it can see it would move into place again before every product.
+  constexpr uint32_t M = P::MAGIC, LO = 0x000f000fu, HI = 0x00f000f0u, NEG = M | 0x80008000u;
+  const uint32_t cbase = smem_u32(constants);
+  const uint4 z4 = lds128_at<0>(cbase), k1 = lds128_at<16>(cbase), k2 = lds128_at<32>(cbase);
+  const float4 none = make_float4(__uint_as_float(z4.x), __uint_as_float(z4.y),
+                                  __uint_as_float(z4.z), __uint_as_float(z4.w));
+  auto unit4 = [&](auto q, const Rows& x, uint32_t rc, uint32_t rs) {
+    constexpr int Q = decltype(q)::value % HALF, R = decltype(q)::value * RECORD;
+    constexpr int Z = R + GROUPS * 32;
     const uint4 cw = lds128_at<R>(rc);
     const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};  // rows g, g + 8 of k 0..31, then of 32..63
     const uint32_t sc0 = lds32_at<R>(rs), sc1 = G32 ? lds32_at<R + 32>(rs) : sc0;
-    constexpr uint32_t M = P::MAGIC, LO = 0x000f000fu, HI = 0x00f000f0u, NEG = M | 0x80008000u;
-    // -(m + z) of rows g and g + 8, twice each; fp16: for the first and second form
-    uint32_t n0[4], n1[4];
-    auto negatives = [&](uint32_t (&n)[4], uint32_t z) {
-      const uint32_t zl = ZP ? (z & 0xffu) * 0x10001u : 0x00080008u;
-      const uint32_t zh = ZP ? (z >> 8) * 0x10001u : 0x00080008u;
-      n[0] = NEG | zl;
-      n[1] = NEG | zh;
-      n[2] = BF16 ? n[0] : NEG | zl << 4;
-      n[3] = BF16 ? n[1] : NEG | zh << 4;
-    };
-    negatives(n0, ZP ? lds16_at<Z>(rs - g * 2) : 0);
-    negatives(n1, ZP && G32 ? lds16_at<Z + 16>(rs - g * 2) : 0);
+    const uint32_t zp0 = ZP ? lds16_at<Z>(rs - g * 2) : 0;
+    const uint32_t zp1 = ZP && G32 ? lds16_at<Z + 16>(rs - g * 2) : zp0;
     float4 p[NT], r[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) p[nt] = r[nt] = zero;
+    for (int nt = 0; nt < NT; ++nt) p[nt] = r[nt] = none;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
-      const uint32_t(&n)[4] = G32 && h ? n1 : n0;
       const uint32_t f0 = and_or<LO>(lo, M), f1 = and_or<LO>(hi, M);
       const uint32_t f2 = and_or<LO>(lo >> 8, M), f3 = and_or<LO>(hi >> 8, M);
       const uint32_t s0 = BF16 ? and_or<LO>(lo >> 4, M) : and_or<HI>(lo, M);
       const uint32_t s1 = BF16 ? and_or<LO>(hi >> 4, M) : and_or<HI>(hi, M);
       const uint32_t s2 = BF16 ? and_or<LO>(lo >> 12, M) : and_or<HI>(lo >> 8, M);
       const uint32_t s3 = BF16 ? and_or<LO>(hi >> 12, M) : and_or<HI>(hi >> 8, M);
+      // -(m + z) of rows g and g + 8; fp16: the second form's codes are 16 times larger
+      const uint32_t zp = h ? zp1 : zp0;
+      const uint32_t zl = (zp & 0xffu) * 0x10001u, zh = (zp >> 8) * 0x10001u;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 v = x[nt][Q][h];
-        p[nt] = mma_ws<BF16>(p[nt], n[0], n[1], n[0], n[1], v.x, v.z);
-        r[nt] = mma_ws<BF16>(r[nt], n[2], n[3], n[2], n[3], v.y, v.w);
-        p[nt] = mma_ws<BF16>(p[nt], f0, f1, f2, f3, v.x, v.z);
-        r[nt] = mma_ws<BF16>(r[nt], s0, s1, s2, s3, v.y, v.w);
-        if (G32 || h) {  // fp16: the second form's sums are 16 times too large
+        float4& u = BF16 ? p[nt] : r[nt];  // fp16: the second form's sums are 16 times too large
+        if (ZP) {
+          p[nt] = mma_ws<BF16>(p[nt], NEG | zl, NEG | zh, NEG | zl, NEG | zh, v.x, v.y);
+          const uint32_t yl = BF16 ? zl : zl << 4, yh = BF16 ? zh : zh << 4;
+          u = mma_ws<BF16>(u, NEG | yl, NEG | yh, NEG | yl, NEG | yh, v.z, v.w);
+        } else {
+          p[nt] = mma_ws<BF16>(p[nt], k1.x, k1.y, k1.z, k1.w, v.x, v.y);
+          u = mma_ws<BF16>(u, k2.x, k2.y, k2.z, k2.w, v.z, v.w);
+        }
+        p[nt] = mma_ws<BF16>(p[nt], f0, f1, f2, f3, v.x, v.y);
+        u = mma_ws<BF16>(u, s0, s1, s2, s3, v.z, v.w);
+        if (G32 || h) {
           const uint32_t sc = h ? sc1 : sc0;
-          const float sg = P::lo(sc), sh = P::hi(sc), by = BF16 ? 1.0f : 0.0625f;
-          acc[nt].x = fmaf(sg, fmaf(by, r[nt].x, p[nt].x), acc[nt].x);
-          acc[nt].y = fmaf(sg, fmaf(by, r[nt].y, p[nt].y), acc[nt].y);
-          acc[nt].z = fmaf(sh, fmaf(by, r[nt].z, p[nt].z), acc[nt].z);
-          acc[nt].w = fmaf(sh, fmaf(by, r[nt].w, p[nt].w), acc[nt].w);
-          p[nt] = r[nt] = zero;
+          const float sg = P::lo(sc), sh = P::hi(sc);
+          if (!BF16) {
+            p[nt] = make_float4(fmaf(0.0625f, u.x, p[nt].x), fmaf(0.0625f, u.y, p[nt].y),
+                                fmaf(0.0625f, u.z, p[nt].z), fmaf(0.0625f, u.w, p[nt].w));
+            u = none;
+          }
+          acc[nt].x = fmaf(sg, p[nt].x, acc[nt].x);
+          acc[nt].y = fmaf(sg, p[nt].y, acc[nt].y);
+          acc[nt].z = fmaf(sh, p[nt].z, acc[nt].z);
+          acc[nt].w = fmaf(sh, p[nt].w, acc[nt].w);
+          p[nt] = none;
         }
       }
     }
@@ -294,36 +332,21 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
   bool live = true;  // false after a wait ran out: go through the motions, read nothing
   if (at.run < runs) {
     tokens_of(at);
-    load_x(x, at.c);
+    load_x(xa, at.c * UNITS);
   }
   uint16_t* const out = static_cast<uint16_t*>(a.out);
   for (int run = 0; run < runs; ++run) {
     while (at.run == run) {
-      if (live && !mbar_try_wait(bar_at, parity))
-        live = mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);
-      live = __all_sync(0xffffffffu, live);
       const int j = at.j, left = nk - at.c * UNITS;
-      const bool last = step(at);  // of this piece
-      uint4 xn[NT][UNITS][2];
-      if (at.run < runs) {
-        if (last) tokens_of(at);
-        load_x(xn, at.c);
-      }
-      if (live) {
-        const uint32_t rec = ring + slot_at;
-        auto unit = [&](auto q) {
-          if (W4)
-            unit4(q, rec + lane * 16, rec + 512 + g * 4);
-          else
-            unit16(q, rec);
-        };
-        unit(WsInt<0>{});
-        // past the end of a row the stage is stale: its products are not added
-        if (left > 1) unit(WsInt<1>{});
-        if constexpr (UNITS == 4) {
-          if (left > 2) unit(WsInt<2>{});
-          if (left > 3) unit(WsInt<3>{});
-        }
+      uint32_t rec;
+      auto acquire = [&]() {  // the next stage
+        if (live && !mbar_try_wait(bar_at, parity))
+          live = mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);
+        live = __all_sync(0xffffffffu, live);
+        rec = ring + slot_at;
+      };
+      auto release = [&]() {
+        if (!live) return;
         __syncwarp();
         --filled;
         slot_at += STAGE;
@@ -334,25 +357,57 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
           parity ^= 1u;
         }
         fill();
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int q = 0; q < UNITS; ++q) {
-          x[nt][q][0] = xn[nt][q][0];
-          x[nt][q][1] = xn[nt][q][1];
+      };
+      auto unit = [&](auto q, const Rows& x) {
+        if (W4)
+          unit4(q, x, rec + lane * 16, rec + 512 + g * 4);
+        else
+          unit16(q, x, rec);
+      };
+      auto units = [&](auto first, const Rows& x) {  // past the end of a row the stage is stale
+        constexpr int Q = decltype(first)::value;
+        if (left >= Q + HALF) {
+          unit(WsInt<Q>{}, x);
+          if constexpr (HALF > 1) unit(WsInt<Q + 1>{}, x);
+          if constexpr (HALF > 2) {
+            unit(WsInt<Q + 2>{}, x);
+            unit(WsInt<Q + 3>{}, x);
+          }
+        } else {
+          if (left > Q) unit(WsInt<Q>{}, x);
+          if constexpr (HALF > 2) {
+            if (left > Q + 1) unit(WsInt<Q + 1>{}, x);
+            if (left > Q + 2) unit(WsInt<Q + 2>{}, x);
+          }
         }
+      };
+      if (left > HALF) load_x(xb, at.c * UNITS + HALF);
+      acquire();
+      if (live) units(WsInt<0>{}, xa);
+      if (!W4) {
+        release();
+        if (left > HALF) acquire();
+      }
+      const bool last = step(at);  // of this piece
+      if (at.run < runs) {
+        if (last) tokens_of(at);
+        load_x(xa, at.c * UNITS);
+      }
+      if (live) units(WsInt<HALF>{}, xb);
+      if (W4 || left > HALF) release();
       if (last) flush(run, j);
     }
     __syncthreads();
     if (combine) {
       const int tile = item0 + run;
       for (int i = threadIdx.x; i < a.M * 16; i += WX_THREADS) {
-        float v = 0.0f;
+        float part[WX_WARPS], v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WX_WARPS; ++w) part[w] = red[w * a.M * 16 + i];
 #pragma unroll
         for (int w = 0; w < WX_WARPS; ++w) {
-          v += red[w * a.M * 16 + i];
-          red[w * a.M * 16 + i] = 0.0f;
+          v += part[w];
+          red[w * a.M * 16 + i] = 0.0f;  // for the next run
         }
         const int r = tile * 16 + (i & 15);
         if (r < a.rows) {

@@ -84,7 +84,7 @@ template <bool BF16, bool W4, int NT, bool G32, bool ZP>
 cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, FtArgs a,
                            cudaStream_t st) {
   using S = WxShape<W4, NT, G32, ZP>;
-  constexpr int ring = WX_WARPS * S::STAGE;
+  constexpr int ring = S::WARPS * S::STAGE;
   constexpr auto kern = experts_kernel<BF16, W4, NT, G32, ZP>;
   cudaError_t e = allow_smem<kern>(WX_SMEM + 1024);  // the ring's alignment
   if (e != cudaSuccess) return e;
@@ -97,7 +97,7 @@ cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, FtArgs
   a.run = (int)(most < 64 / NT ? most : 64 / NT);
   a.list_off = 0;
   a.red_off = ft_lists_bytes(a.M, a.topk, a.E, S::TOKENS);
-  a.ring_off = a.red_off + (combine ? WX_WARPS * a.M * 64 : (a.run + WX_WARPS - 1) * NT * 512);
+  a.ring_off = a.red_off + (combine ? S::WARPS * a.M * 64 : (a.run + S::WARPS - 1) * NT * 512);
   a.stages = (WX_SMEM - a.ring_off) / ring;
   if (a.stages > WX_MAX_STAGES) a.stages = WX_MAX_STAGES;
   if (a.stages < 1) return cudaErrorInvalidConfiguration;
@@ -106,7 +106,7 @@ cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, FtArgs
   host::Prof prof(id, st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(WX_THREADS);
+  cfg.blockDim = dim3(S::WARPS * 32);
   cfg.dynamicSmemBytes = a.ring_off + a.stages * ring + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -241,9 +241,14 @@ swiglu_status check_moe(int64_t T, int64_t D, int64_t H, int64_t E, int64_t topk
 }
 
 // 8-token columns per pass over an expert's weights: an expert meets T topk / E
-// tokens on average, and one with more takes several passes.
-int moe_columns(int64_t T, int64_t E, int64_t topk) {
-  return T <= 8 || 3 * T * topk <= 8 * E ? 1 : 2;
+// tokens on average, and one with more takes several passes.  16 columns cost
+// 16-bit experts little more than 8 (64 experts, 8 of them per token, D = 2048,
+// H = 1024: at 64 tokens 166 against 219 us, at 16 tokens 135 against 130),
+// 4-bit ones, bound by issue slots, 1.6 times as much (64 tokens: 133 against
+// 117 us).
+int moe_columns(int64_t T, int64_t E, int64_t topk, bool w4) {
+  if (T <= 8) return 1;
+  return (w4 ? T * topk <= 12 * E : 3 * T * topk <= 8 * E) ? 1 : 2;
 }
 
 // The experts of a layer: gate/up over the active experts' rows into the
@@ -280,7 +285,7 @@ swiglu_status run_experts(const void* X, const int* idx, const float* wts, const
   a.wts = wts;
   a.first = after_router ? 0 : 1;
   a.err = reinterpret_cast<int*>(ws);
-  const int nt = moe_columns(T, E, topk);
+  const int nt = moe_columns(T, E, topk, w4);
   SET_WINDOWS(a, {{ws, ws_bytes},
                   {idx, (size_t)T * topk * 4},
                   {wts, (size_t)T * topk * 4},

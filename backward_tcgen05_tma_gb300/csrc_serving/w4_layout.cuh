@@ -5,8 +5,8 @@
 // Wg and the 8 rows of Wu of the same hidden units), each a run of records of
 // 64 k, each
 //   codes   512 bytes; lane l = 4 g + t of a warp has 16 bytes at 16 l: word
-//           2 c + r holds the k = 32 c + 8 t + {0..7} of row g + 8 r: k + 0, 2,
-//           4, 6 in nibbles 0..3, k + 1, 3, 5, 7 in nibbles 4..7;
+//           2 c + r holds the k = 32 c + 8 t + {0..7} of row g + 8 r: k + 0, 4,
+//           2, 6 in nibbles 0..3, k + 1, 5, 3, 7 in nibbles 4..7;
 //   scales  one set of 16 (groups of 32: two, one per half), 16-bit, rows in
 //           the order 0, 8, 1, 9, ...; a scale of a group of 128 is in both of
 //           the group's records, so that a record is all a unit needs (3% more
@@ -57,6 +57,11 @@ __device__ __forceinline__ int64_t w4_row(const W4Geom& w, int tile, int r) {
   return n < w.N ? n : -1;
 }
 
+// The nibble of elements 2 n (and, 4 further on, 2 n + 1) of a word's 8: the
+// first four elements lie where one mask finds them, the others where the
+// other does, so that each meets two neighbouring registers of token elements.
+__host__ __device__ constexpr int w4_nibble(int n) { return n == 1 ? 2 : n == 2 ? 1 : n; }
+
 // One warp per record of the packed copy.
 __global__ void w4_pack_kernel(W4Geom w, int64_t experts, const uint8_t* codes,
                                const uint16_t* scales, const uint8_t* zeros, uint8_t* packed) {
@@ -79,8 +84,10 @@ __global__ void w4_pack_kernel(W4Geom w, int64_t experts, const uint8_t* codes,
           v = *reinterpret_cast<const uint32_t*>(codes + ((e * w.N + row) * w.K + k) / 2);
         uint32_t x = 0;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          x |= ((v >> (8 * n)) & 15u) << (4 * n) | ((v >> (8 * n + 4)) & 15u) << (16 + 4 * n);
+        for (int n = 0; n < 4; ++n) {  // elements 2 n and 2 n + 1
+          const int at = 4 * w4_nibble(n);
+          x |= ((v >> (8 * n)) & 15u) << at | ((v >> (8 * n + 4)) & 15u) << (16 + at);
+        }
         o[2 * c + r] = x;
       }
     reinterpret_cast<uint4*>(out)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -121,7 +128,7 @@ __global__ void w4_unpack_kernel(W4Geom w, int64_t experts, const uint8_t* packe
         uint32_t o[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const uint32_t x = word[2 * c + r] >> (4 * n);
+          const uint32_t x = word[2 * c + r] >> (4 * w4_nibble(n));
           o[n] = Ft16<BF16>::rnd(s * (float)((int)(x & 15u) - z)) |
                  (uint32_t)Ft16<BF16>::rnd(s * (float)((int)((x >> 16) & 15u) - z)) << 16;
         }

@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
       const uint32_t p = sbase + min(nt * 8 + g, count - 1) * xrow + u * 128 + t * 16;
       const uint4 x0 = lds128_at<0>(p), x1 = lds128_at<64>(p);
       auto half = [&](float4 c, uint4 x, uint32_t k1, uint32_t k2) {
-        c = mma_ws<BF16>(c, k1, k1, k1, k1, x.x, x.z);
-        return mma_ws<BF16>(c, k2, k2, k2, k2, x.y, x.w);
+        c = mma_ws<BF16>(c, k1, k1, k1, k1, x.x, x.y);
+        return mma_ws<BF16>(c, k2, k2, k2, k2, x.z, x.w);
       };
       float* o = reinterpret_cast<float*>(smem + a.sum_off + u * S::SUMS + nt * 64 + t * 16);
       float4 c = half(zero, x0, C::C1, C::C2), z = ZP ? half(zero, x0, C::ONE, C::ONE) : c;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
         z0 = lds16_at<Z>(rs - g * 2);
         z1 = G32 ? lds16_at<Z + 16>(rs - g * 2) : z0;
       }
-      // A[h][f]: half h, elements k + {0, 1}, {4, 5} (f = 0) and k + {2, 3}, {6, 7}
+      // A[h][f]: half h, elements k + {0..3} (f = 0) and k + {4..7}
       uint32_t A[2][2][4];
       constexpr uint32_t M = P::MAGIC, LO = 0x000f000fu, HI = 0x00f000f0u;
 #pragma unroll
@@ -390,11 +390,11 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
       for (int nt = 0; nt < NT; ++nt) {
         auto first = [&](float4 c, int h) {
           return mma_ws<BF16>(c, A[h][0][0], A[h][0][1], A[h][0][2], A[h][0][3],
-                              h ? x1[nt].x : x0[nt].x, h ? x1[nt].z : x0[nt].z);
+                              h ? x1[nt].x : x0[nt].x, h ? x1[nt].y : x0[nt].y);
         };
         auto second = [&](float4 c, int h) {
           return mma_ws<BF16>(c, A[h][1][0], A[h][1][1], A[h][1][2], A[h][1][3],
-                              h ? x1[nt].y : x0[nt].y, h ? x1[nt].w : x0[nt].w);
+                              h ? x1[nt].z : x0[nt].z, h ? x1[nt].w : x0[nt].w);
         };
         // fp16: the second form's sums are 16 times too large
         float4& o = acc[I][nt];
