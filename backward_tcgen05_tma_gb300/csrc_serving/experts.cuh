@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(WxShape<W4, NT, G32, ZP>::WARPS * 32, 1)
   };
   uint32_t slot_in = 0, bar_in = bar0;
   int filled = 0;
-  bool skip = a.inject && warp == 0;  // test hook
+  bool skip = a.inject != 0;  // test hook
   int in_half = 0;  // 16-bit: a chunk's halves are stages of their own
   auto fill = [&]() {
     if (in.run >= runs) return;

@@ -32,7 +32,7 @@ struct FtArgs {
   const float* wts;  // [M, topk]
   int first;         // first kernel of a call
   int idx_ready;     // idx was complete before the kernel before this one began
-  int inject;        // test hook: a first copy is never made
+  int inject;        // test hook: no warp's first stage is ever filled
   // shared-memory plan: chunks a warp's ring holds, items of a run, offsets
   int stages, run;
   int list_off, red_off, ring_off;

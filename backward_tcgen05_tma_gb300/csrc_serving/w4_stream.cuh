@@ -57,7 +57,7 @@ struct WsArgs {
   int first;         // first kernel of a call: waits for the work before it at once, and
                      //   block 0 clears the error word; else the weights are read before
                      //   the kernel before it, which writes X, is waited for
-  int inject;        // test hook: warp 0's first stage is never filled
+  int inject;        // test hook: no warp's first stage is ever filled
   // plan: k-units of a phase, tiles of a run, ring stages, shared-memory offsets
   int phases, phase_units, run, stages;
   int sum_off, part_off, tile_off, ring_off;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
   int filled = 0;                     // stages filled and not yet consumed
   const uint32_t ring = sbase + a.ring_off + warp * a.stages * S::STAGE;
   const uint32_t ring_bytes = a.stages * S::STAGE, bar_end = bar0 + 8 * a.stages;
-  bool skip = a.inject && warp == 0;  // test hook
+  bool skip = a.inject != 0;  // test hook
   auto fill = [&]() {  // the next stage: the units of one chunk
     if (in.pass >= passes) return;
     const uint32_t bytes = in.c == in_per - 1 ? in_last : S::PIECE;
