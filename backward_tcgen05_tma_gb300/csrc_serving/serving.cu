@@ -139,8 +139,39 @@ cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, const 
   return nt == 1 ? launch_experts<false, 1>(id, tm, a, f, st) : launch_experts<false, 2>(id, tm, a, f, st);
 }
 
-// One product with packed 4-bit weights: the shared-memory plan (as few phases
-// of the contraction as leave the ring two stages) and the launch.
+// Clusters of `size` blocks of a kernel that fit the device at once (a cluster
+// lies within a GPU processing cluster), cached per kernel and size.
+template <auto KERNEL>
+int max_clusters(int size, int threads, int smem) {
+  static std::atomic<int> known[4];  // sizes 1, 2, 4, 8
+  const int at = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
+  int n = known[at].load();
+  if (n > 0) return n;
+  const int nsm = host::sms() > 0 ? host::sms() : 1;
+  n = nsm / size;
+  if (size > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(nsm / size * size));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)size, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int q = 0;
+    if (cudaOccupancyMaxActiveClusters(&q, KERNEL, &cfg) == cudaSuccess && q > 0) n = q;
+    cudaGetLastError();  // a failed query is not an error of the call
+  }
+  if (n < 1) n = 1;
+  known[at].store(n);
+  return n;
+}
+
+// One product with packed 4-bit weights: the shared-memory plan and the launch.
+// The contraction is split over the smallest cluster whose blocks can each hold
+// their part of the tokens' rows beside a ring of two stages; the largest one
+// goes through its part in phases.
 template <bool BF16, int RT, int NT, bool G32, bool ZP>
 cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_t st) {
   using S = WsShape<RT, NT, G32, ZP>;
@@ -148,62 +179,77 @@ cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_
   cudaError_t e = allow_smem<kern>(WS_SMEM);
   if (e != cudaSuccess) return e;
   auto up = [](int v) { return (v + 127) & ~127; };
-  const int nsm = host::sms() > 0 ? host::sms() : 1;
-  const int tiles = (tiles16 + RT - 1) / RT, grid = tiles < nsm ? tiles : nsm;
+  const int tiles = (tiles16 + RT - 1) / RT;
   a.tiles16 = tiles16;
-  a.tile_quot = tiles / grid;
-  a.tile_rem = tiles % grid;
-  const int per_block = a.tile_quot + (a.tile_rem != 0), most = 24 / (RT * NT);
-  a.run = per_block < most ? per_block : most;
   const int nk = (a.K + 63) / 64, rows = a.M < S::TOKENS ? a.M : S::TOKENS;
-  const int ring = WS_WARPS * S::STAGE, part = (a.run + WS_WARPS - 1) * S::PART;
-  for (int phases = 1;; ++phases) {
-    a.phase_units = (nk + phases - 1) / phases;
+  constexpr int ring = S::WARPS * S::STAGE;
+  int clusters = 0;
+  auto plan = [&](int split, int phases) {
+    const int most = max_clusters<kern>(split, S::WARPS * 32, WS_SMEM);
+    clusters = tiles < most ? tiles : most;
+    a.split = split;
+    a.tile_quot = tiles / clusters;
+    a.tile_rem = tiles % clusters;
+    const int per = a.tile_quot + (a.tile_rem != 0);
+    a.run = per < S::RUN ? per : S::RUN;
+    a.phase_units = ((nk + split - 1) / split + phases - 1) / phases;
     if (phases > 1) a.phase_units = (a.phase_units + S::UNITS - 1) / S::UNITS * S::UNITS;
-    a.phases = (nk + a.phase_units - 1) / a.phase_units;
     a.sum_off = up(rows * S::xrow(a.phase_units));
     a.part_off = up(a.sum_off + a.phase_units * S::SUMS);
-    a.tile_off = up(a.part_off + part);
-    a.ring_off = up(a.tile_off + (a.phases > 1 ? a.run * S::PART : 0));
+    a.tile_off = up(a.part_off + (a.run + S::WARPS - 1) * S::PART);
+    a.phased = phases > 1;
+    a.ring_off = up(a.tile_off + (a.phased ? a.run * S::PART : 0));
     a.stages = a.ring_off < WS_SMEM ? (WS_SMEM - a.ring_off) / ring : 0;
-    if (a.stages >= 2) break;
+    return a.stages >= 2;
+  };
+  bool fits = false;
+  for (int split = 1; !fits && split <= 8 && split <= nk; split *= 2) fits = plan(split, 1);
+  for (int phases = 2, split = a.split; !fits; ++phases) {
     if (a.phase_units <= S::UNITS) return cudaErrorInvalidConfiguration;
+    fits = plan(split, phases);
   }
   if (a.stages > WS_MAX_STAGES) a.stages = WS_MAX_STAGES;
   a.wait_limit_ns = host::wait_limit_ns();
   a.inject = host::take_stall() ? 1 : 0;
   host::Prof prof(id, st);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(WS_THREADS);
+  cfg.gridDim = dim3((unsigned)(clusters * a.split));
+  cfg.blockDim = dim3(S::WARPS * 32);
   cfg.dynamicSmemBytes = a.ring_off + a.stages * ring;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
   // per-kernel event timing would serialise the launches, so no overlap then
+  if (!host::profiling()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (a.split > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n++].val.clusterDim = {(unsigned)a.split, 1, 1};
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = host::profiling() ? 0 : 1;
+  cfg.numAttrs = n;
   e = cudaLaunchKernelEx(&cfg, kern, a);
   host::count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Token columns of a pass: 8, 16 or 32.
+template <bool BF16, bool G32, bool ZP>
+cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, int tiles16, cudaStream_t st) {
+  if (a.M <= 8) return launch_ws<BF16, 1, 1, G32, ZP>(id, a, tiles16, st);
+  if (a.M <= 16) return launch_ws<BF16, 2, 2, G32, ZP>(id, a, tiles16, st);
+  return launch_ws<BF16, 2, 4, G32, ZP>(id, a, tiles16, st);
+}
+
 template <bool BF16>
 cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, cudaStream_t st) {
-  const bool zeros = w.zeros != 0, g32 = w.sets == 2;
-  if (a.M <= 8) {
-    if (g32)
-      return zeros ? launch_ws<BF16, 1, 1, true, true>(id, a, w.tiles, st)
-                   : launch_ws<BF16, 1, 1, true, false>(id, a, w.tiles, st);
-    return zeros ? launch_ws<BF16, 1, 1, false, true>(id, a, w.tiles, st)
-                 : launch_ws<BF16, 1, 1, false, false>(id, a, w.tiles, st);
-  }
-  if (g32)
-    return zeros ? launch_ws<BF16, 2, 2, true, true>(id, a, w.tiles, st)
-                 : launch_ws<BF16, 2, 2, true, false>(id, a, w.tiles, st);
-  return zeros ? launch_ws<BF16, 2, 2, false, true>(id, a, w.tiles, st)
-               : launch_ws<BF16, 2, 2, false, false>(id, a, w.tiles, st);
+  if (w.sets == 2)
+    return w.zeros ? launch_ws<BF16, true, true>(id, a, w.tiles, st)
+                   : launch_ws<BF16, true, false>(id, a, w.tiles, st);
+  return w.zeros ? launch_ws<BF16, false, true>(id, a, w.tiles, st)
+                 : launch_ws<BF16, false, false>(id, a, w.tiles, st);
 }
 
 cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, swiglu_dtype dt,

@@ -26,22 +26,23 @@
 // Work: a block takes a contiguous run of tiles of 16 RT weight rows (gate/up:
 // each 16 are 8 rows of Wg and the 8 rows of Wu of the same hidden units), cuts
 // each into chunks of units, lays the chunks end to end and gives each of its
-// 12 warps an equal share.  A share that ends inside a tile leaves a partial
+// warps an equal share.  A share that ends inside a tile leaves a partial
 // tile in shared memory; at the end of the run the block adds each tile's
 // partials in order, applies the epilogue and writes, so results are
-// deterministic.  Where the tokens' rows do not fit shared memory the
-// contraction is taken in phases; more than 16 tokens take several passes over
-// the weights, which the L2 cache then holds.  From 9 tokens on a tile has 32
-// rows (RT = 2): shared memory, which delivers 128 bytes a cycle, would
-// otherwise give most of them to the token rows.
+// deterministic.  Where the tokens' rows do not fit a block's shared memory the
+// contraction is split over a cluster of 2, 4 or 8 blocks: each holds its part
+// of the rows and works on all the cluster's tiles, and at the end of a run the
+// blocks add up each other's sums through distributed shared memory, in rank
+// order.  (What still does not fit is taken in phases; 33 and more tokens take
+// two passes over the weights, which the L2 cache then holds.)  From 9 tokens
+// on a tile has 32 rows (RT = 2): shared memory, which delivers 128 bytes a
+// cycle, would otherwise give most of them to the token rows.
 #pragma once
 
 #include "fewtok.cuh"
 
 namespace swiglu {
 
-constexpr int WS_WARPS = 12;
-constexpr int WS_THREADS = WS_WARPS * 32;
 constexpr int WS_MAX_STAGES = 8;
 
 struct WsArgs {
@@ -49,7 +50,8 @@ struct WsArgs {
   int M, K;          // tokens; contraction, a multiple of 8
   int rows;          // rows of out: output features, or hidden units (gate/up)
   int tiles16;       // 16-row tiles
-  int tile_quot, tile_rem;  // tiles of 16 RT rows: quot a block, one more in the first rem
+  int split;         // blocks of a cluster, which share the contraction
+  int tile_quot, tile_rem;  // tiles of 16 RT rows: quot a cluster, one more in the first rem
   const uint8_t* W;  // packed
   const void* X;     // [M, K]
   void* out;         // [M, rows]
@@ -59,7 +61,8 @@ struct WsArgs {
                      //   the kernel before it, which writes X, is waited for
   int inject;        // test hook: no warp's first stage is ever filled
   // plan: k-units of a phase, tiles of a run, ring stages, shared-memory offsets
-  int phases, phase_units, run, stages;
+  int phase_units, run, stages;
+  int phased;        // the contraction (or a block's part of it) takes several phases
   int sum_off, part_off, tile_off, ring_off;
   uint64_t wait_limit_ns;
   int* err;
@@ -70,14 +73,17 @@ struct WsArgs {
 
 template <int RT, int NT, bool G32, bool ZP>
 struct WsShape {
+  // more columns need more registers a warp (and give it more to do at once)
+  static constexpr int WARPS = NT == 1 ? 12 : 8;
   static constexpr int TOKENS = 8 * NT;
-  static constexpr int UNITS = RT == 1 ? 8 : 2;                    // units of a chunk
+  static constexpr int UNITS = 8 / RT;                             // units of a chunk
   static constexpr int GROUPS = G32 ? 2 : 1;                       // scales of a unit and row
   static constexpr int RECORD = 512 + GROUPS * (ZP ? 48 : 32);     // bytes of a unit
   static constexpr int PIECE = UNITS * RECORD;                     // one 16-row tile's chunk
   static constexpr int STAGE = RT * PIECE;
   static constexpr int SUMS = GROUPS * NT * 64;                    // bytes of a unit's sums
   static constexpr int PART = RT * NT * 512;                       // a partial tile
+  static constexpr int RUN = NT == 1 ? 24 : NT == 2 ? 12 : 10;     // tiles of a run, at most
   static __host__ __device__ constexpr int xrow(int units) { return units * 128 + 64; }
 };
 
@@ -153,9 +159,11 @@ struct WsWalk {
 };
 
 template <bool BF16, int RT, int NT, bool G32, bool ZP>
-__global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a) {
+__global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
+    w4_stream_kernel(const WsArgs a) {
   using S = WsShape<RT, NT, G32, ZP>;
   using P = Ft16<BF16>;
+  constexpr int WS_WARPS = S::WARPS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[WS_WARPS * WS_MAX_STAGES + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -179,14 +187,17 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
   __syncwarp();
 
   const int nk = (a.K + 63) >> 6;
-  const int b = blockIdx.x;
+  // this block's part of the contraction, units [kbase, kbase + kunits)
+  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+  const int kbase = nk * rank / a.split, kunits = nk * (rank + 1) / a.split - kbase;
+  const int b = a.split > 1 ? blockIdx.x / a.split : blockIdx.x;
   const int tile0 = b * a.tile_quot + min(b, a.tile_rem);
   const int tiles = a.tile_quot + (b < a.tile_rem ? 1 : 0);
   const int passes = (a.M + S::TOKENS - 1) / S::TOKENS;
   const int runs = tiles <= a.run ? 1 : (tiles + a.run - 1) / a.run;
-  const int phases = a.phases;
+  const int phases = (kunits + a.phase_units - 1) / a.phase_units;
   auto run_tiles = [&](int r) { return min(a.run, tiles - r * a.run); };
-  auto phase_len = [&](int p) { return min(a.phase_units, nk - p * a.phase_units); };  // units
+  auto phase_len = [&](int p) { return min(a.phase_units, kunits - p * a.phase_units); };  // units
   auto chunks_of = [&](int len) { return (len + S::UNITS - 1) / S::UNITS; };
   auto enter = [&](WsWalk& w) {  // this warp's share from here on, skipping empty ones
     for (; w.pass < passes; ++w.pass, w.run = 0) {
@@ -212,8 +223,8 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
     const int len = phase_len(in.phase);
     in_per = chunks_of(len);
     in_last = (len - (in_per - 1) * S::UNITS) * S::RECORD;
-    src = a.W + ((int64_t)(tile0 + in.run * a.run + in.j) * RT * nk + in.phase * a.phase_units +
-                 in.c * S::UNITS) * S::RECORD;
+    src = a.W + ((int64_t)(tile0 + in.run * a.run + in.j) * RT * nk + kbase +
+                 in.phase * a.phase_units + in.c * S::UNITS) * S::RECORD;
   };
   enter(in);
   locate();
@@ -340,10 +351,8 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
     for (int nt = 0; nt < NT; ++nt) {
       x0[nt] = lds128_at<Q * 128>(xu[nt]);
       x1[nt] = lds128_at<Q * 128 + 64>(xu[nt]);
-      s0[nt] = nt == 0 ? lds128_at<Q * S::SUMS>(su) : lds128_at<Q * S::SUMS + (NT > 1) * 64>(su);
-      if (G32)
-        s1[nt] = nt == 0 ? lds128_at<Q * S::SUMS + NT * 64>(su)
-                         : lds128_at<Q * S::SUMS + NT * 64 + (NT > 1) * 64>(su);
+      s0[nt] = lds128_at<Q * S::SUMS>(su + nt * 64);
+      if (G32) s1[nt] = lds128_at<Q * S::SUMS + NT * 64>(su + nt * 64);
     }
     auto tile = [&](auto which) {
       constexpr int I = decltype(which)::value, RI = R + I * S::PIECE, Z = RI + S::GROUPS * 32;
@@ -425,6 +434,36 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
   uint32_t slot_at = 0, bar_at = bar0, parity = 0;  // the next stage to consume
   bool live = true;  // false after a wait ran out: go through the motions, read nothing
   uint16_t* const out = static_cast<uint16_t*>(a.out);
+  // The warps whose shares, of n tiles of `per` chunks laid end to end, meet
+  // tile jt: their partials are at (jt + warp) * PART.
+  auto meeting = [&](int n, int per, int jt) {
+    const int total = n * per;
+    const int s0 = total * lane / WS_WARPS, s1 = total * (lane + 1) / WS_WARPS;  // lane's share
+    return __ballot_sync(0xffffffffu, lane < WS_WARPS && s0 < s1 && s0 < (jt + 1) * per &&
+                                          s1 > jt * per);
+  };
+  auto plus = [](float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+  };
+  // The epilogue of 16 rows and 8 tokens, part `rest` of the run's tile jt: lane
+  // (g, t) has rows g and g + 8 of tokens 2 t and 2 t + 1.
+  auto finish = [&](int jt, int rest, float4 v, int run, int m0, int count) {
+    const int t16 = (tile0 + run * a.run + jt) * RT + rest / NT, m = rest % NT * 8 + 2 * t;
+    auto put = [&](int row, int token, float x) {
+      if (row >= a.rows || token >= count) return;
+      uint16_t* o = out + (int64_t)(m0 + token) * a.rows + row;
+      if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(x);
+    };
+    if (a.gate_up) {
+      put(t16 * 8 + g, m, ft_silu(a.scale * v.x) * v.z);
+      put(t16 * 8 + g, m + 1, ft_silu(a.scale * v.y) * v.w);
+    } else {
+      put(t16 * 16 + g, m, a.scale * v.x);
+      put(t16 * 16 + g, m + 1, a.scale * v.y);
+      put(t16 * 16 + g + 8, m, a.scale * v.z);
+      put(t16 * 16 + g + 8, m + 1, a.scale * v.w);
+    }
+  };
   for (int pass = 0; pass < passes; ++pass) {
     const int m0 = pass * S::TOKENS, count = min(S::TOKENS, a.M - m0);
     uint32_t xa[NT];  // this lane's token rows; columns past the last repeat it, unread
@@ -436,7 +475,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
       for (int phase = 0; phase < phases; ++phase) {
         const int len = phase_len(phase);
         if (phases > 1 || run == 0) {
-          stage_rows(m0, count, phase * a.phase_units, len);
+          stage_rows(m0, count, kbase + phase * a.phase_units, len);
         }
         const int per = chunks_of(len), total = n * per;  // chunks of a tile, of the run
         const int v0 = total * warp / WS_WARPS, v1 = total * (warp + 1) / WS_WARPS;
@@ -496,48 +535,54 @@ __global__ void __launch_bounds__(WS_THREADS, 1) w4_stream_kernel(const WsArgs a
         }
         if (c != 0) flush(j);
         __syncthreads();
-        // a tile's partials, in warp order: those of the warps whose shares meet
-        // it.  A warp takes a 16-row tile and 8 tokens; lane (g, t) has rows g and
-        // g + 8 of tokens 2 t and 2 t + 1.
-        const int s0 = total * lane / WS_WARPS, s1 = total * (lane + 1) / WS_WARPS;  // lane's share
+        // a tile's partials, in warp order; a warp takes 16 rows and 8 tokens at
+        // a time.  Sums that are not final yet wait in tsum (for the next phase)
+        // or in the place of the first partial (for the cluster).
         for (int i = warp; i < n * RT * NT; i += WS_WARPS) {
-          const int jt = i / (RT * NT), rest = i % (RT * NT), nt = rest % NT;
-          uint32_t meet = __ballot_sync(0xffffffffu, lane < WS_WARPS && s0 < s1 &&
-                                                         s0 < (jt + 1) * per && s1 > jt * per);
-          const float4* p = reinterpret_cast<const float4*>(part) + rest * 32 + lane;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (; meet != 0; meet &= meet - 1) {
-            const float4 q = p[(jt + __ffs(meet) - 1) * (S::PART / 16)];
-            v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
-          }
-          if (phases > 1) {
+          const int jt = i / (RT * NT), rest = i % (RT * NT);
+          const uint32_t meet = meeting(n, per, jt);
+          float4* const p = reinterpret_cast<float4*>(part) + rest * 32 + lane;
+          float4* const p0 = p + (jt + __ffs(meet) - 1) * (S::PART / 16);
+          float4 v = *p0;
+          for (uint32_t m = meet & (meet - 1); m != 0; m &= m - 1)
+            v = plus(v, p[(jt + __ffs(m) - 1) * (S::PART / 16)]);
+          if (a.phased) {
             float4* ts = reinterpret_cast<float4*>(tsum) + jt * (S::PART / 16) + rest * 32 + lane;
-            if (phase > 0) {
-              const float4 q = *ts;
-              v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
-            }
-            if (phase + 1 < phases) {
-              *ts = v;
-              continue;
-            }
+            if (phase > 0) v = plus(*ts, v);
+            *ts = v;
+          } else if (a.split > 1) {
+            *p0 = v;
           }
-          const int t16 = (tile0 + run * a.run + jt) * RT + rest / NT, m = nt * 8 + 2 * t;
-          auto put = [&](int row, int token, float x) {
-            if (row >= a.rows || token >= count) return;
-            uint16_t* o = out + (int64_t)(m0 + token) * a.rows + row;
-            if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(x);
-          };
-          if (a.gate_up) {
-            put(t16 * 8 + g, m, ft_silu(a.scale * v.x) * v.z);
-            put(t16 * 8 + g, m + 1, ft_silu(a.scale * v.y) * v.w);
-          } else {
-            put(t16 * 16 + g, m, a.scale * v.x);
-            put(t16 * 16 + g, m + 1, a.scale * v.y);
-            put(t16 * 16 + g + 8, m, a.scale * v.z);
-            put(t16 * 16 + g + 8, m + 1, a.scale * v.w);
-          }
+          if (a.split == 1 && phase + 1 == phases) finish(jt, rest, v, run, m0, count);
         }
         __syncthreads();
+      }
+      if (a.split > 1) {
+        // the blocks' sums, in rank order
+        cluster_arrive();
+        cluster_wait();
+        for (int i = warp * a.split + rank; i < n * RT * NT; i += WS_WARPS * a.split) {
+          const int jt = i / (RT * NT), rest = i % (RT * NT);
+          float4 q[8];  // all loads at once: they are all latency
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < a.split) {
+              uint32_t at = a.tile_off + jt * S::PART;
+              if (!a.phased) {
+                const int per = chunks_of(nk * (r + 1) / a.split - nk * r / a.split);
+                at = a.part_off + (jt + __ffs(meeting(n, per, jt)) - 1) * S::PART;
+              }
+              q[r] = cluster_load4(cluster_map(sbase + at + rest * 512 + lane * 16, r));
+            }
+          float4 v = q[0];
+#pragma unroll
+          for (int r = 1; r < 8; ++r)
+            if (r < a.split) v = plus(v, q[r]);
+          finish(jt, rest, v, run, m0, count);
+        }
+        __syncwarp();
+        cluster_arrive();  // before the partials are written again, or the block goes
+        cluster_wait();
       }
     }
   }
