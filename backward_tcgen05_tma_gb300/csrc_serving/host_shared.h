@@ -32,6 +32,14 @@ bool profiling();
 // b2 x b1 x b0 elements, 128-byte swizzle; elements outside read as 0.
 bool encode_3d(CUtensorMap* tm, bool bf16, const void* base, int64_t n0, int64_t n1, int64_t n2,
                int b0, int b1, int b2);
+// The same array [rows][K], K a multiple of 64, seen as [K / 64][rows][64]:
+// boxes of `blocks` 64-element blocks of `brows` rows.
+bool encode_blocks(CUtensorMap* tm, bool bf16, const void* base, int64_t K, int64_t rows, int brows,
+                   int blocks);
+// Records of `record` bytes (a multiple of 16), [n2][n1] of them, with boxes of
+// b2 x b1 records, no swizzle.
+bool encode_records(CUtensorMap* tm, const void* base, int record, int64_t n1, int64_t n2, int b1,
+                    int b2);
 
 // Brackets one launch with events while per-kernel timing is enabled.
 class Prof {

@@ -15,10 +15,17 @@
 #include "moe_route.cuh"
 #include "w4_layout.cuh"
 #include "w4_stream.cuh"
+#include "w4_tensor.cuh"
 
 using namespace swiglu;
 
 namespace {
+
+#ifdef SWIGLU_DEBUG
+#define SET_WINDOWS(args, ...) (args).dbg = host::windows(__VA_ARGS__)
+#else
+#define SET_WINDOWS(args, ...) (void)0
+#endif
 
 constexpr int64_t LIMIT = 0x7fffffffLL;
 constexpr size_t HEADER = 256;  // workspace header: the error word
@@ -78,6 +85,7 @@ cudaError_t allow_smem(int bytes) {
 }
 
 constexpr int WS_SMEM = 224 * 1024;
+constexpr int WT_MIN_TOKENS = 16;  // more tokens take the tensor-core form
 constexpr int WX_SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
 
 template <bool BF16, bool W4, int NT, bool G32, bool ZP>
@@ -235,6 +243,101 @@ cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// The tensor-core form: its split over the blocks and its part of the workspace
+// (header, counters of gate/up and of down, partial tiles).
+constexpr size_t WT_COUNTERS = 2 * WT_MAX_TILES * 4;
+struct WtPlan {
+  int grid, sk_tiles, seg_max;
+};
+int wt_columns(int64_t M) { return M <= 32 ? 32 : M <= 48 ? 48 : 64; }
+bool wt_serves(int64_t M, int64_t tiles16) {
+  return M > WT_MIN_TOKENS && M <= FT_MAX_TOKENS && (tiles16 + 7) / 8 <= WT_MAX_TILES;
+}
+WtPlan wt_plan(int tiles, int nk) {
+  const int nsm = host::sms() > 0 ? host::sms() : 1, spt = (nk + WT_KB - 1) / WT_KB;
+  WtPlan p;
+  // whole tiles where every block gets one; the others' stages are shared evenly
+  p.sk_tiles = tiles >= nsm ? tiles % nsm : tiles;
+  const int64_t total = (int64_t)p.sk_tiles * spt;
+  p.grid = tiles < nsm && total < nsm ? (int)total : nsm;
+  const int64_t range = (total + p.grid - 1) / p.grid;
+  p.seg_max = (int)((range + spt - 1) / spt) + 1;
+  return p;
+}
+size_t wt_workspace(int64_t M, int64_t tiles16, int64_t K) {
+  if (!wt_serves(M, tiles16)) return HEADER;
+  const WtPlan p = wt_plan((int)((tiles16 + 7) / 8), (int)((K + 63) / 64));
+  return HEADER + WT_COUNTERS + (size_t)p.grid * p.seg_max * wt_columns(M) * 512;
+}
+
+template <bool BF16, int NT, bool G32, bool ZP>
+cudaError_t launch_wt(host::ServingKernel id, const WsArgs& s, int pair, int tiles16,
+                      cudaStream_t st) {
+  using S = WtShape<NT, G32, ZP>;
+  constexpr auto kern = w4_tensor_kernel<BF16, NT, G32, ZP>;
+  constexpr int fixed = WT_OUT + 1024;
+  cudaError_t e = allow_smem<kern>(WS_SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tw, tx;
+  const int nk = (s.K + 63) / 64;
+  // token rows: in whole 64-k blocks as [K / 64][M][64], one box a stage, else
+  // as [M][K] with boxes of one block
+  if (!host::encode_records(&tw, s.W, S::RECORD, nk, tiles16, WT_KB, 8) ||
+      !(s.K % 64 == 0 ? host::encode_blocks(&tx, BF16, s.X, s.K, s.M, NT, WT_KB)
+                      : host::encode_3d(&tx, BF16, s.X, s.K, s.M, 1, 64, NT, 1)))
+    return cudaErrorInvalidValue;
+  const int tiles = (tiles16 + 7) / 8;
+  const WtPlan p = wt_plan(tiles, nk);
+  char* ws = reinterpret_cast<char*>(s.err);
+  WtArgs a = {};
+  a.gate_up = s.gate_up;
+  a.M = s.M;
+  a.K = s.K;
+  a.rows = s.rows;
+  a.tiles16 = tiles16;
+  a.tiles = tiles;
+  a.sk_tiles = p.sk_tiles;
+  a.seg_max = p.seg_max;
+  a.pair = pair;
+  a.W = s.W;
+  a.out = s.out;
+  a.scale = s.scale;
+  a.first = s.first;
+  a.stages = (WS_SMEM - fixed) / S::STAGE < WT_MAX_STAGES ? (WS_SMEM - fixed) / S::STAGE : WT_MAX_STAGES;
+  a.counters = reinterpret_cast<int*>(ws + HEADER) + (s.gate_up ? 0 : WT_MAX_TILES);
+  a.part = reinterpret_cast<float*>(ws + HEADER + WT_COUNTERS);
+  a.wait_limit_ns = host::wait_limit_ns();
+  a.err = s.err;
+  a.inject = host::take_stall() ? 1 : 0;
+  SET_WINDOWS(a, {{s.out, (size_t)s.M * s.rows * 2},
+                  {s.W, (size_t)tiles16 * nk * S::RECORD},
+                  {ws, wt_workspace(s.M, tiles16, s.K)}});
+  host::Prof prof(id, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.grid);
+  cfg.blockDim = dim3(WT_THREADS);
+  cfg.dynamicSmemBytes = fixed + a.stages * S::STAGE;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // per-kernel event timing would serialise the launches, so no overlap then
+  cfg.attrs = attr;
+  cfg.numAttrs = host::profiling() ? 0 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
+  host::count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool BF16, bool G32, bool ZP>
+cudaError_t launch_wt(host::ServingKernel id, const WsArgs& s, int pair, int tiles16,
+                      cudaStream_t st) {
+  const int nt = wt_columns(s.M);
+  if (nt == 32) return launch_wt<BF16, 32, G32, ZP>(id, s, pair, tiles16, st);
+  if (nt == 48) return launch_wt<BF16, 48, G32, ZP>(id, s, pair, tiles16, st);
+  return launch_wt<BF16, 64, G32, ZP>(id, s, pair, tiles16, st);
+}
+
 // Token columns of a pass: 8, 16 or 32.
 template <bool BF16, bool G32, bool ZP>
 cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, int tiles16, cudaStream_t st) {
@@ -245,6 +348,14 @@ cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, int tiles16, cuda
 
 template <bool BF16>
 cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, cudaStream_t st) {
+  if (wt_serves(a.M, w.tiles)) {
+    const int pair = w.group_log2 == 7 ? 2 : 1;
+    if (w.sets == 2)
+      return w.zeros ? launch_wt<BF16, true, true>(id, a, pair, w.tiles, st)
+                     : launch_wt<BF16, true, false>(id, a, pair, w.tiles, st);
+    return w.zeros ? launch_wt<BF16, false, true>(id, a, pair, w.tiles, st)
+                   : launch_wt<BF16, false, false>(id, a, pair, w.tiles, st);
+  }
   if (w.sets == 2)
     return w.zeros ? launch_ws<BF16, true, true>(id, a, w.tiles, st)
                    : launch_ws<BF16, true, false>(id, a, w.tiles, st);
@@ -257,11 +368,6 @@ cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, 
   return dt == SWIGLU_BF16 ? launch_ws<true>(id, a, w, st) : launch_ws<false>(id, a, w, st);
 }
 
-#ifdef SWIGLU_DEBUG
-#define SET_WINDOWS(args, ...) (args).dbg = host::windows(__VA_ARGS__)
-#else
-#define SET_WINDOWS(args, ...) (void)0
-#endif
 
 int grid_for(int64_t threads) {
   const int64_t want = (threads + 255) / 256, most = (int64_t)(host::sms() > 0 ? host::sms() : 1) * 8;
@@ -467,14 +573,12 @@ swiglu_status swiglu_mlp_w4_unpack(const void* packed, void* W, int64_t E, int64
 }
 
 size_t swiglu_mlp_w4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return HEADER;
+  return N <= 0 || K <= 0 ? HEADER : wt_workspace(M, (N + 15) / 16, K);
 }
 
 size_t swiglu_mlp_fwd_nograd_w4_workspace_bytes(int64_t M, int64_t D, int64_t H) {
-  const size_t a = swiglu_mlp_w4_workspace_bytes(M, 2 * H, D), b = swiglu_mlp_w4_workspace_bytes(M, D, H);
+  if (D <= 0 || H <= 0) return HEADER;
+  const size_t a = wt_workspace(M, (H + 7) / 8, D), b = wt_workspace(M, (D + 15) / 16, H);
   return a > b ? a : b;
 }
 
