@@ -85,7 +85,6 @@ cudaError_t allow_smem(int bytes) {
 }
 
 constexpr int WS_SMEM = 224 * 1024;
-constexpr int WT_MIN_TOKENS = 16;  // more tokens take the tensor-core form
 constexpr int WX_SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
 
 template <bool BF16, bool W4, int NT, bool G32, bool ZP>
@@ -245,13 +244,19 @@ cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_
 
 // The tensor-core form: its split over the blocks and its part of the workspace
 // (header, counters of gate/up and of down, partial tiles).
-constexpr size_t WT_COUNTERS = 2 * WT_MAX_TILES * 4;
+constexpr size_t WT_COUNTERS = 2 * WT_MAX_SHARED * 4;
 struct WtPlan {
-  int grid, sk_tiles, seg_max;
+  int grid, sk_tiles, sharers, seg_max;
 };
 int wt_columns(int64_t M) { return M <= 32 ? 32 : M <= 48 ? 48 : 64; }
-bool wt_serves(int64_t M, int64_t tiles16) {
-  return M > WT_MIN_TOKENS && M <= FT_MAX_TOKENS && (tiles16 + 7) / 8 <= WT_MAX_TILES;
+// Which form a product takes.  Up to 32 tokens w4_stream.cuh reads the weights
+// once as well and starts up faster: 32 tokens, 4096 x 4096 weights 12.4 against
+// 15.4 us; with 33 to 64 it would read them twice (64 tokens, 4096 x 11008: 49.3
+// against 24.3 us; only 1024 x 1024 and less come out even).  Near 32 tokens
+// large matrices favour the tensor core too: MLP 4096/11008 at 32 tokens 62.6
+// against 51.8 us, at 17 tokens 50.6 against 51.4.
+bool wt_serves(int64_t M, int64_t tiles16, int64_t K) {
+  return M > 32 || (M > 24 && tiles16 * 16 * K >= (int64_t)1 << 25);
 }
 WtPlan wt_plan(int tiles, int nk) {
   const int nsm = host::sms() > 0 ? host::sms() : 1, spt = (nk + WT_KB - 1) / WT_KB;
@@ -260,12 +265,13 @@ WtPlan wt_plan(int tiles, int nk) {
   p.sk_tiles = tiles >= nsm ? tiles % nsm : tiles;
   const int64_t total = (int64_t)p.sk_tiles * spt;
   p.grid = tiles < nsm && total < nsm ? (int)total : nsm;
-  const int64_t range = (total + p.grid - 1) / p.grid;
+  p.sharers = total < p.grid ? (int)total : p.grid;
+  const int64_t range = p.sharers > 0 ? (total + p.sharers - 1) / p.sharers : 0;
   p.seg_max = (int)((range + spt - 1) / spt) + 1;
   return p;
 }
 size_t wt_workspace(int64_t M, int64_t tiles16, int64_t K) {
-  if (!wt_serves(M, tiles16)) return HEADER;
+  if (M > FT_MAX_TOKENS || !wt_serves(M, tiles16, K)) return HEADER;
   const WtPlan p = wt_plan((int)((tiles16 + 7) / 8), (int)((K + 63) / 64));
   return HEADER + WT_COUNTERS + (size_t)p.grid * p.seg_max * wt_columns(M) * 512;
 }
@@ -297,6 +303,7 @@ cudaError_t launch_wt(host::ServingKernel id, const WsArgs& s, int pair, int til
   a.tiles16 = tiles16;
   a.tiles = tiles;
   a.sk_tiles = p.sk_tiles;
+  a.sharers = p.sharers;
   a.seg_max = p.seg_max;
   a.pair = pair;
   a.W = s.W;
@@ -304,14 +311,14 @@ cudaError_t launch_wt(host::ServingKernel id, const WsArgs& s, int pair, int til
   a.scale = s.scale;
   a.first = s.first;
   a.stages = (WS_SMEM - fixed) / S::STAGE < WT_MAX_STAGES ? (WS_SMEM - fixed) / S::STAGE : WT_MAX_STAGES;
-  a.counters = reinterpret_cast<int*>(ws + HEADER) + (s.gate_up ? 0 : WT_MAX_TILES);
+  a.counters = reinterpret_cast<int*>(ws + HEADER) + (s.gate_up ? 0 : WT_MAX_SHARED);
   a.part = reinterpret_cast<float*>(ws + HEADER + WT_COUNTERS);
   a.wait_limit_ns = host::wait_limit_ns();
   a.err = s.err;
   a.inject = host::take_stall() ? 1 : 0;
-  SET_WINDOWS(a, {{s.out, (size_t)s.M * s.rows * 2},
-                  {s.W, (size_t)tiles16 * nk * S::RECORD},
-                  {ws, wt_workspace(s.M, tiles16, s.K)}});
+#ifdef SWIGLU_DEBUG
+  a.dbg = s.dbg;
+#endif
   host::Prof prof(id, st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
@@ -348,7 +355,7 @@ cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, int tiles16, cuda
 
 template <bool BF16>
 cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, cudaStream_t st) {
-  if (wt_serves(a.M, w.tiles)) {
+  if (wt_serves(a.M, w.tiles, a.K)) {
     const int pair = w.group_log2 == 7 ? 2 : 1;
     if (w.sets == 2)
       return w.zeros ? launch_wt<BF16, true, true>(id, a, pair, w.tiles, st)
@@ -410,7 +417,7 @@ swiglu_status run_experts(const void* X, const int* idx, const float* wts, const
                           const swiglu_mlp_w4_format* f, swiglu_dtype dt, const Muls& mu, char* ws,
                           size_t ws_bytes, bool after_router, cudaStream_t st) {
   (void)ws_bytes;
-  void* A = ws + HEADER;
+  void* A = ws + HEADER + WT_COUNTERS;  // past the counters of the products above
   const bool w4 = f != nullptr, bf = dt == SWIGLU_BF16;
   const W4Geom gu = w4 ? w4_geom(2 * (int64_t)H, D, log2_group(f->group), f->zeros, 1) : W4Geom{};
   const W4Geom dn = w4 ? w4_geom(D, H, log2_group(f->group), f->zeros, 0) : W4Geom{};
@@ -605,7 +612,7 @@ swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, i
   a.scale = 1.0f;
   a.first = 1;
   a.err = static_cast<int*>(ws);
-  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {X, (size_t)(M * K * 2)}, {packed, (size_t)w.bytes}});
+  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {X, (size_t)(M * K * 2)}, {packed, (size_t)w.bytes}, {ws, ws_bytes}});
   return status_of(launch_ws(host::SK_W4_LINEAR, a, w, dtype,
                              static_cast<cudaStream_t>(stream)));
 }
@@ -641,7 +648,7 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   a.scale = mu.gate;
   a.first = 1;
   a.err = static_cast<int*>(ws);
-  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {X, (size_t)(M * D * 2)}, {Wgu, (size_t)gu.bytes}});
+  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {X, (size_t)(M * D * 2)}, {Wgu, (size_t)gu.bytes}, {ws, ws_bytes}});
   if (launch_ws(host::SK_W4_GATE_UP, a, gu, dtype, s) != cudaSuccess)
     return SWIGLU_ERR_CUDA;
   const W4Geom dn = w4_geom(D, H, log2_group(group), zeros, 0);
@@ -653,7 +660,7 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   a.out = Y;
   a.scale = mu.down;
   a.first = 0;
-  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {A, (size_t)(M * H * 2)}, {Wd, (size_t)dn.bytes}});
+  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {A, (size_t)(M * H * 2)}, {Wd, (size_t)dn.bytes}, {ws, ws_bytes}});
   return status_of(launch_ws(host::SK_W4_DOWN, a, dn, dtype, s));
 }
 
@@ -661,7 +668,7 @@ size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E
   (void)D;
   (void)E;
   if (T < 0 || H <= 0 || topk <= 0) return 0;
-  return HEADER + moe_inner_bytes(T, H, topk);
+  return HEADER + WT_COUNTERS + moe_inner_bytes(T, H, topk);
 }
 
 swiglu_status swiglu_mlp_moe_route(const void* X, const void* Wr, int32_t* idx, float* weights,

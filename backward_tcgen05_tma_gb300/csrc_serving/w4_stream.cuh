@@ -1,4 +1,4 @@
-// w4_stream.cuh -- products of a few tokens (1..64) with 4-bit weights:
+// w4_stream.cuh -- products of a few tokens (1..32) with 4-bit weights:
 //   Y[m, r] = sum_k X[m, k] W[r, k],   W[r, k] = s[r, k/G] (q[r, k] - z[r, k/G])
 // and the SwiGLU of such products (gate/up).
 //
@@ -33,9 +33,7 @@
 // contraction is split over a cluster of 2, 4 or 8 blocks: each holds its part
 // of the rows and works on all the cluster's tiles, and at the end of a run the
 // blocks add up each other's sums through distributed shared memory, in rank
-// order.  (What still does not fit is taken in phases; 33 and more tokens take
-// two passes over the weights, which the L2 cache then holds.)  From 9 tokens
-// on a tile has 32 rows (RT = 2): shared memory, which delivers 128 bytes a
+// order.  (What still does not fit is taken in phases.)  From 9 tokens on a tile has 32 rows (RT = 2): shared memory, which delivers 128 bytes a
 // cycle, would otherwise give most of them to the token rows.
 #pragma once
 
@@ -151,11 +149,11 @@ struct WsConst {
   static constexpr uint32_t ONE = BF16 ? 0x3f803f80u : 0x3c003c00u;
 };
 
-// One warp's place in the block's work: token pass, run of tiles, phase of the
+// One warp's place in the block's work: run of tiles, phase of the
 // contraction, and the chunks [v, v_end) of the run and phase laid end to end;
 // chunk v is chunk c of the run's tile j.
 struct WsWalk {
-  int pass, run, phase, v, v_end, j, c;
+  int run, phase, v, v_end, j, c;
 };
 
 template <bool BF16, int RT, int NT, bool G32, bool ZP>
@@ -193,33 +191,30 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
   const int b = a.split > 1 ? blockIdx.x / a.split : blockIdx.x;
   const int tile0 = b * a.tile_quot + min(b, a.tile_rem);
   const int tiles = a.tile_quot + (b < a.tile_rem ? 1 : 0);
-  const int passes = (a.M + S::TOKENS - 1) / S::TOKENS;
   const int runs = tiles <= a.run ? 1 : (tiles + a.run - 1) / a.run;
   const int phases = (kunits + a.phase_units - 1) / a.phase_units;
   auto run_tiles = [&](int r) { return min(a.run, tiles - r * a.run); };
   auto phase_len = [&](int p) { return min(a.phase_units, kunits - p * a.phase_units); };  // units
   auto chunks_of = [&](int len) { return (len + S::UNITS - 1) / S::UNITS; };
   auto enter = [&](WsWalk& w) {  // this warp's share from here on, skipping empty ones
-    for (; w.pass < passes; ++w.pass, w.run = 0) {
-      for (; w.run < runs; ++w.run, w.phase = 0) {
-        for (; w.phase < phases; ++w.phase) {
-          const int per = chunks_of(phase_len(w.phase)), total = run_tiles(w.run) * per;
-          w.v = total * warp / WS_WARPS;
-          w.v_end = total * (warp + 1) / WS_WARPS;
-          w.j = w.v / per;
-          w.c = w.v - w.j * per;
-          if (w.v < w.v_end) return;
-        }
+    for (; w.run < runs; ++w.run, w.phase = 0) {
+      for (; w.phase < phases; ++w.phase) {
+        const int per = chunks_of(phase_len(w.phase)), total = run_tiles(w.run) * per;
+        w.v = total * warp / WS_WARPS;
+        w.v_end = total * (warp + 1) / WS_WARPS;
+        w.j = w.v / per;
+        w.c = w.v - w.j * per;
+        if (w.v < w.v_end) return;
       }
     }
   };
 
   // ---------------------------------------------------------------- weights in
-  WsWalk in = {0, 0, 0, 0, 0, 0, 0};
+  WsWalk in = {0, 0, 0, 0, 0, 0};
   const uint8_t* src = nullptr;       // the next chunk
   int in_per = 0, in_last = 0;        // chunks of a tile; bytes of its last chunk (16 rows)
   auto locate = [&]() {
-    if (in.pass >= passes) return;
+    if (in.run >= runs) return;
     const int len = phase_len(in.phase);
     in_per = chunks_of(len);
     in_last = (len - (in_per - 1) * S::UNITS) * S::RECORD;
@@ -235,7 +230,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
   const uint32_t ring_bytes = a.stages * S::STAGE, bar_end = bar0 + 8 * a.stages;
   bool skip = a.inject != 0;  // test hook
   auto fill = [&]() {  // the next stage: the units of one chunk
-    if (in.pass >= passes) return;
+    if (in.run >= runs) return;
     const uint32_t bytes = in.c == in_per - 1 ? in_last : S::PIECE;
     if (lane == 0 && !skip) {
       // the second half of the last tile may lie past the matrix
@@ -272,27 +267,27 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
   if (!a.first) pdl_wait();  // before the first read of a token row
 
   // ---------------------------------------------------------------- token rows
-  // Units [u0, u0 + len) of the rows [m0, m0 + count): bulk copies bring them,
+  // Units [u0, u0 + len) of the rows: bulk copies bring them,
   // and the warps add up each unit's elements per token.
   uint32_t xparity = 0;
   bool xlive = true;
-  auto stage_rows = [&](int m0, int count, int u0, int len) {
+  auto stage_rows = [&](int u0, int len) {
     const int xrow = S::xrow(a.phase_units);
     const int inside = min(len * 64, a.K - u0 * 64);  // elements of a row
     if (warp == 0) {
       // what was read or written here before is ordered with the copies
       fence_proxy_async_shared();
-      if (lane == 0) mbar_arrive_expect_tx(xbar, count * inside * 2);
+      if (lane == 0) mbar_arrive_expect_tx(xbar, a.M * inside * 2);
       __syncwarp();
-      if (lane < count) {
-        const uint8_t* p = static_cast<const uint8_t*>(a.X) + ((int64_t)(m0 + lane) * a.K + u0 * 64) * 2;
+      if (lane < a.M) {
+        const uint8_t* p = static_cast<const uint8_t*>(a.X) + ((int64_t)lane * a.K + u0 * 64) * 2;
         if (SWIGLU_CHECK_PTR(a.dbg, p, inside * 2, a.err))
           bulk_load(sbase + lane * xrow, p, inside * 2, xbar);
       }
     }
     // zeros from the end of a row to the end of its last unit
     const int gap = (len * 64 - inside) / 8;  // 16-byte pieces, 0..7
-    if ((int)threadIdx.x < count * gap) {
+    if ((int)threadIdx.x < a.M * gap) {
       const int m = threadIdx.x / gap, c = threadIdx.x - m * gap;
       *reinterpret_cast<uint4*>(smem + m * xrow + inside * 2 + c * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -303,7 +298,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i = warp; i < len * NT; i += WS_WARPS) {
       const int u = i / NT, nt = i - u * NT;
-      const uint32_t p = sbase + min(nt * 8 + g, count - 1) * xrow + u * 128 + t * 16;
+      const uint32_t p = sbase + min(nt * 8 + g, a.M - 1) * xrow + u * 128 + t * 16;
       const uint4 x0 = lds128_at<0>(p), x1 = lds128_at<64>(p);
       auto half = [&](float4 c, uint4 x, uint32_t k1, uint32_t k2) {
         c = mma_ws<BF16>(c, k1, k1, k1, k1, x.x, x.y);
@@ -447,11 +442,11 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
   };
   // The epilogue of 16 rows and 8 tokens, part `rest` of the run's tile jt: lane
   // (g, t) has rows g and g + 8 of tokens 2 t and 2 t + 1.
-  auto finish = [&](int jt, int rest, float4 v, int run, int m0, int count) {
+  auto finish = [&](int jt, int rest, float4 v, int run) {
     const int t16 = (tile0 + run * a.run + jt) * RT + rest / NT, m = rest % NT * 8 + 2 * t;
     auto put = [&](int row, int token, float x) {
-      if (row >= a.rows || token >= count) return;
-      uint16_t* o = out + (int64_t)(m0 + token) * a.rows + row;
+      if (row >= a.rows || token >= a.M) return;
+      uint16_t* o = out + (int64_t)token * a.rows + row;
       if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = P::rnd(x);
     };
     if (a.gate_up) {
@@ -464,126 +459,123 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
       put(t16 * 16 + g + 8, m + 1, a.scale * v.w);
     }
   };
-  for (int pass = 0; pass < passes; ++pass) {
-    const int m0 = pass * S::TOKENS, count = min(S::TOKENS, a.M - m0);
-    uint32_t xa[NT];  // this lane's token rows; columns past the last repeat it, unread
+  uint32_t xa[NT];  // this lane's token rows; columns past the last repeat it, unread
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      xa[nt] = sbase + min(nt * 8 + g, count - 1) * S::xrow(a.phase_units) + t * 16;
-    for (int run = 0; run < runs; ++run) {
-      const int n = run_tiles(run);
-      for (int phase = 0; phase < phases; ++phase) {
-        const int len = phase_len(phase);
-        if (phases > 1 || run == 0) {
-          stage_rows(m0, count, kbase + phase * a.phase_units, len);
-        }
-        const int per = chunks_of(len), total = n * per;  // chunks of a tile, of the run
-        const int v0 = total * warp / WS_WARPS, v1 = total * (warp + 1) / WS_WARPS;
-        int j = v0 / per, c = v0 - j * per;
-        const int tail = len - (per - 1) * S::UNITS;  // units of a tile's last chunk
-        uint32_t xu[NT], su = sbase + a.sum_off + t * 16 + c * (S::UNITS * S::SUMS);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt] + c * (S::UNITS * 128);
-        for (int v = v0; v < v1; ++v) {
-          if (live && !mbar_try_wait(bar_at, parity))
-            live = mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);
-          live = __all_sync(0xffffffffu, live);
-          const bool last = ++c == per;
-          if (live) {
-            uint32_t rc = ring + slot_at + lane * 16, rs = ring + slot_at + 512 + g * 4;
-            int left = last ? tail : S::UNITS;
-            constexpr int STEP = 4 / RT;  // independent chains in flight
-            for (; left >= STEP; left -= STEP) {
-              multiply(WsInt<0>{}, rc, rs, xu, su);
-              multiply(WsInt<1>{}, rc, rs, xu, su);
-              if constexpr (STEP == 4) {
-                multiply(WsInt<2>{}, rc, rs, xu, su);
-                multiply(WsInt<3>{}, rc, rs, xu, su);
-              }
-              rc += STEP * S::RECORD;
-              rs += STEP * S::RECORD;
-              su += STEP * S::SUMS;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) xu[nt] += STEP * 128;
-            }
-            for (; left > 0; --left) {
-              multiply(WsInt<0>{}, rc, rs, xu, su);
-              rc += S::RECORD;
-              rs += S::RECORD;
-              su += S::SUMS;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) xu[nt] += 128;
-            }
-            __syncwarp();
-            --filled;
-            slot_at += S::STAGE;
-            bar_at += 8;
-            if (slot_at == ring_bytes) {
-              slot_at = 0;
-              bar_at = bar0;
-              parity ^= 1u;
-            }
-            fill();
-          }
-          if (last) {
-            c = 0;
-            flush(j++);
-            su = sbase + a.sum_off + t * 16;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt];
-          }
-        }
-        if (c != 0) flush(j);
-        __syncthreads();
-        // a tile's partials, in warp order; a warp takes 16 rows and 8 tokens at
-        // a time.  Sums that are not final yet wait in tsum (for the next phase)
-        // or in the place of the first partial (for the cluster).
-        for (int i = warp; i < n * RT * NT; i += WS_WARPS) {
-          const int jt = i / (RT * NT), rest = i % (RT * NT);
-          const uint32_t meet = meeting(n, per, jt);
-          float4* const p = reinterpret_cast<float4*>(part) + rest * 32 + lane;
-          float4* const p0 = p + (jt + __ffs(meet) - 1) * (S::PART / 16);
-          float4 v = *p0;
-          for (uint32_t m = meet & (meet - 1); m != 0; m &= m - 1)
-            v = plus(v, p[(jt + __ffs(m) - 1) * (S::PART / 16)]);
-          if (a.phased) {
-            float4* ts = reinterpret_cast<float4*>(tsum) + jt * (S::PART / 16) + rest * 32 + lane;
-            if (phase > 0) v = plus(*ts, v);
-            *ts = v;
-          } else if (a.split > 1) {
-            *p0 = v;
-          }
-          if (a.split == 1 && phase + 1 == phases) finish(jt, rest, v, run, m0, count);
-        }
-        __syncthreads();
+  for (int nt = 0; nt < NT; ++nt)
+    xa[nt] = sbase + min(nt * 8 + g, a.M - 1) * S::xrow(a.phase_units) + t * 16;
+  for (int run = 0; run < runs; ++run) {
+    const int n = run_tiles(run);
+    for (int phase = 0; phase < phases; ++phase) {
+      const int len = phase_len(phase);
+      if (phases > 1 || run == 0) {
+        stage_rows(kbase + phase * a.phase_units, len);
       }
-      if (a.split > 1) {
-        // the blocks' sums, in rank order
-        cluster_arrive();
-        cluster_wait();
-        for (int i = warp * a.split + rank; i < n * RT * NT; i += WS_WARPS * a.split) {
-          const int jt = i / (RT * NT), rest = i % (RT * NT);
-          float4 q[8];  // all loads at once: they are all latency
+      const int per = chunks_of(len), total = n * per;  // chunks of a tile, of the run
+      const int v0 = total * warp / WS_WARPS, v1 = total * (warp + 1) / WS_WARPS;
+      int j = v0 / per, c = v0 - j * per;
+      const int tail = len - (per - 1) * S::UNITS;  // units of a tile's last chunk
+      uint32_t xu[NT], su = sbase + a.sum_off + t * 16 + c * (S::UNITS * S::SUMS);
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (r < a.split) {
-              uint32_t at = a.tile_off + jt * S::PART;
-              if (!a.phased) {
-                const int per = chunks_of(nk * (r + 1) / a.split - nk * r / a.split);
-                at = a.part_off + (jt + __ffs(meeting(n, per, jt)) - 1) * S::PART;
-              }
-              q[r] = cluster_load4(cluster_map(sbase + at + rest * 512 + lane * 16, r));
+      for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt] + c * (S::UNITS * 128);
+      for (int v = v0; v < v1; ++v) {
+        if (live && !mbar_try_wait(bar_at, parity))
+          live = mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);
+        live = __all_sync(0xffffffffu, live);
+        const bool last = ++c == per;
+        if (live) {
+          uint32_t rc = ring + slot_at + lane * 16, rs = ring + slot_at + 512 + g * 4;
+          int left = last ? tail : S::UNITS;
+          constexpr int STEP = 4 / RT;  // independent chains in flight
+          for (; left >= STEP; left -= STEP) {
+            multiply(WsInt<0>{}, rc, rs, xu, su);
+            multiply(WsInt<1>{}, rc, rs, xu, su);
+            if constexpr (STEP == 4) {
+              multiply(WsInt<2>{}, rc, rs, xu, su);
+              multiply(WsInt<3>{}, rc, rs, xu, su);
             }
-          float4 v = q[0];
+            rc += STEP * S::RECORD;
+            rs += STEP * S::RECORD;
+            su += STEP * S::SUMS;
 #pragma unroll
-          for (int r = 1; r < 8; ++r)
-            if (r < a.split) v = plus(v, q[r]);
-          finish(jt, rest, v, run, m0, count);
+            for (int nt = 0; nt < NT; ++nt) xu[nt] += STEP * 128;
+          }
+          for (; left > 0; --left) {
+            multiply(WsInt<0>{}, rc, rs, xu, su);
+            rc += S::RECORD;
+            rs += S::RECORD;
+            su += S::SUMS;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) xu[nt] += 128;
+          }
+          __syncwarp();
+          --filled;
+          slot_at += S::STAGE;
+          bar_at += 8;
+          if (slot_at == ring_bytes) {
+            slot_at = 0;
+            bar_at = bar0;
+            parity ^= 1u;
+          }
+          fill();
         }
-        __syncwarp();
-        cluster_arrive();  // before the partials are written again, or the block goes
-        cluster_wait();
+        if (last) {
+          c = 0;
+          flush(j++);
+          su = sbase + a.sum_off + t * 16;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt];
+        }
       }
+      if (c != 0) flush(j);
+      __syncthreads();
+      // a tile's partials, in warp order; a warp takes 16 rows and 8 tokens at
+      // a time.  Sums that are not final yet wait in tsum (for the next phase)
+      // or in the place of the first partial (for the cluster).
+      for (int i = warp; i < n * RT * NT; i += WS_WARPS) {
+        const int jt = i / (RT * NT), rest = i % (RT * NT);
+        const uint32_t meet = meeting(n, per, jt);
+        float4* const p = reinterpret_cast<float4*>(part) + rest * 32 + lane;
+        float4* const p0 = p + (jt + __ffs(meet) - 1) * (S::PART / 16);
+        float4 v = *p0;
+        for (uint32_t m = meet & (meet - 1); m != 0; m &= m - 1)
+          v = plus(v, p[(jt + __ffs(m) - 1) * (S::PART / 16)]);
+        if (a.phased) {
+          float4* ts = reinterpret_cast<float4*>(tsum) + jt * (S::PART / 16) + rest * 32 + lane;
+          if (phase > 0) v = plus(*ts, v);
+          *ts = v;
+        } else if (a.split > 1) {
+          *p0 = v;
+        }
+        if (a.split == 1 && phase + 1 == phases) finish(jt, rest, v, run);
+      }
+      __syncthreads();
+    }
+    if (a.split > 1) {
+      // the blocks' sums, in rank order
+      cluster_arrive();
+      cluster_wait();
+      for (int i = warp * a.split + rank; i < n * RT * NT; i += WS_WARPS * a.split) {
+        const int jt = i / (RT * NT), rest = i % (RT * NT);
+        float4 q[8];  // all loads at once: they are all latency
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < a.split) {
+            uint32_t at = a.tile_off + jt * S::PART;
+            if (!a.phased) {
+              const int per = chunks_of(nk * (r + 1) / a.split - nk * r / a.split);
+              at = a.part_off + (jt + __ffs(meeting(n, per, jt)) - 1) * S::PART;
+            }
+            q[r] = cluster_load4(cluster_map(sbase + at + rest * 512 + lane * 16, r));
+          }
+        float4 v = q[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < a.split) v = plus(v, q[r]);
+        finish(jt, rest, v, run);
+      }
+      __syncwarp();
+      cluster_arrive();  // before the partials are written again, or the block goes
+      cluster_wait();
     }
   }
   // after a wait ran out: no copy may land after the block has gone

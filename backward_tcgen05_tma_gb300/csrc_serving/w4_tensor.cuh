@@ -37,13 +37,14 @@ constexpr int WT_SETS = 2;        // pairs of TMEM accumulators, columns 0 to 25
 constexpr int WT_ABUFS = 2;       // unpacked A operands of a stage, 128 columns each from 256 on
 constexpr int WT_OUT = 8 * 2048;  // epilogue warps' [16][32] sums on their way out
 constexpr int WT_MAX_STAGES = 4;
-constexpr int WT_MAX_TILES = 512; // 128-row tiles (counters of a kernel)
+constexpr int WT_MAX_SHARED = 512; // counters of a kernel: its shared tiles, fewer than SMs
 
 struct WtArgs {
   int gate_up;       // out = rnd(SiLU(scale g) u), else rnd(scale v)
   int M, K;          // tokens; contraction, a multiple of 8
   int rows;          // rows of out: output features, or hidden units (gate/up)
-  int tiles16, tiles, sk_tiles, seg_max;  // 16- and 128-row tiles; tiles shared between blocks
+  int tiles16, tiles;           // 16- and 128-row tiles
+  int sk_tiles, sharers, seg_max;  // tiles shared between blocks, by how many, in segments a block
   int pair;          // 64-k blocks of one accumulator (2: groups of 128)
   const uint8_t* W;  // packed
   void* out;         // [M, rows]
@@ -56,7 +57,7 @@ struct WtArgs {
   uint64_t wait_limit_ns;
   int* err;
 #ifdef SWIGLU_DEBUG
-  DbgWin dbg;        // out, packed weights, workspace
+  DbgWin dbg;        // out, X, packed weights, workspace
 #endif
 };
 
@@ -118,13 +119,15 @@ struct WtSegs {
     return false;
   }
 };
-__device__ __forceinline__ int wt_start(int c, int total) {
-  return (int)((int64_t)c * total / gridDim.x);
+// The shared tiles' stages lie over the first `sharers` blocks, none of which
+// gets nothing (there are at least as many stages).
+__device__ __forceinline__ int wt_start(int c, int total, int sharers) {
+  return c >= sharers ? total : (int)((int64_t)c * total / sharers);
 }
-__device__ __forceinline__ int wt_owner(int x, int total) {  // the block that holds stage x
-  int c = (int)((int64_t)x * gridDim.x / total);
-  while (c + 1 < (int)gridDim.x && wt_start(c + 1, total) <= x) ++c;
-  while (c > 0 && wt_start(c, total) > x) --c;
+__device__ __forceinline__ int wt_owner(int x, int total, int sharers) {  // the block that holds stage x
+  int c = (int)((int64_t)x * sharers / total);
+  while (c + 1 < sharers && wt_start(c + 1, total, sharers) <= x) ++c;
+  while (c > 0 && wt_start(c, total, sharers) > x) --c;
   return c;
 }
 
@@ -187,7 +190,8 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
   const int nk = (a.K + 63) >> 6, spt = (nk + WT_KB - 1) / WT_KB;  // 64-k blocks, stages of a tile
   const int total = a.sk_tiles * spt;
   auto segs = [&]() {
-    return WtSegs{wt_start(blockIdx.x, total), wt_start(blockIdx.x + 1, total), 0,
+    return WtSegs{wt_start(blockIdx.x, total, a.sharers),
+                  wt_start(blockIdx.x + 1, total, a.sharers), 0,
                   (a.tiles - a.sk_tiles) / (int)gridDim.x, spt, a.sk_tiles};
   };
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -518,11 +522,12 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) mine[c * 128] = sum[c];
       }
-      const int c_first = wt_owner(tile * spt, total), c_last = wt_owner((tile + 1) * spt - 1, total);
+      const int c_first = wt_owner(tile * spt, total, a.sharers);
+      const int c_last = wt_owner((tile + 1) * spt - 1, total, a.sharers);
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (warp == 10 && lane == 0) {
         __threadfence();  // the 256 threads' stores before the count
-        last_word = live && !*abort_flag && SWIGLU_CHECK(tile < WT_MAX_TILES, a.err) &&
+        last_word = live && !*abort_flag && SWIGLU_CHECK(tile < WT_MAX_SHARED, a.err) &&
                     atomicAdd(a.counters + tile, 1) == c_last - c_first;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) sum[c] = 0.0f;
         for (int b = c_first; b <= c_last; ++b) {  // in block order
-          const int j = tile - wt_start(b, total) / spt;
+          const int j = tile - wt_start(b, total, a.sharers) / spt;
           const float* p = a.part + ((int64_t)b * a.seg_max + j) * NT * 128 + col0 * 128 + e;
           if (!SWIGLU_CHECK(j >= 0 && j < a.seg_max, a.err)) continue;
 #pragma unroll

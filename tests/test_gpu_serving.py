@@ -186,7 +186,9 @@ def test_pack_and_unpack_of_experts():
     ("bf16", 13, 1000, 11008, 128, False), ("f16", 16, 5000, 640, 64, False),
     ("bf16", 17, 47, 136, 32, True), ("f16", 33, 700, 2816, 128, False),
     ("bf16", 64, 5632, 2048, 64, True), ("f16", 64, 100, 5632, 32, False),
-    ("bf16", 5, 40000, 64, 64, False)])
+    ("bf16", 5, 40000, 64, 64, False), ("bf16", 29, 8208, 4104, 32, True),
+    ("f16", 25, 16400, 2056, 128, False), ("bf16", 40, 70001, 72, 64, True),
+    ("f16", 50, 20000, 1096, 64, False)])
 def test_w4_linear(dtn, M, N, K, group, zeros):
     g = gen(M * 7 + N)
     w = codes(g, (), N, K, group, zeros, DT[dtn])
@@ -212,17 +214,18 @@ def test_w4_mlp(dtn, M, D, H, group, zeros, muls):
     near(Y, muls[1] * (A.double() @ weights64(*dn, group).T), U[dtn] + SLACK)  # on the stored A
 
 
-def test_w4_zero_tokens_and_non_finite_tokens():
+@pytest.mark.parametrize("M", [12, 45])
+def test_w4_zero_tokens_and_non_finite_tokens(M):
     g = gen(3)
     w = codes(g, (), 48, 128, 64, True, torch.bfloat16)
     W = api.swiglu_mlp_w4_pack(*w, 64)
     assert api.swiglu_mlp_w4_linear(torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"), W).shape == (0, 48)
-    X = normal(g, 12, 128, dtype=torch.bfloat16)
+    X = normal(g, M, 128, dtype=torch.bfloat16)
     clean = api.swiglu_mlp_w4_linear(X, W)
     X[3, 5], X[9, 100] = float("nan"), float("inf")
     Y = api.swiglu_mlp_w4_linear(X, W)
     assert torch.isnan(Y[3]).all() and not torch.isfinite(Y[9]).any()
-    keep = [i for i in range(12) if i not in (3, 9)]  # no token reaches another
+    keep = [i for i in range(M) if i not in (3, 9)]  # no token reaches another
     assert torch.equal(Y[keep], clean[keep])
 
 
@@ -401,7 +404,7 @@ def same(a, b):
 
 
 @pytest.mark.parametrize("op", OPS)
-@pytest.mark.parametrize("T", [1, 6, 20])
+@pytest.mark.parametrize("T", [1, 6, 20, 41])
 def test_deterministic_and_workspace_reusable(op, T):
     _, calls = make_calls(T)
     call, out, ws = calls[op]
@@ -507,11 +510,12 @@ def test_out_and_inputs_are_checked():
         api.swiglu_mlp_w4_pack(*codes(g, (), 32, 64, 64, False, X.dtype)[:2], group=32)
 
 
+@pytest.mark.parametrize("T", [4, 41])
 @pytest.mark.parametrize("op", OPS)
-def test_a_wait_that_runs_out_is_reported(op):
+def test_a_wait_that_runs_out_is_reported(op, T):
     # a copy that is never made: the wait gives up at its limit, the status
     # says so, and the next call is right again
-    _, calls = make_calls(4)
+    _, calls = make_calls(T)
     call, out, ws = calls[op]
     call()
     torch.cuda.synchronize()
@@ -532,11 +536,12 @@ def test_a_wait_that_runs_out_is_reported(op):
     assert api.swiglu_mlp_query_error(ws) == 0 and same(snap(out), first)
 
 
+@pytest.mark.parametrize("T", [9, 41])
 @pytest.mark.parametrize("op", OPS)
-def test_debug_build(op):
+def test_debug_build(op, T):
     prev = api.use_debug_library(True)
     try:
-        _, calls = make_calls(9)
+        _, calls = make_calls(T)
         call, out, ws = calls[op]
         call()  # raises on a failed index check
         first = snap(out)
