@@ -9,6 +9,9 @@
 // than an eighth of Wr.  The logits meet in the first block's shared memory,
 // where one warp per token picks the experts.  Products of two 32-element
 // runs of d go through the tensor core; the runs are added in fp32.
+// Measured: 2048 x 64 experts, 1 to 64 tokens, 3.4 us in front of the experts'
+// kernels (11.3 us as a call of its own from Python), all of it latency: two
+// rounds of loads, the cluster's exchange, a warp's topk passes.
 #pragma once
 
 #include "fewtok.cuh"

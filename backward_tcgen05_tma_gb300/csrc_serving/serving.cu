@@ -612,7 +612,8 @@ swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, i
   a.scale = 1.0f;
   a.first = 1;
   a.err = static_cast<int*>(ws);
-  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {X, (size_t)(M * K * 2)}, {packed, (size_t)w.bytes}, {ws, ws_bytes}});
+  SET_WINDOWS(a, {{Y, (size_t)(M * N * 2)}, {X, (size_t)(M * K * 2)}, {packed, (size_t)w.bytes},
+                  {ws, ws_bytes}});
   return status_of(launch_ws(host::SK_W4_LINEAR, a, w, dtype,
                              static_cast<cudaStream_t>(stream)));
 }
@@ -648,7 +649,8 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   a.scale = mu.gate;
   a.first = 1;
   a.err = static_cast<int*>(ws);
-  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {X, (size_t)(M * D * 2)}, {Wgu, (size_t)gu.bytes}, {ws, ws_bytes}});
+  SET_WINDOWS(a, {{A, (size_t)(M * H * 2)}, {X, (size_t)(M * D * 2)}, {Wgu, (size_t)gu.bytes},
+                  {ws, ws_bytes}});
   if (launch_ws(host::SK_W4_GATE_UP, a, gu, dtype, s) != cudaSuccess)
     return SWIGLU_ERR_CUDA;
   const W4Geom dn = w4_geom(D, H, log2_group(group), zeros, 0);
@@ -660,7 +662,8 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   a.out = Y;
   a.scale = mu.down;
   a.first = 0;
-  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {A, (size_t)(M * H * 2)}, {Wd, (size_t)dn.bytes}, {ws, ws_bytes}});
+  SET_WINDOWS(a, {{Y, (size_t)(M * D * 2)}, {A, (size_t)(M * H * 2)}, {Wd, (size_t)dn.bytes},
+                  {ws, ws_bytes}});
   return status_of(launch_ws(host::SK_W4_DOWN, a, dn, dtype, s));
 }
 

@@ -1,30 +1,43 @@
-// w4_tensor.cuh -- products of 17 to 64 tokens with 4-bit weights on the
-// tcgen05 tensor core (the packed weights and the results of w4_stream.cuh).
+// w4_tensor.cuh -- products of 25 to 64 tokens with 4-bit weights on the
+// tcgen05 tensor core (the packed weights and the results of w4_stream.cuh):
+//   Y[m, r] = sum_G s[r, G] sum_{k in G} (q[r, k] - z[r, G]) X[m, k].
 //
-// From about 17 tokens on mma.sync's rate (1024 products a cycle and SM,
-// measured) bounds w4_stream.cuh, and its blocks' share of the token rows grows;
-// here the tensor core is far from its bound again and the SM's issue slots,
-// spent on unpacking, are what counts.
+// Beyond some 24 tokens the rate of mma.sync (1024 products a cycle and SM,
+// measured) and the shared-memory reads of the token rows bound w4_stream.cuh;
+// on tcgen05 the products are far from a bound again (tensor pipe 16% busy).
 //
 // Swap-AB: 128 weight rows (8 of the packed 16-row tiles) take the MMA's M
 // dimension, the tokens its N dimension (NT = 32, 48 or 64).  Roles of a block:
 //   producer  (1 thread) stages of 256 k, two tensor-map boxes each: the 8
 //                        tiles' records, and the token rows;
-//   unpackers (8 warps)  32 weight rows each, a thread per row, a stage at a time:
-//                        codes -> whole numbers q - z in 16 bits (exact) -> the
-//                        A operand, which the MMA reads from TMEM (written to
-//                        shared memory and read from there again it bounded the
-//                        loop: 750 now 450 cycles per 64 k);
+//   unpackers (8 warps)  32 weight rows each, a thread per row: codes -> whole
+//                        numbers q - z in 16 bits (exact) -> the A operand, which
+//                        the MMA reads from TMEM;
 //   MMA       (1 warp)   4 MMAs per 64 k into one of 4 TMEM accumulators, a
 //                        new one for each group of k that shares its scales;
 //   epilogue  (8 warps)  a thread per weight row and half of the tokens: adds
 //                        scale * accumulator to its fp32 sums, group by group,
 //                        so no weight is rounded here either.
-// The stages of all tiles are laid end to end and shared evenly by the blocks
-// (the tiles beyond a multiple of the blocks; the rest are whole): partial
-// tiles meet in the workspace, and the last block of a tile to finish
-// (a counter per tile) adds them in order and writes.  No block waits for
-// another.
+// The roles meet once per stage and once per pair of accumulators: a barrier
+// that is ready still costs a warp some 200 cycles of dependent instructions,
+// and with one per 64 or 128 k those bounded the loop (64 tokens, 22016 x 4096:
+// 42 us, now 37).  Before that the same product took 58 us with A in shared
+// memory (written and read there once more) and an epilogue unrolled over its
+// registers (its code, run once and cold, took 10 us to fetch), and 44 without
+// the two.  16 unpacking warps (72 registers a thread) take 42 us, 8 take 38.
+//
+// The stages of the tiles beyond a multiple of the blocks are laid end to end
+// and shared evenly by the blocks; the other tiles are whole.  Partial tiles
+// meet in the workspace, and the last block of a tile to finish (a counter per
+// tile) adds them in block order and writes.  No block waits for another.
+//
+// Measured (bf16, groups of 128): MLP 4096/11008, 72 MB, 10.7 us at the HBM
+// rate, 60 us at 64 tokens (w4_stream.cuh: 122), 52 at 32 (63); groups of 32:
+// 79 at 64 tokens, where an accumulator per 32 k makes the epilogue the bound.
+// Gate/up alone at 64 tokens: 41.6 us, issue slots 48% and ALU 44% used; the
+// unpackers never wait (some 950 cycles per 64 k and warp).  Next after that: each
+// tile reads all token rows, 88 MB through L2, 24 us with the weights at the
+// 5.8 TB/s that reach the SMs; some 5 us are start and shared tiles' sums.
 #pragma once
 
 #include "fewtok.cuh"
@@ -335,12 +348,11 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
     // ---------------------------------------------------------------- unpackers
     // a warp reaches the TMEM lanes of its quarter: rows 32 (warp % 4).. of
     // the tile, and takes the even or the odd 64-k blocks
-    const int p = (warp - 2) >> 2, t16 = (warp & 3) * 2 + (lane >> 4), g = lane & 7, hi = (lane >> 3) & 1;
+    const int p = (warp - 2) >> 2, t16 = (warp & 3) * 2 + (lane >> 4), g = (lane >> 1) & 7, hi = lane & 1;
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + 256;
-    // Row g or g + 8's words of a record lie at (4 g + t) 16 + 8 half + 4 hi.
-    // Each lane starts at another t, and the lanes of the second 16-row tile
-    // with the other half, so that 32 lanes hit 32 banks.
-    const int turn = g >> 1, swap = lane >> 4;
+    // TMEM lane 2 g + hi of a 16-row tile holds row g + 8 hi: neighbouring lanes
+    // read the same 16 bytes, at (4 g + t) 16 of a record, and 8 lanes meet a
+    // bank twice.
     int slot = 0, ab = 0;
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
@@ -358,23 +370,14 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
           const uint32_t rec = rec0 + q * S::RECORD;
           uint32_t v[2][4], z[2] = {8u, 8u};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t at = rec + g * 64 + ((j + turn) & 3) * 16 + hi * 4;
-            const uint32_t x = lds32(at + swap * 8), y = lds32(at + 8 - swap * 8);
-            v[0][j] = swap ? y : x;
-            v[1][j] = swap ? x : y;
+          for (int t = 0; t < 4; ++t) {
+            const uint4 x = lds128(rec + g * 64 + t * 16);
+            v[0][t] = hi ? x.y : x.x;
+            v[1][t] = hi ? x.w : x.z;
           }
           if (ZP) {
             z[0] = lds8(rec + 512 + S::GROUPS * 32 + g * 2 + hi);
             z[1] = G32 ? lds8(rec + 512 + S::GROUPS * 32 + 16 + g * 2 + hi) : z[0];
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // turn the words back
-            uint32_t r[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) r[t] = turn & 1 ? v[h][(t + 3) & 3] : v[h][t];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) v[h][t] = turn & 2 ? r[(t + 2) & 3] : r[t];
           }
           uint32_t out[32];
 #pragma unroll
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
     const int col0 = warp < 14 ? 0 : NC;
     const uint32_t tacc = tmem + ((uint32_t)(e & 96) << 16) + col0;
     const uint32_t stage = sbase + (warp - 10) * 2048;
-    const int slot16 = (e & 7) * 2 + ((e >> 3) & 1);  // this row's place among 16 scales
+    const int slot16 = e & 15;  // this row's place among 16 scales
+    const int row32 = (lane & 16) + (lane & 1) * 8 + ((lane >> 1) & 7);  // its place among 32 rows
     int set = 0, seg = 0;
     uint32_t setphase = 0;
     bool live = true;  // false after a wait ran out: go through the motions, add nothing
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
 #pragma unroll
         for (int c0 = 0; c0 < NC; c0 += 16) {
 #pragma unroll
-          for (int c = c0; c < c0 + 16 && c < NC; ++c) sts32(stage + ((c - c0) * 32 + lane) * 4, sum[c]);
+          for (int c = c0; c < c0 + 16 && c < NC; ++c) sts32(stage + ((c - c0) * 32 + row32) * 4, sum[c]);
           __syncwarp();
           const int n = min(min(16, NC - c0), a.M - col0 - c0);
           if (a.gate_up) {  // 16 units of two tokens

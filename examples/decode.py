@@ -16,12 +16,32 @@ from backward_tcgen05_tma_gb300.module import SwiGLUMLP  # noqa: E402
 from backward_tcgen05_tma_gb300.serving import MoESwiGLU, W4SwiGLUMLP  # noqa: E402
 
 
+def step(layers, x):
+    for layer in layers:
+        x = x + layer(x)
+    return x / x.float().square().mean(-1, keepdim=True).sqrt().to(x.dtype)
+
+
 def decode(layers, x, steps):
+    """Microseconds of a step: one is captured as a CUDA graph and replayed."""
+    x = x.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):  # what a first call sets up is not captured
+            x.copy_(step(layers, x))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.copy_(step(layers, x))
+    graph.replay()
+    beg, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    beg.record()
     for _ in range(steps):
-        for layer in layers:
-            x = x + layer(x)
-        x = x / x.float().square().mean(-1, keepdim=True).sqrt().to(x.dtype)
-    return x
+        graph.replay()
+    end.record()
+    end.synchronize()
+    return beg.elapsed_time(end) / steps * 1e3
 
 
 def main():
@@ -41,14 +61,8 @@ def main():
             if bits == 4:
                 moe.quantize(group=128)
             first[bits] = moe(x).float()
-            decode((mlp, moe), x, 4)
-            beg, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-            beg.record()
-            decode((mlp, moe), x, a.steps)
-            end.record()
-            end.synchronize()
             print("%2d-bit experts: %.1f us a step of %d token(s)"
-                  % (bits, beg.elapsed_time(end) / a.steps * 1e3, a.streams))
+                  % (bits, decode((mlp, moe), x, a.steps), a.streams))
         off = (first[4] - first[16]).norm() / first[16].norm()
         print("4-bit against 16-bit experts, one layer: %.1f%% apart" % (100 * off))
 

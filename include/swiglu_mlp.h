@@ -316,7 +316,15 @@ swiglu_status swiglu_mlp_bwd_ex(const void* dY, const void* X, const void* Wgu, 
  * 0 tokens launch nothing; more than 64 tokens and SWIGLU_F32_IEEE return
  * SWIGLU_ERR_UNSUPPORTED (expand the weights with swiglu_mlp_w4_unpack and
  * use the training or no-grad calls).  Workspaces follow the workspace rules
- * (zero-filled before first use, error word for swiglu_mlp_query_error). */
+ * (zero-filled before first use and after a timeout, error word for
+ * swiglu_mlp_query_error): one that is large enough serves the calls of this
+ * section in turn, whatever their sizes; after calls of other sections its
+ * first 4352 bytes (header and counters) have to be zero again.
+ *
+ * A NaN or an infinity in a token's row makes that token's outputs NaN (where
+ * exact arithmetic would leave an infinity, NaN too) and no other token's.
+ * Gate and up values meet in fp32; A is rounded once to 16 bits and Y is the
+ * product of the rounded A, as in the calls above. */
 
 /* Bytes of E packed matrices; gate_up: each is a pair [Wg; Wu], N = 2H.  0 for
  * invalid arguments. */
@@ -347,7 +355,9 @@ swiglu_status swiglu_mlp_w4_unpack(const void* packed, void* W, int64_t E, int64
                                    int group, int zeros, int gate_up, swiglu_dtype dtype,
                                    void* stream);
 
-/* Workspace bytes of swiglu_mlp_w4_linear and swiglu_mlp_fwd_nograd_w4. */
+/* Workspace bytes of swiglu_mlp_w4_linear and swiglu_mlp_fwd_nograd_w4: the
+ * header, and where the tensor-core form serves the call (from 33 tokens, for
+ * large matrices from 25) counters and fp32 partial tiles. */
 size_t swiglu_mlp_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t swiglu_mlp_fwd_nograd_w4_workspace_bytes(int64_t M, int64_t D, int64_t H);
 
