@@ -69,6 +69,14 @@ struct Ft16<false> {
   }
 };
 
+// (v & mask) | bits in one instruction
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "r"(bits));
+  return r;
+}
+
 // a - b of both halves
 template <bool BF16>
 __device__ __forceinline__ uint32_t ft_sub2(uint32_t a, uint32_t b) {

@@ -254,7 +254,7 @@ int wt_columns(int64_t M) { return M <= 32 ? 32 : M <= 48 ? 48 : 64; }
 // 15.4 us; with 33 to 64 it would read them twice (64 tokens, 4096 x 11008: 49.3
 // against 24.3 us; only 1024 x 1024 and less come out even).  Near 32 tokens
 // large matrices favour the tensor core too: MLP 4096/11008 at 32 tokens 62.6
-// against 51.8 us, at 17 tokens 50.6 against 51.4.
+// against 50.3 us; at 17 tokens the two come out even.
 bool wt_serves(int64_t M, int64_t tiles16, int64_t K) {
   return M > 32 || (M > 24 && tiles16 * 16 * K >= (int64_t)1 << 25);
 }

@@ -122,14 +122,6 @@ struct WsInt {
   static constexpr int value = N;
 };
 
-// (v & mask) | bits in one instruction
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "r"(bits));
-  return r;
-}
-
 template <bool BF16>
 __device__ __forceinline__ float4 mma_ws(float4 c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {

@@ -21,10 +21,12 @@
 // The roles meet once per stage and once per pair of accumulators: a barrier
 // that is ready still costs a warp some 200 cycles of dependent instructions,
 // and with one per 64 or 128 k those bounded the loop (64 tokens, 22016 x 4096:
-// 42 us, now 37).  Before that the same product took 58 us with A in shared
+// 42 us, then 37).  Before that the same product took 58 us with A in shared
 // memory (written and read there once more) and an epilogue unrolled over its
 // registers (its code, run once and cold, took 10 us to fetch), and 44 without
-// the two.  16 unpacking warps (72 registers a thread) take 42 us, 8 take 38.
+// the two.  16 unpacking warps (72 registers a thread) take 42 us, 8 took 38.
+// With neighbouring lanes on one chunk and mask-and-or in one instruction (a
+// third fewer instructions in all to unpack 64 k) it is 35.4.
 //
 // The stages of the tiles beyond a multiple of the blocks are laid end to end
 // and shared evenly by the blocks; the other tiles are whole.  Partial tiles
@@ -32,10 +34,11 @@
 // tile) adds them in block order and writes.  No block waits for another.
 //
 // Measured (bf16, groups of 128): MLP 4096/11008, 72 MB, 10.7 us at the HBM
-// rate, 60 us at 64 tokens (w4_stream.cuh: 122), 52 at 32 (63); groups of 32:
+// rate, 58 us at 64 tokens (w4_stream.cuh: 122), 50 at 32 (63); groups of 32:
 // 79 at 64 tokens, where an accumulator per 32 k makes the epilogue the bound.
-// Gate/up alone at 64 tokens: 41.6 us, issue slots 48% and ALU 44% used; the
-// unpackers never wait (some 950 cycles per 64 k and warp).  Next after that: each
+// At 64 tokens issue slots were 48% and the ALU 44% used when the pair took 60 us
+// (over the whole kernel; the unpackers never wait in the loop, some 950 cycles
+// per 64 k and warp then).  Next after that: each
 // tile reads all token rows, 88 MB through L2, 24 us with the weights at the
 // 5.8 TB/s that reach the SMs; some 5 us are start and shared tiles' sums.
 #pragma once
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
             for (int t = 0; t < 4; ++t) {
               const uint32_t m = P::MAGIC | (z[h] * 0x10001u);
               auto number = [&](uint32_t x) {
-                return ft_sub2<BF16>((x & 0x000f000fu) | P::MAGIC, m);
+                return ft_sub2<BF16>(and_or<0x000f000fu>(x, P::MAGIC), m);
               };
               uint32_t* o = out + h * 16 + t * 4;
               o[0] = number(v[h][t]);
