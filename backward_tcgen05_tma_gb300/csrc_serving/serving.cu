@@ -252,11 +252,12 @@ int wt_columns(int64_t M) { return M <= 32 ? 32 : M <= 48 ? 48 : 64; }
 // Which form a product takes.  Up to 32 tokens w4_stream.cuh reads the weights
 // once as well and starts up faster: 32 tokens, 4096 x 4096 weights 12.4 against
 // 15.4 us; with 33 to 64 it would read them twice (64 tokens, 4096 x 11008: 49.3
-// against 24.3 us; only 1024 x 1024 and less come out even).  Near 32 tokens
-// large matrices favour the tensor core too: MLP 4096/11008 at 32 tokens 62.6
-// against 50.3 us; at 17 tokens the two come out even.
+// against 24.3 us; only 1024 x 1024 and less come out even).  Large matrices
+// favour the tensor core from 17 tokens on: MLP 4096/11008 50.6 against some 50
+// us there, 59.2 at 24, 62.6 at 32 against 50.1 (groups of 32: 63.0 against 66.3
+// at 17, 71.1 against 66.6 at 32).
 bool wt_serves(int64_t M, int64_t tiles16, int64_t K) {
-  return M > 32 || (M > 24 && tiles16 * 16 * K >= (int64_t)1 << 25);
+  return M > 32 || (M > 16 && tiles16 * 16 * K >= (int64_t)1 << 25);
 }
 WtPlan wt_plan(int tiles, int nk) {
   const int nsm = host::sms() > 0 ? host::sms() : 1, spt = (nk + WT_KB - 1) / WT_KB;

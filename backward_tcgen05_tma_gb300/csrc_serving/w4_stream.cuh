@@ -38,8 +38,8 @@
 // would otherwise give most of them to the token rows.
 //
 // Measured (bf16, groups of 128, MLP 4096/11008, 70 MB, 10.3 us at the HBM rate):
-// 21.4 to 24.8 us at 1 to 8 tokens (2.8 to 3.3 TB/s), 34 at 16, 51 at 17, 63 at
-// 32; one token times 11008 x 4096 8.5 us, times 2816 x 1024 4.0 us back to back.
+// 21.4 to 24.8 us at 1 to 8 tokens (2.8 to 3.3 TB/s), 34 at 16 (51 at 17, 63 at
+// 32, where w4_tensor.cuh takes over); one token times 11008 x 4096 8.5 us, times 2816 x 1024 4.0 us back to back.
 // At one token gate/up takes 18.4 us alone: issue slots 37% used, DRAM 33%; some
 // 6 us of each kernel are its start (tensor cores idle until the token rows and
 // the first records are in) and its end (partials meet, 16-bit stores).  Before

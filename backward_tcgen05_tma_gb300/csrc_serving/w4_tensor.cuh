@@ -1,8 +1,8 @@
-// w4_tensor.cuh -- products of 25 to 64 tokens with 4-bit weights on the
+// w4_tensor.cuh -- products of 17 to 64 tokens with 4-bit weights on the
 // tcgen05 tensor core (the packed weights and the results of w4_stream.cuh):
 //   Y[m, r] = sum_G s[r, G] sum_{k in G} (q[r, k] - z[r, G]) X[m, k].
 //
-// Beyond some 24 tokens the rate of mma.sync (1024 products a cycle and SM,
+// Beyond 16 tokens the rate of mma.sync (1024 products a cycle and SM,
 // measured) and the shared-memory reads of the token rows bound w4_stream.cuh;
 // on tcgen05 the products are far from a bound again (tensor pipe 16% busy).
 //
@@ -38,9 +38,9 @@
 // 79 at 64 tokens, where an accumulator per 32 k makes the epilogue the bound.
 // At 64 tokens issue slots were 48% and the ALU 44% used when the pair took 60 us
 // (over the whole kernel; the unpackers never wait in the loop, some 950 cycles
-// per 64 k and warp then).  Next after that: each
-// tile reads all token rows, 88 MB through L2, 24 us with the weights at the
-// 5.8 TB/s that reach the SMs; some 5 us are start and shared tiles' sums.
+// per 64 k and warp then).  Next after that: each tile reads all token rows, 88
+// MB through L2, 24 us with the weights at the 5.8 TB/s that reach the SMs; some
+// 5 us are start and shared tiles' sums.
 #pragma once
 
 #include "fewtok.cuh"
