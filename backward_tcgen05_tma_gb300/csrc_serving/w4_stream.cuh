@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
     if (warp == 0) mbar_init(xbar, 1);
     fence_mbar_init();
   }
-  __syncwarp();
+  __syncthreads();  // every warp waits on xbar
 
   const int nk = (a.K + 63) >> 6;
   // this block's part of the contraction, units [kbase, kbase + kunits)
