@@ -128,8 +128,9 @@ __device__ __forceinline__ void sts32(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
-// 16 bytes through the L1 cache.  Not the read-only path: the rows may be
-// written while this kernel's prologue runs (before griddepcontrol.wait).
+// 16 bytes through the L1 cache.  Not the read-only path, which asks for data
+// that nothing writes while the kernel runs: token rows and router weights may
+// be written while its prologue does (before griddepcontrol.wait).
 __device__ __forceinline__ uint4 ft_load16(const void* p) {
   uint4 v;
   asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"

@@ -77,11 +77,11 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RtArgs a) {
         const bool in = k + t * 8 < a.D;
         x[i] = wl[i] = wh[i] = make_uint4(0, 0, 0, 0);
         if (in && hx && SWIGLU_CHECK_PTR(a.dbg, px + k * 2, 16, a.err))
-          x[i] = __ldg(reinterpret_cast<const uint4*>(px + k * 2));
+          x[i] = ft_load16(px + k * 2);
         if (in && hl && SWIGLU_CHECK_PTR(a.dbg, pl + k * 2, 16, a.err))
-          wl[i] = __ldg(reinterpret_cast<const uint4*>(pl + k * 2));
+          wl[i] = ft_load16(pl + k * 2);
         if (in && hh && SWIGLU_CHECK_PTR(a.dbg, ph + k * 2, 16, a.err))
-          wh[i] = __ldg(reinterpret_cast<const uint4*>(ph + k * 2));
+          wh[i] = ft_load16(ph + k * 2);
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {

@@ -36,3 +36,11 @@ def test_list_building_synchronises_the_block():
         body = text[text.index("void %s(" % name):]
         body = body[:body.index("\n}\n")]
         assert body.rstrip().endswith("__syncthreads();")
+
+
+@pytest.mark.parametrize("name", KERNELS + ["moe_route.cuh", "fewtok.cuh"])
+def test_no_read_only_loads(name):
+    # every launch is a programmatic dependent: what it reads may still be
+    # written while it runs, which the read-only path does not allow
+    text = source(name)
+    assert "__ldg(" not in text and "ld.global.nc" not in text
