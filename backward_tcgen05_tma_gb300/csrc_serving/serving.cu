@@ -27,7 +27,11 @@ namespace {
 #define SET_WINDOWS(args, ...) (void)0
 #endif
 
-constexpr int64_t LIMIT = 0x7fffffffLL;
+// Sizes up to which the kernels' 32-bit indexes hold, with their last tiles'
+// overhang: rows of a matrix, its contraction (byte offsets within one tile's
+// records: K / 64 of 608 bytes), and the sizes of a mixture's experts (items:
+// up to 640 entries of H / 8 or D / 16 tiles; chunks of a run times warps).
+constexpr int64_t MAX_ROWS = 0x7fffffffLL - 256, MAX_K = 1LL << 27, MAX_EXPERT = 1LL << 24;
 constexpr size_t HEADER = 256;  // workspace header: the error word
 
 swiglu_status status_of(cudaError_t e) { return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA; }
@@ -49,7 +53,7 @@ swiglu_status check_w4(int64_t E, int64_t N, int64_t K, int group, int zeros) {
   if (E <= 0 || N <= 0 || K <= 0) return SWIGLU_ERR_INVALID_ARG;
   if (log2_group(group) < 0 || (zeros != 0 && zeros != 1)) return SWIGLU_ERR_INVALID_ARG;
   if (K % 8 != 0) return SWIGLU_ERR_ALIGNMENT;
-  if (E > LIMIT || N > LIMIT || K > LIMIT) return SWIGLU_ERR_UNSUPPORTED;
+  if (E > MAX_ROWS || N > MAX_ROWS || K > MAX_K) return SWIGLU_ERR_UNSUPPORTED;
   return SWIGLU_OK;
 }
 
@@ -201,6 +205,7 @@ cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_
     a.run = per < S::RUN ? per : S::RUN;
     a.phase_units = ((nk + split - 1) / split + phases - 1) / phases;
     if (phases > 1) a.phase_units = (a.phase_units + S::UNITS - 1) / S::UNITS * S::UNITS;
+    if (a.phase_units > WS_SMEM / 128) return false;  // no row of them fits, nor its offsets 32 bits
     a.sum_off = up(rows * S::xrow(a.phase_units));
     a.part_off = up(a.sum_off + a.phase_units * S::SUMS);
     a.tile_off = up(a.part_off + (a.run + S::WARPS - 1) * S::PART);
@@ -395,7 +400,8 @@ swiglu_status check_moe(int64_t T, int64_t D, int64_t H, int64_t E, int64_t topk
   if (f != nullptr && (log2_group(f->group) < 0 || (f->zeros != 0 && f->zeros != 1)))
     return SWIGLU_ERR_INVALID_ARG;
   if (D % 8 != 0 || H % 8 != 0) return SWIGLU_ERR_ALIGNMENT;
-  if (T > FT_MAX_TOKENS || E > FT_MAX_EXPERTS || topk > FT_MAX_TOPK || D > LIMIT / 2 || H > LIMIT / 2)
+  if (T > FT_MAX_TOKENS || E > FT_MAX_EXPERTS || topk > FT_MAX_TOPK || D > MAX_EXPERT ||
+      H > MAX_EXPERT)
     return SWIGLU_ERR_UNSUPPORTED;
   return SWIGLU_OK;
 }
@@ -632,7 +638,7 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   if (M < 0) return SWIGLU_ERR_INVALID_ARG;
   if ((st = check_w4(1, D, H, group, zeros)) != SWIGLU_OK) return st;
   if (D % 8 != 0) return SWIGLU_ERR_ALIGNMENT;
-  if (M > FT_MAX_TOKENS || H > LIMIT / 2) return SWIGLU_ERR_UNSUPPORTED;
+  if (M > FT_MAX_TOKENS || D > MAX_K) return SWIGLU_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, swiglu_mlp_fwd_nograd_w4_workspace_bytes(M, D, H))) != SWIGLU_OK)
     return st;
   if (M == 0) return SWIGLU_OK;

@@ -315,7 +315,9 @@ swiglu_status swiglu_mlp_bwd_ex(const void* dY, const void* X, const void* Wgu, 
  * argument errors before any launch, asynchronous on `stream`, deterministic;
  * 0 tokens launch nothing; more than 64 tokens and SWIGLU_F32_IEEE return
  * SWIGLU_ERR_UNSUPPORTED (expand the weights with swiglu_mlp_w4_unpack and
- * use the training or no-grad calls).  Workspaces follow the workspace rules
+ * use the training or no-grad calls).  So do sizes beyond what the kernels
+ * index: K (the MLP: D and H) above 2^27, N above 2^31 - 257, and for mixtures
+ * of experts D or H above 2^24.  Workspaces follow the workspace rules
  * (zero-filled before first use and after a timeout, error word for
  * swiglu_mlp_query_error): one that is large enough serves the calls of this
  * section in turn, whatever their sizes; after calls of other sections its

@@ -1,12 +1,18 @@
 """Rules of the few-token serving operators that need no GPU to be checked: the
 order of synchronisation in the kernels' sources, launch plans, size limits,
 and the state of the modules."""
+import ctypes
 import os
 import re
 
 import pytest
 
-from backward_tcgen05_tma_gb300 import build
+from backward_tcgen05_tma_gb300 import api, build
+
+UNSUP = 3
+P = ctypes.c_void_p(0x10000)  # an aligned fake device address (never dereferenced)
+N = ctypes.c_void_p(0)
+BIG = 1 << 50
 
 KERNELS = ["w4_stream.cuh", "w4_tensor.cuh", "experts.cuh"]
 
@@ -44,3 +50,29 @@ def test_no_read_only_loads(name):
     # written while it runs, which the read-only path does not allow
     text = source(name)
     assert "__ldg(" not in text and "ld.global.nc" not in text
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return api.lib()
+
+
+def test_sizes_beyond_the_indexes_are_refused(L):
+    # before any CUDA call: the plans and the kernels count in 32 bits
+    lin = lambda M, rows, K: L.swiglu_mlp_w4_linear(P, P, P, M, rows, K, 128, 0, 0, P, BIG, N)
+    mlp = lambda D, H: L.swiglu_mlp_fwd_nograd_w4(P, P, P, P, P, 1, D, H, 128, 0, 0, N, P, BIG, N)
+    moe = lambda D, H: L.swiglu_mlp_moe_fwd_nograd(P, P, P, P, P, P, P, 64, D, H, 512, 16, 1, 1.0, N, 0,
+                                                   N, P, BIG, N)
+    for M in (1, 8, 32, 64):
+        assert lin(M, 16, (1 << 27) + 8) == UNSUP and lin(M, 16, 1 << 30) == UNSUP
+        assert lin(M, (1 << 31) - 8, 64) == UNSUP
+    assert mlp((1 << 27) + 8, 64) == UNSUP and mlp(64, (1 << 27) + 8) == UNSUP
+    assert moe((1 << 24) + 8, 64) == UNSUP and moe(64, (1 << 24) + 8) == UNSUP
+    assert L.swiglu_mlp_w4_pack(P, P, N, P, 1, 16, (1 << 27) + 8, 128, 0, 0, N) == UNSUP
+    assert L.swiglu_mlp_w4_unpack(P, P, 1, 16, (1 << 27) + 8, 128, 0, 0, 0, N) == UNSUP
+    assert L.swiglu_mlp_w4_quantize(P, P, P, N, 16, (1 << 27) + 8, 128, 0, N) == UNSUP
+    # the largest ones that are not are taken (there is no GPU here: not by these checks)
+    assert L.swiglu_mlp_w4_packed_bytes(1, (1 << 31) - 264, 64, 128, 0, 0) > 0
+    assert L.swiglu_mlp_w4_packed_bytes(1, 16, 1 << 27, 128, 0, 0) > 0
+    assert L.swiglu_mlp_w4_packed_bytes(1, 16, (1 << 27) + 8, 128, 0, 0) == 0
