@@ -273,11 +273,11 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
   // Units [u0, u0 + len) of the rows: bulk copies bring them,
   // and the warps add up each unit's elements per token.
   uint32_t xparity = 0;
-  bool xlive = true;
+  bool xlive = true;  // false, for the whole block, after a wait for the rows ran out: no more copies
   auto stage_rows = [&](int u0, int len) {
     const int xrow = S::xrow(a.phase_units);
     const int inside = min(len * 64, a.K - u0 * 64);  // elements of a row
-    if (warp == 0) {
+    if (warp == 0 && xlive) {
       // what was read or written here before is ordered with the copies
       fence_proxy_async_shared();
       if (lane == 0) mbar_arrive_expect_tx(xbar, a.M * inside * 2);
@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
       *reinterpret_cast<uint4*>(smem + m * xrow + inside * 2 + c * 16) = make_uint4(0, 0, 0, 0);
     }
     if (xlive) xlive = mbar_wait_bounded(xbar, xparity, a.wait_limit_ns, nullptr, a.err);
-    xparity ^= 1u;
-    __syncthreads();
+    xlive = __syncthreads_and(xlive) != 0;
+    if (xlive) xparity ^= 1u;
     using C = WsConst<BF16, ZP>;
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i = warp; i < len * NT; i += WS_WARPS) {
@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
     }
   }
   // after a wait ran out: no copy may land after the block has gone
+  if (!xlive) mbar_wait_bounded(xbar, xparity, a.wait_limit_ns, nullptr, a.err);
   if (!live)
     for (; filled > 0; --filled) {
       mbar_wait_bounded(bar_at, parity, a.wait_limit_ns, nullptr, a.err);

@@ -44,6 +44,17 @@ def test_list_building_synchronises_the_block():
         assert body.rstrip().endswith("__syncthreads();")
 
 
+def test_rows_copies_are_waited_for_before_the_block_goes():
+    # after a wait for the token rows ran out: no further copy on their barrier,
+    # and the one under way is waited for (with the same limit) at the end
+    text = source("w4_stream.cuh")
+    stage = text[text.index("auto stage_rows"):]
+    stage = stage[:stage.index("\n  };")]
+    assert "warp == 0 && xlive" in stage and "__syncthreads_and(xlive)" in stage
+    end = text[text.rindex("cluster_wait();"):]
+    assert re.search(r"if \(!xlive\) mbar_wait_bounded\(xbar", end)
+
+
 @pytest.mark.parametrize("name", KERNELS + ["moe_route.cuh", "fewtok.cuh"])
 def test_no_read_only_loads(name):
     # every launch is a programmatic dependent: what it reads may still be
