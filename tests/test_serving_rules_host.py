@@ -1,13 +1,17 @@
 """Rules of the few-token serving operators that need no GPU to be checked: the
 order of synchronisation in the kernels' sources, launch plans, size limits,
 and the state of the modules."""
+import copy
 import ctypes
+import io
 import os
 import re
 
 import pytest
+import torch
 
 from backward_tcgen05_tma_gb300 import api, build
+from backward_tcgen05_tma_gb300.serving import MoESwiGLU, PackedW4, W4SwiGLUMLP
 
 UNSUP = 3
 P = ctypes.c_void_p(0x10000)  # an aligned fake device address (never dereferenced)
@@ -87,3 +91,84 @@ def test_sizes_beyond_the_indexes_are_refused(L):
     assert L.swiglu_mlp_w4_packed_bytes(1, (1 << 31) - 264, 64, 128, 0, 0) > 0
     assert L.swiglu_mlp_w4_packed_bytes(1, 16, 1 << 27, 128, 0, 0) > 0
     assert L.swiglu_mlp_w4_packed_bytes(1, 16, (1 << 27) + 8, 128, 0, 0) == 0
+
+
+# ---------------------------------------------------------------------------
+# modules: quantised weights are state
+# ---------------------------------------------------------------------------
+def w4(seed, n, k, pair, experts=None, group=64, zeros=True):
+    """Packed weights of random bytes (nothing on the host reads them)."""
+    n_bytes = api.lib().swiglu_mlp_w4_packed_bytes(experts or 1, n, k, group, int(zeros), int(pair))
+    g = torch.Generator().manual_seed(seed)
+    packed = torch.randint(0, 256, (n_bytes,), dtype=torch.uint8, generator=g)
+    return api.W4Weights(packed, n, k, group, zeros, pair, torch.float16, experts)
+
+
+def through_a_file(state):
+    f = io.BytesIO()
+    torch.save(state, f)
+    f.seek(0)
+    return torch.load(f, weights_only=True)
+
+
+def alike(a, b):
+    keys = ("N", "K", "group", "zeros", "gate_up", "experts", "dtype", "shape")
+    return all(getattr(a, k) == getattr(b, k) for k in keys) and torch.equal(a.packed, b.packed)
+
+
+@pytest.fixture
+def quantized(L):
+    """A 4-bit MLP and a mixture with 4-bit experts, as quantising leaves them."""
+    mlp = W4SwiGLUMLP()
+    mlp.gate_up_w4, mlp.down_w4 = PackedW4(w4(1, 32, 72, True)), PackedW4(w4(2, 72, 16, False))
+    mlp.gate_multiplier, mlp.down_multiplier = 0.3, 1.7
+    moe = MoESwiGLU(72, 16, 4, 2, dtype=torch.float16)
+    moe._experts_w4(PackedW4(w4(3, 32, 72, True, 4)), PackedW4(w4(4, 72, 16, False, 4)))
+    return mlp, moe
+
+
+def test_quantized_modules_keep_their_weights_in_their_state(quantized):
+    mlp, moe = quantized
+    new_mlp, new_moe = W4SwiGLUMLP(), MoESwiGLU(72, 16, 4, 2, dtype=torch.float16)
+    new_mlp.load_state_dict(through_a_file(mlp.state_dict()))
+    assert alike(new_mlp.gate_up, mlp.gate_up) and alike(new_mlp.down, mlp.down)
+    assert (new_mlp.gate_multiplier, new_mlp.down_multiplier) == (0.3, 1.7)
+    new_moe.load_state_dict(through_a_file(moe.state_dict()))  # replaces the 16-bit experts
+    assert new_moe.gate_up_weight is None and torch.equal(new_moe.router_weight, moe.router_weight)
+    for name in ("gate_up_w4", "down_w4"):
+        assert alike(getattr(new_moe, name).weights, getattr(moe, name).weights)
+        assert getattr(new_moe, name).packed is not getattr(moe, name).packed
+    # and again, into modules that hold other 4-bit weights, as parts of a model
+    other = copy.deepcopy(moe)
+    other.gate_up_w4 = PackedW4(w4(5, 32, 72, True, 4, group=32, zeros=False))
+    model = torch.nn.Sequential(other, W4SwiGLUMLP())
+    model.load_state_dict(through_a_file(torch.nn.Sequential(moe, mlp).state_dict()))
+    assert alike(other.gate_up_w4.weights, moe.gate_up_w4.weights) and alike(model[1].down, mlp.down)
+
+
+def test_quantized_modules_refuse_a_state_without_the_weights(quantized):
+    mlp, moe = quantized
+    with pytest.raises(RuntimeError, match="gate_up_w4.packed"):
+        moe.load_state_dict(MoESwiGLU(72, 16, 4, 2, dtype=torch.float16).state_dict())
+    with pytest.raises(RuntimeError, match="router_weight"):
+        MoESwiGLU(72, 16, 4, 2, dtype=torch.float16).load_state_dict(
+            {k: v for k, v in moe.state_dict().items() if k != "router_weight"})
+    with pytest.raises(RuntimeError, match="no 4-bit weights"):
+        W4SwiGLUMLP().gate_up
+
+
+def test_quantized_modules_move_with_their_weights(quantized):
+    for m in quantized:
+        moved = copy.deepcopy(m).to("meta")
+        assert moved.gate_up_w4.packed.is_meta and moved.down_w4.weights.device.type == "meta"
+        assert moved.gate_up_w4.weights.shape == m.gate_up_w4.weights.shape
+        cast = copy.deepcopy(m).to(torch.bfloat16)  # the bytes are no numbers of the module's type
+        assert alike(cast.gate_up_w4.weights, m.gate_up_w4.weights)
+
+
+def test_modules_before_quantizing_have_their_old_state(L):
+    m = MoESwiGLU(64, 32, 4, 2, dtype=torch.float16)
+    assert set(m.state_dict()) == {"router_weight", "gate_up_weight", "down_weight"}
+    n = MoESwiGLU(64, 32, 4, 2, dtype=torch.float16)
+    n.load_state_dict(m.state_dict())
+    assert torch.equal(n.down_weight, m.down_weight)
