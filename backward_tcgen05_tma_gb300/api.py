@@ -443,8 +443,9 @@ def swiglu_mlp_bwd(dY, X, Wgu, Wd, saved, out: dict | None = None, ws=None,
 
 
 # The few-token calls below last a few microseconds, so their Python part is
-# kept short: plain integers for pointers and streams, no temporaries.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# kept short: plain integers for pointers and streams, no temporaries.  (A torch
+# without CUDA lacks this function, and has no tensors that would need it.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _serving_checks(X, *others) -> int:

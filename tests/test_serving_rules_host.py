@@ -6,6 +6,8 @@ import ctypes
 import io
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -172,3 +174,16 @@ def test_modules_before_quantizing_have_their_old_state(L):
     n = MoESwiGLU(64, 32, 4, 2, dtype=torch.float16)
     n.load_state_dict(m.state_dict())
     assert torch.equal(n.down_weight, m.down_weight)
+
+
+def test_the_binding_imports_on_a_torch_without_cuda():
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'):\n"
+            "    del torch._C._cuda_getCurrentRawStream\n"
+            "from backward_tcgen05_tma_gb300 import api, serving\n"
+            "try:\n"
+            "    api.swiglu_mlp_w4_quantize(torch.zeros(16, 64, dtype=torch.bfloat16))\n"
+            "except ValueError:\n"
+            "    print('refused')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=build.ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
