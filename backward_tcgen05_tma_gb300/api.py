@@ -520,7 +520,9 @@ def swiglu_mlp_w4_pack(codes, scales, zeros=None, group: int = 128,
                        gate_up: bool = False) -> W4Weights:
     """The packed copy of 4-bit weights (codes uint8 [.., N, K/2], scales
     [.., N, ceil(K/group)] in the activations' type, optional zero points) that
-    the few-token products stream."""
+    the few-token products stream.  Zero points are whole numbers of 0..15, and
+    others are refused (one wait for the device where there are zero points);
+    formats that hold a zero point of 16 have no such copy."""
     st = _serving_checks(codes, scales, *(() if zeros is None else (zeros,)))
     if codes.dim() not in (2, 3) or codes.dtype != torch.uint8:
         raise ValueError("expected uint8 codes [N, K/2] or [E, N, K/2]")
@@ -531,6 +533,8 @@ def swiglu_mlp_w4_pack(codes, scales, zeros=None, group: int = 128,
         raise ValueError("expected scales of shape %s, got %s" % (want, tuple(scales.shape)))
     if zeros is not None and (tuple(zeros.shape) != want or zeros.dtype != torch.uint8):
         raise ValueError("expected uint8 zero points of shape %s" % (want,))
+    if zeros is not None and zeros.numel() and int(zeros.max()) > 15:
+        raise ValueError("zero points must be 0..15, got %d" % int(zeros.max()))
     zp = zeros is not None
     n = int(lib().swiglu_mlp_w4_packed_bytes(E, N, K, group, int(zp), int(gate_up)))
     packed = torch.empty(n, dtype=torch.uint8, device=codes.device)

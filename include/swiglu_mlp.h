@@ -347,7 +347,10 @@ swiglu_status swiglu_mlp_w4_quantize(const void* W, void* codes, void* scales, v
 
 /* Writes the packed copy of E matrices (codes [E, N, K/2], scales, zeros or
  * NULL) that the calls below stream.  gate_up: the rows are [Wg; Wu] pairs (N
- * = 2H, H a multiple of 8), laid out so that a hidden unit's two rows meet. */
+ * = 2H, H a multiple of 8), laid out so that a hidden unit's two rows meet.
+ * The call is asynchronous and does not look at the values: of a zero point
+ * only the low four bits are kept, so one above 15 has to be refused by the
+ * caller (the Python binding does). */
 swiglu_status swiglu_mlp_w4_pack(const void* codes, const void* scales, const void* zeros,
                                  void* packed, int64_t E, int64_t N, int64_t K, int group,
                                  int gate_up, swiglu_dtype dtype, void* stream);

@@ -42,3 +42,17 @@ def test_quantized_modules_through_a_file():
         with pytest.raises(ValueError):
             new(x)
         assert torch.equal(new.cuda()(x), y)
+
+
+@pytest.mark.parametrize("lead", [(), (3,)])
+def test_zero_points_above_15_are_refused(lead):
+    g = gen(2)
+    c = torch.randint(0, 256, (*lead, 16, 64), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.ones(*lead, 16, 2, device="cuda", dtype=torch.float16)
+    z = torch.randint(0, 16, (*lead, 16, 2), generator=g, device="cuda", dtype=torch.uint8)
+    assert api.swiglu_mlp_w4_pack(c, s, z, 64).zeros
+    z.view(-1)[-1] = 16  # some formats store a zero point less one and add it on loading
+    with pytest.raises(ValueError, match="0..15"):
+        api.swiglu_mlp_w4_pack(c, s, z, 64)
+    with pytest.raises(ValueError, match="0..15"):
+        W4SwiGLUMLP.from_codes((c, s, z), (c, s, z), 64)
