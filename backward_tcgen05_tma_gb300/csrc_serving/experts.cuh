@@ -13,10 +13,6 @@
 //     weights.  Token rows are read by the lanes that need them, a chunk ahead
 //     in registers, through L1 (gate/up: all experts read rows of the same few
 //     tokens) or L2 (down: the hidden values of the expert's own assignments).
-//   * 4-bit: the sums that cancel the magic numbers are not prepared as in
-//     w4_stream.cuh, where all rows share them; an accumulator starts with the
-//     product of the same token elements and a constant row, -(m + z) in 16
-//     bits, which doubles the tensor core's work, idle otherwise.
 //
 // Work: gate/up gives a block a contiguous run of (expert, tile) items; down
 // gives it the tiles of its output rows and goes through all experts.  Either
@@ -70,17 +66,11 @@ __global__ void __launch_bounds__(WxShape<W4, NT, G32, ZP>::WARPS * 32, 1)
                 HALF = S::HALF, WX_WARPS = S::WARPS, WX_THREADS = WX_WARPS * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[WX_WARPS * WX_MAX_STAGES];
-  __shared__ uint4 constants[3];  // 0; minus the magic number plus 8, for each form of code
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t bar0 = smem_u32(bars) + warp * WX_MAX_STAGES * 8;
   const bool combine = a.mode == FT_COMBINE;
 
   ft_begin(a);
-  if (threadIdx.x < 12) {
-    const uint32_t c1 = P::MAGIC | 0x80088008u, c2 = BF16 ? c1 : P::MAGIC | 0x80808080u;
-    reinterpret_cast<uint32_t*>(constants)[threadIdx.x] =
-        threadIdx.x < 4 ? 0 : threadIdx.x < 8 ? c1 : c2;
-  }
   if (lane == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(bar0 + 8 * i, 1);
     fence_mbar_init();
@@ -274,64 +264,38 @@ __global__ void __launch_bounds__(WxShape<W4, NT, G32, ZP>::WARPS * 32, 1)
       acc[nt] = mma_ws<BF16>(p, g1.z, h1.z, g1.w, h1.w, x1.z, x1.w);
     }
   };
-  // Operands that never change, four registers each as the tensor core takes
-  // them, read from shared memory so that the compiler keeps them: constants
-  // that it can see it would move into place again before every product.
-  constexpr uint32_t M = P::MAGIC, LO = 0x000f000fu, HI = 0x00f000f0u, NEG = M | 0x80008000u;
-  const uint32_t cbase = smem_u32(constants);
-  const uint4 z4 = lds128_at<0>(cbase), k1 = lds128_at<16>(cbase), k2 = lds128_at<32>(cbase);
-  const float4 none = make_float4(__uint_as_float(z4.x), __uint_as_float(z4.y),
-                                  __uint_as_float(z4.z), __uint_as_float(z4.w));
   auto unit4 = [&](auto q, const Rows& x, uint32_t rc, uint32_t rs) {
     constexpr int Q = decltype(q)::value % HALF, R = decltype(q)::value * RECORD;
     constexpr int Z = R + GROUPS * 32;
     const uint4 cw = lds128_at<R>(rc);
     const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};  // rows g, g + 8 of k 0..31, then of 32..63
     const uint32_t sc0 = lds32_at<R>(rs), sc1 = G32 ? lds32_at<R + 32>(rs) : sc0;
-    const uint32_t zp0 = ZP ? lds16_at<Z>(rs - g * 2) : 0;
+    const uint32_t zp0 = ZP ? lds16_at<Z>(rs - g * 2) : 0x808u;
     const uint32_t zp1 = ZP && G32 ? lds16_at<Z + 16>(rs - g * 2) : zp0;
-    float4 p[NT], r[NT];
+    float4 p[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) p[nt] = r[nt] = none;
+    for (int nt = 0; nt < NT; ++nt) p[nt] = zero;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
-      const uint32_t f0 = and_or<LO>(lo, M), f1 = and_or<LO>(hi, M);
-      const uint32_t f2 = and_or<LO>(lo >> 8, M), f3 = and_or<LO>(hi >> 8, M);
-      const uint32_t s0 = BF16 ? and_or<LO>(lo >> 4, M) : and_or<HI>(lo, M);
-      const uint32_t s1 = BF16 ? and_or<LO>(hi >> 4, M) : and_or<HI>(hi, M);
-      const uint32_t s2 = BF16 ? and_or<LO>(lo >> 12, M) : and_or<HI>(lo >> 8, M);
-      const uint32_t s3 = BF16 ? and_or<LO>(hi >> 12, M) : and_or<HI>(hi >> 8, M);
-      // -(m + z) of rows g and g + 8; fp16: the second form's codes are 16 times larger
-      const uint32_t zp = h ? zp1 : zp0;
-      const uint32_t zl = (zp & 0xffu) * 0x10001u, zh = (zp >> 8) * 0x10001u;
+      const uint32_t lo = w[2 * h], hi = w[2 * h + 1], zp = h ? zp1 : zp0;
+      const W4Off<BF16> zl(zp & 0xffu), zh(zp >> 8);
+      const uint32_t f0 = w4_first<BF16>(lo, zl), f1 = w4_first<BF16>(hi, zh);
+      const uint32_t f2 = w4_first<BF16>(lo >> 8, zl), f3 = w4_first<BF16>(hi >> 8, zh);
+      const uint32_t s0 = w4_second<BF16>(lo, zl), s1 = w4_second<BF16>(hi, zh);
+      const uint32_t s2 = w4_second<BF16>(lo >> 8, zl), s3 = w4_second<BF16>(hi >> 8, zh);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 v = x[nt][Q][h];
-        float4& u = BF16 ? p[nt] : r[nt];  // fp16: the second form's sums are 16 times too large
-        if (ZP) {
-          p[nt] = mma_ws<BF16>(p[nt], NEG | zl, NEG | zh, NEG | zl, NEG | zh, v.x, v.y);
-          const uint32_t yl = BF16 ? zl : zl << 4, yh = BF16 ? zh : zh << 4;
-          u = mma_ws<BF16>(u, NEG | yl, NEG | yh, NEG | yl, NEG | yh, v.z, v.w);
-        } else {
-          p[nt] = mma_ws<BF16>(p[nt], k1.x, k1.y, k1.z, k1.w, v.x, v.y);
-          u = mma_ws<BF16>(u, k2.x, k2.y, k2.z, k2.w, v.z, v.w);
-        }
         p[nt] = mma_ws<BF16>(p[nt], f0, f1, f2, f3, v.x, v.y);
-        u = mma_ws<BF16>(u, s0, s1, s2, s3, v.z, v.w);
+        p[nt] = mma_ws<BF16>(p[nt], s0, s1, s2, s3, v.z, v.w);
         if (G32 || h) {
           const uint32_t sc = h ? sc1 : sc0;
           const float sg = P::lo(sc), sh = P::hi(sc);
-          if (!BF16) {
-            p[nt] = make_float4(fmaf(0.0625f, u.x, p[nt].x), fmaf(0.0625f, u.y, p[nt].y),
-                                fmaf(0.0625f, u.z, p[nt].z), fmaf(0.0625f, u.w, p[nt].w));
-            u = none;
-          }
           acc[nt].x = fmaf(sg, p[nt].x, acc[nt].x);
           acc[nt].y = fmaf(sg, p[nt].y, acc[nt].y);
           acc[nt].z = fmaf(sh, p[nt].z, acc[nt].z);
           acc[nt].w = fmaf(sh, p[nt].w, acc[nt].w);
-          p[nt] = none;
+          p[nt] = zero;
         }
       }
     }

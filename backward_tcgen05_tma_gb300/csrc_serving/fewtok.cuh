@@ -88,6 +88,36 @@ __device__ __forceinline__ uint32_t ft_sub2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Codes to numbers.  OR-ed into the mantissa of 128 (bf16) or 1024 (fp16) a
+// code is a 16-bit number, 128 + q or 1024 + q; the fp16 codes in bits 4..7 can
+// stay there, as 1024 + 16 q.  Taking 128 + z or 1024 + z off (the second fp16
+// form: multiplied by 1/16 it is 64 + q, and 64 + z goes off in the same
+// instruction) leaves the whole number q - z, exactly: every operand and result
+// is a whole number that the type holds.
+template <bool BF16>
+struct W4Off {
+  uint32_t a, b;  // 128 + z or 1024 + z, for both halves; fp16: -(64 + z)
+  __device__ __forceinline__ explicit W4Off(uint32_t z = 8) {
+    a = Ft16<BF16>::MAGIC | z * 0x10001u;
+    b = 0xd400d400u | z * 0x100010u;
+  }
+};
+// two elements of each form: the codes in bits 0..3 of v's halves, and those in
+// bits 4..7
+template <bool BF16>
+__device__ __forceinline__ uint32_t w4_first(uint32_t v, const W4Off<BF16>& z) {
+  return ft_sub2<BF16>(and_or<0x000f000fu>(v, Ft16<BF16>::MAGIC), z.a);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t w4_second(uint32_t v, const W4Off<BF16>& z) {
+  if (BF16) return w4_first<BF16>(v >> 4, z);
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;"
+      : "=r"(r)
+      : "r"(and_or<0x00f000f0u>(v, Ft16<BF16>::MAGIC)), "r"(0x2c002c00u), "r"(z.b));
+  return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {

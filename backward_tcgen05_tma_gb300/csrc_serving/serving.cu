@@ -206,8 +206,7 @@ cudaError_t launch_ws(host::ServingKernel id, WsArgs a, int tiles16, cudaStream_
     a.phase_units = ((nk + split - 1) / split + phases - 1) / phases;
     if (phases > 1) a.phase_units = (a.phase_units + S::UNITS - 1) / S::UNITS * S::UNITS;
     if (a.phase_units > WS_SMEM / 128) return false;  // no row of them fits, nor its offsets 32 bits
-    a.sum_off = up(rows * S::xrow(a.phase_units));
-    a.part_off = up(a.sum_off + a.phase_units * S::SUMS);
+    a.part_off = up(rows * S::xrow(a.phase_units));
     a.tile_off = up(a.part_off + (a.run + S::WARPS - 1) * S::PART);
     a.phased = phases > 1;
     a.ring_off = up(a.tile_off + (a.phased ? a.run * S::PART : 0));

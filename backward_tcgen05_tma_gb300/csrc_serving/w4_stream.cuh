@@ -5,23 +5,17 @@
 // What bounds it: half a byte per weight, so at the HBM rate an SM meets 46
 // weights per cycle, and unpacking them takes most of its issue slots.  The
 // design spends as few instructions per weight as it can:
-//   * A code becomes a 16-bit number by OR-ing it into the mantissa of 128
-//     (bf16) or 1024 (fp16).  In fp16 bits 4..7 can stay where they are, as
-//     1024 + 16 q: one shift serves two nibbles, and the products of the two
-//     forms are added up apart, the second sum scaled by 1/16.
-//   * Nothing is subtracted from the codes.  The accumulator of a unit (64 k,
-//     or with groups of 32 half of one) starts at
-//         -(m1 + z) S1 - (m2 + z) S2
-//     with S1, S2 the sums of the token elements that meet the two forms (m1 =
-//     m2 = 128 in bf16; 1024 and 64 in fp16), which are computed once per token
-//     (on the tensor core, as products with constant rows) and shared by all
-//     weight rows.  What the products then add leaves sum (q - z) x up to fp32
-//     rounding, 2^-24 of some 30 (bf16) or 200 (fp16) times the mean term: far
-//     below the output's own rounding.
+//   * Each pair of codes becomes a pair of 16-bit whole numbers q - z in two
+//     instructions (W4Off in fewtok.cuh): OR-ed into a mantissa, and the
+//     constant taken off; in fp16 one shift serves two nibbles.  The tensor core
+//     then adds up terms of the formula itself, so a sum is as good as a plain
+//     fp32 one whatever the elements.  (Leaving 128 + q or 1024 + q in the
+//     products and taking the rest off each sum, from sums of the token's
+//     elements, was no faster and lost ten roundings of an fp16 output where an
+//     element of 30000 met weights of 0.)
 //   * A warp's weights are runs of unit records (codes, then scales, then zero
 //     points) that bulk copies bring into a ring of its own, 8 records a copy.
-// Each group's sum is scaled in fp32; no weight is rounded.  (A token with an
-// infinity gives NaN where exact arithmetic might give an infinity.)
+// Each group's sum is scaled in fp32; no weight is rounded.
 //
 // Work: a block takes a contiguous run of tiles of 16 RT weight rows (gate/up:
 // each 16 are 8 rows of Wg and the 8 rows of Wu of the same hidden units), cuts
@@ -72,7 +66,7 @@ struct WsArgs {
   // plan: k-units of a phase, tiles of a run, ring stages, shared-memory offsets
   int phase_units, run, stages;
   int phased;        // the contraction (or a block's part of it) takes several phases
-  int sum_off, part_off, tile_off, ring_off;
+  int part_off, tile_off, ring_off;
   uint64_t wait_limit_ns;
   int* err;
 #ifdef SWIGLU_DEBUG
@@ -90,7 +84,6 @@ struct WsShape {
   static constexpr int RECORD = 512 + GROUPS * (ZP ? 48 : 32);     // bytes of a unit
   static constexpr int PIECE = UNITS * RECORD;                     // one 16-row tile's chunk
   static constexpr int STAGE = RT * PIECE;
-  static constexpr int SUMS = GROUPS * NT * 64;                    // bytes of a unit's sums
   static constexpr int PART = RT * NT * 512;                       // a partial tile
   static constexpr int RUN = NT == 1 ? 24 : NT == 2 ? 12 : 10;     // tiles of a run, at most
   static __host__ __device__ constexpr int xrow(int units) { return units * 128 + 64; }
@@ -140,17 +133,6 @@ __device__ __forceinline__ float4 mma_ws(float4 c, uint32_t a0, uint32_t a1, uin
           "f"(c.w));
   return d;
 }
-
-// 16-bit pairs of the constants that the token sums are products with: the
-// magic numbers of the first and the second form (negative; with -8 where there
-// are no zero points), and 1.
-template <bool BF16, bool ZP>
-struct WsConst {
-  static constexpr uint32_t C1 = BF16 ? (ZP ? 0xc300c300u : 0xc308c308u)   // -128, -136
-                                      : (ZP ? 0xe400e400u : 0xe408e408u);  // -1024, -1032
-  static constexpr uint32_t C2 = BF16 ? C1 : (ZP ? 0xd400d400u : 0xd480d480u);  // -64, -72
-  static constexpr uint32_t ONE = BF16 ? 0x3f803f80u : 0x3c003c00u;
-};
 
 // One warp's place in the block's work: run of tiles, phase of the
 // contraction, and the chunks [v, v_end) of the run and phase laid end to end;
@@ -270,8 +252,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
   if (!a.first) pdl_wait();  // before the first read of a token row
 
   // ---------------------------------------------------------------- token rows
-  // Units [u0, u0 + len) of the rows: bulk copies bring them,
-  // and the warps add up each unit's elements per token.
+  // Units [u0, u0 + len) of the rows: bulk copies bring them.
   uint32_t xparity = 0;
   bool xlive = true;  // false, for the whole block, after a wait for the rows ran out: no more copies
   auto stage_rows = [&](int u0, int len) {
@@ -297,28 +278,6 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
     if (xlive) xlive = mbar_wait_bounded(xbar, xparity, a.wait_limit_ns, nullptr, a.err);
     xlive = __syncthreads_and(xlive) != 0;
     if (xlive) xparity ^= 1u;
-    using C = WsConst<BF16, ZP>;
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = warp; i < len * NT; i += WS_WARPS) {
-      const int u = i / NT, nt = i - u * NT;
-      const uint32_t p = sbase + min(nt * 8 + g, a.M - 1) * xrow + u * 128 + t * 16;
-      const uint4 x0 = lds128_at<0>(p), x1 = lds128_at<64>(p);
-      auto half = [&](float4 c, uint4 x, uint32_t k1, uint32_t k2) {
-        c = mma_ws<BF16>(c, k1, k1, k1, k1, x.x, x.y);
-        return mma_ws<BF16>(c, k2, k2, k2, k2, x.z, x.w);
-      };
-      float* o = reinterpret_cast<float*>(smem + a.sum_off + u * S::SUMS + nt * 64 + t * 16);
-      float4 c = half(zero, x0, C::C1, C::C2), z = ZP ? half(zero, x0, C::ONE, C::ONE) : c;
-      if (G32) {
-        if (g == 0) *reinterpret_cast<float4*>(o) = make_float4(c.x, c.y, z.x, z.y);
-        o += NT * 16;
-        c = z = zero;
-      }
-      c = half(c, x1, C::C1, C::C2);
-      z = ZP ? half(z, x1, C::ONE, C::ONE) : c;
-      if (g == 0) *reinterpret_cast<float4*>(o) = make_float4(c.x, c.y, z.x, z.y);
-    }
-    __syncthreads();
   };
 
   // ---------------------------------------------------------------- products
@@ -341,52 +300,37 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
     clear();
   };
   // Unit Q of a chunk: base addresses of the chunk's records (rc, the lane's
-  // codes; rs, its scales), of its token rows and of its sums.
-  auto multiply = [&](auto q, uint32_t rc, uint32_t rs, const uint32_t (&xu)[NT], uint32_t su) {
+  // codes; rs, its scales) and of its token rows.
+  auto multiply = [&](auto q, uint32_t rc, uint32_t rs, const uint32_t (&xu)[NT]) {
     constexpr int Q = decltype(q)::value, R = Q * S::RECORD;
-    uint4 x0[NT], x1[NT], s0[NT], s1[NT];
+    uint4 x0[NT], x1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       x0[nt] = lds128_at<Q * 128>(xu[nt]);
       x1[nt] = lds128_at<Q * 128 + 64>(xu[nt]);
-      s0[nt] = lds128_at<Q * S::SUMS>(su + nt * 64);
-      if (G32) s1[nt] = lds128_at<Q * S::SUMS + NT * 64>(su + nt * 64);
     }
     auto tile = [&](auto which) {
       constexpr int I = decltype(which)::value, RI = R + I * S::PIECE, Z = RI + S::GROUPS * 32;
       const uint4 cw = lds128_at<RI>(rc);
       const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};  // rows g, g + 8 of k 0..31, then of 32..63
       const uint32_t sc0 = lds32_at<RI>(rs), sc1 = G32 ? lds32_at<RI + 32>(rs) : sc0;
-      uint32_t z0 = 0, z1 = 0;
-      if (ZP) {
-        z0 = lds16_at<Z>(rs - g * 2);
-        z1 = G32 ? lds16_at<Z + 16>(rs - g * 2) : z0;
-      }
+      const uint32_t z0 = ZP ? lds16_at<Z>(rs - g * 2) : 0x808u;
+      const uint32_t z1 = ZP && G32 ? lds16_at<Z + 16>(rs - g * 2) : z0;
       // A[h][f]: half h, elements k + {0..3} (f = 0) and k + {4..7}
       uint32_t A[2][2][4];
-      constexpr uint32_t M = P::MAGIC, LO = 0x000f000fu, HI = 0x00f000f0u;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t v = w[2 * h + r];
-          A[h][0][r] = and_or<LO>(v, M);
-          A[h][0][2 + r] = and_or<LO>(v >> 8, M);
-          A[h][1][r] = BF16 ? and_or<LO>(v >> 4, M) : and_or<HI>(v, M);
-          A[h][1][2 + r] = BF16 ? and_or<LO>(v >> 12, M) : and_or<HI>(v >> 8, M);
+          const uint32_t v = w[2 * h + r], z = h ? z1 : z0;
+          const W4Off<BF16> off(r ? z >> 8 : z & 0xffu);
+          A[h][0][r] = w4_first<BF16>(v, off);
+          A[h][0][2 + r] = w4_first<BF16>(v >> 8, off);
+          A[h][1][r] = w4_second<BF16>(v, off);
+          A[h][1][2 + r] = w4_second<BF16>(v >> 8, off);
         }
-      auto sum_of = [&](uint4 v, uint32_t z) {  // what a unit's (half's) products start from
-        float4 c = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                               __uint_as_float(v.w));
-        if (ZP) {
-          const float zg = -(float)(z & 0xffu), zh = -(float)(z >> 8);
-          c = make_float4(fmaf(zg, c.z, c.x), fmaf(zg, c.w, c.y), fmaf(zh, c.z, c.x),
-                          fmaf(zh, c.w, c.y));
-        }
-        return c;
-      };
-      auto scale_in = [&](float4& o, float4 p, uint32_t sc, float by) {
-        const float sg = P::lo(sc) * by, sh = P::hi(sc) * by;
+      auto scale_in = [&](float4& o, float4 p, uint32_t sc) {
+        const float sg = P::lo(sc), sh = P::hi(sc);
         o.x = fmaf(sg, p.x, o.x);
         o.y = fmaf(sg, p.y, o.y);
         o.z = fmaf(sh, p.z, o.z);
@@ -395,34 +339,16 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
       const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        auto first = [&](float4 c, int h) {
-          return mma_ws<BF16>(c, A[h][0][0], A[h][0][1], A[h][0][2], A[h][0][3],
-                              h ? x1[nt].x : x0[nt].x, h ? x1[nt].y : x0[nt].y);
+        auto half = [&](float4 c, int h, uint4 x) {
+          c = mma_ws<BF16>(c, A[h][0][0], A[h][0][1], A[h][0][2], A[h][0][3], x.x, x.y);
+          return mma_ws<BF16>(c, A[h][1][0], A[h][1][1], A[h][1][2], A[h][1][3], x.z, x.w);
         };
-        auto second = [&](float4 c, int h) {
-          return mma_ws<BF16>(c, A[h][1][0], A[h][1][1], A[h][1][2], A[h][1][3],
-                              h ? x1[nt].z : x0[nt].z, h ? x1[nt].w : x0[nt].w);
-        };
-        // fp16: the second form's sums are 16 times too large
-        float4& o = acc[I][nt];
-        float4 p = first(sum_of(s0[nt], z0), 0), r = zero;
-        if (BF16)
-          p = second(p, 0);
-        else
-          r = second(r, 0);
+        float4 p = half(zero, 0, x0[nt]);
         if (G32) {
-          scale_in(o, p, sc0, 1.0f);
-          if (!BF16) scale_in(o, r, sc0, 0.0625f);
-          p = sum_of(s1[nt], z1);
-          r = zero;
+          scale_in(acc[I][nt], p, sc0);
+          p = zero;
         }
-        p = first(p, 1);
-        if (BF16)
-          p = second(p, 1);
-        else
-          r = second(r, 1);
-        scale_in(o, p, sc1, 1.0f);
-        if (!BF16) scale_in(o, r, sc1, 0.0625f);
+        scale_in(acc[I][nt], half(p, 1, x1[nt]), sc1);
       }
     };
     tile(WsInt<0>{});
@@ -477,7 +403,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
       const int v0 = total * warp / WS_WARPS, v1 = total * (warp + 1) / WS_WARPS;
       int j = v0 / per, c = v0 - j * per;
       const int tail = len - (per - 1) * S::UNITS;  // units of a tile's last chunk
-      uint32_t xu[NT], su = sbase + a.sum_off + t * 16 + c * (S::UNITS * S::SUMS);
+      uint32_t xu[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt] + c * (S::UNITS * 128);
       for (int v = v0; v < v1; ++v) {
@@ -490,23 +416,21 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
           int left = last ? tail : S::UNITS;
           constexpr int STEP = 4 / RT;  // independent chains in flight
           for (; left >= STEP; left -= STEP) {
-            multiply(WsInt<0>{}, rc, rs, xu, su);
-            multiply(WsInt<1>{}, rc, rs, xu, su);
+            multiply(WsInt<0>{}, rc, rs, xu);
+            multiply(WsInt<1>{}, rc, rs, xu);
             if constexpr (STEP == 4) {
-              multiply(WsInt<2>{}, rc, rs, xu, su);
-              multiply(WsInt<3>{}, rc, rs, xu, su);
+              multiply(WsInt<2>{}, rc, rs, xu);
+              multiply(WsInt<3>{}, rc, rs, xu);
             }
             rc += STEP * S::RECORD;
             rs += STEP * S::RECORD;
-            su += STEP * S::SUMS;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) xu[nt] += STEP * 128;
           }
           for (; left > 0; --left) {
-            multiply(WsInt<0>{}, rc, rs, xu, su);
+            multiply(WsInt<0>{}, rc, rs, xu);
             rc += S::RECORD;
             rs += S::RECORD;
-            su += S::SUMS;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) xu[nt] += 128;
           }
@@ -524,7 +448,6 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
         if (last) {
           c = 0;
           flush(j++);
-          su = sbase + a.sum_off + t * 16;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) xu[nt] = xa[nt];
         }

@@ -323,8 +323,10 @@ swiglu_status swiglu_mlp_bwd_ex(const void* dY, const void* X, const void* Wgu, 
  * section in turn, whatever their sizes; after calls of other sections its
  * first 4352 bytes (header and counters) have to be zero again.
  *
- * A NaN or an infinity in a token's row makes that token's outputs NaN (where
- * exact arithmetic would leave an infinity, NaN too) and no other token's.
+ * A NaN or an infinity in a token's row gives that token's outputs what the
+ * formula gives (an infinity times a weight of 0 is NaN, and so are gate values
+ * of minus infinity; other products with it are infinities), and touches no
+ * other token's.
  * Gate and up values meet in fp32; A is rounded once to 16 bits and Y is the
  * product of the rounded A, as in the calls above. */
 
