@@ -34,8 +34,6 @@
 
 namespace swiglu {
 
-constexpr int WX_MAX_STAGES = 8;
-
 template <bool W4, int NT, bool G32, bool ZP>
 struct WxShape {
   // 4-bit: 12 warps of 168 registers (16 of 128 spill); 16-bit weights need more

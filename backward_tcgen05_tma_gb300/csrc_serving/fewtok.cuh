@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "../csrc/sm103_ptx.cuh"
+#include "experts_plan.h"
 
 namespace swiglu {
 
@@ -225,14 +226,6 @@ struct FtLists {
   uint16_t* at;              // [M * topk] assignment, by position
   int* n;                    // entries
 };
-__host__ __device__ inline int ft_max_entries(int M, int topk, int E, int per) {
-  const int a = M * topk, b = (E < a ? E : a) + a / per;
-  return a < b ? a : b;
-}
-__host__ __device__ inline int ft_lists_bytes(int M, int topk, int E, int per) {
-  const int b = 16 + E * 12 + ft_max_entries(M, topk, E, per) * 8 + M * topk * 14;
-  return (b + 127) & ~127;
-}
 __device__ __forceinline__ FtLists ft_lists(uint8_t* p, const FtArgs& a, int per) {
   FtLists l;
   l.n = reinterpret_cast<int*>(p);

@@ -10,6 +10,7 @@
 
 #include "../../include/swiglu_mlp.h"
 #include "experts.cuh"
+#include "experts_plan.h"
 #include "fewtok.cuh"
 #include "host_shared.h"
 #include "moe_route.cuh"
@@ -89,15 +90,13 @@ cudaError_t allow_smem(int bytes) {
 }
 
 constexpr int WS_SMEM = 224 * 1024;
-constexpr int WX_SMEM = 200 * 1024;  // the rest of an SM's 256 KB caches the token rows
 
 template <bool BF16, bool W4, int NT, bool G32, bool ZP>
 cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, FtArgs a,
                            cudaStream_t st) {
   using S = WxShape<W4, NT, G32, ZP>;
-  constexpr int ring = S::WARPS * S::STAGE;
   constexpr auto kern = experts_kernel<BF16, W4, NT, G32, ZP>;
-  cudaError_t e = allow_smem<kern>(WX_SMEM + 1024);  // the ring's alignment
+  cudaError_t e = allow_smem<kern>(WX_SMEM_MOST);
   if (e != cudaSuccess) return e;
   const bool combine = a.mode == FT_COMBINE;
   const int nsm = host::sms() > 0 ? host::sms() : 1;
@@ -105,20 +104,20 @@ cudaError_t launch_experts(host::ServingKernel id, const CUtensorMap& tm, FtArgs
       combine ? a.tiles : (int64_t)a.tiles * ft_max_entries(a.M, a.topk, a.E, S::TOKENS);
   const int grid = (int)(items < nsm ? items : nsm);
   const int64_t most = (items + grid - 1) / grid;  // items of a block
-  a.run = (int)(most < 64 / NT ? most : 64 / NT);
-  a.list_off = 0;
-  a.red_off = ft_lists_bytes(a.M, a.topk, a.E, S::TOKENS);
-  a.ring_off = a.red_off + (combine ? S::WARPS * a.M * 64 : (a.run + S::WARPS - 1) * NT * 512);
-  a.stages = (WX_SMEM - a.ring_off) / ring;
-  if (a.stages > WX_MAX_STAGES) a.stages = WX_MAX_STAGES;
-  if (a.stages < 1) return cudaErrorInvalidConfiguration;
+  const WxPlan plan = wx_plan(S::WARPS, NT, S::STAGE, combine, a.M, a.topk, a.E, most);
+  if (plan.stages < 2) return cudaErrorInvalidConfiguration;
+  a.run = plan.run;
+  a.list_off = plan.list_off;
+  a.red_off = plan.red_off;
+  a.ring_off = plan.ring_off;
+  a.stages = plan.stages;
   a.wait_limit_ns = host::wait_limit_ns();
   a.inject = host::take_stall() ? 1 : 0;
   host::Prof prof(id, st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(S::WARPS * 32);
-  cfg.dynamicSmemBytes = a.ring_off + a.stages * ring + 1024;
+  cfg.dynamicSmemBytes = plan.bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

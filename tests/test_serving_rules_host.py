@@ -187,3 +187,42 @@ def test_the_binding_imports_on_a_torch_without_cuda():
             "    print('refused')\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=build.ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
+
+
+PLANS = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "experts_plan.h"
+int main() {
+  using namespace swiglu;
+  // warps and stage bytes of the experts kernels: 16-bit (2 units of 2 KB), 4-bit (8 or 4 records)
+  struct { int warps, nt, stage; } f[] = {{16, 1, 4096}, {16, 2, 4096}, {12, 1, 8 * 608}, {12, 2, 4 * 608},
+                                          {12, 1, 8 * 544}, {12, 2, 4 * 544}};
+  for (auto k : f)
+    for (int combine = 0; combine < 2; ++combine)
+      for (int M = 1; M <= 64; ++M)
+        for (int E : {1, 2, 8, 27, 64, 128, 130, 512})
+          for (int topk = 1; topk <= 16 && topk <= E; ++topk)
+            for (int most : {1, 7, 1000000}) {
+              const WxPlan p = wx_plan(k.warps, k.nt, k.stage, combine, M, topk, E, most);
+              const int used = p.ring_off + 1024 + p.stages * k.warps * k.stage;
+              if (p.stages < 2 || p.stages > WX_MAX_STAGES || used > p.bytes || p.bytes > WX_SMEM_MOST ||
+                  p.ring_off % 16 != 0 || (p.stages > 2 && p.bytes > WX_SMEM + 1024)) {
+                printf("warps %d nt %d combine %d M %d E %d topk %d: %d stages, %d bytes\n", k.warps, k.nt,
+                       combine, M, E, topk, p.stages, p.bytes);
+                return 1;
+              }
+            }
+  return 0;
+}
+"""
+
+
+def test_experts_rings_fetch_ahead_at_every_size(tmp_path):
+    # a ring of one stage fetches nothing while its stage is in use
+    (tmp_path / "plans.cpp").write_text(PLANS)
+    exe = str(tmp_path / "plans")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", build.CSRC_SERVING, "-o", exe,
+                    str(tmp_path / "plans.cpp")], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
