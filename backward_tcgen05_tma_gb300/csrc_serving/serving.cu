@@ -523,7 +523,7 @@ extern "C" {
 
 size_t swiglu_mlp_w4_packed_bytes(int64_t E, int64_t N, int64_t K, int group, int zeros,
                                   int gate_up) {
-  if (check_w4(E, N, K, group, zeros) != SWIGLU_OK || (gate_up && N % 2 != 0)) return 0;
+  if (check_w4(E, N, K, group, zeros) != SWIGLU_OK || (gate_up && N % 16 != 0)) return 0;
   return (size_t)(w4_geom(N, K, log2_group(group), zeros, gate_up ? 1 : 0).bytes) * (size_t)E;
 }
 

@@ -331,7 +331,7 @@ swiglu_status swiglu_mlp_bwd_ex(const void* dY, const void* X, const void* Wgu, 
  * product of the rounded A, as in the calls above. */
 
 /* Bytes of E packed matrices; gate_up: each is a pair [Wg; Wu], N = 2H.  0 for
- * invalid arguments. */
+ * arguments that swiglu_mlp_w4_pack refuses. */
 size_t swiglu_mlp_w4_packed_bytes(int64_t E, int64_t N, int64_t K, int group, int zeros,
                                   int gate_up);
 

@@ -95,6 +95,13 @@ def test_sizes_beyond_the_indexes_are_refused(L):
     assert L.swiglu_mlp_w4_packed_bytes(1, 16, (1 << 27) + 8, 128, 0, 0) == 0
 
 
+def test_packed_bytes_of_what_packing_refuses(L):
+    for n in (8, 24, 40):  # a pair's H is a multiple of 8
+        assert L.swiglu_mlp_w4_pack(P, P, N, P, 1, n, 64, 64, 1, 0, N) == 2
+        assert L.swiglu_mlp_w4_packed_bytes(1, n, 64, 64, 0, 1) == 0
+    assert L.swiglu_mlp_w4_packed_bytes(1, 48, 64, 64, 0, 1) == 3 * 544
+
+
 # ---------------------------------------------------------------------------
 # modules: quantised weights are state
 # ---------------------------------------------------------------------------
