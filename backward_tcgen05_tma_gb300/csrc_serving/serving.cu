@@ -39,6 +39,10 @@ swiglu_status status_of(cudaError_t e) { return e == cudaSuccess ? SWIGLU_OK : S
 
 bool sixteen_bit(swiglu_dtype dt) { return dt == SWIGLU_BF16 || dt == SWIGLU_F16; }
 
+swiglu_status check_dtype(swiglu_dtype dt) {
+  return sixteen_bit(dt) ? SWIGLU_OK : dt == SWIGLU_F32_IEEE ? SWIGLU_ERR_UNSUPPORTED : SWIGLU_ERR_INVALID_ARG;
+}
+
 swiglu_status check_ptrs(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p == nullptr) return SWIGLU_ERR_INVALID_ARG;
@@ -392,8 +396,8 @@ size_t moe_inner_bytes(int64_t T, int64_t H, int topk) {
 // Sizes, types and formats of a mixture-of-experts layer.
 swiglu_status check_moe(int64_t T, int64_t D, int64_t H, int64_t E, int64_t topk,
                         const swiglu_mlp_w4_format* f, swiglu_dtype dt) {
-  if (dt != SWIGLU_F32_IEEE && !sixteen_bit(dt)) return SWIGLU_ERR_INVALID_ARG;
-  if (!sixteen_bit(dt)) return SWIGLU_ERR_UNSUPPORTED;
+  const swiglu_status st = check_dtype(dt);
+  if (st != SWIGLU_OK) return st;
   if (T < 0 || D <= 0 || H <= 0 || E <= 0 || topk <= 0 || topk > E) return SWIGLU_ERR_INVALID_ARG;
   if (f != nullptr && (log2_group(f->group) < 0 || (f->zeros != 0 && f->zeros != 1)))
     return SWIGLU_ERR_INVALID_ARG;
@@ -531,8 +535,9 @@ swiglu_status swiglu_mlp_w4_quantize(const void* W, void* codes, void* scales, v
                                      int64_t N, int64_t K, int group, swiglu_dtype dtype,
                                      void* stream) {
   host::reset_launches();
-  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
-  swiglu_status st = check_w4(1, N, K, group, zeros != nullptr);
+  swiglu_status st = check_dtype(dtype);
+  if (st != SWIGLU_OK) return st;
+  st = check_w4(1, N, K, group, zeros != nullptr);
   if (st != SWIGLU_OK) return st;
   if ((st = check_ptrs({W, codes, scales})) != SWIGLU_OK) return st;
   if (reinterpret_cast<uintptr_t>(zeros) & 15u) return SWIGLU_ERR_ALIGNMENT;
@@ -551,8 +556,9 @@ swiglu_status swiglu_mlp_w4_pack(const void* codes, const void* scales, const vo
                                  void* packed, int64_t E, int64_t N, int64_t K, int group,
                                  int gate_up, swiglu_dtype dtype, void* stream) {
   host::reset_launches();
-  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
-  swiglu_status st = check_w4(E, N, K, group, zeros != nullptr);
+  swiglu_status st = check_dtype(dtype);
+  if (st != SWIGLU_OK) return st;
+  st = check_w4(E, N, K, group, zeros != nullptr);
   if (st != SWIGLU_OK) return st;
   if (gate_up && N % 16 != 0) return SWIGLU_ERR_ALIGNMENT;
   if ((st = check_ptrs({codes, scales, packed})) != SWIGLU_OK) return st;
@@ -570,8 +576,9 @@ swiglu_status swiglu_mlp_w4_unpack(const void* packed, void* W, int64_t E, int64
                                    int group, int zeros, int gate_up, swiglu_dtype dtype,
                                    void* stream) {
   host::reset_launches();
-  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
-  swiglu_status st = check_w4(E, N, K, group, zeros);
+  swiglu_status st = check_dtype(dtype);
+  if (st != SWIGLU_OK) return st;
+  st = check_w4(E, N, K, group, zeros);
   if (st != SWIGLU_OK) return st;
   if (gate_up && N % 16 != 0) return SWIGLU_ERR_ALIGNMENT;
   if ((st = check_ptrs({packed, W})) != SWIGLU_OK) return st;
@@ -598,9 +605,10 @@ swiglu_status swiglu_mlp_w4_linear(const void* X, const void* packed, void* Y, i
                                    int64_t K, int group, int zeros, swiglu_dtype dtype, void* ws,
                                    size_t ws_bytes, void* stream) {
   host::reset_launches();
-  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  swiglu_status st = check_dtype(dtype);
+  if (st != SWIGLU_OK) return st;
   if (M < 0) return SWIGLU_ERR_INVALID_ARG;
-  swiglu_status st = check_w4(1, N, K, group, zeros);
+  st = check_w4(1, N, K, group, zeros);
   if (st != SWIGLU_OK) return st;
   if (M > FT_MAX_TOKENS) return SWIGLU_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, swiglu_mlp_w4_workspace_bytes(M, N, K))) != SWIGLU_OK) return st;
@@ -632,7 +640,7 @@ swiglu_status swiglu_mlp_fwd_nograd_w4(const void* X, const void* Wgu, const voi
   Muls mu;
   swiglu_status st = read_muls(options, &mu);
   if (st != SWIGLU_OK) return st;
-  if (!sixteen_bit(dtype)) return SWIGLU_ERR_UNSUPPORTED;
+  if ((st = check_dtype(dtype)) != SWIGLU_OK) return st;
   if (M < 0) return SWIGLU_ERR_INVALID_ARG;
   if ((st = check_w4(1, D, H, group, zeros)) != SWIGLU_OK) return st;
   if (D % 8 != 0) return SWIGLU_ERR_ALIGNMENT;

@@ -102,6 +102,17 @@ def test_packed_bytes_of_what_packing_refuses(L):
     assert L.swiglu_mlp_w4_packed_bytes(1, 48, 64, 64, 0, 1) == 3 * 544
 
 
+def test_no_type_is_an_invalid_argument(L):
+    # fp32 is a type that these calls do not support; 7 is none
+    for dt, status in ((2, UNSUP), (7, 1)):
+        assert L.swiglu_mlp_w4_linear(P, P, P, 4, 16, 64, 64, 0, dt, P, BIG, N) == status
+        assert L.swiglu_mlp_fwd_nograd_w4(P, P, P, P, P, 4, 64, 64, 64, 0, dt, N, P, BIG, N) == status
+        assert L.swiglu_mlp_w4_quantize(P, P, P, N, 16, 64, 64, dt, N) == status
+        assert L.swiglu_mlp_w4_pack(P, P, N, P, 1, 16, 64, 64, 0, dt, N) == status
+        assert L.swiglu_mlp_w4_unpack(P, P, 1, 16, 64, 64, 0, 0, dt, N) == status
+        assert L.swiglu_mlp_moe_route(P, P, P, P, 4, 64, 8, 2, 1, 1.0, dt, N) == status
+
+
 # ---------------------------------------------------------------------------
 # modules: quantised weights are state
 # ---------------------------------------------------------------------------
