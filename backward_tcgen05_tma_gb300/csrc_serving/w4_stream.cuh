@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(WsShape<RT, NT, G32, ZP>::WARPS * 32, 1)
     ++filled;
     if (++in.c == in_per) {
       in.c = 0;
+      ++in.j;
       src += (int64_t)(RT * nk - phase_len(in.phase)) * S::RECORD;  // the next tile
     }
     if (++in.v == in.v_end) {
