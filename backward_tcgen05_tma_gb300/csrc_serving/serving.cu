@@ -256,15 +256,24 @@ struct WtPlan {
   int grid, sk_tiles, sharers, seg_max;
 };
 int wt_columns(int64_t M) { return M <= 32 ? 32 : M <= 48 ? 48 : 64; }
-// Which form a product takes.  Up to 32 tokens w4_stream.cuh reads the weights
-// once as well and starts up faster: 32 tokens, 4096 x 4096 weights 12.4 against
-// 15.4 us; with 33 to 64 it would read them twice (64 tokens, 4096 x 11008: 49.3
-// against 24.3 us; only 1024 x 1024 and less come out even).  Large matrices
-// favour the tensor core from 17 tokens on: MLP 4096/11008 50.6 against some 50
-// us there, 59.2 at 24, 62.6 at 32 against 50.1 (groups of 32: 63.0 against 66.3
-// at 17, 71.1 against 66.6 at 32).
-bool wt_serves(int64_t M, int64_t tiles16, int64_t K) {
-  return M > 32 || (M > 16 && tiles16 * 16 * K >= (int64_t)1 << 25);
+// Which form a product takes.  With 33 to 64 tokens w4_stream.cuh would read the
+// weights twice.  Up to 32 both read them once; it starts up faster, and is bound
+// by products and shared-memory reads that grow with rows x K x tokens, in steps
+// (clusters, columns).  Measured in us, w4_stream.cuh first, groups of 128:
+//   tokens  8192 x 4096  4096 x 11008  8192 x 8192  22016 x 4096  14336 x 8192
+//     17    14.5, 17.8    18.0, 20.6    23.4, 24.0   28.9, 30.4    38.6, 31.9
+//     24    14.7, 17.8    22.1, 20.7    33.4, 24.0   35.9, 30.4    54.3, 31.9
+//     32    16.1, 17.8    22.3, 20.7    33.2, 24.0   35.6, 30.7    54.2, 32.0
+// In groups of 32 the tensor core needs an accumulator per 32 k and comes into its
+// own later:
+//     24    15.3, 21.5    23.0, 26.0    34.3, 31.8   37.0, 41.3    56.4, 45.2
+// Where this takes the slower one of the two it costs 5 to 12% as a rule, and
+// at worst 20% (20 tokens, 40000 x 2048) or, in groups of 32 with zero points,
+// 29% (32 tokens, 2048 x 40000).
+constexpr int64_t WT_MIN_PRODUCTS = (int64_t)21 << 26;
+bool wt_serves(int64_t M, int64_t tiles16, int64_t K, int group_log2) {
+  const int64_t least = group_log2 == 5 ? 2 * WT_MIN_PRODUCTS : WT_MIN_PRODUCTS;
+  return M > 32 || (M > 16 && tiles16 * 16 * K >= least / M);
 }
 WtPlan wt_plan(int tiles, int nk) {
   const int nsm = host::sms() > 0 ? host::sms() : 1, spt = (nk + WT_KB - 1) / WT_KB;
@@ -279,7 +288,7 @@ WtPlan wt_plan(int tiles, int nk) {
   return p;
 }
 size_t wt_workspace(int64_t M, int64_t tiles16, int64_t K) {
-  if (M > FT_MAX_TOKENS || !wt_serves(M, tiles16, K)) return HEADER;
+  if (M > FT_MAX_TOKENS || !wt_serves(M, tiles16, K, 7)) return HEADER;  // whatever the groups
   const WtPlan p = wt_plan((int)((tiles16 + 7) / 8), (int)((K + 63) / 64));
   return HEADER + WT_COUNTERS + (size_t)p.grid * p.seg_max * wt_columns(M) * 512;
 }
@@ -363,7 +372,7 @@ cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, int tiles16, cuda
 
 template <bool BF16>
 cudaError_t launch_ws(host::ServingKernel id, const WsArgs& a, const W4Geom& w, cudaStream_t st) {
-  if (wt_serves(a.M, w.tiles, a.K)) {
+  if (wt_serves(a.M, w.tiles, a.K, w.group_log2)) {
     const int pair = w.group_log2 == 7 ? 2 : 1;
     if (w.sets == 2)
       return w.zeros ? launch_wt<BF16, true, true>(id, a, pair, w.tiles, st)

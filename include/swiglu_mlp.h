@@ -363,8 +363,8 @@ swiglu_status swiglu_mlp_w4_unpack(const void* packed, void* W, int64_t E, int64
                                    void* stream);
 
 /* Workspace bytes of swiglu_mlp_w4_linear and swiglu_mlp_fwd_nograd_w4: the
- * header, and where the tensor-core form serves the call (from 33 tokens, for
- * large matrices from 17) counters and fp32 partial tiles. */
+ * header, and where the tensor-core form may serve the call (from 33 tokens,
+ * for large matrices from 17) counters and fp32 partial tiles. */
 size_t swiglu_mlp_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t swiglu_mlp_fwd_nograd_w4_workspace_bytes(int64_t M, int64_t D, int64_t H);
 

@@ -73,7 +73,12 @@ def close(got, y, terms, u, K):
     ("f16", 16, 70000, 264, 64, False),     # 1 x 1 x 2
     ("bf16", 5, 70008, 328, 128, True),     # 1 x 1 x 2
     ("f16", 29, 300, 1032, 32, False), ("bf16", 32, 4000, 2056, 128, False),
-    ("f16", 18, 8000, 4096, 64, True), ("bf16", 17, 31, 4096, 32, True)])
+    ("f16", 18, 8000, 4096, 64, True), ("bf16", 17, 31, 4096, 32, True),
+    # large ones on either side of the rule by which the tensor-core form takes
+    # 17 to 32 tokens: rows x K x tokens (twice as many in groups of 32)
+    ("f16", 32, 11016, 4104, 128, False), ("f16", 31, 11016, 4104, 128, False),
+    ("bf16", 19, 4104, 18440, 64, True), ("bf16", 18, 4104, 18440, 64, True),
+    ("bf16", 32, 21000, 4232, 32, True), ("bf16", 31, 21000, 4232, 32, True)])
 def test_w4_linear_split_phased_and_in_runs(dtn, M, N, K, group, zeros):
     g = gen(M + N + K)
     w, X = codes(g, (), N, K, group, zeros, DT[dtn]), normal(g, M, K, dtype=DT[dtn])
