@@ -21,13 +21,15 @@
 // memory in warp order, so results are deterministic.
 //
 // Measured (whole layer with the router, bf16): 16-bit weights, 16 tokens over 8
-// of 64 experts, 2048/1024: 124 us for 711 MB (5.7 TB/s of 6.8; gate/up 84 us
-// alone, DRAM 72%), 64 tokens 160 us; one token, 8 experts of 1024/2816 18.8 us,
-// of which the router and the two kernels' starts are some 12.  4 tokens, all of
-// 8 experts of 4096/11008: 221 us = 6.7 TB/s.  4-bit: one token 22 us, 32 tokens
-// over 8 of 128 experts of 2048/512 in groups of 32 82 us (199 MB; issue slots
-// 41%, ALU 39%: unpacking and the constant rows' products, 86 instructions a
-// unit, and each expert's two to three tokens cannot share more).
+// of 64 experts, 2048/1024: 124 us for 711 MB (5.7 TB/s of 6.8; gate/up 85 us
+// alone, DRAM 71%), 64 tokens 158 us; one token, 2 of 8 experts of 1024/2816 18.5
+// us, of which the router and the two kernels' starts are some 12.  One token over
+// all 8 experts of 4096/11008: 342 us for 2.16 GB = 6.3 TB/s, 8 tokens 369 us.
+// 4-bit: one token 20 us, 32 tokens over 8 of 128 experts of 2048/512 in groups of
+// 32 73 us (199 MB; gate/up: issue slots 51%, ALU 44%, 96 instructions to unpack
+// and multiply a unit, and each expert's two to three tokens cannot share more).
+// (With constant rows' products in place of subtractions: 82 us.)
+// An expert with more than 8 NT tokens is streamed once per 8 NT of them.
 #pragma once
 
 #include "w4_stream.cuh"

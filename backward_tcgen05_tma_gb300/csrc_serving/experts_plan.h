@@ -16,7 +16,8 @@ namespace swiglu {
 constexpr int WX_MAX_STAGES = 8;
 // What a block takes as a rule (the rest of an SM's 256 KB caches the token
 // rows), and the most where that leaves a ring of one stage, in which nothing
-// would be fetched ahead: both with 1024 bytes for the ring's alignment, beside
+// would be fetched ahead (64 tokens over 8 of 64 16-bit experts of 2048/1024: 160.0
+// us, with two stages 158.4): both with 1024 bytes for the ring's alignment, beside
 // static shared memory of 1 KB.
 constexpr int WX_SMEM = 200 * 1024, WX_SMEM_MOST = 224 * 1024;
 

@@ -11,8 +11,8 @@
 //     then adds up terms of the formula itself, so a sum is as good as a plain
 //     fp32 one whatever the elements.  (Leaving 128 + q or 1024 + q in the
 //     products and taking the rest off each sum, from sums of the token's
-//     elements, was no faster and lost ten roundings of an fp16 output where an
-//     element of 30000 met weights of 0.)
+//     elements, was slower, 34 us at 16 tokens, and put fp16 outputs 3% off, bf16
+//     ones 0.5%, where elements of 30000 met weights of 0.)
 //   * A warp's weights are runs of unit records (codes, then scales, then zero
 //     points) that bulk copies bring into a ring of its own, 8 records a copy.
 // Each group's sum is scaled in fp32; no weight is rounded.
@@ -32,14 +32,14 @@
 // would otherwise give most of them to the token rows.
 //
 // Measured (bf16, groups of 128, MLP 4096/11008, 70 MB, 10.3 us at the HBM rate):
-// 21.4 to 24.8 us at 1 to 8 tokens (2.8 to 3.3 TB/s), 34 at 16 (51 at 17, 63 at
-// 32, where w4_tensor.cuh takes over); one token times 11008 x 4096 8.5 us, times 2816 x 1024 4.0 us back to back.
-// At one token gate/up takes 18.4 us alone: issue slots 37% used, DRAM 33%; some
-// 6 us of each kernel are its start (tensor cores idle until the token rows and
-// the first records are in) and its end (partials meet, 16-bit stores).  Before
-// the present layout (codes apart from scales, one code form, sums on the scalar
-// cores) the same MLP took 47 us; before clusters split the contraction 44 us at
-// 16 tokens.
+// 23.7 to 24.5 us at 1 to 8 tokens (2.9 TB/s), 31.3 at 16 (46 at 17, 57 at 32,
+// where w4_tensor.cuh takes over); one token times 11008 x 4096 8.6 us, times
+// 2816 x 1024 3.8 us back to back.  At one token gate/up takes 18.6 us alone:
+// issue slots 42% used, DRAM 33%; some 6 us of each kernel are its start (tensor
+// cores idle until the token rows and the first records are in) and its end
+// (partials meet, 16-bit stores).  Before the present layout (codes apart from
+// scales, one code form, sums on the scalar cores) the same MLP took 47 us; before
+// clusters split the contraction 44 us at 16 tokens.
 #pragma once
 
 #include "fewtok.cuh"

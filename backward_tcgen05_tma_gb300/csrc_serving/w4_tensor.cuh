@@ -4,7 +4,8 @@
 //
 // Beyond 16 tokens the rate of mma.sync (1024 products a cycle and SM,
 // measured) and the shared-memory reads of the token rows bound w4_stream.cuh;
-// on tcgen05 the products are far from a bound again (tensor pipe 16% busy).
+// on tcgen05 the products are far from a bound again (tensor pipe 18% busy).
+// wt_serves in serving.cu says which of the two takes a product.
 //
 // Swap-AB: 128 weight rows (8 of the packed 16-row tiles) take the MMA's M
 // dimension, the tokens its N dimension (NT = 32, 48 or 64).  Roles of a block:
@@ -34,11 +35,11 @@
 // tile) adds them in block order and writes.  No block waits for another.
 //
 // Measured (bf16, groups of 128): MLP 4096/11008, 72 MB, 10.7 us at the HBM
-// rate, 58 us at 64 tokens (w4_stream.cuh: 122), 50 at 32 (63); groups of 32:
-// 79 at 64 tokens, where an accumulator per 32 k makes the epilogue the bound.
-// At 64 tokens issue slots were 48% and the ALU 44% used when the pair took 60 us
-// (over the whole kernel; the unpackers never wait in the loop, some 950 cycles
-// per 64 k and warp then).  Next after that: each tile reads all token rows, 88
+// rate, 58 us at 64 tokens (w4_stream.cuh, reading the weights twice, 122), 50 at
+// 32 (57); groups of 32: 79 at 64 tokens, where an accumulator per 32 k makes the
+// epilogue the bound.  At 64 tokens gate/up takes 38.9 us alone, issue slots 44%
+// and the ALU 35% used (over the whole kernel; the unpackers never wait in the
+// loop).  Next after that: each tile reads all token rows, 88
 // MB through L2, 24 us with the weights at the 5.8 TB/s that reach the SMs; some
 // 5 us are start and shared tiles' sums.
 #pragma once
