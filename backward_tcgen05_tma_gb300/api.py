@@ -192,6 +192,21 @@ def _load(path: str) -> ctypes.CDLL:
     L.swiglu_mlp_moe_fwd_nograd.restype = ci
     L.swiglu_mlp_moe_fwd_nograd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, ci,
                                             cf, vp, ci, op, vp, sz, vp]
+    L.swiglu_mlp_layer_norm_fwd.restype = ci
+    L.swiglu_mlp_layer_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, cf, ci, vp, sz,
+                                            vp]
+    L.swiglu_mlp_layer_norm_workspace_bytes.restype = sz
+    L.swiglu_mlp_layer_norm_workspace_bytes.argtypes = [i64, i64, ci]
+    L.swiglu_mlp_layer_norm_bwd.restype = ci
+    L.swiglu_mlp_layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, ci, ci, vp,
+                                            sz, vp]
+    L.swiglu_mlp_linear_workspace_bytes.restype = sz
+    L.swiglu_mlp_linear_workspace_bytes.argtypes = [i64, i64, i64, ci, ci]
+    L.swiglu_mlp_linear_fwd.restype = ci
+    L.swiglu_mlp_linear_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, vp, sz, vp]
+    L.swiglu_mlp_linear_bwd.restype = ci
+    L.swiglu_mlp_linear_bwd.argtypes = [vp, vp, vp, vp, ci, vp, ci, vp, vp, vp, vp, i64, i64, i64, ci,
+                                        ci, vp, sz, vp]
     L.swiglu_mlp_debug_build.restype = ci
     L.swiglu_mlp_debug_build.argtypes = []
     L.swiglu_mlp_debug_narrow_once.restype = None
@@ -703,6 +718,183 @@ def swiglu_mlp_moe_fwd_nograd(X, Wr, Wgu, Wd, top_k: int, norm_topk: bool = True
            "swiglu_mlp_moe_fwd_nograd")
     _device_check(ws, "swiglu_mlp_moe_fwd_nograd")
     return Y, idx, w
+
+
+# ---------------------------------------------------------------------------
+# layer norm and linear layers
+# ---------------------------------------------------------------------------
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def activation_code(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError("unknown activation %r (one of %s)" % (name, ", ".join(ACTIVATIONS)))
+    return ACTIVATIONS[name]
+
+
+def _block_call(f, where, ws, device, *args):
+    """One call on ``device`` (made current where it is not) and its current
+    stream; ``ws`` None: a call without a workspace."""
+    dev = device.index
+    n = 0 if ws is None else ws.numel()
+    w = 0 if ws is None else ws.data_ptr()
+    if dev == torch.cuda.current_device():
+        code = f(*args, w, n, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, w, n, _raw_stream(dev))
+    if code != 0:
+        raise SwigluError(code, where)
+    if _use_debug and ws is not None:
+        with torch.cuda.device(dev):
+            _device_check(ws, where)
+
+
+def _same(where, X, shapes):
+    """Each (name, tensor or None, shape): X's dtype and device, contiguous."""
+    dev, dt = X.get_device(), X.dtype
+    for name, t, shape in shapes:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype != dt or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("%s: %s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s"
+                             % (where, name, dt, tuple(shape), X.device, t.dtype, tuple(t.shape),
+                                t.device))
+
+
+def _rows(where, X):
+    if X.dim() != 2 or not X.is_cuda or not X.is_contiguous():
+        raise ValueError("%s: expected contiguous CUDA rows [M, D], got %s" % (where, tuple(X.shape)))
+    return X.shape
+
+
+def _sized_ws(ws, size, device, where):
+    """The caller's workspace (its size is checked by the call) or a new one."""
+    if ws is None:
+        return torch.zeros(int(size()), dtype=torch.uint8, device=device)
+    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("%s: ws must be a contiguous uint8 tensor on %s" % (where, device))
+    return ws
+
+
+def layer_norm_workspace(M: int, D: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """A zero-filled workspace for swiglu_mlp_layer_norm_bwd."""
+    with torch.cuda.device(device):
+        return _ws(None, lambda: lib().swiglu_mlp_layer_norm_workspace_bytes(M, D, dtype_code(dtype)),
+                   device)
+
+
+def linear_workspace(M: int, N: int, K: int, dtype: torch.dtype, op: int, device) -> torch.Tensor:
+    """A zero-filled workspace for swiglu_mlp_linear_fwd (op SWIGLU_OP_FWD) or
+    swiglu_mlp_linear_bwd (op SWIGLU_OP_BWD)."""
+    with torch.cuda.device(device):
+        return _ws(None, lambda: lib().swiglu_mlp_linear_workspace_bytes(M, N, K, dtype_code(dtype), op),
+                   device)
+
+
+def swiglu_mlp_layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, residual=None,
+                              out: dict | None = None, stats: bool = True):
+    """Layer norm over rows X [M, D], of X + residual where that is given:
+    (Y, S, mean, rstd).  S is X itself or the rounded sum; mean and rstd (fp32
+    [M], for the backward pass) are None without ``stats``."""
+    where = "swiglu_mlp_layer_norm_fwd"
+    M, D = _rows(where, X)
+    _same(where, X, (("weight", weight, (D,)), ("bias", bias, (D,)), ("residual", residual, (M, D))))
+    dev = X.device
+    Y = _out(out, "Y", (M, D), X.dtype, dev)
+    S = None if residual is None else _out(out, "S", (M, D), X.dtype, dev)
+    mean = _out(out, "mean", (M,), torch.float32, dev) if stats else None
+    rstd = _out(out, "rstd", (M,), torch.float32, dev) if stats else None
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev) if _use_debug else None
+    _block_call((_lib or lib()).swiglu_mlp_layer_norm_fwd, where, ws, dev, X.data_ptr(), ptr(residual),
+                ptr(weight), ptr(bias), ptr(S), Y.data_ptr(), ptr(mean), ptr(rstd), M, D, eps,
+                dtype_code(X.dtype))
+    return Y, X if S is None else S, mean, rstd
+
+
+def swiglu_mlp_layer_norm_bwd(dY, S, weight, mean, rstd, dS=None, need_dweight: bool = True,
+                              need_dbias: bool = True, out: dict | None = None, ws=None,
+                              accumulate: bool = False):
+    """Backward of swiglu_mlp_layer_norm_fwd, whose S, mean and rstd it takes:
+    (dX, dweight, dbias).  dS: the gradient that reaches S on its own (the
+    residual stream's), added into dX.  dX is the residual's gradient too.
+    ``accumulate``: add into the dweight and dbias given in ``out``."""
+    where = "swiglu_mlp_layer_norm_bwd"
+    M, D = _rows(where, S)
+    _same(where, S, (("dY", dY, (M, D)), ("weight", weight, (D,)), ("dS", dS, (M, D))))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.shape != (M,) or t.dtype != torch.float32 or t.device != S.device or not t.is_contiguous():
+            raise ValueError("%s: %s must be a contiguous fp32 tensor of shape (%d,)" % (where, name, M))
+    dev, want = S.device, {"dweight": need_dweight, "dbias": need_dbias}
+    if accumulate and not all((out or {}).get(k) is not None for k, v in want.items() if v):
+        raise ValueError("accumulate needs the held dweight and dbias in out")
+    dX = _out(out, "dX", (M, D), S.dtype, dev)
+    dw, db = (_out(out, k, (D,), S.dtype, dev) if v else None for k, v in want.items())
+    L = _lib or lib()
+    dt = dtype_code(S.dtype)
+    ws = _sized_ws(ws, lambda: L.swiglu_mlp_layer_norm_workspace_bytes(M, D, dt), dev, where)
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    _block_call(L.swiglu_mlp_layer_norm_bwd, where, ws, dev, dY.data_ptr(), S.data_ptr(), ptr(weight),
+                mean.data_ptr(), rstd.data_ptr(), ptr(dS), dX.data_ptr(), ptr(dw), ptr(db), M, D,
+                int(accumulate), dt)
+    return dX, dw, db
+
+
+def swiglu_mlp_linear_fwd(X, W, bias=None, activation: str = "none", residual=None,
+                          keep: bool = False, out: dict | None = None, ws=None):
+    """Y [M, N] = act(X [M, K] W^T + bias) + residual: (Y, Z).  Z [M, N] is the
+    rounded pre-activation, which the backward pass of an activation needs,
+    with ``keep``, else None."""
+    where = "swiglu_mlp_linear_fwd"
+    M, K = _rows(where, X)
+    act = activation_code(activation)
+    N = W.shape[0]
+    _same(where, X, (("W", W, (N, K)), ("bias", bias, (N,)), ("residual", residual, (M, N))))
+    dev = X.device
+    Y = _out(out, "Y", (M, N), X.dtype, dev)
+    Z = _out(out, "Z", (M, N), X.dtype, dev) if keep else None
+    L = _lib or lib()
+    dt = dtype_code(X.dtype)
+    ws = _sized_ws(ws, lambda: L.swiglu_mlp_linear_workspace_bytes(M, N, K, dt, SWIGLU_OP_FWD), dev, where)
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    _block_call(L.swiglu_mlp_linear_fwd, where, ws, dev, X.data_ptr(), W.data_ptr(), ptr(bias),
+                ptr(residual), ptr(Z), Y.data_ptr(), M, N, K, act, dt)
+    return Y, Z
+
+
+def swiglu_mlp_linear_bwd(dY, X, W, Z=None, activation: str = "none", X_pre=None,
+                          x_activation: str = "none", need_dX: bool = True, need_dW: bool = True,
+                          need_dbias: bool = True, out: dict | None = None, ws=None,
+                          accumulate: bool = False):
+    """Backward of swiglu_mlp_linear_fwd: (dX [M, K], dW [N, K], dbias [N]),
+    None in the place of one that is not needed; the residual's gradient is dY.
+    Z: the pre-activation that forward kept.  With ``x_activation``, X is that
+    activation of X_pre, and dX becomes the gradient of X_pre.  The gradient of
+    the pre-activation is left in out["dZ"] where that is given.
+    ``accumulate``: add into the dW and dbias given in ``out``."""
+    where = "swiglu_mlp_linear_bwd"
+    M, N = _rows(where, dY)
+    act, x_act = activation_code(activation), activation_code(x_activation)
+    K = W.shape[1]
+    _same(where, dY, (("X", X, (M, K)), ("W", W, (N, K)), ("Z", Z, (M, N)), ("X_pre", X_pre, (M, K))))
+    if (act and Z is None) or (x_act and need_dX and X_pre is None):
+        raise ValueError("%s: activation needs Z, x_activation needs X_pre" % where)
+    if accumulate and any(v and (out or {}).get(k) is None for k, v in (("dW", need_dW), ("dbias", need_dbias))):
+        raise ValueError("accumulate needs the held dW and dbias in out")
+    dev, dtype = dY.device, dY.dtype
+    dZ = _out(out, "dZ", (M, N), dtype, dev) if act else None
+    dX = _out(out, "dX", (M, K), dtype, dev) if need_dX else None
+    dW = _out(out, "dW", (N, K), dtype, dev) if need_dW else None
+    db = _out(out, "dbias", (N,), dtype, dev) if need_dbias else None
+    L = _lib or lib()
+    dt = dtype_code(dtype)
+    ws = _sized_ws(ws, lambda: L.swiglu_mlp_linear_workspace_bytes(M, N, K, dt, SWIGLU_OP_BWD), dev, where)
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    _block_call(L.swiglu_mlp_linear_bwd, where, ws, dev, dY.data_ptr(), X.data_ptr(), W.data_ptr(),
+                ptr(Z), act, ptr(X_pre), x_act, ptr(dZ), ptr(dX), ptr(dW), ptr(db), M, N, K,
+                int(accumulate), dt)
+    return dX, dW, db
 
 
 def swiglu_mlp_query_error(ws) -> int:

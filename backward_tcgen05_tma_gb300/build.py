@@ -10,6 +10,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 CSRC_SERVING = os.path.join(HERE, "csrc_serving")
+CSRC_BLOCK = os.path.join(HERE, "csrc_block")
 ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libswiglu_mlp.so")
 SO_DEBUG = os.path.join(HERE, "libswiglu_mlp_debug.so")
@@ -19,6 +20,7 @@ BUILD = os.path.join(HERE, "_build")  # objects, kept for the next build
 SOURCES = {
     os.path.join(CSRC, "swiglu_mlp.cu"): [CSRC, os.path.join(CSRC_SERVING, "host_shared.h")],
     os.path.join(CSRC_SERVING, "serving.cu"): [CSRC_SERVING, os.path.join(CSRC, "sm103_ptx.cuh")],
+    os.path.join(CSRC_BLOCK, "block.cu"): [CSRC_BLOCK, CSRC, os.path.join(CSRC_SERVING, "host_shared.h")],
 }
 
 NVCC_FLAGS = [

@@ -19,7 +19,7 @@ enum : int { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 6, DEV_ERR_BOUNDS = 7 };
 // so the kernel finishes and the host reads the error (no trap, no fault).
 // TMA accesses need no check: the tensor map clips them to the tensor.  In
 // release builds every check is the constant `true` and compiles away.
-constexpr int DBG_WINS = 4;
+constexpr int DBG_WINS = 8;
 struct DbgWin {
   uint64_t lo[DBG_WINS];  // window i = [lo[i], hi[i]); empty when lo == hi
   uint64_t hi[DBG_WINS];

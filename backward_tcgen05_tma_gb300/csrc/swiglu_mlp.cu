@@ -23,29 +23,17 @@
 #include <vector>
 
 #include "../../include/swiglu_mlp.h"
-#include "../csrc_serving/host_shared.h"
 #include "ng_fused.cuh"
-#include "ng_gemm.cuh"
-#include "simt_gemm.cuh"
-#include "tc2_gemm.cuh"
-#include "tc_gemm.cuh"
+#include "tc_host.cuh"
 
 using namespace swiglu;
+using namespace swiglu::host;
 
 namespace {
-
-constexpr size_t WS_HEADER = 256;  // error word + reserved
-constexpr int TC_STAGES = 4;
-constexpr int TC_BN = 256;
 
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 
 swiglu_status cuda_status(cudaError_t e);
-
-// Debug builds (SWIGLU_DEBUG): the buffers (base, bytes) a launch may touch
-// with plain loads and stores, its output first; the kernels check every
-// such access against them.  Release builds carry no windows.
-using Win = std::pair<const void*, size_t>;
 
 // Test hook (swiglu_mlp_debug_narrow_once): halve the next launch's first
 // window, its output buffer.
@@ -65,28 +53,6 @@ DbgWin make_windows(std::initializer_list<Win> wins) {
   return w;
 }
 #endif
-
-template <class T>
-void set_windows(T& args, std::initializer_list<Win> wins) {
-#ifdef SWIGLU_DEBUG
-  args.dbg = make_windows(wins);
-#else
-  (void)args;
-  (void)wins;
-#endif
-}
-
-SimtCheck simt_check(int* err, std::initializer_list<Win> wins) {
-  SimtCheck c;
-#ifdef SWIGLU_DEBUG
-  c.err = err;
-  c.win = make_windows(wins);
-#else
-  (void)err;
-  (void)wins;
-#endif
-  return c;
-}
 
 // The multiplier / accumulation options of the _ex entry points (see the
 // header); {1, 1, 0} is the standard MLP with gradients overwritten.
@@ -108,22 +74,18 @@ std::atomic<int> g_last_launches{0};
 std::atomic<int> g_cta_pairs{1};  // SM pairs (cta_group::2): 0 never, 1 by size, 2 always
 std::atomic<int> g_wide_tiles{1};  // 512-column pair tiles for dWd, dWgu, dX: 0 never, 1 by size, 2 always
 std::atomic<int> g_ng_fused{0};   // few-token no-grad: fused kernel 0 never, 1 for 33..64 tokens, 2 always
-constexpr int TC2_STAGES = 6;
 
 // ---------------------------------------------------------------------------
 // optional per-kernel timing: CUDA events bracket each launch on its stream
 // ---------------------------------------------------------------------------
-enum KernelId : int {
-  K_GATE_UP = 0, K_DOWN, K_DGU, K_DWD, K_DWGU, K_DX, K_GATE_UP_NOGRAD, K_DOWN_NOGRAD,
-  K_SIMT_GATE_UP, K_SIMT_DOWN, K_SIMT_DGU, K_SIMT_DWD, K_SIMT_DWGU, K_SIMT_DX, K_NG_GATE_UP,
-  K_NG_DOWN, K_NG_FUSED, K_SERVING, K_COUNT = K_SERVING + swiglu::host::SK_COUNT
-};
 const char* const kKernelNames[K_COUNT] = {
     "gate_up_swiglu", "down_proj", "dgu_inplace", "dwd", "dwgu", "dx", "gate_up_nograd",
     "down_proj_nograd", "simt_gate_up_swiglu", "simt_down_proj", "simt_dgu_inplace", "simt_dwd",
     "simt_dwgu", "simt_dx", "nograd_small_gate_up", "nograd_small_down", "nograd_small_fused",
     "w4_linear", "w4_gate_up", "w4_down", "moe_route", "moe_gate_up", "moe_down",
-    "moe_w4_gate_up", "moe_w4_down"};
+    "moe_w4_gate_up", "moe_w4_down", "layer_norm", "dlayer_norm", "linear", "linear_few",
+    "simt_linear", "dlinear_act", "column_sums", "linear_dw", "linear_dx", "simt_linear_dw",
+    "simt_linear_dx"};
 
 struct ProfRec {
   int id;
@@ -147,224 +109,13 @@ cudaEvent_t prof_event() {
   return e;
 }
 
-// Brackets one launch with events when timing is enabled.
-struct ProfScope {
-  int id;
-  cudaStream_t st;
-  cudaEvent_t b = nullptr;
-  ProfScope(int id_, cudaStream_t st_) : id(id_), st(st_) {
-    if (!g_prof_on.load()) return;
-    std::lock_guard<std::mutex> g(g_prof_mu);
-    cudaEvent_t a = prof_event();
-    b = prof_event();
-    cudaEventRecord(a, st);
-    g_prof_pending.push_back(ProfRec{id, a, b});
-  }
-  ~ProfScope() {
-    if (b != nullptr) cudaEventRecord(b, st);
-  }
-};
-
 // ---------------------------------------------------------------------------
-// driver entry point for tensor-map encoding (no link-time libcuda dependency)
+// sizes of the training workspace
 // ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
-}
-
-// 2-D tiled map over a row-major matrix [outer][inner] (inner contiguous) with
-// a row stride in bytes; 128-byte swizzle unless given; out-of-range elements
-// read as 0 (and are not written by a store).
-bool encode_2d(CUtensorMap* tm, bool bf16, const void* base, uint64_t inner, uint64_t outer,
-               uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (enc == nullptr) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_stride_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Wgu [2H][D] seen as [2][H][D]: one box brings rows j0.. of Wg and of Wu
-// (depth 2), or of one of them (depth 1: the two CTAs of a pair each bring one).
-bool encode_gateup(CUtensorMap* tm, bool bf16, const void* Wgu, uint64_t D, uint64_t H,
-                   uint32_t rows, uint32_t depth = 2) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (enc == nullptr) return false;
-  cuuint64_t dims[3] = {D, H, 2};
-  cuuint64_t strides[2] = {D * 2, H * D * 2};
-  cuuint32_t box[3] = {64, rows, depth};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(Wgu), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// K-major operand: rows of K elements, box {64, rows_per_tile}.
-bool map_kmajor(CUtensorMap* tm, bool bf16, const void* base, int64_t K, int64_t rows, int64_t ld,
-                uint32_t box_rows) {
-  return encode_2d(tm, bf16, base, (uint64_t)K, (uint64_t)rows, (uint64_t)ld * 2, 64, box_rows);
-}
-
-// MN-major operand stored [K][MN]: boxes {64 MN, 64 K}.
-bool map_mnmajor(CUtensorMap* tm, bool bf16, const void* base, int64_t MN, int64_t K, int64_t ld) {
-  return encode_2d(tm, bf16, base, (uint64_t)MN, (uint64_t)K, (uint64_t)ld * 2, 64, 64);
-}
-
-// ---------------------------------------------------------------------------
-// stream-K hybrid for the tensor-core kernels
-// ---------------------------------------------------------------------------
-// Workspace of a training call: [0, 256) header (error word), then the
-// shared-tile counters, then the fp32 partial tiles.
-constexpr size_t TC_SK_COUNTER_BYTES = 1024;  // up to 256 shared tiles
-constexpr int TC_SK_MAX_SMS = 256;
-
-struct TcPlan {
-  int grid, sk_tiles, seg_max;
-};
-
-// Whole tiles round-robin, unless the last round would leave more than 3% of
-// the SMs' time idle: then the (tiles mod SMs) tiles of that round (all of
-// them when there are fewer tiles than SMs) are shared stream-K style.  A
-// CTA's shared range is at most one tile long, so it meets at most two tiles.
-TcPlan tc_plan(int64_t tiles, int64_t kb, int nsm) {
-  TcPlan p{(int)(tiles < nsm ? tiles : nsm), 0, 1};
-  const int64_t waves = (tiles + nsm - 1) / nsm;
-  const double fill = (double)tiles / ((double)waves * nsm);
-  if (fill >= 0.97 || kb < 8) return p;
-  p.sk_tiles = (int)(tiles >= nsm ? tiles % nsm : tiles);
-  const int64_t total = (int64_t)p.sk_tiles * kb;
-  p.grid = nsm;
-  if (tiles < nsm && total < nsm) p.grid = (int)total;
-  const int64_t range = (total + p.grid - 1) / p.grid;
-  p.seg_max = (int)((range + kb - 1) / kb) + 1;
-  return p;
-}
-
 // Bytes of the workspace that must be zero when a training call starts: the
 // error word, and the shared-tile counters of the tensor-core kernels.
 size_t ws_clear_bytes(swiglu_dtype dt) {
   return dt == SWIGLU_F32_IEEE ? sizeof(int) : WS_HEADER + TC_SK_COUNTER_BYTES;
-}
-
-// Workspace bytes left for stream-K partial tiles after the header and the
-// tile counters.
-size_t part_capacity(size_t ws_bytes) {
-  const size_t fixed = WS_HEADER + TC_SK_COUNTER_BYTES;
-  return ws_bytes > fixed ? ws_bytes - fixed : 0;
-}
-
-size_t tc_part_bytes(const TcPlan& p, int64_t bn = TC_BN) {
-  return p.sk_tiles ? (size_t)p.grid * p.seg_max * TC_BM * bn * 4 : 0;
-}
-
-// 512-column pair tiles for the weight-gradient and dX GEMMs (use_wide)
-constexpr int TC2_WIDE_BN = 512;
-constexpr int64_t TC2_WIDE_MIN_K = 16384;
-
-int tc_nsm() {
-  const int n = sm_count();
-  return n < 1 ? 1 : (n > TC_SK_MAX_SMS ? TC_SK_MAX_SMS : n);
-}
-
-// Pairs of SMs that can hold a pair kernel's cluster at once (each TPC
-// whose two SMs are both usable), queried once per device.
-int tc2_units() {
-  static std::mutex mu;
-  static int cached[64];
-  static bool done[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::lock_guard<std::mutex> g(mu);
-  if (!done[dev]) {
-    int n = 0;
-    auto kern = tc2_gemm_kernel<TC2_STAGES, LOAD_KMAJOR, LOAD_KMAJOR, true, EpiStore>;
-    constexpr int smem = Tc2Smem<TC2_STAGES>::DYN_BYTES;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
-        cudaSuccess) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2);
-      cfg.blockDim = dim3(TC_THREADS);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
-    }
-    const int cap = tc_nsm() / 2;
-    cached[dev] = n < cap ? n : cap;
-    done[dev] = true;
-  }
-  return cached[dev];
-}
-
-// 512-column pair tiles (one accumulator, no epilogue overlap) for an
-// M x N GEMM over K: by size, where the main loop dwarfs a tile's epilogue
-// (K >= 16384) and every pair gets at least two whole tiles.  Measured at
-// B=8 S=8192 D=4096 H=11008: dWd 3.74 -> 3.61, dWgu 7.46 -> 6.96, dX 7.17
-// -> 6.88 ms; at S=4096 D=2048 H=5632 dWgu 0.975 -> 0.897 ms, while dX
-// (K = 11264) and dWd (88 tiles for 76 pairs) were slower, which the rule
-// leaves on 256-column tiles.
-bool use_wide(bool pairs, int64_t M, int64_t N, int64_t K) {
-  const int mode = g_wide_tiles.load();
-  if (!pairs || mode == 0) return false;
-  if (mode == 2) return true;
-  const int64_t tiles = ((M + TC2_BM - 1) / TC2_BM) * ((N + TC2_WIDE_BN - 1) / TC2_WIDE_BN);
-  return K >= TC2_WIDE_MIN_K && tiles >= 2 * (int64_t)tc2_units();
-}
-
-// Whether one GEMM runs on SM pairs.  Measured per kernel on GB300: pairs
-// win when the main loop dominates -- long K and several rounds of tiles, or
-// the very long K of the weight gradients -- while short-K GEMMs with heavy
-// epilogues or few tiles run faster on single SMs (the pair's fixed costs and
-// its coupled epilogues are not amortised).
-bool use_pairs(int64_t Mg, int64_t N, int64_t n_per_tile, int64_t K) {
-  const int mode = g_cta_pairs.load();
-  if (mode == 0 || tc2_units() < 1) return false;
-  if (mode == 2) return true;
-  // pairs once every pair gets at least one of their 256-row tiles and the
-  // 256-row tiles add no padding beyond the 128-row ones; measured per GEMM
-  // at B=8, S=2048-8192 (D = 1024-4096): as fast or faster on pairs for
-  // every GEMM there, including the short contractions (gate/up and dX at
-  // D = 1024: 0.151 vs 0.171 and 0.126 vs 0.143 ms); no-grad calls with
-  // 65-128 or 384 tokens, whose pair tiles would be partly empty, are 3% and
-  // 11% faster on single SMs
-  const int64_t pair_tiles = ((Mg + TC2_BM - 1) / TC2_BM) * ((N + n_per_tile - 1) / n_per_tile);
-  const bool no_pad = (Mg + TC2_BM - 1) / TC2_BM * TC2_BM == (Mg + TC_BM - 1) / TC_BM * TC_BM;
-  const int64_t kb = (K + TC_BK - 1) / TC_BK;
-  return (kb >= 16 && no_pad && pair_tiles >= (int64_t)tc2_units()) || kb >= 256;
 }
 
 // pairs: tiles of 256 rows handed out per CTA pair (tc2_gemm_kernel).
@@ -384,7 +135,7 @@ size_t tc_ws_part_bytes(int64_t M, int64_t D, int64_t H, int op) {
     const int64_t kb = (g[3] + TC_BK - 1) / TC_BK, nt = (g[1] + g[2] - 1) / g[2];
     // one SM per CTA, or pairs of SMs (two CTAs, so two slots sets per unit)
     const size_t b1 = tc_part_bytes(tc_plan(((g[0] + TC_BM - 1) / TC_BM) * nt, kb, nsm));
-    const int units = tc2_units();  // the pair kernel plans with the same count
+    const int units = host::pair_units();  // the pair kernel plans with the same count
     const size_t b2 =
         units >= 1 ? 2 * tc_part_bytes(tc_plan(((g[0] + TC2_BM - 1) / TC2_BM) * nt, kb, units)) : 0;
     if (b1 > best) best = b1;
@@ -398,118 +149,6 @@ size_t tc_ws_part_bytes(int64_t M, int64_t D, int64_t H, int op) {
     }
   }
   return best;
-}
-
-// part_cap: workspace bytes available for stream-K partial tiles; a GEMM
-// whose plan needs more runs whole tiles only (same results within
-// rounding, without the last round's balancing).
-TcShape make_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, int* err, bool pairs,
-                   size_t part_cap) {
-  TcShape s;
-  s.M = (int)M;
-  s.N = (int)N;
-  s.K = (int)K;
-  const int64_t bm = pairs ? TC2_BM : TC_BM;
-  s.m_tiles = (int)((M + bm - 1) / bm);
-  s.n_tiles = (int)((N + n_per_tile - 1) / n_per_tile);
-  s.k_blocks = (int)((K + TC_BK - 1) / TC_BK);
-  s.group_m = 16;
-  s.wait_limit_ns = g_wait_limit_ns.load();
-  s.err = err;
-  s.inject_stall = take_inject() ? 1 : 0;
-  // the workspace (whose first word is err) carries the stream-K scratch
-  const TcPlan p = tc_plan((int64_t)s.m_tiles * s.n_tiles, s.k_blocks,
-                           pairs ? tc2_units() : tc_nsm());
-  s.sk_tiles = p.sk_tiles;
-  s.seg_max = p.seg_max;
-  if (tc_part_bytes(p, n_per_tile) * (pairs ? 2 : 1) > part_cap) {
-    s.sk_tiles = 0;
-    s.seg_max = 1;
-  }
-  s.counters = reinterpret_cast<int*>(reinterpret_cast<char*>(err) + WS_HEADER);
-  s.part = reinterpret_cast<float*>(reinterpret_cast<char*>(err) + WS_HEADER + TC_SK_COUNTER_BYTES);
-  return s;
-}
-
-// CTAs (or pairs) to launch: the stream-K plan's grid, or one per tile up to
-// `units` when the GEMM runs whole tiles only.
-int launch_units(const TcShape& s, int units) {
-  const int64_t tiles = (int64_t)s.m_tiles * s.n_tiles;
-  if (s.sk_tiles) return tc_plan(tiles, s.k_blocks, units).grid;
-  return (int)(tiles < units ? tiles : units);
-}
-
-// The training kernels are launched in plain stream order: with a static
-// round-robin tile split, a programmatic dependent whose CTAs start late on
-// SMs still held by the predecessor's last wave also finishes late (measured
-// slower than plain order).
-template <int AM, int BMODE, bool BF16, class Epi>
-cudaError_t launch_tc(int kid, const CUtensorMap& ta, const CUtensorMap& tb, const TcShape& s,
-                      const typename Epi::Params& ep, cudaStream_t st) {
-  auto kern = tc_gemm_kernel<TC_BN, TC_STAGES, AM, BMODE, BF16, Epi>;
-  constexpr int smem = TcSmem<TC_BN, TC_STAGES>::DYN_BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int grid = launch_units(s, tc_nsm());
-  ProfScope prof(kid, st);
-  kern<<<grid, TC_THREADS, smem, st>>>(ta, tb, s, ep);
-  g_last_launches.fetch_add(1);
-  return cudaGetLastError();
-}
-
-// The pair kernel: clusters of two CTAs on the two SMs of a TPC.
-// tg, tu: the TMA dG/dU epilogue's maps of G and U (other epilogues: unused)
-template <int AM, int BMODE, bool BF16, class Epi, int BN = TC2_BN>
-cudaError_t launch_tc2(int kid, const CUtensorMap& ta, const CUtensorMap& tb, const TcShape& s,
-                       const typename Epi::Params& ep, cudaStream_t st,
-                       const CUtensorMap* tg = nullptr, const CUtensorMap* tu = nullptr) {
-  // the TMA dG/dU epilogue's slots (GU_SLOTS x 4 KB per epilogue warp) take
-  // the room of GU_SLOTS - 1 ring stages; 512-column tiles (48 KB stages)
-  // keep four
-  constexpr bool gu = epi_tma_gu<Epi>::value;
-  constexpr int stages = BN > 256 ? 4 : (gu ? TC2_STAGES + 1 - GU_SLOTS : TC2_STAGES);
-  auto kern = tc2_gemm_kernel<stages, AM, BMODE, BF16, Epi, BN>;
-  constexpr int smem = Tc2Smem<stages, gu, BN>::DYN_BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int units = launch_units(s, tc2_units());
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * units));
-  cfg.blockDim = dim3(TC_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  ProfScope prof(kid, st);
-  e = cudaLaunchKernelEx(&cfg, kern, ta, tb, s, ep, tg != nullptr ? *tg : ta,
-                         tu != nullptr ? *tu : tb);
-  g_last_launches.fetch_add(1);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
-}
-
-template <int AM, int BMODE, bool BF16, class Epi>
-cudaError_t launch_gemm(bool pairs, int kid, const CUtensorMap& ta, const CUtensorMap& tb,
-                        const TcShape& s, const typename Epi::Params& ep, cudaStream_t st) {
-  return pairs ? launch_tc2<AM, BMODE, BF16, Epi>(kid, ta, tb, s, ep, st)
-               : launch_tc<AM, BMODE, BF16, Epi>(kid, ta, tb, s, ep, st);
-}
-
-template <bool DUAL, class Epi>
-cudaError_t launch_simt(int kid, SimtOperand A, SimtOperand B, SimtOperand B2, int64_t M,
-                        int64_t N, int64_t K, const Epi& epi, const SimtCheck& chk,
-                        cudaStream_t st) {
-  dim3 grid((unsigned)((N + SG_BN - 1) / SG_BN), (unsigned)((M + SG_BM - 1) / SG_BM));
-  ProfScope prof(kid, st);
-  simt_gemm_kernel<DUAL, Epi>
-      <<<grid, SG_THREADS, 0, st>>>(A, B, B2, (int)M, (int)N, (int)K, epi, chk);
-  g_last_launches.fetch_add(1);
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -564,8 +203,6 @@ __global__ void pack_weights_kernel(const uint8_t* __restrict__ Wgu, const uint8
 // ---------------------------------------------------------------------------
 // no-grad forward for M <= 64 tokens: split-contraction swap-AB kernels
 // ---------------------------------------------------------------------------
-constexpr int NG_MAX_M = 64;
-constexpr int NG_MAX_CTAS = 256;  // stream-K CTAs per launch (one per SM, capped)
 
 struct NgPlan {
   int NT;
@@ -601,29 +238,6 @@ NgPlan ng_plan(int64_t M, int64_t D, int64_t H, int nt = 0) {
 
 NgPlan ng_fused_plan(int64_t M, int64_t D, int64_t H) {
   return ng_plan(M, D, H, M <= 16 ? 16 : (M <= 32 ? 32 : 64));
-}
-
-// CTAs, stream-K tiles and partial slots per CTA of one GEMM over at most
-// `grid` CTAs.  With tiles >= CTAs, all but (tiles mod CTAs) tiles are taken
-// whole, the same number per CTA; with fewer k-blocks than CTAs to share, the
-// count shrinks so that every sharing CTA owns at least one.
-void ng_split(int tiles, int kb, int grid, int& ctas, int& sk_tiles, int& seg_max) {
-  int64_t c = grid < 1 ? 1 : grid;
-  sk_tiles = tiles >= c ? (int)(tiles % c) : tiles;
-  const int64_t total = (int64_t)sk_tiles * kb;
-  if (total > 0 && c > total && tiles < c) c = total;
-  ctas = (int)c;
-  const int64_t range = total > 0 ? (total + c - 1) / c : 0;
-  seg_max = (int)((range + kb - 1) / kb) + 1;
-}
-
-int ng_max_grid() {
-  const int nsm = sm_count();
-  return nsm < 1 ? 1 : (nsm < NG_MAX_CTAS ? nsm : NG_MAX_CTAS);
-}
-
-void ng_grid(int tiles, int kb, int& ctas, int& sk_tiles, int& seg_max) {
-  ng_split(tiles, kb, ng_max_grid(), ctas, sk_tiles, seg_max);
 }
 
 // The fused kernel's work units.  gate/up: runs of 64 k-blocks (the
@@ -689,37 +303,6 @@ size_t ng_two_bytes(const NgPlan& p) {
   ng_grid(p.t2, p.kb2, c2, k2, s2);
   const size_t slots1 = (size_t)c1 * s1, slots2 = (size_t)c2 * s2;
   return WS_HEADER + p.counter_bytes + (slots1 > slots2 ? slots1 : slots2) * 128 * p.NT * 4;
-}
-
-template <int NT, bool GATE_UP, bool BF16, bool PACKED = false>
-cudaError_t launch_ng(int kid, const CUtensorMap& tw, const CUtensorMap& tx, NgArgs a,
-                      cudaStream_t st) {
-  auto kern = ng_gemm_kernel<NT, GATE_UP, BF16, PACKED>;
-  constexpr int smem = NgSmem<NT>::DYN_BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  int grid = 1;
-  ng_grid(a.tiles, a.kb_tile, grid, a.sk_tiles, a.seg_max);
-  a.ctas = grid;
-  ProfScope prof(kid, st);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(NG_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  // the down kernel overlaps its prologue and weight prefetch with gate/up's tail
-  // (per-kernel event timing would serialise the two, so it is not used then)
-  const bool pdl = a.dependent && !g_prof_on.load();
-  if (!pdl) a.dependent = 0;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
-  g_last_launches.fetch_add(1);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
 }
 
 // ws layout: [0, 256) header (error word at 0); per-tile counters of the
@@ -816,7 +399,7 @@ swiglu_status ng_forward_fused(const void* X, const void* Wgu, const void* Wd, v
   f.ph[1].scale = o.dm;
   set_windows(f.ph[0], {{A, (size_t)(M * H * 2)}, {ws, ws_cap}});
   set_windows(f.ph[1], {{Y, (size_t)(M * D * 2)}, {ws, ws_cap}});
-  ProfScope prof(K_NG_FUSED, st);
+  host::Prof prof(K_NG_FUSED, st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)d.grid);
   cfg.blockDim = dim3(NG_THREADS);
@@ -1195,6 +778,79 @@ void reset_launches() { g_last_launches.store(0); }
 void count_launch() { g_last_launches.fetch_add(1); }
 int sms() { return sm_count(); }
 bool profiling() { return g_prof_on.load() != 0; }
+int cta_pairs() { return g_cta_pairs.load(); }
+int wide_tiles() { return g_wide_tiles.load(); }
+
+int pair_units() {
+  static std::mutex mu;
+  static int cached[64];
+  static bool done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> g(mu);
+  if (!done[dev]) {
+    int n = 0;
+    auto kern = tc2_gemm_kernel<TC2_STAGES, LOAD_KMAJOR, LOAD_KMAJOR, true, EpiStore>;
+    constexpr int smem = Tc2Smem<TC2_STAGES>::DYN_BYTES;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+        cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2);
+      cfg.blockDim = dim3(TC_THREADS);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    }
+    const int cap = tc_nsm() / 2;
+    cached[dev] = n < cap ? n : cap;
+    done[dev] = true;
+  }
+  return cached[dev];
+}
+
+template <bool BF16>
+static cudaError_t gemm_dw(int id, const void* G, const void* X, void* dW, int64_t M, int64_t N, int64_t K,
+                           int accumulate, int* err, size_t ws_bytes, cudaStream_t st) {
+  CUtensorMap mg, mx;
+  if (!map_mnmajor(&mg, BF16, G, N, M, N) || !map_mnmajor(&mx, BF16, X, K, M, K)) return cudaErrorInvalidValue;
+  const bool pairs = use_pairs(N, K, TC_BN, M), wide = use_wide(pairs, N, K, M);
+  TcShape s = make_shape(N, K, M, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
+  set_windows(s, {{dW, (size_t)(N * K * 2)}, {err, ws_bytes}});
+  const EpiStore::Params p{dW, K, 1.0f, accumulate};
+  return wide ? launch_tc2<LOAD_MNMAJOR, LOAD_MNMAJOR, BF16, EpiStore, TC2_WIDE_BN>(id, mg, mx, s, p, st)
+              : launch_gemm<LOAD_MNMAJOR, LOAD_MNMAJOR, BF16, EpiStore>(pairs, id, mg, mx, s, p, st);
+}
+
+cudaError_t gemm_dw(int id, bool bf16, const void* G, const void* X, void* dW, int64_t M, int64_t N,
+                    int64_t K, int accumulate, int* err, size_t ws_bytes, cudaStream_t st) {
+  return bf16 ? gemm_dw<true>(id, G, X, dW, M, N, K, accumulate, err, ws_bytes, st)
+              : gemm_dw<false>(id, G, X, dW, M, N, K, accumulate, err, ws_bytes, st);
+}
+
+template <bool BF16>
+static cudaError_t gemm_dx(int id, const void* G, const void* W, void* dX, int64_t M, int64_t N, int64_t K,
+                           int* err, size_t ws_bytes, cudaStream_t st) {
+  CUtensorMap mg, mw;
+  if (!map_kmajor(&mg, BF16, G, N, M, N, TC_BM) || !map_mnmajor(&mw, BF16, W, K, N, K)) return cudaErrorInvalidValue;
+  const bool pairs = use_pairs(M, K, TC_BN, N), wide = use_wide(pairs, M, K, N);
+  TcShape s = make_shape(M, K, N, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
+  set_windows(s, {{dX, (size_t)(M * K * 2)}, {err, ws_bytes}});
+  const EpiStore::Params p{dX, K, 1.0f, 0};
+  return wide ? launch_tc2<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiStore, TC2_WIDE_BN>(id, mg, mw, s, p, st)
+              : launch_gemm<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiStore>(pairs, id, mg, mw, s, p, st);
+}
+
+cudaError_t gemm_dx(int id, bool bf16, const void* G, const void* W, void* dX, int64_t M, int64_t N, int64_t K,
+                    int* err, size_t ws_bytes, cudaStream_t st) {
+  return bf16 ? gemm_dx<true>(id, G, W, dX, M, N, K, err, ws_bytes, st)
+              : gemm_dx<false>(id, G, W, dX, M, N, K, err, ws_bytes, st);
+}
 
 static bool encode_any(CUtensorMap* tm, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
                        const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
@@ -1233,13 +889,13 @@ bool encode_records(CUtensorMap* tm, const void* base, int record, int64_t n1, i
                     CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-Prof::Prof(ServingKernel id, cudaStream_t st) : st_(st) {
+Prof::Prof(int id, cudaStream_t st) : st_(st) {
   if (!g_prof_on.load()) return;
   std::lock_guard<std::mutex> g(g_prof_mu);
   cudaEvent_t a = prof_event();
   end_ = prof_event();
   cudaEventRecord(a, st);
-  g_prof_pending.push_back(ProfRec{K_SERVING + (int)id, a, end_});
+  g_prof_pending.push_back(ProfRec{id, a, end_});
 }
 
 Prof::~Prof() {
@@ -1520,7 +1176,7 @@ swiglu_status swiglu_mlp_graph_create_fwd_nograd(const void* X, const void* Wgu,
   }
   // device queries that are cached on first use run here, outside the capture
   sm_count();
-  if (dtype != SWIGLU_F32_IEEE) tc2_units();
+  if (dtype != SWIGLU_F32_IEEE) host::pair_units();
   cudaStream_t cs = nullptr;
   if (cudaStreamCreateWithFlags(&cs, cudaStreamNonBlocking) != cudaSuccess) {
     delete g;

@@ -1,0 +1,501 @@
+// block.cu -- C ABI of the operators around an MLP in a transformer block
+// (include/swiglu_mlp.h): layer norm, and linear layers with bias, activation
+// and residual.  Argument checks, plans and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/swiglu_mlp.h"
+#include "../csrc/tc_host.cuh"
+#include "column_sums.cuh"
+#include "layer_norm.cuh"
+#include "linear_epi.cuh"
+
+using namespace swiglu;
+
+namespace {
+
+constexpr int64_t LN_MAX_D = 16384;            // a row fits the registers of a block
+constexpr int64_t MAX_ROWS = 0x7fffffffLL - 256;  // the kernels' 32-bit row and column indexes
+constexpr size_t FIXED = WS_HEADER + TC_SK_COUNTER_BYTES;  // error word and counters of shared tiles
+static_assert(NG_MAX_CTAS * 4 <= TC_SK_COUNTER_BYTES, "the few-token kernel counts fewer shared tiles than blocks");
+
+swiglu_status status_of(cudaError_t e) { return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA; }
+
+size_t bytes_of(swiglu_dtype dt) { return dt == SWIGLU_F32_IEEE ? 4 : 2; }
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// Needed pointers are not null; all of them, given or null, are aligned.
+swiglu_status check_ptrs(std::initializer_list<const void*> needed,
+                         std::initializer_list<const void*> optional = {}) {
+  for (const void* p : needed)
+    if (p == nullptr) return SWIGLU_ERR_INVALID_ARG;
+  for (const void* p : needed)
+    if (misaligned(p)) return SWIGLU_ERR_ALIGNMENT;
+  for (const void* p : optional)
+    if (misaligned(p)) return SWIGLU_ERR_ALIGNMENT;
+  return SWIGLU_OK;
+}
+
+swiglu_status check_dtype(swiglu_dtype dt) {
+  return dt == SWIGLU_BF16 || dt == SWIGLU_F16 || dt == SWIGLU_F32_IEEE ? SWIGLU_OK
+                                                                        : SWIGLU_ERR_INVALID_ARG;
+}
+
+swiglu_status check_ws(const void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr || bytes < need) return SWIGLU_ERR_WORKSPACE;
+  return misaligned(ws) ? SWIGLU_ERR_ALIGNMENT : SWIGLU_OK;
+}
+
+int nsm() { return host::sms() > 0 ? host::sms() : 1; }
+
+RowCheck row_check(void* ws, std::initializer_list<Win> wins) {
+  RowCheck c;
+#ifdef SWIGLU_DEBUG
+  c.err = static_cast<int*>(ws);
+  c.win = host::windows(wins);
+#else
+  (void)ws;
+  (void)wins;
+#endif
+  return c;
+}
+
+// A launch that may start while the kernel before it on the stream ends; the
+// kernels wait for it before they touch anything.
+template <class... P, class... A>
+cudaError_t launch(int id, void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                   A... args) {
+  host::Prof prof(id, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // per-kernel event timing would serialise the launches, so no overlap then
+  cfg.attrs = attr;
+  cfg.numAttrs = host::profiling() ? 0 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  host::count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// f(a value of the storage type)
+template <class F>
+auto by_type(swiglu_dtype dt, F f) {
+  if (dt == SWIGLU_BF16) return f(__nv_bfloat16{});
+  if (dt == SWIGLU_F16) return f(__half{});
+  return f(float{});
+}
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+swiglu_status check_ln(int64_t M, int64_t D, swiglu_dtype dt) {
+  swiglu_status st = check_dtype(dt);
+  if (st != SWIGLU_OK) return st;
+  if (M < 0 || D <= 0) return SWIGLU_ERR_INVALID_ARG;
+  if (D % (16 / (int64_t)bytes_of(dt)) != 0) return SWIGLU_ERR_ALIGNMENT;
+  return M > MAX_ROWS || D > LN_MAX_D ? SWIGLU_ERR_UNSUPPORTED : SWIGLU_OK;
+}
+
+template <class T>
+cudaError_t ln_forward(const LnFwdArgs& a, cudaStream_t st) {
+  const int nv = a.D / Vec<T>::N;
+  auto rows4 = [&](auto k) { return launch(host::K_LN, k, dim3((unsigned)((a.M + 3) / 4)), 128, 0, st, a); };
+  auto row = [&](auto k, int tpr) { return launch(host::K_LN, k, dim3((unsigned)a.M), tpr, 0, st, a); };
+  if (nv <= 32) return rows4(ln_fwd_kernel<T, 32, 1, 4>);
+  if (nv <= 64) return rows4(ln_fwd_kernel<T, 32, 2, 4>);
+  if (nv <= 128) return rows4(ln_fwd_kernel<T, 32, 4, 4>);
+  if (nv <= 256) return row(ln_fwd_kernel<T, 128, 2, 1>, 128);
+  if (nv <= 512) return row(ln_fwd_kernel<T, 128, 4, 1>, 128);
+  if (nv <= 1024) return row(ln_fwd_kernel<T, 256, 4, 1>, 256);
+  if (nv <= 2048) return row(ln_fwd_kernel<T, 512, 4, 1>, 512);
+  return row(ln_fwd_kernel<T, 1024, 4, 1>, 1024);
+}
+
+// Threads of a row and vectors of a thread in the backward pass: two vectors
+// of every thread's as far as a block has threads for it.
+int lnb_tpr(int nv) {
+  int t = 32;
+  while (t < LNB_THREADS && t * 2 < nv) t *= 2;
+  return t;
+}
+int lnb_grid(int64_t M, int64_t D, swiglu_dtype dt) {
+  const int groups = LNB_THREADS / lnb_tpr((int)(D * (int64_t)bytes_of(dt) / 16));
+  return (int)std::min<int64_t>((M + groups - 1) / groups, nsm());
+}
+size_t ln_part_bytes(int64_t M, int64_t D, swiglu_dtype dt) {
+  return (size_t)lnb_grid(M, D, dt) * 2 * D * 4;
+}
+
+constexpr int LNB_SMEM = 200 * 1024;
+
+template <class T, int TPR, int VPT, bool DS>
+cudaError_t ln_backward(LnBwdArgs a, int grid, cudaStream_t st) {
+  constexpr auto kern = ln_bwd_kernel<T, TPR, VPT, DS>;
+  constexpr int stage = (DS ? 3 : 2) * VPT * LNB_THREADS * 16;
+  a.stages = std::min(5, LNB_SMEM / stage);
+  // the ring, and then the block's sums in its place
+  const int smem = std::max(a.stages * stage, 2 * a.D * 4);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LNB_SMEM);
+  if (e != cudaSuccess) return e;
+  return launch(host::K_DLN, kern, dim3((unsigned)grid), LNB_THREADS, (size_t)smem, st, a);
+}
+
+template <class T, int TPR, int VPT>
+cudaError_t ln_backward(const LnBwdArgs& a, int grid, cudaStream_t st) {
+  return a.ds != nullptr ? ln_backward<T, TPR, VPT, true>(a, grid, st)
+                         : ln_backward<T, TPR, VPT, false>(a, grid, st);
+}
+
+template <class T>
+cudaError_t ln_backward(const LnBwdArgs& a, int grid, cudaStream_t st) {
+  const int nv = a.D / Vec<T>::N;
+  if (nv <= 32) return ln_backward<T, 32, 1>(a, grid, st);
+  switch (lnb_tpr(nv)) {
+    case 32: return ln_backward<T, 32, 2>(a, grid, st);
+    case 64: return ln_backward<T, 64, 2>(a, grid, st);
+    case 128: return ln_backward<T, 128, 2>(a, grid, st);
+    case 256: return ln_backward<T, 256, 2>(a, grid, st);
+  }
+  if (nv <= 1024) return ln_backward<T, 512, 2>(a, grid, st);
+  if (nv <= 2048) return ln_backward<T, 512, 4>(a, grid, st);
+  if constexpr (sizeof(T) == 4) return ln_backward<T, 512, 8>(a, grid, st);
+  return cudaErrorInvalidConfiguration;
+}
+
+// out0, out1 = sums of the parts' columns [0, n) and [n, cols)
+cudaError_t column_sums(const float* part, int parts, int cols, void* out0, void* out1, int n, int add,
+                        swiglu_dtype dt, void* ws, size_t ws_bytes, cudaStream_t st) {
+  ColumnSumArgs a = {part, out0, out1, parts, cols, n, add, {}};
+  const size_t e = bytes_of(dt);
+  a.chk = row_check(ws, {{out0 != nullptr ? out0 : out1, (size_t)n * e}, {out1, out1 ? (size_t)(cols - n) * e : 0},
+                         {ws, ws_bytes}});
+  const dim3 grid((unsigned)((cols + CS_COLS - 1) / CS_COLS));
+  return by_type(dt, [&](auto t) {
+    return launch(host::K_COLUMN_SUMS, column_sum_kernel<decltype(t)>, grid, 256, 0, st, a);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// linear
+// ---------------------------------------------------------------------------
+bool few_tokens(int64_t M, swiglu_dtype dt) { return dt != SWIGLU_F32_IEEE && M <= NG_MAX_M; }
+
+swiglu_status check_linear(int64_t M, int64_t N, int64_t K, int act, swiglu_dtype dt) {
+  swiglu_status st = check_dtype(dt);
+  if (st != SWIGLU_OK) return st;
+  if (M < 0 || N <= 0 || K <= 0 || act < SWIGLU_ACT_NONE || act > SWIGLU_ACT_SILU)
+    return SWIGLU_ERR_INVALID_ARG;
+  const int64_t unit = 16 / (int64_t)bytes_of(dt);
+  if (N % unit != 0 || K % unit != 0) return SWIGLU_ERR_ALIGNMENT;
+  if (M > MAX_ROWS || N > MAX_ROWS || K > MAX_ROWS) return SWIGLU_ERR_UNSUPPORTED;
+  // tiles (of 64 x 64 at least) are counted in 32 bits
+  auto tiles = [](int64_t a, int64_t b) { return ((a + 63) / 64) * ((b + 63) / 64); };
+  return std::max({tiles(M, N), tiles(M, K), tiles(N, K)}) > 0x7fffffffLL ? SWIGLU_ERR_UNSUPPORTED
+                                                                         : SWIGLU_OK;
+}
+
+// Partial-tile bytes of one GEMM [Mg, N] over K on the tensor cores, either
+// form; without a device the bound for any GPU of up to 256 SMs.
+size_t gemm_part_bytes(int64_t Mg, int64_t N, int64_t K, bool may_be_wide) {
+  if (host::sms() < 1) return (size_t)2 * TC_SK_MAX_SMS * TC_BM * (may_be_wide ? TC2_WIDE_BN : TC_BN) * 4;
+  const int64_t kb = (K + TC_BK - 1) / TC_BK, nt = (N + TC_BN - 1) / TC_BN, rows2 = (Mg + TC2_BM - 1) / TC2_BM;
+  const int units = host::pair_units();
+  size_t best = tc_part_bytes(tc_plan(((Mg + TC_BM - 1) / TC_BM) * nt, kb, tc_nsm()));
+  if (units >= 1) {
+    best = std::max(best, 2 * tc_part_bytes(tc_plan(rows2 * nt, kb, units)));
+    if (may_be_wide)
+      best = std::max(best, 2 * tc_part_bytes(tc_plan(rows2 * ((N + TC2_WIDE_BN - 1) / TC2_WIDE_BN), kb, units),
+                                              TC2_WIDE_BN));
+  }
+  return best;
+}
+
+struct FewPlan {
+  int NT, tiles, kb, ctas, sk_tiles, seg_max;
+  size_t bytes;
+};
+// Only tiles that blocks share are counted, fewer than there are blocks: the
+// counters take the place of the training GEMMs', and like theirs are zero
+// between calls.
+FewPlan few_plan(int64_t M, int64_t N, int64_t K) {
+  FewPlan p;
+  p.NT = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 48 ? 48 : 64));
+  p.tiles = (int)((N + 127) / 128);
+  p.kb = (int)((K + TC_BK - 1) / TC_BK);
+  ng_grid(p.tiles, p.kb, p.ctas, p.sk_tiles, p.seg_max);
+  size_t slots = (size_t)p.ctas * p.seg_max;
+  if (host::sms() < 1) slots = (size_t)p.tiles + 3 * NG_MAX_CTAS;  // for any GPU
+  p.bytes = FIXED + slots * 128 * p.NT * 4;
+  return p;
+}
+
+// Parts of the rows whose column sums are taken apart, in the pass over dY:
+// about four blocks on each SM.
+int dact_parts(int64_t M, int64_t N, swiglu_dtype dt) {
+  const int64_t strips = (N * (int64_t)bytes_of(dt) + 511) / 512;
+  const int64_t most = (M + DA_WARPS * DA_BATCH - 1) / (DA_WARPS * DA_BATCH);
+  const int64_t want = (4 * (int64_t)(host::sms() > 0 ? host::sms() : TC_SK_MAX_SMS) + strips - 1) / strips;
+  return (int)std::max<int64_t>(1, std::min(want, most));
+}
+
+size_t linear_bwd_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dt) {
+  size_t n = (size_t)dact_parts(M, N, dt) * N * 4;
+  if (dt != SWIGLU_F32_IEEE) {
+    n = std::max(n, gemm_part_bytes(N, K, M, true));
+    n = std::max(n, gemm_part_bytes(M, K, N, true));
+  }
+  return FIXED + n;
+}
+
+template <int NT, bool BF16>
+cudaError_t linear_few(const FewPlan& p, const void* X, const void* W, NgArgs a, int64_t K, cudaStream_t st) {
+  CUtensorMap tw, tx;
+  if (!map_kmajor(&tw, BF16, W, K, a.rows, K, 128) || !map_kmajor(&tx, BF16, X, K, a.M, K, ng_x_rows(NT, a.M)))
+    return cudaErrorInvalidValue;
+  return launch_ng<NT, false, BF16, false, NgLinear>(host::K_LINEAR_FEW, tw, tx, a, st);
+}
+
+template <bool BF16>
+cudaError_t linear_forward(const void* X, const void* W, const EpiLinear::Params& ep, int64_t M, int64_t N,
+                           int64_t K, int* err, size_t ws_bytes, cudaStream_t st) {
+  const Win y{ep.y, (size_t)(M * N * 2)}, z{ep.z, ep.z ? (size_t)(M * N * 2) : 0},
+      res{ep.res, ep.res ? (size_t)(M * N * 2) : 0}, bias{ep.bias, ep.bias ? (size_t)N * 2 : 0}, w{err, ws_bytes};
+  if (M <= NG_MAX_M) {
+    const FewPlan p = few_plan(M, N, K);
+    NgArgs a{(int)M, (int)N, p.kb, p.tiles, 0, 0, nullptr, nullptr, nullptr, 0, 1, 0, 0, ep.y, N,
+             host::wait_limit_ns(), err};
+    a.counters = reinterpret_cast<int*>(reinterpret_cast<char*>(err) + WS_HEADER);
+    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(err) + FIXED);
+    a.zero_ptr = a.counters;
+    a.bias = ep.bias;
+    a.res = ep.res;
+    a.z = ep.z;
+    a.act = ep.act;
+    set_windows(a, {y, w, z, res, bias});
+    switch (p.NT) {
+      case 16: return linear_few<16, BF16>(p, X, W, a, K, st);
+      case 32: return linear_few<32, BF16>(p, X, W, a, K, st);
+      case 48: return linear_few<48, BF16>(p, X, W, a, K, st);
+      default: return linear_few<64, BF16>(p, X, W, a, K, st);
+    }
+  }
+  const bool pairs = use_pairs(M, N, TC_BN, K);
+  CUtensorMap tx, tw;
+  if (!map_kmajor(&tx, BF16, X, K, M, K, TC_BM) || !map_kmajor(&tw, BF16, W, K, N, K, pairs ? 128 : TC_BN))
+    return cudaErrorInvalidValue;
+  TcShape s = make_shape(M, N, K, TC_BN, err, pairs, part_capacity(ws_bytes));
+  set_windows(s, {y, w, z, res, bias});
+  return launch_gemm<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinear>(pairs, host::K_LINEAR, tx, tw, s, ep, st);
+}
+
+// dX = rnd(G W act'(Xpre)), G [M, N], W [N, K]
+template <bool BF16>
+cudaError_t linear_dx(const void* G, const void* W, const EpiDAct::Params& ep, int64_t M, int64_t N,
+                      int64_t K, int* err, size_t ws_bytes, cudaStream_t st) {
+  const bool pairs = use_pairs(M, K, TC_BN, N);
+  CUtensorMap tg, tw;
+  if (!map_kmajor(&tg, BF16, G, N, M, N, TC_BM) || !map_mnmajor(&tw, BF16, W, K, N, K))
+    return cudaErrorInvalidValue;
+  TcShape s = make_shape(M, K, N, TC_BN, err, pairs, part_capacity(ws_bytes));
+  set_windows(s, {{ep.out, (size_t)(M * K * 2)}, {err, ws_bytes}, {ep.pre, (size_t)(M * K * 2)}});
+  return launch_gemm<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiDAct>(pairs, host::K_LINEAR_DX, tg, tw, s, ep, st);
+}
+
+template <class Epi>
+cudaError_t simt_linear(int id, const float* A, int64_t am, int64_t ak, const float* B, int64_t bn, int64_t bk,
+                        int64_t Mg, int64_t N, int64_t K, const Epi& epi, int* err,
+                        std::initializer_list<Win> wins, cudaStream_t st) {
+  return launch_simt<false>(id, SimtOperand{A, am, ak}, SimtOperand{B, bn, bk}, SimtOperand{B, bn, bk}, Mg, N, K, epi,
+                            simt_check(err, wins), st);
+}
+
+}  // namespace
+
+extern "C" {
+
+swiglu_status swiglu_mlp_layer_norm_fwd(const void* X, const void* residual, const void* weight,
+                                        const void* bias, void* S, void* Y, float* mean, float* rstd,
+                                        int64_t M, int64_t D, float eps, swiglu_dtype dtype, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  host::reset_launches();
+  swiglu_status st = check_ln(M, D, dtype);
+  if (st != SWIGLU_OK) return st;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return SWIGLU_ERR_INVALID_ARG;
+  if (ws != nullptr && (st = check_ws(ws, ws_bytes, WS_HEADER)) != SWIGLU_OK) return st;
+  if (M == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, Y}, {residual, weight, bias, S, mean, rstd})) != SWIGLU_OK) return st;
+  if ((residual == nullptr) != (S == nullptr)) return SWIGLU_ERR_INVALID_ARG;
+  const size_t n = (size_t)(M * D) * bytes_of(dtype), d = (size_t)D * bytes_of(dtype);
+  LnFwdArgs a = {X, residual, weight, bias, S, Y, mean, rstd, M, (int)D, eps, {}};
+  a.chk = row_check(ws, {{Y, n}, {X, n}, {residual, residual ? n : 0}, {S, S ? n : 0}, {weight, weight ? d : 0}, {bias, bias ? d : 0},
+                         {mean, mean ? (size_t)M * 4 : 0}, {rstd, rstd ? (size_t)M * 4 : 0}});
+  return status_of(by_type(dtype, [&](auto t) { return ln_forward<decltype(t)>(a, static_cast<cudaStream_t>(stream)); }));
+}
+
+size_t swiglu_mlp_layer_norm_workspace_bytes(int64_t M, int64_t D, swiglu_dtype dtype) {
+  if (check_ln(M, D, dtype) != SWIGLU_OK) return 0;
+  if (host::sms() < 1) return FIXED + (size_t)TC_SK_MAX_SMS * 2 * D * 4;
+  return FIXED + ln_part_bytes(M, D, dtype);
+}
+
+swiglu_status swiglu_mlp_layer_norm_bwd(const void* dY, const void* S, const void* weight,
+                                        const float* mean, const float* rstd, const void* dS, void* dX,
+                                        void* dweight, void* dbias, int64_t M, int64_t D, int accumulate,
+                                        swiglu_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
+  host::reset_launches();
+  swiglu_status st = check_ln(M, D, dtype);
+  if (st != SWIGLU_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return SWIGLU_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, swiglu_mlp_layer_norm_workspace_bytes(M, D, dtype))) != SWIGLU_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t d = (size_t)D * bytes_of(dtype), n = (size_t)M * d;
+  if ((st = check_ptrs({}, {weight, dS, dweight, dbias})) != SWIGLU_OK) return st;
+  if (M == 0) {  // an empty batch adds nothing
+    cudaError_t e = cudaSuccess;
+    if (!accumulate && dweight != nullptr) e = cudaMemsetAsync(dweight, 0, d, s);
+    if (!accumulate && dbias != nullptr && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, d, s);
+    return status_of(e);
+  }
+  if ((st = check_ptrs({dY, S, mean, rstd, dX})) != SWIGLU_OK) return st;
+  if (cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return SWIGLU_ERR_CUDA;
+  LnBwdArgs a = {};
+  a.dy = dY;
+  a.s = S;
+  a.ds = dS;
+  a.w = weight;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = dX;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED);
+  a.M = M;
+  a.D = (int)D;
+  a.want = dweight != nullptr || dbias != nullptr;
+  const int grid = lnb_grid(M, D, dtype);
+  a.chk = row_check(ws, {{dX, n}, {ws, ws_bytes}, {dY, n}, {S, n}, {dS, dS ? n : 0}, {weight, weight ? d : 0}, {mean, (size_t)M * 4}, {rstd, (size_t)M * 4}});
+  st = status_of(by_type(dtype, [&](auto t) { return ln_backward<decltype(t)>(a, grid, s); }));
+  if (st != SWIGLU_OK || !a.want) return st;
+  return status_of(column_sums(a.part, grid, 2 * (int)D, dweight, dbias, (int)D, accumulate, dtype, ws, ws_bytes, s));
+}
+
+size_t swiglu_mlp_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dtype, int op) {
+  if (check_linear(M, N, K, 0, dtype) != SWIGLU_OK || (op != SWIGLU_OP_FWD && op != SWIGLU_OP_BWD)) return 0;
+  if (op == SWIGLU_OP_BWD) return linear_bwd_bytes(M, N, K, dtype);
+  if (dtype == SWIGLU_F32_IEEE) return FIXED;
+  if (few_tokens(M, dtype)) return few_plan(M, N, K).bytes;
+  return FIXED + gemm_part_bytes(M, N, K, false);
+}
+
+swiglu_status swiglu_mlp_linear_fwd(const void* X, const void* W, const void* bias, const void* residual,
+                                    void* Z, void* Y, int64_t M, int64_t N, int64_t K,
+                                    swiglu_activation act, swiglu_dtype dtype, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  host::reset_launches();
+  swiglu_status st = check_linear(M, N, K, act, dtype);
+  if (st != SWIGLU_OK) return st;
+  st = check_ws(ws, ws_bytes, swiglu_mlp_linear_workspace_bytes(M, N, K, dtype, SWIGLU_OP_FWD));
+  if (st != SWIGLU_OK) return st;
+  if (M == 0) return SWIGLU_OK;
+  if ((st = check_ptrs({X, W, Y}, {bias, residual, Z})) != SWIGLU_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = static_cast<int*>(ws);
+  if (dtype == SWIGLU_F32_IEEE) {
+    if (cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return SWIGLU_ERR_CUDA;
+    const SimtEpiLinear epi{(const float*)bias, (const float*)residual, (float*)Z, (float*)Y, N, act};
+    const size_t mn = (size_t)(M * N * 4);
+    return status_of(simt_linear(host::K_SIMT_LINEAR, (const float*)X, K, 1, (const float*)W, K, 1, M, N, K, epi, err,
+                                 {{Y, mn}, {X, (size_t)(M * K * 4)}, {W, (size_t)(N * K * 4)}, {bias, bias ? (size_t)N * 4 : 0},
+                                  {residual, residual ? mn : 0}, {Z, Z ? mn : 0}}, s));
+  }
+  if (!few_tokens(M, dtype) && cudaMemsetAsync(ws, 0, FIXED, s) != cudaSuccess) return SWIGLU_ERR_CUDA;
+  const EpiLinear::Params ep{bias, residual, Z, Y, N, act};
+  return status_of(dtype == SWIGLU_BF16 ? linear_forward<true>(X, W, ep, M, N, K, err, ws_bytes, s)
+                                        : linear_forward<false>(X, W, ep, M, N, K, err, ws_bytes, s));
+}
+
+swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W, const void* Z,
+                                    swiglu_activation act, const void* X_pre, swiglu_activation x_act,
+                                    void* dZ, void* dX, void* dW, void* dbias, int64_t M, int64_t N,
+                                    int64_t K, int accumulate, swiglu_dtype dtype, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  host::reset_launches();
+  swiglu_status st = check_linear(M, N, K, act, dtype);
+  if (st == SWIGLU_OK) st = check_linear(M, N, K, x_act, dtype);
+  if (st != SWIGLU_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return SWIGLU_ERR_INVALID_ARG;
+  st = check_ws(ws, ws_bytes, swiglu_mlp_linear_workspace_bytes(M, N, K, dtype, SWIGLU_OP_BWD));
+  if (st != SWIGLU_OK) return st;
+  const int64_t e = (int64_t)bytes_of(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = check_ptrs({}, {Z, X_pre, dZ, dX, dW, dbias})) != SWIGLU_OK) return st;
+  if (M == 0) {  // an empty batch adds nothing
+    cudaError_t c = cudaSuccess;
+    if (!accumulate && dW != nullptr) c = cudaMemsetAsync(dW, 0, (size_t)(N * K * e), s);
+    if (!accumulate && dbias != nullptr && c == cudaSuccess) c = cudaMemsetAsync(dbias, 0, (size_t)(N * e), s);
+    return status_of(c);
+  }
+  if ((st = check_ptrs({dY})) != SWIGLU_OK) return st;
+  if (act != SWIGLU_ACT_NONE && (st = check_ptrs({Z, dZ})) != SWIGLU_OK) return st;
+  if (dX != nullptr && (st = check_ptrs({W})) != SWIGLU_OK) return st;
+  if (dX != nullptr && x_act != SWIGLU_ACT_NONE && (st = check_ptrs({X_pre})) != SWIGLU_OK) return st;
+  if (dW != nullptr && (st = check_ptrs({X})) != SWIGLU_OK) return st;
+  if (cudaMemsetAsync(ws, 0, dtype == SWIGLU_F32_IEEE ? sizeof(int) : FIXED, s) != cudaSuccess) return SWIGLU_ERR_CUDA;
+  int* err = static_cast<int*>(ws);
+  const size_t mn = (size_t)(M * N * e), mk = (size_t)(M * K * e), nk = (size_t)(N * K * e);
+  const void* G = dY;
+  if (act != SWIGLU_ACT_NONE || dbias != nullptr) {
+    const bool has = act != SWIGLU_ACT_NONE;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED);
+    const int parts = dact_parts(M, N, dtype);
+    DactArgs a = {dY, has ? Z : nullptr, has ? dZ : nullptr, dbias != nullptr ? part : nullptr, M, (int)N, act, {}};
+    a.chk = row_check(ws, {{has ? dZ : ws, has ? mn : ws_bytes}, {ws, ws_bytes}, {dY, mn}, {Z, has ? mn : 0}});
+    const dim3 grid((unsigned)((N * e + 511) / 512), (unsigned)parts);
+    cudaError_t c = by_type(dtype, [&](auto t) {
+      return launch(host::K_DACT, dact_kernel<decltype(t)>, grid, DA_THREADS, 0, s, a);
+    });
+    if (c == cudaSuccess && dbias != nullptr)
+      c = column_sums(part, parts, (int)N, dbias, nullptr, (int)N, accumulate, dtype, ws, ws_bytes, s);
+    if (c != cudaSuccess) return SWIGLU_ERR_CUDA;
+    if (has) G = dZ;
+  }
+  if (dtype == SWIGLU_F32_IEEE) {
+    const float *g = (const float*)G, *x = (const float*)X, *w = (const float*)W;
+    if (dW != nullptr) {
+      const SimtEpiStore epi{(float*)dW, K, 1.0f, accumulate};
+      if (simt_linear(host::K_SIMT_LINEAR_DW, g, 1, N, x, 1, K, N, K, M, epi, err, {{dW, nk}, {G, mn}, {X, mk}}, s) != cudaSuccess)
+        return SWIGLU_ERR_CUDA;
+    }
+    if (dX != nullptr) {
+      const bool pre = x_act != SWIGLU_ACT_NONE;
+      const SimtEpiDAct epi{pre ? (const float*)X_pre : nullptr, (float*)dX, K, x_act};
+      if (simt_linear(host::K_SIMT_LINEAR_DX, g, N, 1, w, 1, K, M, K, N, epi, err,
+                      {{dX, mk}, {G, mn}, {W, nk}, {X_pre, pre ? mk : 0}}, s) != cudaSuccess)
+        return SWIGLU_ERR_CUDA;
+    }
+    return SWIGLU_OK;
+  }
+  const bool bf = dtype == SWIGLU_BF16;
+  if (dW != nullptr &&
+      host::gemm_dw(host::K_LINEAR_DW, bf, G, X, dW, M, N, K, accumulate, err, ws_bytes, s) != cudaSuccess)
+    return SWIGLU_ERR_CUDA;
+  if (dX != nullptr) {
+    const EpiDAct::Params ep{X_pre, dX, K, x_act};
+    const cudaError_t c = x_act == SWIGLU_ACT_NONE ? host::gemm_dx(host::K_LINEAR_DX, bf, G, W, dX, M, N, K, err, ws_bytes, s)
+                          : bf ? linear_dx<true>(G, W, ep, M, N, K, err, ws_bytes, s)
+                               : linear_dx<false>(G, W, ep, M, N, K, err, ws_bytes, s);
+    if (c != cudaSuccess) return SWIGLU_ERR_CUDA;
+  }
+  return SWIGLU_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,228 @@
+// linear_epi.cuh -- the epilogues of the linear operators, for the tensor-core
+// kernels (tc_gemm.cuh, tc2_gemm.cuh), the few-token kernel (ng_gemm.cuh) and
+// the fp32 kernel.
+//
+//   forward   z = acc + bias[n],  Z = rnd(z) where it is kept,  Y = rnd(act(z) + R)
+//   backward  dX = rnd(acc act'(Xpre)), the gradient of what X = act(Xpre) was made from
+//
+// Bias, activation and residual meet in fp32 and are rounded once.
+#pragma once
+
+#include "../csrc/ng_gemm.cuh"
+#include "../csrc/simt_gemm.cuh"
+#include "../csrc/tc2_gemm.cuh"
+#include "act.cuh"
+
+namespace swiglu {
+
+// Row pointers of one 32 x 32 chunk (first row mw, first column nc) of a
+// row-major 16-bit matrix; rows past the matrix are null.
+__device__ __forceinline__ auto chunk_rows(const TcShape& s, const void* base, int64_t ld, int mw,
+                                           int nc) {
+  return [=, &s](int r) -> uint8_t* {
+    const int m = mw + r;
+    return m < s.M ? static_cast<uint8_t*>(const_cast<void*>(base)) + ((int64_t)m * ld + nc) * 2
+                   : nullptr;
+  };
+}
+
+struct EpiLinear {
+  struct Params {
+    const void* bias;  // [N] or null
+    const void* res;   // [M, N] or null
+    void* z;           // [M, N] or null
+    void* y;           // [M, N]
+    int64_t ld;        // elements
+    int act;
+  };
+  template <int BN, bool BF16>
+  static __device__ __forceinline__ void run(const Params& p, const TcShape& s, uint32_t tacc,
+                                             int m0, int nt, int row, int half, uint8_t* buf) {
+    using P = Pack<BF16>;
+    const int lane = row & 31;
+    const int mw = m0 + (row & ~31);
+    const int n0 = nt * BN;
+#pragma unroll 1
+    for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
+      const int nc = n0 + c * 32;
+      auto ok = [&](int q) { return nc + q * 8 + 8 <= s.N; };
+      uint4 rw[4];
+      if (p.res != nullptr)
+        warp_load_issue(rw, lane, checked_rows(s, chunk_rows(s, p.res, p.ld, mw, nc), ok), ok);
+      uint4 bq[4];
+      const uint4* bias = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.bias) +
+                                                         (int64_t)nc * 2);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        bq[q] = p.bias != nullptr && ok(q) && SWIGLU_CHECK_PTR(s.dbg, bias + q, 16, s.err)
+                    ? bias[q]
+                    : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tacc + c * 32, r);
+      tmem_ld_wait();
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 b = P::unpack((&bq[i >> 2].x)[i & 3]);
+        v[2 * i] = __uint_as_float(r[2 * i]) + b.x;
+        v[2 * i + 1] = __uint_as_float(r[2 * i + 1]) + b.y;
+      }
+      uint32_t w[16];
+      if (p.z != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = P::two(v[2 * i], v[2 * i + 1]);
+        warp_store_tile(buf, w, lane, checked_rows(s, chunk_rows(s, p.z, p.ld, mw, nc), ok), ok);
+      }
+      act_switch(p.act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = ActMath<false>::value<decltype(a)::value>(v[i]);
+      });
+      if (p.res != nullptr) {
+        uint4 rr[4];
+        warp_load_finish(buf, rw, lane, rr);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 b = P::unpack((&rr[i >> 2].x)[i & 3]);
+          v[2 * i] += b.x;
+          v[2 * i + 1] += b.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = P::two(v[2 * i], v[2 * i + 1]);
+      warp_store_tile(buf, w, lane, checked_rows(s, chunk_rows(s, p.y, p.ld, mw, nc), ok), ok);
+    }
+  }
+};
+
+struct EpiDAct {
+  struct Params {
+    const void* pre;  // [M, N]
+    void* out;        // [M, N]
+    int64_t ld;       // elements
+    int act;
+  };
+  template <int BN, bool BF16>
+  static __device__ __forceinline__ void run(const Params& p, const TcShape& s, uint32_t tacc,
+                                             int m0, int nt, int row, int half, uint8_t* buf) {
+    using P = Pack<BF16>;
+    const int lane = row & 31;
+    const int mw = m0 + (row & ~31);
+    const int n0 = nt * BN;
+    constexpr int CH = BN / 64;
+    uint4 zw[4];  // the next chunk's
+    auto issue = [&](int c) {
+      const int nc = n0 + c * 32;
+      auto ok = [&](int q) { return nc + q * 8 + 8 <= s.N; };
+      warp_load_issue(zw, lane, checked_rows(s, chunk_rows(s, p.pre, p.ld, mw, nc), ok), ok);
+    };
+    issue(half * CH);
+#pragma unroll 1
+    for (int c = half * CH; c < (half + 1) * CH; ++c) {
+      const int nc = n0 + c * 32;
+      auto ok = [&](int q) { return nc + q * 8 + 8 <= s.N; };
+      uint4 zr[4];
+      warp_load_finish(buf, zw, lane, zr);
+      if (c + 1 < (half + 1) * CH) issue(c + 1);
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tacc + c * 32, r);
+      tmem_ld_wait();
+      uint32_t w[16];
+      act_switch(p.act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 z = P::unpack((&zr[i >> 2].x)[i & 3]);
+          w[i] = P::two(
+              __uint_as_float(r[2 * i]) * ActMath<false>::slope<decltype(a)::value>(z.x),
+              __uint_as_float(r[2 * i + 1]) * ActMath<false>::slope<decltype(a)::value>(z.y));
+        }
+      });
+      warp_store_tile(buf, w, lane, checked_rows(s, chunk_rows(s, p.out, p.ld, mw, nc), ok), ok);
+    }
+  }
+};
+
+// Few tokens: one thread has output feature d of all tokens.
+struct NgLinear {
+  static constexpr bool WAIT_FIRST = true;
+  template <bool BF16>
+  static __device__ __forceinline__ float get(const NgArgs& a, const void* base, int64_t at) {
+    using T = typename Pack<BF16>::T;
+    const T* p = static_cast<const T*>(base) + at;
+    if (!SWIGLU_CHECK_PTR(a.dbg, p, 2, a.err)) return 0.0f;
+    if constexpr (BF16)
+      return __bfloat162float(*p);
+    else
+      return __half2float(*p);
+  }
+  template <int NT, bool BF16>
+  static __device__ __forceinline__ void store(const NgArgs& a, int d, const float (&v)[NT]) {
+    const float b = a.bias != nullptr ? get<BF16>(a, a.bias, d) : 0.0f;
+    constexpr int G = 16;  // tokens at a time: their residuals are loaded together
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += G) {
+      if (n0 >= a.M) break;
+      float y[G], r[G];
+      if (a.res != nullptr) {
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          r[i] = n0 + i < a.M ? get<BF16>(a, a.res, (int64_t)(n0 + i) * a.ld_out + d) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) y[i] = v[n0 + i] + b;
+      if (a.z != nullptr) {
+        NgArgs z = a;
+        z.out = a.z;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          if (n0 + i < a.M) ng_put<BF16>(z, n0 + i, d, y[i]);
+      }
+      act_switch(a.act, [&](auto t) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) y[i] = ActMath<false>::value<decltype(t)::value>(y[i]);
+      });
+      if (a.res != nullptr) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) y[i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        if (n0 + i < a.M) ng_put<BF16>(a, n0 + i, d, y[i]);
+    }
+  }
+};
+
+// fp32
+struct SimtEpiLinear {
+  const float* bias;
+  const float* res;
+  float* z;
+  float* y;
+  int64_t ld;
+  int act;
+  __device__ __forceinline__ void apply(int m, int n, float acc, float, const SimtCheck& chk) const {
+    const int64_t o = (int64_t)m * ld + n;
+    float v = acc + (bias != nullptr ? simt_ld(bias + n, chk) : 0.0f);
+    if (z != nullptr && SWIGLU_CHECK_PTR(chk.win, z + o, 4, chk.err)) z[o] = v;
+    act_switch(act, [&](auto a) { v = ActMath<true>::value<decltype(a)::value>(v); });
+    if (res != nullptr) v = __fadd_rn(v, simt_ld(res + o, chk));
+    if (SWIGLU_CHECK_PTR(chk.win, y + o, 4, chk.err)) y[o] = v;
+  }
+};
+
+struct SimtEpiDAct {
+  const float* pre;
+  float* out;
+  int64_t ld;
+  int act;
+  __device__ __forceinline__ void apply(int m, int n, float acc, float, const SimtCheck& chk) const {
+    const int64_t o = (int64_t)m * ld + n;
+    float v = acc;
+    if (pre != nullptr) {
+      const float z = simt_ld(pre + o, chk);
+      act_switch(act, [&](auto a) { v = __fmul_rn(v, ActMath<true>::slope<decltype(a)::value>(z)); });
+    }
+    if (SWIGLU_CHECK_PTR(chk.win, out + o, 4, chk.err)) out[o] = v;
+  }
+};
+
+}  // namespace swiglu

@@ -428,6 +428,97 @@ swiglu_status swiglu_mlp_moe_fwd_nograd(const void* X, const void* Wr, const voi
                                         const swiglu_mlp_options* options, void* ws,
                                         size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * What stands around an MLP in a transformer block: layer norm, and linear
+ * layers with bias, activation and residual (the two halves of an MLP without
+ * a gate), each with its backward pass.  The pages have no counterpart: they
+ * are this library's forms of the layers next to its own.
+ *
+ * All three storage types; every rule above holds: row-major contiguous device
+ * tensors, 16-byte aligned, D, N and K multiples of 8 (4 for fp32), argument
+ * errors before any launch, asynchronous on `stream`, deterministic, one
+ * rounding per output.  Sizes beyond what the kernels index return
+ * SWIGLU_ERR_UNSUPPORTED: M, N or K above 2^31 - 257, more than 2^31 - 1 tiles
+ * of 64 x 64 in a product, rows of a layer norm longer than 16384.
+ * M = 0 launches nothing; the backward passes then set the weights' and
+ * biases' gradients to zero (or leave them, with `accumulate`).
+ * `accumulate` (0 or 1): 1 adds to the gradients of weights and biases that are
+ * there, with one rounding of the fp32 sum.
+ *
+ * Workspaces follow the workspace rules (zero-filled before first use and
+ * after a timeout; calls that share one must not overlap).  One that is large
+ * enough serves the calls of this section in turn, whatever their kinds and
+ * sizes; after calls of other sections its first 1280 bytes (header and
+ * counters) have to be zero again.
+ *
+ * Infinities and NaN give what the formulas give, in their own rows (and in
+ * the sums over rows); the activations' derivatives take their limits at
+ * infinities. */
+
+/* S = rnd(X + residual), or X where residual is NULL (then S is NULL too);
+ *   mu = mean of S's row,  rstd = (mean of (S - mu)^2 + eps)^-1/2,
+ *   Y = rnd((S - mu) rstd weight + bias).
+ * weight, bias [D]: NULL for 1 and 0.  mean, rstd: fp32 [M], kept for the
+ * backward pass, each NULL if not wanted.  S may be X's or the residual's
+ * buffer, and Y may be any of theirs where S is not.  ws: NULL, or a workspace of 256 bytes whose
+ * error word the debug build's checks record in.  One kernel. */
+swiglu_status swiglu_mlp_layer_norm_fwd(const void* X, const void* residual, const void* weight,
+                                        const void* bias, void* S, void* Y, float* mean, float* rstd,
+                                        int64_t M, int64_t D, float eps, swiglu_dtype dtype, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the backward pass (partial sums of the weight's and the
+ * bias's gradients); 0 for sizes that it refuses. */
+size_t swiglu_mlp_layer_norm_workspace_bytes(int64_t M, int64_t D, swiglu_dtype dtype);
+
+/* With h = (S - mean) rstd and t = dY weight, all of them the forward pass's:
+ *   dX = rnd(rstd (t - mean(t) - h mean(t h)) + dS)      (X's gradient, and the residual's)
+ *   dweight = sum over rows of dY h,   dbias = sum over rows of dY.
+ * dS: the gradient that reaches S on the residual stream's own way, or NULL.
+ * dweight, dbias: NULL if not wanted.  dX may be dY's or dS's buffer. */
+swiglu_status swiglu_mlp_layer_norm_bwd(const void* dY, const void* S, const void* weight,
+                                        const float* mean, const float* rstd, const void* dS, void* dX,
+                                        void* dweight, void* dbias, int64_t M, int64_t D, int accumulate,
+                                        swiglu_dtype dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Activations of the linear layers. */
+typedef enum {
+  SWIGLU_ACT_NONE = 0,
+  SWIGLU_ACT_RELU = 1,
+  SWIGLU_ACT_GELU = 2,       /* z Phi(z) */
+  SWIGLU_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  SWIGLU_ACT_SILU = 4        /* z / (1 + e^-z) */
+} swiglu_activation;
+
+/* Workspace bytes of a linear layer's pass (op: SWIGLU_OP_FWD, SWIGLU_OP_BWD);
+ * 0 for sizes that it refuses.  The size is for the current device. */
+size_t swiglu_mlp_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dtype, int op);
+
+/* z = X W^T + bias in fp32;  Y = rnd(act(z) + residual);  Z = rnd(z).
+ * X [M, K], W [N, K], bias [N] or NULL, residual [M, N] or NULL, Z [M, N] or
+ * NULL (kept for the backward pass of an activation), Y [M, N].  Y may be the
+ * residual's buffer.  One kernel: bf16 and fp16 up to 64 tokens stream the
+ * weights over all SMs, beyond that tcgen05 tiles; fp32 IEEE products. */
+swiglu_status swiglu_mlp_linear_fwd(const void* X, const void* W, const void* bias, const void* residual,
+                                    void* Z, void* Y, int64_t M, int64_t N, int64_t K,
+                                    swiglu_activation act, swiglu_dtype dtype, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* The backward pass for Y's gradient dY (the residual's gradient is dY):
+ *   dZ = rnd(dY act'(Z))                with an activation; dZ = dY without
+ *   dbias = sum over rows of dY act'(Z)  (the unrounded products)
+ *   dW [N, K] = dZ^T X,   dX [M, K] = dZ W.
+ * With x_act, X is act_x(X_pre) and dX becomes X_pre's gradient,
+ * rnd((dZ W) act_x'(X_pre)): the two halves of an MLP meet without a pass of
+ * their own.  Z and dZ [M, N] are needed where act is not SWIGLU_ACT_NONE (dZ is
+ * written), X_pre [M, K] where x_act is not and dX is wanted.  dX, dW, dbias:
+ * NULL if not wanted.  dZ may be dY's or Z's buffer, dX X_pre's. */
+swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W, const void* Z,
+                                    swiglu_activation act, const void* X_pre, swiglu_activation x_act,
+                                    void* dZ, void* dX, void* dW, void* dbias, int64_t M, int64_t N,
+                                    int64_t K, int accumulate, swiglu_dtype dtype, void* ws,
+                                    size_t ws_bytes, void* stream);
+
 /* Synchronises ``stream`` and reads the device error word in ``ws``:
  * SWIGLU_OK, SWIGLU_ERR_DEVICE_TIMEOUT, SWIGLU_ERR_DEVICE_BOUNDS (debug
  * builds), or SWIGLU_ERR_CUDA if the stream reported an error. */
