@@ -40,14 +40,11 @@ swiglu_status cuda_status(cudaError_t e);
 std::atomic<int> g_narrow_once{0};
 
 #ifdef SWIGLU_DEBUG
-DbgWin make_windows(std::initializer_list<Win> wins) {
+DbgWin make_windows(const Win* wins, int n) {
   DbgWin w = {};
-  int i = 0;
-  for (const Win& b : wins) {
-    if (i == DBG_WINS) break;
-    w.lo[i] = reinterpret_cast<uint64_t>(b.first);
-    w.hi[i] = w.lo[i] + b.second;
-    ++i;
+  for (int i = 0; i < n && i < DBG_WINS; ++i) {
+    w.lo[i] = reinterpret_cast<uint64_t>(wins[i].first);
+    w.hi[i] = w.lo[i] + wins[i].second;
   }
   if (g_narrow_once.exchange(0)) w.hi[0] = w.lo[0] + (w.hi[0] - w.lo[0]) / 2;
   return w;
@@ -904,8 +901,9 @@ Prof::~Prof() {
 
 #ifdef SWIGLU_DEBUG
 DbgWin windows(std::initializer_list<std::pair<const void*, size_t>> wins) {
-  return make_windows(wins);
+  return make_windows(wins.begin(), (int)wins.size());
 }
+DbgWin windows(const std::pair<const void*, size_t>* wins, int n) { return make_windows(wins, n); }
 #endif
 
 }  // namespace host

@@ -14,6 +14,8 @@
 #include "column_sums.cuh"
 #include "layer_norm.cuh"
 #include "linear_epi.cuh"
+#include "linear_few.cuh"
+#include "simt_linear.cuh"
 
 using namespace swiglu;
 
@@ -249,9 +251,34 @@ int dact_parts(int64_t M, int64_t N, swiglu_dtype dt) {
   return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
+// fp32 products: tile rows, and parts of the contraction.  Two blocks fit an SM;
+// with fewer tiles than that the contraction is split so that every SM has its
+// two (parts of 64 k at least), whose sums pass through the workspace.
+struct SlPlan {
+  int tm, m_tiles, n_tiles, parts, per;
+};
+SlPlan sl_plan(int64_t M, int64_t N, int64_t K) {
+  SlPlan p;
+  p.tm = M <= 32 ? 2 : 8;
+  p.m_tiles = (int)((M + 16 * p.tm - 1) / (16 * p.tm));
+  p.n_tiles = (int)((N + SL_BN - 1) / SL_BN);
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, room = 2 * (int64_t)nsm();
+  int64_t parts = std::max<int64_t>(1, std::min(room / std::max<int64_t>(tiles, 1), (K + 63) / 64));
+  p.per = (int)(((K + parts - 1) / parts + SL_BK - 1) / SL_BK * SL_BK);
+  p.parts = (int)((K + p.per - 1) / p.per);
+  return p;
+}
+size_t sl_bytes(int64_t M, int64_t N, int64_t K) {
+  if (host::sms() < 1) return (size_t)2 * TC_SK_MAX_SMS * 128 * SL_BN * 4;
+  const SlPlan p = sl_plan(M, N, K);
+  return p.parts > 1 ? (size_t)p.parts * M * N * 4 : 0;
+}
+
 size_t linear_bwd_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dt) {
   size_t n = (size_t)dact_parts(M, N, dt) * N * 4;
-  if (dt != SWIGLU_F32_IEEE) {
+  if (dt == SWIGLU_F32_IEEE) {
+    n = std::max({n, sl_bytes(N, K, M), sl_bytes(M, K, N)});
+  } else {
     n = std::max(n, gemm_part_bytes(N, K, M, true));
     n = std::max(n, gemm_part_bytes(M, K, N, true));
   }
@@ -266,11 +293,135 @@ cudaError_t linear_few(const FewPlan& p, const void* X, const void* W, NgArgs a,
   return launch_ng<NT, false, BF16, false, NgLinear>(host::K_LINEAR_FEW, tw, tx, a, st);
 }
 
+// Clusters of `split` blocks of a kernel that fit the device at once, kept per
+// device and size.
+template <auto KERNEL>
+int few_clusters(int split) {
+  static std::atomic<int> known[64][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  std::atomic<int>& at = known[dev][split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
+  int n = at.load();
+  if (n > 0) return n;
+  n = nsm() / split;
+  if (split > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n * split));
+    cfg.blockDim = dim3(LF_THREADS);
+    cfg.dynamicSmemBytes = LF_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int q = 0;
+    if (cudaOccupancyMaxActiveClusters(&q, KERNEL, &cfg) == cudaSuccess && q > 0) n = std::min(n, q);
+    cudaGetLastError();  // a failed query is not an error of the call
+  }
+  at.store(n = std::max(n, 1));
+  return n;
+}
+
+struct StreamPlan {
+  int nt, blocks, halves, xstride, recv_off, smem;
+  bool fits;
+};
+// Clusters of 4 blocks, whose warps in pairs split the contraction 8 ways, as
+// they reach every SM (38 clusters; of 8 blocks 15 fit, 120 SMs); of 8 where a
+// quarter of the token rows does not fit a block.
+// Large products of many tokens are left to the tcgen05 kernel, which streams
+// tokens with every tile but whose products cost it nothing.  Measured in us, this
+// form first, tokens 8 / 16 / 32 / 48 / 64:
+//   11008 x 4096   20.6, 27.0   21.8, 26.1   24.3, 31.1   34.3, 34.2   45.3, 39.6
+//   4096 x 11008   22.2, 23.7   23.5, 24.2   33.2, 27.6*  45.1, 31.8*  (* 8 blocks)
+//   2048 x 5632     8.6, 14.8    8.9, 15.0   10.2, 19.1   16.0, 23.0   18.3, 28.6*
+//   2816 x 1024     5.5, 12.3    5.8, 12.5    6.4, 16.4    7.9, 19.9    8.0, 24.7
+StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
+  StreamPlan p = {};
+  p.nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
+  const int64_t nk = (K + 31) / 32;
+  int parts = LF_MAX_PARTS;
+  while (parts > nk) parts /= 2;
+  for (p.blocks = std::min(parts, 4); p.blocks <= parts; p.blocks *= 2) {
+    p.halves = parts / p.blocks;
+    const int64_t per = (nk + p.blocks - 1) / p.blocks;
+    // rows an odd number of 64 bytes apart: 8 lanes' 16-byte reads of two rows meet no bank twice
+    const int64_t xs = (per | 1) * 64, bytes = M * xs + (int64_t)LF_WARPS * 2 * lf_recv(p.nt, parts);
+    if (bytes > LF_SMEM || (double)M * N * K >= (p.blocks <= 4 ? 0x1p31 : 0x1p30)) continue;
+    p.fits = true;
+    p.xstride = (int)xs;
+    p.recv_off = (int)(M * xs);
+    p.smem = (int)bytes;
+    break;
+  }
+  return p;
+}
+
+template <bool BF16, int NT>
+cudaError_t linear_stream(const StreamPlan& p, LfArgs a, cudaStream_t st) {
+  constexpr auto kern = linear_few_kernel<BF16, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LF_SMEM);
+  if (e != cudaSuccess) return e;
+  a.blocks = p.blocks;
+  a.halves = p.halves;
+  a.xstride = p.xstride;
+  a.recv_off = p.recv_off;
+  a.units = (a.N + 15) / 16;
+  const int groups = LF_WARPS / p.halves;
+  a.clusters = std::min(few_clusters<kern>(p.blocks), (a.units + groups - 1) / groups);
+  a.inject = host::take_stall() ? 1 : 0;
+  host::Prof prof(host::K_LINEAR_FEW, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.clusters * p.blocks));
+  cfg.blockDim = dim3(LF_THREADS);
+  cfg.dynamicSmemBytes = (size_t)p.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  // per-kernel event timing would serialise the launches, so no overlap then
+  if (!host::profiling()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (p.blocks > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n++].val.clusterDim = {(unsigned)p.blocks, 1, 1};
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  host::count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <bool BF16>
 cudaError_t linear_forward(const void* X, const void* W, const EpiLinear::Params& ep, int64_t M, int64_t N,
                            int64_t K, int* err, size_t ws_bytes, cudaStream_t st) {
   const Win y{ep.y, (size_t)(M * N * 2)}, z{ep.z, ep.z ? (size_t)(M * N * 2) : 0},
       res{ep.res, ep.res ? (size_t)(M * N * 2) : 0}, bias{ep.bias, ep.bias ? (size_t)N * 2 : 0}, w{err, ws_bytes};
+  const StreamPlan sp = M <= NG_MAX_M ? stream_plan(M, N, K) : StreamPlan{};
+  if (sp.fits) {
+    LfArgs a = {};
+    a.X = static_cast<const uint8_t*>(X);
+    a.W = static_cast<const uint8_t*>(W);
+    a.bias = static_cast<const uint8_t*>(ep.bias);
+    a.res = static_cast<const uint8_t*>(ep.res);
+    a.z = static_cast<uint8_t*>(ep.z);
+    a.y = static_cast<uint8_t*>(ep.y);
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.act = ep.act;
+    a.wait_limit_ns = host::wait_limit_ns();
+    a.err = err;
+    set_windows(a, {y, w, z, res, bias, {X, (size_t)(M * K * 2)}, {W, (size_t)(N * K * 2)}});
+    switch (sp.nt) {
+      case 1: return linear_stream<BF16, 1>(sp, a, st);
+      case 2: return linear_stream<BF16, 2>(sp, a, st);
+      case 4: return linear_stream<BF16, 4>(sp, a, st);
+      default: return linear_stream<BF16, 8>(sp, a, st);
+    }
+  }
   if (M <= NG_MAX_M) {
     const FewPlan p = few_plan(M, N, K);
     NgArgs a{(int)M, (int)N, p.kb, p.tiles, 0, 0, nullptr, nullptr, nullptr, 0, 1, 0, 0, ep.y, N,
@@ -312,12 +463,43 @@ cudaError_t linear_dx(const void* G, const void* W, const EpiDAct::Params& ep, i
   return launch_gemm<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiDAct>(pairs, host::K_LINEAR_DX, tg, tw, s, ep, st);
 }
 
-template <class Epi>
-cudaError_t simt_linear(int id, const float* A, int64_t am, int64_t ak, const float* B, int64_t bn, int64_t bk,
-                        int64_t Mg, int64_t N, int64_t K, const Epi& epi, int* err,
-                        std::initializer_list<Win> wins, cudaStream_t st) {
-  return launch_simt<false>(id, SimtOperand{A, am, ak}, SimtOperand{B, bn, bk}, SimtOperand{B, bn, bk}, Mg, N, K, epi,
-                            simt_check(err, wins), st);
+template <bool A_KC, bool B_KC, class Epi>
+cudaError_t simt_product(int id, const float* A, int64_t lda, const float* B, int64_t ldb, int64_t M, int64_t N,
+                         int64_t K, const Epi& epi, void* ws, std::initializer_list<Win> wins, cudaStream_t st) {
+  const SlPlan p = sl_plan(M, N, K);
+  SlArgs a = {A, B, lda, ldb, (int)M, (int)N, (int)K, p.m_tiles, p.n_tiles, p.per, nullptr, {}};
+  if (p.parts > 1) a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED);
+#ifdef SWIGLU_DEBUG
+  // the partial sums take the output's place in the first kernel, and follow it in the second
+  Win with[DBG_WINS];
+  const int nw = (int)(std::copy(wins.begin(), wins.end(), with) - with);
+  with[nw] = Win{a.part, p.parts > 1 ? (size_t)p.parts * M * N * 4 : 0};
+  if (p.parts > 1) std::swap(with[0], with[nw]);
+  a.chk.err = static_cast<int*>(ws);
+  a.chk.win = host::windows(with, nw + 1);
+#endif
+  const dim3 grid((unsigned)(p.m_tiles * p.n_tiles), (unsigned)p.parts);
+  {
+    host::Prof prof(id, st);
+    if (p.tm == 2)
+      simt_linear_kernel<2, A_KC, B_KC, Epi><<<grid, SL_THREADS, 0, st>>>(a, epi);
+    else
+      simt_linear_kernel<8, A_KC, B_KC, Epi><<<grid, SL_THREADS, 0, st>>>(a, epi);
+    host::count_launch();
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.parts == 1) return e;
+  const int64_t blocks = (M * N / 4 + 255) / 256;
+  SimtCheck chk = a.chk;
+#ifdef SWIGLU_DEBUG
+  std::swap(with[0], with[nw]);
+  chk.win = host::windows(with, nw + 1);
+#endif
+  host::Prof prof(id, st);
+  simt_sum_kernel<Epi><<<(unsigned)std::min<int64_t>(blocks, 8 * (int64_t)nsm()), 256, 0, st>>>(
+      a.part, p.parts, (int)M, (int)N, epi, chk);
+  host::count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -391,7 +573,7 @@ swiglu_status swiglu_mlp_layer_norm_bwd(const void* dY, const void* S, const voi
 size_t swiglu_mlp_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dtype, int op) {
   if (check_linear(M, N, K, 0, dtype) != SWIGLU_OK || (op != SWIGLU_OP_FWD && op != SWIGLU_OP_BWD)) return 0;
   if (op == SWIGLU_OP_BWD) return linear_bwd_bytes(M, N, K, dtype);
-  if (dtype == SWIGLU_F32_IEEE) return FIXED;
+  if (dtype == SWIGLU_F32_IEEE) return FIXED + sl_bytes(M, N, K);
   if (few_tokens(M, dtype)) return few_plan(M, N, K).bytes;
   return FIXED + gemm_part_bytes(M, N, K, false);
 }
@@ -411,11 +593,12 @@ swiglu_status swiglu_mlp_linear_fwd(const void* X, const void* W, const void* bi
   int* err = static_cast<int*>(ws);
   if (dtype == SWIGLU_F32_IEEE) {
     if (cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return SWIGLU_ERR_CUDA;
-    const SimtEpiLinear epi{(const float*)bias, (const float*)residual, (float*)Z, (float*)Y, N, act};
+    const SlEpiLinear epi{(const float*)bias, (const float*)residual, (float*)Z, (float*)Y, N, act};
     const size_t mn = (size_t)(M * N * 4);
-    return status_of(simt_linear(host::K_SIMT_LINEAR, (const float*)X, K, 1, (const float*)W, K, 1, M, N, K, epi, err,
-                                 {{Y, mn}, {X, (size_t)(M * K * 4)}, {W, (size_t)(N * K * 4)}, {bias, bias ? (size_t)N * 4 : 0},
-                                  {residual, residual ? mn : 0}, {Z, Z ? mn : 0}}, s));
+    return status_of(simt_product<true, true>(
+        host::K_SIMT_LINEAR, (const float*)X, K, (const float*)W, K, M, N, K, epi, ws,
+        {{Y, mn}, {X, (size_t)(M * K * 4)}, {W, (size_t)(N * K * 4)}, {bias, bias ? (size_t)N * 4 : 0},
+         {residual, residual ? mn : 0}, {Z, Z ? mn : 0}}, s));
   }
   if (!few_tokens(M, dtype) && cudaMemsetAsync(ws, 0, FIXED, s) != cudaSuccess) return SWIGLU_ERR_CUDA;
   const EpiLinear::Params ep{bias, residual, Z, Y, N, act};
@@ -471,15 +654,16 @@ swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W
   if (dtype == SWIGLU_F32_IEEE) {
     const float *g = (const float*)G, *x = (const float*)X, *w = (const float*)W;
     if (dW != nullptr) {
-      const SimtEpiStore epi{(float*)dW, K, 1.0f, accumulate};
-      if (simt_linear(host::K_SIMT_LINEAR_DW, g, 1, N, x, 1, K, N, K, M, epi, err, {{dW, nk}, {G, mn}, {X, mk}}, s) != cudaSuccess)
+      const SlEpiGrad epi{nullptr, (float*)dW, K, 0, accumulate};
+      if (simt_product<false, false>(host::K_SIMT_LINEAR_DW, g, N, x, K, N, K, M, epi, ws,
+                                     {{dW, nk}, {G, mn}, {X, mk}}, s) != cudaSuccess)
         return SWIGLU_ERR_CUDA;
     }
     if (dX != nullptr) {
       const bool pre = x_act != SWIGLU_ACT_NONE;
-      const SimtEpiDAct epi{pre ? (const float*)X_pre : nullptr, (float*)dX, K, x_act};
-      if (simt_linear(host::K_SIMT_LINEAR_DX, g, N, 1, w, 1, K, M, K, N, epi, err,
-                      {{dX, mk}, {G, mn}, {W, nk}, {X_pre, pre ? mk : 0}}, s) != cudaSuccess)
+      const SlEpiGrad epi{pre ? (const float*)X_pre : nullptr, (float*)dX, K, x_act, 0};
+      if (simt_product<true, false>(host::K_SIMT_LINEAR_DX, g, N, w, K, M, K, N, epi, ws,
+                                    {{dX, mk}, {G, mn}, {W, nk}, {X_pre, pre ? mk : 0}}, s) != cudaSuccess)
         return SWIGLU_ERR_CUDA;
     }
     return SWIGLU_OK;

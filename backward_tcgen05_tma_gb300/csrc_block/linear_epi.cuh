@@ -1,6 +1,5 @@
-// linear_epi.cuh -- the epilogues of the linear operators, for the tensor-core
-// kernels (tc_gemm.cuh, tc2_gemm.cuh), the few-token kernel (ng_gemm.cuh) and
-// the fp32 kernel.
+// linear_epi.cuh -- the epilogues of the linear operators for the tensor-core
+// kernels (tc_gemm.cuh, tc2_gemm.cuh) and the few-token one (ng_gemm.cuh).
 //
 //   forward   z = acc + bias[n],  Z = rnd(z) where it is kept,  Y = rnd(act(z) + R)
 //   backward  dX = rnd(acc act'(Xpre)), the gradient of what X = act(Xpre) was made from
@@ -9,7 +8,6 @@
 #pragma once
 
 #include "../csrc/ng_gemm.cuh"
-#include "../csrc/simt_gemm.cuh"
 #include "../csrc/tc2_gemm.cuh"
 #include "act.cuh"
 
@@ -188,40 +186,6 @@ struct NgLinear {
       for (int i = 0; i < G; ++i)
         if (n0 + i < a.M) ng_put<BF16>(a, n0 + i, d, y[i]);
     }
-  }
-};
-
-// fp32
-struct SimtEpiLinear {
-  const float* bias;
-  const float* res;
-  float* z;
-  float* y;
-  int64_t ld;
-  int act;
-  __device__ __forceinline__ void apply(int m, int n, float acc, float, const SimtCheck& chk) const {
-    const int64_t o = (int64_t)m * ld + n;
-    float v = acc + (bias != nullptr ? simt_ld(bias + n, chk) : 0.0f);
-    if (z != nullptr && SWIGLU_CHECK_PTR(chk.win, z + o, 4, chk.err)) z[o] = v;
-    act_switch(act, [&](auto a) { v = ActMath<true>::value<decltype(a)::value>(v); });
-    if (res != nullptr) v = __fadd_rn(v, simt_ld(res + o, chk));
-    if (SWIGLU_CHECK_PTR(chk.win, y + o, 4, chk.err)) y[o] = v;
-  }
-};
-
-struct SimtEpiDAct {
-  const float* pre;
-  float* out;
-  int64_t ld;
-  int act;
-  __device__ __forceinline__ void apply(int m, int n, float acc, float, const SimtCheck& chk) const {
-    const int64_t o = (int64_t)m * ld + n;
-    float v = acc;
-    if (pre != nullptr) {
-      const float z = simt_ld(pre + o, chk);
-      act_switch(act, [&](auto a) { v = __fmul_rn(v, ActMath<true>::slope<decltype(a)::value>(z)); });
-    }
-    if (SWIGLU_CHECK_PTR(chk.win, out + o, 4, chk.err)) out[o] = v;
   }
 };
 

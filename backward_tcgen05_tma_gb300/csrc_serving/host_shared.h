@@ -77,6 +77,7 @@ class Prof {
 
 #ifdef SWIGLU_DEBUG
 DbgWin windows(std::initializer_list<std::pair<const void*, size_t>> wins);
+DbgWin windows(const std::pair<const void*, size_t>* wins, int n);
 #endif
 
 }  // namespace host
