@@ -13,6 +13,10 @@
 // whose error in erf is at most 1.5e-7, below 2^-13 of half a step of either
 // 16-bit type around 1.  With w = |z| / sqrt 2 its exponential is e^(-z^2/2),
 // which is also what Phi' needs, so the derivative costs two products more.
+// Values go in pairs through fma.rn.f32x2 and the like, as the epilogues that
+// apply them are bound by the instructions they issue; for the same reason gelu
+// and gelu_tanh let exponentials below 2^-126 become 0 (the forms that keep them
+// take four instructions more each: 16384 x 2816 x 1024 with gelu 129 -> 93 us).
 //
 // Values that are not numbers pass through every function.  Infinities give
 // what the formulas give (minus infinity times 0 is NaN in gelu, gelu_tanh and
@@ -25,60 +29,147 @@ namespace swiglu {
 
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 
-template <bool PRECISE>
-struct ActMath {
-  static __device__ __forceinline__ float sigmoid(float x) {
-    if constexpr (PRECISE) {
-      const float t = expf(-fabsf(x));
-      return x >= 0.0f ? 1.0f / (1.0f + t) : t / (1.0f + t);
-    } else {
-      return sigmoid_f32(x);
-    }
+// two fp32 values in one register pair
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+  __device__ __forceinline__ explicit F2(uint64_t p) : v(p) {}
+  __device__ __forceinline__ void get(float& a, float& b) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
   }
-  // Phi(z), and e = e^(-z^2 / 2)
-  static __device__ __forceinline__ float phi(float z, float& e) {
-    if constexpr (PRECISE) {
-      e = expf(-0.5f * z * z);
-      return normcdff(z);
-    } else {
-      float t;
-      asm("rcp.approx.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.0f)));
-      e = exp_nonpos_f32(-0.5f * z * z);
-      const float p =
-          t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f),
-                                   0.5f * 1.421413741f), 0.5f * -0.284496736f), 0.5f * 0.254829592f);
-      const float q = p * e;  // Phi(-|z|)
-      return z >= 0.0f ? 1.0f - q : q;
-    }
-  }
-  static constexpr float TANH_K = 1.5957691216057308f;  // 2 sqrt(2/pi)
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
+constexpr float ACT_TANH_K = 1.5957691216057308f;  // 2 sqrt(2/pi)
+
+// e = e^(-z^2 / 2) and h = 1/2 - Phi(-|z|), for both
+__device__ __forceinline__ void phi2(F2 z, float z0, float z1, F2& e, F2& h) {
+  float a0, a1;
+  mul2(mul2(z, z), F2(-0.72134752044448170f)).get(a0, a1);
+  e = F2(ex2_ftz(a0), ex2_ftz(a1));
+  constexpr float P = 0.3275911f * 0.70710678118654752f;
+  const F2 t(rcp_ftz(fmaf(fabsf(z0), P, 1.0f)), rcp_ftz(fmaf(fabsf(z1), P, 1.0f)));
+  F2 p = fma2(t, F2(-0.5f * 1.061405429f), F2(0.5f * 1.453152027f));
+  p = fma2(t, p, F2(-0.5f * 1.421413741f));
+  p = fma2(t, p, F2(0.5f * 0.284496736f));
+  p = fma2(t, p, F2(-0.5f * 0.254829592f));
+  h = fma2(mul2(p, t), e, F2(0.5f));
+}
+// sigma(2 sqrt(2/pi) (z + 0.044715 z^3)); far left 1 / (1 + infinity)
+__device__ __forceinline__ F2 sigma_tanh2(F2 z, F2 zz) {
+  float u0, u1, d0, d1;
+  mul2(mul2(z, F2(-ACT_TANH_K * 1.4426950408889634f)), fma2(zz, F2(0.044715f), F2(1.0f))).get(u0, u1);
+  add2(F2(ex2_ftz(u0), ex2_ftz(u1)), F2(1.0f)).get(d0, d1);
+  return F2(rcp_ftz(d0), rcp_ftz(d1));
+}
+
+// 16-bit storage
+template <int A>
+__device__ __forceinline__ void act_value2(float& a, float& b) {
+  if constexpr (A == ACT_RELU) {
+    a = a < 0.0f ? 0.0f : a;
+    b = b < 0.0f ? 0.0f : b;
+  } else if constexpr (A == ACT_GELU) {
+    const F2 z(a, b);
+    F2 e(0.0f), h(0.0f);
+    phi2(z, a, b, e, h);
+    float h0, h1, y0, y1;
+    h.get(h0, h1);
+    mul2(z, F2(0.5f)).get(y0, y1);
+    a = fmaf(fabsf(a), h0, y0);  // z Phi(z) = z / 2 + |z| h
+    b = fmaf(fabsf(b), h1, y1);
+  } else if constexpr (A == ACT_GELU_TANH) {
+    const F2 z(a, b);
+    mul2(z, sigma_tanh2(z, mul2(z, z))).get(a, b);
+  } else if constexpr (A == ACT_SILU) {
+    a = silu_f32(a);
+    b = silu_f32(b);
+  }
+}
+// the derivatives; past |z| = 128 their last term is 0 in fp32, and is left out so
+// that no infinity meets that 0
+template <int A>
+__device__ __forceinline__ void act_slope2(float& a, float& b) {
+  if constexpr (A == ACT_RELU) {
+    a = a <= 0.0f ? 0.0f : 1.0f;
+    b = b <= 0.0f ? 0.0f : 1.0f;
+  } else if constexpr (A == ACT_GELU) {
+    const F2 z(a, b);
+    F2 e(0.0f), h(0.0f);
+    phi2(z, a, b, e, h);
+    float h0, h1, f0, f1;
+    h.get(h0, h1);
+    mul2(mul2(z, e), F2(0.3989422804014327f)).get(f0, f1);
+    const float p0 = 0.5f + copysignf(h0, a), p1 = 0.5f + copysignf(h1, b);  // Phi(z)
+    a = p0 + (fabsf(a) < 128.0f ? f0 : 0.0f);
+    b = p1 + (fabsf(b) < 128.0f ? f1 : 0.0f);
+  } else if constexpr (A == ACT_GELU_TANH) {
+    const F2 z(a, b), zz = mul2(z, z), p = sigma_tanh2(z, zz);
+    float p0, p1, f0, f1;
+    p.get(p0, p1);
+    const F2 rest = mul2(mul2(z, p), fma2(p, F2(-1.0f), F2(1.0f)));
+    mul2(rest, fma2(zz, F2(ACT_TANH_K * 0.134145f), F2(ACT_TANH_K))).get(f0, f1);
+    a = p0 + (fabsf(a) < 128.0f ? f0 : 0.0f);
+    b = p1 + (fabsf(b) < 128.0f ? f1 : 0.0f);
+  } else if constexpr (A == ACT_SILU) {
+    const float p0 = sigmoid_f32(a), p1 = sigmoid_f32(b);
+    a = fabsf(a) < 128.0f ? fmaf(a * p0, 1.0f - p0, p0) : p0;
+    b = fabsf(b) < 128.0f ? fmaf(b * p1, 1.0f - p1, p1) : p1;
+  } else {
+    a = b = 1.0f;
+  }
+}
+
+// fp32 storage: CUDA's functions
+struct ActPrecise {
+  static __device__ __forceinline__ float sigmoid(float x) {
+    const float t = expf(-fabsf(x));
+    return x >= 0.0f ? 1.0f / (1.0f + t) : t / (1.0f + t);
+  }
   template <int A>
   static __device__ __forceinline__ float value(float z) {
     if constexpr (A == ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if constexpr (A == ACT_GELU) {
-      float e;
-      return z * phi(z, e);
-    }
-    if constexpr (A == ACT_GELU_TANH)
-      return z * sigmoid(TANH_K * z * fmaf(0.044715f * z, z, 1.0f));
+    if constexpr (A == ACT_GELU) return z * normcdff(z);
+    if constexpr (A == ACT_GELU_TANH) return z * sigmoid(ACT_TANH_K * z * fmaf(0.044715f * z, z, 1.0f));
     if constexpr (A == ACT_SILU) return z * sigmoid(z);
     return z;
   }
-  // the derivative; past |z| = 128 its last term is 0 in fp32, and is left out
-  // so that no infinity meets that 0
   template <int A>
   static __device__ __forceinline__ float slope(float z) {
     if constexpr (A == ACT_RELU) return z <= 0.0f ? 0.0f : 1.0f;
     const bool in = fabsf(z) < 128.0f;
     if constexpr (A == ACT_GELU) {
-      float e;
-      const float p = phi(z, e);
-      return in ? fmaf(z * e, 0.3989422804014327f, p) : p;
+      const float p = normcdff(z);
+      return in ? fmaf(z * expf(-0.5f * z * z), 0.3989422804014327f, p) : p;
     }
     if constexpr (A == ACT_GELU_TANH) {
-      const float p = sigmoid(TANH_K * z * fmaf(0.044715f * z, z, 1.0f));
-      return in ? fmaf(z * p * (1.0f - p), TANH_K * fmaf(0.134145f * z, z, 1.0f), p) : p;
+      const float p = sigmoid(ACT_TANH_K * z * fmaf(0.044715f * z, z, 1.0f));
+      return in ? fmaf(z * p * (1.0f - p), ACT_TANH_K * fmaf(0.134145f * z, z, 1.0f), p) : p;
     }
     if constexpr (A == ACT_SILU) {
       const float p = sigmoid(z);

@@ -124,11 +124,11 @@ cudaError_t ln_forward(const LnFwdArgs& a, cudaStream_t st) {
   return row(ln_fwd_kernel<T, 1024, 4, 1>, 1024);
 }
 
-// Threads of a row and vectors of a thread in the backward pass: two vectors
-// of every thread's as far as a block has threads for it.
+// Threads of a row in the backward pass: four vectors each as far as a block has
+// threads for it.
 int lnb_tpr(int nv) {
   int t = 32;
-  while (t < LNB_THREADS && t * 2 < nv) t *= 2;
+  while (t < LNB_THREADS && t * 4 < nv) t *= 2;
   return t;
 }
 int lnb_grid(int64_t M, int64_t D, swiglu_dtype dt) {
@@ -146,8 +146,9 @@ cudaError_t ln_backward(LnBwdArgs a, int grid, cudaStream_t st) {
   constexpr auto kern = ln_bwd_kernel<T, TPR, VPT, DS>;
   constexpr int stage = (DS ? 3 : 2) * VPT * LNB_THREADS * 16;
   a.stages = std::min(5, LNB_SMEM / stage);
-  // the ring, and then the block's sums in its place
-  const int smem = std::max(a.stages * stage, 2 * a.D * 4);
+  // the ring, and then the groups' sums in its place
+  constexpr int groups = LNB_THREADS / TPR, n = Vec<T>::N;
+  const int smem = std::max(a.stages * stage, groups * 2 * (a.D + 4 * n) * 4);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LNB_SMEM);
   if (e != cudaSuccess) return e;
   return launch(host::K_DLN, kern, dim3((unsigned)grid), LNB_THREADS, (size_t)smem, st, a);
@@ -163,13 +164,13 @@ template <class T>
 cudaError_t ln_backward(const LnBwdArgs& a, int grid, cudaStream_t st) {
   const int nv = a.D / Vec<T>::N;
   if (nv <= 32) return ln_backward<T, 32, 1>(a, grid, st);
+  if (nv <= 64) return ln_backward<T, 32, 2>(a, grid, st);
   switch (lnb_tpr(nv)) {
-    case 32: return ln_backward<T, 32, 2>(a, grid, st);
-    case 64: return ln_backward<T, 64, 2>(a, grid, st);
-    case 128: return ln_backward<T, 128, 2>(a, grid, st);
-    case 256: return ln_backward<T, 256, 2>(a, grid, st);
+    case 32: return ln_backward<T, 32, 4>(a, grid, st);
+    case 64: return ln_backward<T, 64, 4>(a, grid, st);
+    case 128: return ln_backward<T, 128, 4>(a, grid, st);
+    case 256: return ln_backward<T, 256, 4>(a, grid, st);
   }
-  if (nv <= 1024) return ln_backward<T, 512, 2>(a, grid, st);
   if (nv <= 2048) return ln_backward<T, 512, 4>(a, grid, st);
   if constexpr (sizeof(T) == 4) return ln_backward<T, 512, 8>(a, grid, st);
   return cudaErrorInvalidConfiguration;
@@ -550,8 +551,8 @@ swiglu_status swiglu_mlp_layer_norm_bwd(const void* dY, const void* S, const voi
     return status_of(e);
   }
   if ((st = check_ptrs({dY, S, mean, rstd, dX})) != SWIGLU_OK) return st;
-  if (cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return SWIGLU_ERR_CUDA;
   LnBwdArgs a = {};
+  a.err = static_cast<int*>(ws);
   a.dy = dY;
   a.s = S;
   a.ds = dS;

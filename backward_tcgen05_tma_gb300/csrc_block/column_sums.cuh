@@ -25,7 +25,7 @@ struct DactArgs {
   RowCheck chk;
 };
 
-constexpr int DA_THREADS = 256, DA_WARPS = DA_THREADS / 32, DA_BATCH = 4;
+constexpr int DA_THREADS = 256, DA_WARPS = DA_THREADS / 32, DA_BATCH = 2;
 
 template <class T>
 __global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
@@ -41,8 +41,9 @@ __global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
 #pragma unroll
   for (int j = 0; j < N; ++j) sum[j] = 0.0f;
   if (col < a.N) {
-    for (int64_t r = r0 + warp; r < r1; r += DA_WARPS * DA_BATCH) {
-      uint4 wy[DA_BATCH], wz[DA_BATCH];
+    // the next rows' loads are on their way while these are used
+    uint4 wy[DA_BATCH], wz[DA_BATCH];
+    auto load = [&](int64_t r) {
 #pragma unroll
       for (int b = 0; b < DA_BATCH; ++b) {
         const int64_t row = r + b * DA_WARPS, o = row * a.N + col;
@@ -56,18 +57,36 @@ __global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
           }
         }
       }
+    };
+    load(r0 + warp);
+    for (int64_t r = r0 + warp; r < r1; r += DA_WARPS * DA_BATCH) {
+      uint4 cy[DA_BATCH], cz[DA_BATCH];
+#pragma unroll
+      for (int b = 0; b < DA_BATCH; ++b) {
+        cy[b] = wy[b];
+        cz[b] = wz[b];
+      }
+      load(r + DA_WARPS * DA_BATCH);
 #pragma unroll
       for (int b = 0; b < DA_BATCH; ++b) {
         const int64_t row = r + b * DA_WARPS;
         if (row >= r1) break;
         float y[N], z[N];
-        V::unpack(wy[b], y);
+        V::unpack(cy[b], y);
         if (a.z != nullptr) {
-          V::unpack(wz[b], z);
+          V::unpack(cz[b], z);
           act_switch(a.act, [&](auto t) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-              y[j] = __fmul_rn(y[j], ActMath<N == 4>::template slope<decltype(t)::value>(z[j]));
+            for (int j = 0; j < N; j += 2) {
+              if constexpr (N == 4) {
+                z[j] = ActPrecise::slope<decltype(t)::value>(z[j]);
+                z[j + 1] = ActPrecise::slope<decltype(t)::value>(z[j + 1]);
+              } else {
+                act_slope2<decltype(t)::value>(z[j], z[j + 1]);
+              }
+              y[j] = __fmul_rn(y[j], z[j]);
+              y[j + 1] = __fmul_rn(y[j + 1], z[j + 1]);
+            }
           });
           T* pd = static_cast<T*>(a.dz) + row * a.N + col;
           if (row_ok(a.chk, pd, 16)) *reinterpret_cast<uint4*>(pd) = V::pack(y);

@@ -10,15 +10,17 @@
 //
 // Everything is fp32 between the loads and the one rounding at the end.  The
 // variance is the mean of squares about the mean (a second pass over registers),
-// not E S^2 - mu^2, which cancels where |mu| is large against the deviation; the
-// same pass finds what the first sum's roundings left in the mean, which a row
-// of small deviation would have multiplied by a large rstd.
+// not E S^2 - mu^2, which cancels where |mu| is large against the deviation.  The
+// mean's sum carries its roundings along: a row of small deviation multiplies
+// what is left of them by a large rstd, and the mean of many unlike channels is
+// small against their sum of sizes.
 //
 // Both are bound by memory: every input is read once and every output written
 // once.  A row is held by TPR threads, VPT vectors of 16 bytes each.
 //
-// Backward is persistent: a block's groups of TPR threads take rows in turn and
-// keep the gradients of w and b of their columns in registers, so that the
+// Backward is persistent: a block's groups of TPR threads (a warp up to 1024
+// 16-bit elements: what bounds short rows is the latency of a row's two sums, so
+// many rows are in progress) take rows in turn and keep the gradients of w and b of their columns in registers, so that the
 // reduction over rows costs one partial row pair per block.  Its rows arrive
 // through a ring in shared memory that each thread fills for itself (cp.async):
 // no thread waits for another's copies.  Partial sums are added in the order of
@@ -44,25 +46,49 @@ struct LnFwdArgs {
   RowCheck chk;
 };
 
-// Sums of v.x and v.y over the TPR threads of a row.  `slots`: TPR / 32 pairs
-// that no other use of this row's sums touches.
+// a + b = sum + err exactly (Knuth's two-sum)
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+  return s;
+}
+
+// Sum of v over the TPR threads of a row.  `slots`: TPR / 32 floats that no
+// other use of this row's sums touches.
 template <int TPR>
-__device__ __forceinline__ float2 row_sums(float2 v, float2* slots) {
-  v.x = warp_sum(v.x);
-  v.y = warp_sum(v.y);
+__device__ __forceinline__ float row_sum(float v, float* slots) {
+  v = warp_sum(v);
   if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    const int warp = (threadIdx.x % TPR) >> 5;
-    if ((threadIdx.x & 31) == 0) slots[warp] = v;
+    if ((threadIdx.x & 31) == 0) slots[(threadIdx.x % TPR) >> 5] = v;
     __syncthreads();
-    v = make_float2(0.0f, 0.0f);
+    v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      v.x += slots[i].x;
-      v.y += slots[i].y;
-    }
+    for (int i = 0; i < TPR / 32; ++i) v += slots[i];
   }
   return v;
+}
+
+// The same of v.x + v.y, v.y being what roundings left out of v.x.
+template <int TPR>
+__device__ __forceinline__ float row_sum_exact(float2 v, float2* slots) {
+  float e;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.x = two_sum(v.x, __shfl_xor_sync(0xffffffffu, v.x, o), e);
+    v.y += e;
+  }
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) slots[(threadIdx.x % TPR) >> 5] = v;
+    __syncthreads();
+    v = slots[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) {
+      v.x = two_sum(v.x, slots[i].x, e);
+      v.y += slots[i].y + e;
+    }
+  }
+  return fabsf(v.x) < INFINITY ? v.x + v.y : v.x;  // (an infinity leaves no roundings but NaN)
 }
 
 // ROWS rows a block of ROWS * TPR threads (ROWS > 1 only with TPR = 32).
@@ -71,7 +97,8 @@ __global__ void __launch_bounds__(TPR* ROWS) ln_fwd_kernel(const LnFwdArgs a) {
   static_assert(ROWS == 1 || TPR == 32, "several rows a block: one warp each");
   using V = Vec<T>;
   constexpr int N = V::N;
-  __shared__ float2 slots[2][TPR > 32 ? TPR / 32 : 1];
+  __shared__ float2 sums[TPR > 32 ? TPR / 32 : 1];
+  __shared__ float squares[TPR > 32 ? TPR / 32 : 1];
   pdl_wait();  // launched early: nothing is touched before the kernel before has ended
   pdl_launch_dependents();
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
@@ -93,7 +120,7 @@ __global__ void __launch_bounds__(TPR* ROWS) ln_fwd_kernel(const LnFwdArgs a) {
       }
     }
   }
-  float sum = 0.0f;
+  float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int at = t + i * TPR;
@@ -109,26 +136,25 @@ __global__ void __launch_bounds__(TPR* ROWS) ln_fwd_kernel(const LnFwdArgs a) {
       if (at < nv && row_ok(a.chk, ps, 16)) *reinterpret_cast<uint4*>(ps) = w;
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j) sum += v[i][j];
+    for (int j = 0; j < N; ++j) {
+      float e;
+      sum.x = two_sum(sum.x, v[i][j], e);
+      sum.y += e;
+    }
   }
   const float n = (float)a.D;
-  float mean = row_sums<TPR>(make_float2(sum, 0.0f), slots[0]).x / n;
-  float2 sq = make_float2(0.0f, 0.0f);  // squares about the mean, and what the mean is off by
+  const float mean = row_sum_exact<TPR>(sum, sums) / n;
+  float sq = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
     if (t + i * TPR < nv) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         v[i][j] -= mean;
-        sq.x = fmaf(v[i][j], v[i][j], sq.x);
-        sq.y += v[i][j];
+        sq = fmaf(v[i][j], v[i][j], sq);
       }
     }
-  sq = row_sums<TPR>(sq, slots[1]);
-  const float off = sq.y / n;
-  const float var = sq.x / n - off * off;
-  const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
-  mean += off;
+  const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, squares) / n + a.eps);
   if (t == 0) {
     if (a.mean != nullptr && row_ok(a.chk, a.mean + row, 4)) a.mean[row] = mean;
     if (a.rstd != nullptr && row_ok(a.chk, a.rstd + row, 4)) a.rstd[row] = rstd;
@@ -148,7 +174,7 @@ __global__ void __launch_bounds__(TPR* ROWS) ln_fwd_kernel(const LnFwdArgs a) {
     if (a.w != nullptr && row_ok(a.chk, pw, 16)) V::unpack(*reinterpret_cast<const uint4*>(pw), w);
     if (a.b != nullptr && row_ok(a.chk, pb, 16)) V::unpack(*reinterpret_cast<const uint4*>(pb), b);
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[i][j] = fmaf((v[i][j] - off) * rstd, w[j], b[j]);
+    for (int j = 0; j < N; ++j) v[i][j] = fmaf(v[i][j] * rstd, w[j], b[j]);
     T* py = static_cast<T*>(a.y) + base + at * N;
     if (row_ok(a.chk, py, 16)) *reinterpret_cast<uint4*>(py) = V::pack(v[i]);
   }
@@ -167,6 +193,7 @@ struct LnBwdArgs {
   int D;
   int stages;          // of the ring
   int want;            // whether any of dw, db is wanted
+  int* err;            // cleared here
   RowCheck chk;
 };
 
@@ -187,6 +214,7 @@ __global__ void __launch_bounds__(LNB_THREADS, 1) ln_bwd_kernel(const LnBwdArgs 
   __shared__ float2 slots[2][LNB_THREADS / 32];
   pdl_wait();  // launched early: nothing is touched before the kernel before has ended
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
   const int group = threadIdx.x / TPR, t = threadIdx.x % TPR, nv = a.D / N;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   const int64_t first = (int64_t)blockIdx.x * GROUPS + group;
@@ -220,15 +248,16 @@ __global__ void __launch_bounds__(LNB_THREADS, 1) ln_bwd_kernel(const LnBwdArgs 
   // the stages' count: stages - 1 rows are on their way
   const int ahead = a.stages - 1;
   for (int i = 0; i < ahead; ++i) fetch(first + i * step, i);
-  float wv[VPT][N];
+  uint4 wv[VPT];  // the weight, as it is stored
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int at = t + i * TPR;
     const T* pw = static_cast<const T*>(a.w) + at * N;
+    float one[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) wv[i][j] = 1.0f;
-    if (a.w != nullptr && at < nv && row_ok(a.chk, pw, 16))
-      V::unpack(*reinterpret_cast<const uint4*>(pw), wv[i]);
+    for (int j = 0; j < N; ++j) one[j] = 1.0f;
+    wv[i] = V::pack(one);
+    if (a.w != nullptr && at < nv && row_ok(a.chk, pw, 16)) wv[i] = *reinterpret_cast<const uint4*>(pw);
   }
   float gw[VPT][N], gb[VPT][N];
 #pragma unroll
@@ -253,13 +282,14 @@ __global__ void __launch_bounds__(LNB_THREADS, 1) ln_bwd_kernel(const LnBwdArgs 
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (t + i * TPR >= nv) continue;
-      float dy[N], s[N];
+      float dy[N], s[N], w[N];
       V::unpack(*slot(stage, 0, i), dy);
       V::unpack(*slot(stage, 1, i), s);
+      V::unpack(wv[i], w);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float h = (s[j] - mean) * rstd, tt = dy[j] * wv[i][j];
-        st = fmaf(dy[j], wv[i][j], st);
+        const float h = (s[j] - mean) * rstd, tt = dy[j] * w[j];
+        st = fmaf(dy[j], w[j], st);
         sth = fmaf(tt, h, sth);
         gw[i][j] = fmaf(dy[j], h, gw[i][j]);
         gb[i][j] += dy[j];
@@ -286,14 +316,15 @@ __global__ void __launch_bounds__(LNB_THREADS, 1) ln_bwd_kernel(const LnBwdArgs 
     for (int i = 0; i < VPT; ++i) {
       const int at = t + i * TPR;
       if (at >= nv) continue;
-      float dy[N], s[N], d[N];
+      float dy[N], s[N], d[N], w[N];
       V::unpack(*slot(stage, 0, i), dy);
       V::unpack(*slot(stage, 1, i), s);
+      V::unpack(wv[i], w);
       if constexpr (DS) V::unpack(*slot(stage, 2, i), d);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float h = (s[j] - mean) * rstd;
-        const float g = fmaf(-h, sth, fmaf(dy[j], wv[i][j], -st));
+        const float g = fmaf(-h, sth, fmaf(dy[j], w[j], -st));
         d[j] = DS ? fmaf(rstd, g, d[j]) : rstd * g;
       }
       T* px = static_cast<T*>(a.dx) + row * a.D + at * N;
@@ -306,30 +337,31 @@ __global__ void __launch_bounds__(LNB_THREADS, 1) ln_bwd_kernel(const LnBwdArgs 
   }
   cp_wait<0>();
   if (!a.want) return;
-  // the block's sums: groups in turn, in shared memory (past the ring's use)
+  // the block's sums, in shared memory past the ring's use: every group's, element
+  // j of the vectors apart so that lanes meet no bank twice, then over the groups
   __syncthreads();
-  float* acc = reinterpret_cast<float*>(ring);  // [2][D]
-  for (int g = 0; g < GROUPS; ++g) {
-    if (group == g) {
+  const int row_floats = N * (nv + 4), slab = 2 * row_floats;
+  float* acc = reinterpret_cast<float*>(ring);  // [GROUPS][2][N][nv + 4]
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int at = t + i * TPR;
-        if (at >= nv) continue;
+  for (int i = 0; i < VPT; ++i) {
+    const int at = t + i * TPR;
+    if (at >= nv) continue;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          float* pw = acc + at * N + j;
-          float* pb = pw + a.D;
-          *pw = g == 0 ? gw[i][j] : *pw + gw[i][j];
-          *pb = g == 0 ? gb[i][j] : *pb + gb[i][j];
-        }
-      }
+    for (int j = 0; j < N; ++j) {
+      acc[group * slab + j * (nv + 4) + at] = gw[i][j];
+      acc[group * slab + row_floats + j * (nv + 4) + at] = gb[i][j];
     }
-    __syncthreads();
   }
+  __syncthreads();
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.D;
-  for (int c = threadIdx.x * 4; c < 2 * a.D; c += LNB_THREADS * 4)
-    if (row_ok(a.chk, out + c, 16))
-      *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(acc + c);
+  for (int c = threadIdx.x; c < 2 * a.D; c += LNB_THREADS) {
+    const int which = c >= a.D, col = c - (which ? a.D : 0);
+    const float* p = acc + which * row_floats + col % N * (nv + 4) + col / N;
+    float v = 0.0f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) v += p[g * slab];
+    if (row_ok(a.chk, out + c, 4)) out[c] = v;
+  }
 }
 
 }  // namespace swiglu

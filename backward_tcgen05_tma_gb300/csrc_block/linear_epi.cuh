@@ -73,7 +73,7 @@ struct EpiLinear {
       }
       act_switch(p.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = ActMath<false>::value<decltype(a)::value>(v[i]);
+        for (int i = 0; i < 32; i += 2) act_value2<decltype(a)::value>(v[i], v[i + 1]);
       });
       if (p.res != nullptr) {
         uint4 rr[4];
@@ -128,10 +128,9 @@ struct EpiDAct {
       act_switch(p.act, [&](auto a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float2 z = P::unpack((&zr[i >> 2].x)[i & 3]);
-          w[i] = P::two(
-              __uint_as_float(r[2 * i]) * ActMath<false>::slope<decltype(a)::value>(z.x),
-              __uint_as_float(r[2 * i + 1]) * ActMath<false>::slope<decltype(a)::value>(z.y));
+          float2 z = P::unpack((&zr[i >> 2].x)[i & 3]);
+          act_slope2<decltype(a)::value>(z.x, z.y);
+          w[i] = P::two(__uint_as_float(r[2 * i]) * z.x, __uint_as_float(r[2 * i + 1]) * z.y);
         }
       });
       warp_store_tile(buf, w, lane, checked_rows(s, chunk_rows(s, p.out, p.ld, mw, nc), ok), ok);
@@ -176,7 +175,7 @@ struct NgLinear {
       }
       act_switch(a.act, [&](auto t) {
 #pragma unroll
-        for (int i = 0; i < G; ++i) y[i] = ActMath<false>::value<decltype(t)::value>(y[i]);
+        for (int i = 0; i < G; i += 2) act_value2<decltype(t)::value>(y[i], y[i + 1]);
       });
       if (a.res != nullptr) {
 #pragma unroll

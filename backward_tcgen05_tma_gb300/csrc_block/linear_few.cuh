@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(LF_THREADS, 1) linear_few_kernel(const LfArgs 
         *reinterpret_cast<uint16_t*>(a.z + o) = Ft16<BF16>::rnd(v[i]);
     }
     act_switch(a.act, [&](auto f) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = ActMath<false>::value<decltype(f)::value>(v[i]);
+      act_value2<decltype(f)::value>(v[0], v[1]);
+      act_value2<decltype(f)::value>(v[2], v[3]);
     });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -62,7 +62,7 @@ struct SlEpiLinear {
     if (z != nullptr) sl_store4(z + o, v, chk);
     act_switch(act, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = ActMath<true>::value<decltype(a)::value>(v[i]);
+      for (int i = 0; i < 4; ++i) v[i] = ActPrecise::value<decltype(a)::value>(v[i]);
     });
     if (res != nullptr) {
       const float4 r = sl_load4(res + o, chk);
@@ -89,7 +89,7 @@ struct SlEpiGrad {
       const float z[4] = {z4.x, z4.y, z4.z, z4.w};
       act_switch(act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], ActMath<true>::slope<decltype(a)::value>(z[i]));
+        for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], ActPrecise::slope<decltype(a)::value>(z[i]));
       });
     }
     if (add) {
