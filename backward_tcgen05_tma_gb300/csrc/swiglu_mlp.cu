@@ -817,7 +817,7 @@ static cudaError_t gemm_dw(int id, const void* G, const void* X, void* dW, int64
   CUtensorMap mg, mx;
   if (!map_mnmajor(&mg, BF16, G, N, M, N) || !map_mnmajor(&mx, BF16, X, K, M, K)) return cudaErrorInvalidValue;
   const bool pairs = use_pairs(N, K, TC_BN, M), wide = use_wide(pairs, N, K, M);
-  TcShape s = make_shape(N, K, M, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(N, K, M, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
   set_windows(s, {{dW, (size_t)(N * K * 2)}, {err, ws_bytes}});
   const EpiStore::Params p{dW, K, 1.0f, accumulate};
   return wide ? launch_tc2<LOAD_MNMAJOR, LOAD_MNMAJOR, BF16, EpiStore, TC2_WIDE_BN>(id, mg, mx, s, p, st)
@@ -836,7 +836,7 @@ static cudaError_t gemm_dx(int id, const void* G, const void* W, void* dX, int64
   CUtensorMap mg, mw;
   if (!map_kmajor(&mg, BF16, G, N, M, N, TC_BM) || !map_mnmajor(&mw, BF16, W, K, N, K)) return cudaErrorInvalidValue;
   const bool pairs = use_pairs(M, K, TC_BN, N), wide = use_wide(pairs, M, K, N);
-  TcShape s = make_shape(M, K, N, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(M, K, N, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
   set_windows(s, {{dX, (size_t)(M * K * 2)}, {err, ws_bytes}});
   const EpiStore::Params p{dX, K, 1.0f, 0};
   return wide ? launch_tc2<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiStore, TC2_WIDE_BN>(id, mg, mw, s, p, st)

@@ -53,6 +53,7 @@ struct TcShape {
   // leave fp32 partial tiles in `part` (slot = CTA x segment); the last CTA to
   // finish a shared tile (counter) sums them in CTA order into its TMEM
   // accumulator and runs the epilogue.
+  int units;       // CTAs (or pairs) that the plan hands tiles to
   int sk_tiles;
   int seg_max;     // partial slots per CTA
   float* part;     // [gridDim.x * seg_max][128 * BN] fp32 in TMEM order

@@ -215,8 +215,9 @@ inline bool use_pairs(int64_t Mg, int64_t N, int64_t n_per_tile, int64_t K) {
 // part_cap: workspace bytes available for stream-K partial tiles; a GEMM
 // whose plan needs more runs whole tiles only (same results within
 // rounding, without the last round's balancing).
+// units: CTAs or pairs to plan for, 0 for all that the device holds.
 inline TcShape make_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, int* err, bool pairs,
-                   size_t part_cap) {
+                   size_t part_cap, int units = 0) {
   TcShape s;
   s.M = (int)M;
   s.N = (int)N;
@@ -230,8 +231,8 @@ inline TcShape make_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, i
   s.err = err;
   s.inject_stall = host::take_stall() ? 1 : 0;
   // the workspace (whose first word is err) carries the stream-K scratch
-  const TcPlan p = tc_plan((int64_t)s.m_tiles * s.n_tiles, s.k_blocks,
-                           pairs ? host::pair_units() : tc_nsm());
+  s.units = units > 0 ? units : pairs ? host::pair_units() : tc_nsm();
+  const TcPlan p = tc_plan((int64_t)s.m_tiles * s.n_tiles, s.k_blocks, s.units);
   s.sk_tiles = p.sk_tiles;
   s.seg_max = p.seg_max;
   if (tc_part_bytes(p, n_per_tile) * (pairs ? 2 : 1) > part_cap) {
@@ -244,11 +245,40 @@ inline TcShape make_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, i
 }
 
 // CTAs (or pairs) to launch: the stream-K plan's grid, or one per tile up to
-// `units` when the GEMM runs whole tiles only.
-inline int launch_units(const TcShape& s, int units) {
+// s.units when the GEMM runs whole tiles only.
+inline int launch_units(const TcShape& s) {
   const int64_t tiles = (int64_t)s.m_tiles * s.n_tiles;
-  if (s.sk_tiles) return tc_plan(tiles, s.k_blocks, units).grid;
-  return (int)(tiles < units ? tiles : units);
+  if (s.sk_tiles) return tc_plan(tiles, s.k_blocks, s.units).grid;
+  return (int)(tiles < s.units ? tiles : s.units);
+}
+
+// The same for a GEMM of a linear layer, shared or not by what it costs.  A shared
+// tile's partial sums (128 KB a CTA) go out and come back, the last CTA of a tile
+// reading everyone's; a k-block takes 0.34 us.  Measured at 16384 x 2816 x 1024 on
+// pairs (whole tiles, shared ones): forward, 16 k-blocks, 9.26 rounds: 86 and 109
+// us; dX, 44 k-blocks, 3.37 rounds: 67 and 77; dW, 256 k-blocks, 0.58 rounds: 87
+// and 77; 32768 x 2048 x 5632: dW, 512 k-blocks, 2.3 rounds: 499 and 455.  So the
+// last round is shared where it leaves 74 k-blocks' time of every CTA idle, and
+// fewer tiles than CTAs go to as many CTAs each as makes their parts, and the
+// reading of them (about 8 k-blocks each), shortest together.
+inline TcShape linear_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, int* err, bool pairs,
+                            size_t part_cap) {
+  const int all = pairs ? host::pair_units() : tc_nsm();
+  const int64_t bm = pairs ? TC2_BM : TC_BM, kb = (K + TC_BK - 1) / TC_BK;
+  const int64_t tiles = ((M + bm - 1) / bm) * ((N + n_per_tile - 1) / n_per_tile);
+  if (tiles >= all) {
+    const int64_t idle = (all - tiles % all) % all;  // CTAs without a tile in the last round
+    return make_shape(M, N, K, n_per_tile, err, pairs, idle * kb >= 74 * (int64_t)all ? part_cap : 0);
+  }
+  int64_t best = kb, units = tiles;
+  for (int64_t s = 2; (s - 1) * tiles < all; ++s) {
+    const int64_t u = s * tiles < all ? s * tiles : all, cost = kb * tiles / u + 18 + 8 * s;
+    if (cost < best) {
+      best = cost;
+      units = u;
+    }
+  }
+  return make_shape(M, N, K, n_per_tile, err, pairs, units > tiles ? part_cap : 0, (int)units);
 }
 
 // The training kernels are launched in plain stream order: with a static
@@ -262,7 +292,7 @@ cudaError_t launch_tc(int kid, const CUtensorMap& ta, const CUtensorMap& tb, con
   constexpr int smem = TcSmem<TC_BN, TC_STAGES>::DYN_BYTES;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = launch_units(s, tc_nsm());
+  const int grid = launch_units(s);
   host::Prof prof(kid, st);
   kern<<<grid, TC_THREADS, smem, st>>>(ta, tb, s, ep);
   host::count_launch();
@@ -278,13 +308,13 @@ cudaError_t launch_tc2(int kid, const CUtensorMap& ta, const CUtensorMap& tb, co
   // the TMA dG/dU epilogue's slots (GU_SLOTS x 4 KB per epilogue warp) take
   // the room of GU_SLOTS - 1 ring stages; 512-column tiles (48 KB stages)
   // keep four
-  constexpr bool gu = epi_tma_gu<Epi>::value;
+  constexpr bool gu = epi_tma_gu<Epi>::value || epi_tma_out<Epi>::value;
   constexpr int stages = BN > 256 ? 4 : (gu ? TC2_STAGES + 1 - GU_SLOTS : TC2_STAGES);
   auto kern = tc2_gemm_kernel<stages, AM, BMODE, BF16, Epi, BN>;
   constexpr int smem = Tc2Smem<stages, gu, BN>::DYN_BYTES;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int units = launch_units(s, host::pair_units());
+  const int units = launch_units(s);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * units));
   cfg.blockDim = dim3(TC_THREADS);

@@ -446,9 +446,14 @@ cudaError_t linear_forward(const void* X, const void* W, const EpiLinear::Params
   CUtensorMap tx, tw;
   if (!map_kmajor(&tx, BF16, X, K, M, K, TC_BM) || !map_kmajor(&tw, BF16, W, K, N, K, pairs ? 128 : TC_BN))
     return cudaErrorInvalidValue;
-  TcShape s = make_shape(M, N, K, TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(M, N, K, TC_BN, err, pairs, part_capacity(ws_bytes));
   set_windows(s, {y, w, z, res, bias});
-  return launch_gemm<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinear>(pairs, host::K_LINEAR, tx, tw, s, ep, st);
+  if (!pairs) return launch_tc<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinear>(host::K_LINEAR, tx, tw, s, ep, st);
+  CUtensorMap ty, tz;  // boxes of 32 rows x 64 columns of the outputs
+  if (!encode_2d(&ty, BF16, ep.y, N, M, N * 2, 64, 32) ||
+      !encode_2d(&tz, BF16, ep.z != nullptr ? ep.z : ep.y, N, M, N * 2, 64, 32))
+    return cudaErrorInvalidValue;
+  return launch_tc2<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinearTma>(host::K_LINEAR, tx, tw, s, ep, st, &ty, &tz);
 }
 
 // dX = rnd(G W act'(Xpre)), G [M, N], W [N, K]
@@ -459,7 +464,7 @@ cudaError_t linear_dx(const void* G, const void* W, const EpiDAct::Params& ep, i
   CUtensorMap tg, tw;
   if (!map_kmajor(&tg, BF16, G, N, M, N, TC_BM) || !map_mnmajor(&tw, BF16, W, K, N, K))
     return cudaErrorInvalidValue;
-  TcShape s = make_shape(M, K, N, TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(M, K, N, TC_BN, err, pairs, part_capacity(ws_bytes));
   set_windows(s, {{ep.out, (size_t)(M * K * 2)}, {err, ws_bytes}, {ep.pre, (size_t)(M * K * 2)}});
   return launch_gemm<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiDAct>(pairs, host::K_LINEAR_DX, tg, tw, s, ep, st);
 }

@@ -92,6 +92,104 @@ struct EpiLinear {
   }
 };
 
+// The same for the kernel on SM pairs, which is where many rows go: tiles leave by
+// TMA.  A lane writes its row of a 32 x 64 chunk into the warp's Z and Y boxes
+// (128-byte swizzle: no bank conflicts) and one lane stores both; they are written
+// again when the stores have read them, a chunk's arithmetic later.  The tensor
+// maps clip at M rows and N columns.  The plain form turns every 32 x 32 chunk
+// round through shared memory to store whole sectors, and is bound by those
+// instructions and their latencies: 16384 x 2816 x 1024 with gelu and Z took 117
+// us with it, 107 with boxes of 32 columns in two slots.
+struct EpiLinearTma {
+  static constexpr bool TMA_OUT = true;
+  using Params = EpiLinear::Params;  // (y and z by the tensor maps tmG, tmU)
+  template <int BN, bool BF16>
+  static __device__ __forceinline__ void run(const Params& p, const TcShape& s, uint32_t tacc, int m0, int nt,
+                                             int row, int half, uint8_t* slots, const CUtensorMap* tmY,
+                                             const CUtensorMap* tmZ) {
+    static_assert(GU_SLOTS * GU_SLOT_BYTES >= 2 * 32 * 128, "a Z box and a Y box");
+    using P = Pack<BF16>;
+    const int lane = row & 31;
+    const int mw = m0 + (row & ~31), m = mw + lane;
+    const int n0 = nt * BN + half * (BN / 2);
+    const uint32_t zbox = smem_u32(slots), ybox = zbox + 4096;
+    constexpr int CH = BN / 128;
+    // 16-byte unit q of row r at q ^ (r mod 8)
+    auto put = [&](uint32_t box, int q, const uint32_t* w) {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                   : "memory");
+    };
+    auto load = [&](uint4 (&v)[8], const void* base, int64_t at, int nc, bool in) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (at + nc) * 2);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        v[q] = in && nc + q * 8 + 8 <= s.N && SWIGLU_CHECK_PTR(s.dbg, src + q, 16, s.err) ? src[q]
+                                                                                         : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (mw >= s.M) return;
+    uint4 bq[8];
+    load(bq, p.bias, 0, n0, p.bias != nullptr);
+#pragma unroll 1
+    for (int c = 0; c < CH; ++c) {
+      const int nc = n0 + c * 64;
+      if (nc >= s.N) return;
+      float v[64];
+      {
+        uint32_t r0[32], r1[32];
+        tmem_ld_32x32b_x32(tacc + (half * CH + c) * 64, r0);
+        tmem_ld_32x32b_x32(tacc + (half * CH + c) * 64 + 32, r1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 b = P::unpack((&bq[i >> 2].x)[i & 3]);
+          const uint32_t a0 = i < 16 ? r0[2 * i & 31] : r1[2 * i & 31], a1 = i < 16 ? r0[(2 * i & 31) + 1] : r1[(2 * i & 31) + 1];
+          add2(F2(__uint_as_float(a0), __uint_as_float(a1)), F2(b.x, b.y)).get(v[2 * i], v[2 * i + 1]);
+        }
+      }
+      if (c + 1 < CH) load(bq, p.bias, 0, nc + 64, p.bias != nullptr);
+      if (lane == 0) bulk_wait_group_read<0>();  // the boxes are free
+      __syncwarp();
+      if (p.z != nullptr) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = P::two(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
+          put(zbox, q, w);
+        }
+      }
+      act_switch(p.act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) act_value2<decltype(a)::value>(v[i], v[i + 1]);
+      });
+      if (p.res != nullptr) {
+        uint4 rr[8];
+        load(rr, p.res, (int64_t)m * p.ld, nc, m < s.M);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 b = P::unpack((&rr[i >> 2].x)[i & 3]);
+          add2(F2(v[2 * i], v[2 * i + 1]), F2(b.x, b.y)).get(v[2 * i], v[2 * i + 1]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = P::two(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
+        put(ybox, q, w);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (p.z != nullptr) tma_store_2d(tmZ, zbox, nc, mw);
+        tma_store_2d(tmY, ybox, nc, mw);
+        bulk_commit_group();
+      }
+    }
+  }
+};
+
 struct EpiDAct {
   struct Params {
     const void* pre;  // [M, N]

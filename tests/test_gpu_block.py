@@ -292,6 +292,35 @@ def test_linear_backward(dtn, M, N, K):
         within(db, dz.sum(0), U[dtn], sb, sq.sum(0).sqrt() + TINY[dtn] / sb)
 
 
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(65, 264, 328), (129, 520, 1032), (257, 392, 2824), (300, 40, 136), (2500, 1032, 264)])
+def test_linear_on_sm_pairs(dtn, M, N, K):
+    # the kernels that large sizes take, on ragged ones
+    old = api.swiglu_mlp_set_cta_pairs(2)
+    try:
+        test_linear_forward(dtn, M, N, K)
+        test_linear_backward(dtn, M, N, K)
+    finally:
+        api.swiglu_mlp_set_cta_pairs(old)
+
+
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(64, 136, 16392), (40, 264, 23000), (1, 24, 120000), (33, 5640, 8200), (64, 2056, 9000),
+                                   (7, 2456, 40), (5, 16, 264), (20, 40, 8)])
+def test_linear_few_tokens_both_forms(dtn, M, N, K):
+    # long contractions whose token rows do not fit a cluster's blocks, and short
+    # ones with fewer 32-k blocks than a cluster has parts
+    g, dt = gen(K), DT[dtn]
+    X, W = normal(g, M, K, dtype=dt), normal(g, N, K, std=K ** -0.5, dtype=dt)
+    b, R = normal(g, N, dtype=dt), normal(g, M, N, dtype=dt)
+    z = X.double() @ W.double().T + b.double()
+    root = (X.double().square() @ W.double().square().T).sqrt() + b.double().abs()
+    Y, Z = api.swiglu_mlp_linear_fwd(X, W, b, "silu", R, keep=True)
+    slack = act_slack(K)
+    within(Z, z, U[dtn], slack, root)
+    within(Y, act64("silu", z) + R.double(), U[dtn], slack, 1.2 * root + z.abs() + R.double().abs())
+
+
 def test_activation_slopes_are_those_of_differences():
     z = torch.linspace(-6, 6, 997, dtype=torch.float64)
     for act in ACTS:
