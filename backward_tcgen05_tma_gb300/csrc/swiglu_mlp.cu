@@ -813,11 +813,11 @@ int pair_units() {
 
 template <bool BF16>
 static cudaError_t gemm_dw(int id, const void* G, const void* X, void* dW, int64_t M, int64_t N, int64_t K,
-                           int accumulate, int* err, size_t ws_bytes, cudaStream_t st) {
+                           int accumulate, int* err, size_t ws_bytes, bool first, cudaStream_t st) {
   CUtensorMap mg, mx;
   if (!map_mnmajor(&mg, BF16, G, N, M, N) || !map_mnmajor(&mx, BF16, X, K, M, K)) return cudaErrorInvalidValue;
   const bool pairs = use_pairs(N, K, TC_BN, M), wide = use_wide(pairs, N, K, M);
-  TcShape s = linear_shape(N, K, M, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(N, K, M, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes), first);
   set_windows(s, {{dW, (size_t)(N * K * 2)}, {err, ws_bytes}});
   const EpiStore::Params p{dW, K, 1.0f, accumulate};
   return wide ? launch_tc2<LOAD_MNMAJOR, LOAD_MNMAJOR, BF16, EpiStore, TC2_WIDE_BN>(id, mg, mx, s, p, st)
@@ -825,18 +825,18 @@ static cudaError_t gemm_dw(int id, const void* G, const void* X, void* dW, int64
 }
 
 cudaError_t gemm_dw(int id, bool bf16, const void* G, const void* X, void* dW, int64_t M, int64_t N,
-                    int64_t K, int accumulate, int* err, size_t ws_bytes, cudaStream_t st) {
-  return bf16 ? gemm_dw<true>(id, G, X, dW, M, N, K, accumulate, err, ws_bytes, st)
-              : gemm_dw<false>(id, G, X, dW, M, N, K, accumulate, err, ws_bytes, st);
+                    int64_t K, int accumulate, int* err, size_t ws_bytes, bool first, cudaStream_t st) {
+  return bf16 ? gemm_dw<true>(id, G, X, dW, M, N, K, accumulate, err, ws_bytes, first, st)
+              : gemm_dw<false>(id, G, X, dW, M, N, K, accumulate, err, ws_bytes, first, st);
 }
 
 template <bool BF16>
 static cudaError_t gemm_dx(int id, const void* G, const void* W, void* dX, int64_t M, int64_t N, int64_t K,
-                           int* err, size_t ws_bytes, cudaStream_t st) {
+                           int* err, size_t ws_bytes, bool first, cudaStream_t st) {
   CUtensorMap mg, mw;
   if (!map_kmajor(&mg, BF16, G, N, M, N, TC_BM) || !map_mnmajor(&mw, BF16, W, K, N, K)) return cudaErrorInvalidValue;
   const bool pairs = use_pairs(M, K, TC_BN, N), wide = use_wide(pairs, M, K, N);
-  TcShape s = linear_shape(M, K, N, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(M, K, N, wide ? TC2_WIDE_BN : TC_BN, err, pairs, part_capacity(ws_bytes), first);
   set_windows(s, {{dX, (size_t)(M * K * 2)}, {err, ws_bytes}});
   const EpiStore::Params p{dX, K, 1.0f, 0};
   return wide ? launch_tc2<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiStore, TC2_WIDE_BN>(id, mg, mw, s, p, st)
@@ -844,9 +844,9 @@ static cudaError_t gemm_dx(int id, const void* G, const void* W, void* dX, int64
 }
 
 cudaError_t gemm_dx(int id, bool bf16, const void* G, const void* W, void* dX, int64_t M, int64_t N, int64_t K,
-                    int* err, size_t ws_bytes, cudaStream_t st) {
-  return bf16 ? gemm_dx<true>(id, G, W, dX, M, N, K, err, ws_bytes, st)
-              : gemm_dx<false>(id, G, W, dX, M, N, K, err, ws_bytes, st);
+                    int* err, size_t ws_bytes, bool first, cudaStream_t st) {
+  return bf16 ? gemm_dx<true>(id, G, W, dX, M, N, K, err, ws_bytes, first, st)
+              : gemm_dx<false>(id, G, W, dX, M, N, K, err, ws_bytes, first, st);
 }
 
 static bool encode_any(CUtensorMap* tm, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,

@@ -90,17 +90,6 @@ struct epi_tma_gu<E, decltype((void)E::TMA_GU)> {
   static constexpr bool value = E::TMA_GU;
 };
 
-// Epilogues that store their tiles by TMA from the same slots (TMA_OUT): run()
-// gets the slots and the kernel's tensor maps tmG, tmU, which then are its outputs'.
-template <class E, class = void>
-struct epi_tma_out {
-  static constexpr bool value = false;
-};
-template <class E>
-struct epi_tma_out<E, decltype((void)E::TMA_OUT)> {
-  static constexpr bool value = E::TMA_OUT;
-};
-
 // Wait until at most n of this thread's committed bulk groups still read
 // shared memory (n clamped to the GU_SLOTS - 1 the pipeline can need).
 __device__ __forceinline__ void bulk_wait_group_read_n(int n) {
@@ -229,9 +218,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     const typename Epi::Params ep, const __grid_constant__ CUtensorMap tmG,
                     const __grid_constant__ CUtensorMap tmU) {
   constexpr bool TMA_GU = epi_tma_gu<Epi>::value;
-  constexpr bool TMA_OUT = epi_tma_out<Epi>::value;
-  using L = Tc2Smem<STAGES, TMA_GU || TMA_OUT, BN>;
-  static_assert(BN == 256 || (BN == 512 && !TMA_GU && !TMA_OUT && B_MODE != LOAD_GATEUP),
+  using L = Tc2Smem<STAGES, TMA_GU, BN>;
+  static_assert(BN == 256 || (BN == 512 && !TMA_GU && B_MODE != LOAD_GATEUP),
                 "512-column tiles serve the plain-store GEMMs");
   constexpr int NACC = L::NACC;
   constexpr int MMA_N = BN > 256 ? 256 : BN;  // columns per tcgen05.mma
@@ -285,6 +273,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   cluster_sync();  // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  tc_begin(s);
 
   const int num_tiles = s.m_tiles * s.n_tiles;
   const int64_t sk_total = (int64_t)s.sk_tiles * s.k_blocks;
@@ -551,10 +540,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                      s.wait_limit_ns, abort_flag, s.err)
                       ? 1
                       : 0;
-        } else if constexpr (TMA_OUT) {
-          Epi::template run<BN, BF16>(ep, s, tacc, mt * TC2_BM + (int)rank * 128, nt, row, half,
-                                      smem + L::GU_OFFSET + (warp - 2) * GU_SLOTS * GU_SLOT_BYTES,
-                                      &tmG, &tmU);
         } else {
           Epi::template run<BN, BF16>(ep, s, tacc, mt * TC2_BM + (int)rank * 128, nt, row, half,
                                       smem + L::EPI_OFFSET + (warp - 2) * 2048);
@@ -577,10 +562,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                             nullptr, s.err);
         bulk_wait_group<0>();
       }
-      __syncwarp();
-    }
-    if constexpr (TMA_OUT) {
-      if (lane == 0) bulk_wait_group<0>();
       __syncwarp();
     }
   }

@@ -54,6 +54,8 @@ struct TcShape {
   // finish a shared tile (counter) sums them in CTA order into its TMEM
   // accumulator and runs the epilogue.
   int units;       // CTAs (or pairs) that the plan hands tiles to
+  int early;       // launched as a programmatic dependent: waits for the kernel before it
+  int clear_err;   // the first kernel of a call that clears the error word itself
   int sk_tiles;
   int seg_max;     // partial slots per CTA
   float* part;     // [gridDim.x * seg_max][128 * BN] fp32 in TMEM order
@@ -62,6 +64,15 @@ struct TcShape {
   DbgWin dbg;      // buffers the epilogue may touch: its output(s) and the workspace
 #endif
 };
+
+// After a block's prologue, before it touches anything.
+__device__ __forceinline__ void tc_begin(const TcShape& s) {
+  if (s.early) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  if (s.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *s.err = 0;
+}
 
 // Stream-K partition of `total` shared k-blocks: CTA c owns
 // [sk_start(c), sk_start(c + 1)).
@@ -635,6 +646,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  tc_begin(s);
 
   const int num_tiles = s.m_tiles * s.n_tiles;
   const int64_t sk_total = (int64_t)s.sk_tiles * s.k_blocks;  // shared k-blocks

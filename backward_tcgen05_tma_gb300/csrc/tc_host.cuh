@@ -231,6 +231,7 @@ inline TcShape make_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, i
   s.err = err;
   s.inject_stall = host::take_stall() ? 1 : 0;
   // the workspace (whose first word is err) carries the stream-K scratch
+  s.early = s.clear_err = 0;
   s.units = units > 0 ? units : pairs ? host::pair_units() : tc_nsm();
   const TcPlan p = tc_plan((int64_t)s.m_tiles * s.n_tiles, s.k_blocks, s.units);
   s.sk_tiles = p.sk_tiles;
@@ -261,8 +262,8 @@ inline int launch_units(const TcShape& s) {
 // last round is shared where it leaves 74 k-blocks' time of every CTA idle, and
 // fewer tiles than CTAs go to as many CTAs each as makes their parts, and the
 // reading of them (about 8 k-blocks each), shortest together.
-inline TcShape linear_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, int* err, bool pairs,
-                            size_t part_cap) {
+inline TcShape linear_plan(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, int* err, bool pairs,
+                           size_t part_cap) {
   const int all = pairs ? host::pair_units() : tc_nsm();
   const int64_t bm = pairs ? TC2_BM : TC_BM, kb = (K + TC_BK - 1) / TC_BK;
   const int64_t tiles = ((M + bm - 1) / bm) * ((N + n_per_tile - 1) / n_per_tile);
@@ -280,9 +281,17 @@ inline TcShape linear_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile,
   }
   return make_shape(M, N, K, n_per_tile, err, pairs, units > tiles ? part_cap : 0, (int)units);
 }
+// first: the first kernel of its call.
+inline TcShape linear_shape(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, int* err, bool pairs,
+                            size_t part_cap, bool first) {
+  TcShape s = linear_plan(M, N, K, n_per_tile, err, pairs, part_cap);
+  s.early = 1;
+  s.clear_err = first ? 1 : 0;
+  return s;
+}
 
-// The training kernels are launched in plain stream order: with a static
-// round-robin tile split, a programmatic dependent whose CTAs start late on
+// The training kernels are launched in plain stream order (the linear layers'
+// set s.early): with a static round-robin tile split, a programmatic dependent whose CTAs start late on
 // SMs still held by the predecessor's last wave also finishes late (measured
 // slower than plain order).
 template <int AM, int BMODE, bool BF16, class Epi>
@@ -294,9 +303,19 @@ cudaError_t launch_tc(int kid, const CUtensorMap& ta, const CUtensorMap& tb, con
   if (e != cudaSuccess) return e;
   const int grid = launch_units(s);
   host::Prof prof(kid, st);
-  kern<<<grid, TC_THREADS, smem, st>>>(ta, tb, s, ep);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(TC_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = s.early && !host::profiling() ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tb, s, ep);
   host::count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // The pair kernel: clusters of two CTAs on the two SMs of a TPC.
@@ -308,7 +327,7 @@ cudaError_t launch_tc2(int kid, const CUtensorMap& ta, const CUtensorMap& tb, co
   // the TMA dG/dU epilogue's slots (GU_SLOTS x 4 KB per epilogue warp) take
   // the room of GU_SLOTS - 1 ring stages; 512-column tiles (48 KB stages)
   // keep four
-  constexpr bool gu = epi_tma_gu<Epi>::value || epi_tma_out<Epi>::value;
+  constexpr bool gu = epi_tma_gu<Epi>::value;
   constexpr int stages = BN > 256 ? 4 : (gu ? TC2_STAGES + 1 - GU_SLOTS : TC2_STAGES);
   auto kern = tc2_gemm_kernel<stages, AM, BMODE, BF16, Epi, BN>;
   constexpr int smem = Tc2Smem<stages, gu, BN>::DYN_BYTES;
@@ -320,13 +339,15 @@ cudaError_t launch_tc2(int kid, const CUtensorMap& ta, const CUtensorMap& tb, co
   cfg.blockDim = dim3(TC_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = s.early && !host::profiling() ? 2 : 1;
   host::Prof prof(kid, st);
   e = cudaLaunchKernelEx(&cfg, kern, ta, tb, s, ep, tg != nullptr ? *tg : ta,
                          tu != nullptr ? *tu : tb);

@@ -446,34 +446,33 @@ cudaError_t linear_forward(const void* X, const void* W, const EpiLinear::Params
   CUtensorMap tx, tw;
   if (!map_kmajor(&tx, BF16, X, K, M, K, TC_BM) || !map_kmajor(&tw, BF16, W, K, N, K, pairs ? 128 : TC_BN))
     return cudaErrorInvalidValue;
-  TcShape s = linear_shape(M, N, K, TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(M, N, K, TC_BN, err, pairs, part_capacity(ws_bytes), true);
   set_windows(s, {y, w, z, res, bias});
-  if (!pairs) return launch_tc<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinear>(host::K_LINEAR, tx, tw, s, ep, st);
-  CUtensorMap ty, tz;  // boxes of 32 rows x 64 columns of the outputs
-  if (!encode_2d(&ty, BF16, ep.y, N, M, N * 2, 64, 32) ||
-      !encode_2d(&tz, BF16, ep.z != nullptr ? ep.z : ep.y, N, M, N * 2, 64, 32))
-    return cudaErrorInvalidValue;
-  return launch_tc2<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinearTma>(host::K_LINEAR, tx, tw, s, ep, st, &ty, &tz);
+  const auto whole = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31u) == 0; };
+  if (N % 16 == 0 && whole(ep.y) && whole(ep.z) && whole(ep.res))
+    return launch_gemm<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinearSectors>(pairs, host::K_LINEAR, tx, tw, s, ep, st);
+  return launch_gemm<LOAD_KMAJOR, LOAD_KMAJOR, BF16, EpiLinear>(pairs, host::K_LINEAR, tx, tw, s, ep, st);
 }
 
 // dX = rnd(G W act'(Xpre)), G [M, N], W [N, K]
 template <bool BF16>
 cudaError_t linear_dx(const void* G, const void* W, const EpiDAct::Params& ep, int64_t M, int64_t N,
-                      int64_t K, int* err, size_t ws_bytes, cudaStream_t st) {
+                      int64_t K, int* err, size_t ws_bytes, bool first, cudaStream_t st) {
   const bool pairs = use_pairs(M, K, TC_BN, N);
   CUtensorMap tg, tw;
   if (!map_kmajor(&tg, BF16, G, N, M, N, TC_BM) || !map_mnmajor(&tw, BF16, W, K, N, K))
     return cudaErrorInvalidValue;
-  TcShape s = linear_shape(M, K, N, TC_BN, err, pairs, part_capacity(ws_bytes));
+  TcShape s = linear_shape(M, K, N, TC_BN, err, pairs, part_capacity(ws_bytes), first);
   set_windows(s, {{ep.out, (size_t)(M * K * 2)}, {err, ws_bytes}, {ep.pre, (size_t)(M * K * 2)}});
   return launch_gemm<LOAD_KMAJOR, LOAD_MNMAJOR, BF16, EpiDAct>(pairs, host::K_LINEAR_DX, tg, tw, s, ep, st);
 }
 
 template <bool A_KC, bool B_KC, class Epi>
 cudaError_t simt_product(int id, const float* A, int64_t lda, const float* B, int64_t ldb, int64_t M, int64_t N,
-                         int64_t K, const Epi& epi, void* ws, std::initializer_list<Win> wins, cudaStream_t st) {
+                         int64_t K, const Epi& epi, void* ws, bool first, std::initializer_list<Win> wins,
+                         cudaStream_t st) {
   const SlPlan p = sl_plan(M, N, K);
-  SlArgs a = {A, B, lda, ldb, (int)M, (int)N, (int)K, p.m_tiles, p.n_tiles, p.per, nullptr, {}};
+  SlArgs a = {A, B, lda, ldb, (int)M, (int)N, (int)K, p.m_tiles, p.n_tiles, p.per, nullptr, first ? static_cast<int*>(ws) : nullptr, {}};
   if (p.parts > 1) a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED);
 #ifdef SWIGLU_DEBUG
   // the partial sums take the output's place in the first kernel, and follow it in the second
@@ -598,15 +597,13 @@ swiglu_status swiglu_mlp_linear_fwd(const void* X, const void* W, const void* bi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = static_cast<int*>(ws);
   if (dtype == SWIGLU_F32_IEEE) {
-    if (cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return SWIGLU_ERR_CUDA;
     const SlEpiLinear epi{(const float*)bias, (const float*)residual, (float*)Z, (float*)Y, N, act};
     const size_t mn = (size_t)(M * N * 4);
     return status_of(simt_product<true, true>(
-        host::K_SIMT_LINEAR, (const float*)X, K, (const float*)W, K, M, N, K, epi, ws,
+        host::K_SIMT_LINEAR, (const float*)X, K, (const float*)W, K, M, N, K, epi, ws, true,
         {{Y, mn}, {X, (size_t)(M * K * 4)}, {W, (size_t)(N * K * 4)}, {bias, bias ? (size_t)N * 4 : 0},
          {residual, residual ? mn : 0}, {Z, Z ? mn : 0}}, s));
   }
-  if (!few_tokens(M, dtype) && cudaMemsetAsync(ws, 0, FIXED, s) != cudaSuccess) return SWIGLU_ERR_CUDA;
   const EpiLinear::Params ep{bias, residual, Z, Y, N, act};
   return status_of(dtype == SWIGLU_BF16 ? linear_forward<true>(X, W, ep, M, N, K, err, ws_bytes, s)
                                         : linear_forward<false>(X, W, ep, M, N, K, err, ws_bytes, s));
@@ -638,15 +635,15 @@ swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W
   if (dX != nullptr && (st = check_ptrs({W})) != SWIGLU_OK) return st;
   if (dX != nullptr && x_act != SWIGLU_ACT_NONE && (st = check_ptrs({X_pre})) != SWIGLU_OK) return st;
   if (dW != nullptr && (st = check_ptrs({X})) != SWIGLU_OK) return st;
-  if (cudaMemsetAsync(ws, 0, dtype == SWIGLU_F32_IEEE ? sizeof(int) : FIXED, s) != cudaSuccess) return SWIGLU_ERR_CUDA;
   int* err = static_cast<int*>(ws);
   const size_t mn = (size_t)(M * N * e), mk = (size_t)(M * K * e), nk = (size_t)(N * K * e);
   const void* G = dY;
+  bool first = true;  // the next kernel clears the error word
   if (act != SWIGLU_ACT_NONE || dbias != nullptr) {
     const bool has = act != SWIGLU_ACT_NONE;
     float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED);
     const int parts = dact_parts(M, N, dtype);
-    DactArgs a = {dY, has ? Z : nullptr, has ? dZ : nullptr, dbias != nullptr ? part : nullptr, M, (int)N, act, {}};
+    DactArgs a = {dY, has ? Z : nullptr, has ? dZ : nullptr, dbias != nullptr ? part : nullptr, M, (int)N, act, err, {}};
     a.chk = row_check(ws, {{has ? dZ : ws, has ? mn : ws_bytes}, {ws, ws_bytes}, {dY, mn}, {Z, has ? mn : 0}});
     const dim3 grid((unsigned)((N * e + 511) / 512), (unsigned)parts);
     cudaError_t c = by_type(dtype, [&](auto t) {
@@ -656,19 +653,21 @@ swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W
       c = column_sums(part, parts, (int)N, dbias, nullptr, (int)N, accumulate, dtype, ws, ws_bytes, s);
     if (c != cudaSuccess) return SWIGLU_ERR_CUDA;
     if (has) G = dZ;
+    first = false;
   }
   if (dtype == SWIGLU_F32_IEEE) {
     const float *g = (const float*)G, *x = (const float*)X, *w = (const float*)W;
     if (dW != nullptr) {
       const SlEpiGrad epi{nullptr, (float*)dW, K, 0, accumulate};
-      if (simt_product<false, false>(host::K_SIMT_LINEAR_DW, g, N, x, K, N, K, M, epi, ws,
+      if (simt_product<false, false>(host::K_SIMT_LINEAR_DW, g, N, x, K, N, K, M, epi, ws, first,
                                      {{dW, nk}, {G, mn}, {X, mk}}, s) != cudaSuccess)
         return SWIGLU_ERR_CUDA;
     }
     if (dX != nullptr) {
+      first = first && dW == nullptr;
       const bool pre = x_act != SWIGLU_ACT_NONE;
       const SlEpiGrad epi{pre ? (const float*)X_pre : nullptr, (float*)dX, K, x_act, 0};
-      if (simt_product<true, false>(host::K_SIMT_LINEAR_DX, g, N, w, K, M, K, N, epi, ws,
+      if (simt_product<true, false>(host::K_SIMT_LINEAR_DX, g, N, w, K, M, K, N, epi, ws, first,
                                     {{dX, mk}, {G, mn}, {W, nk}, {X_pre, pre ? mk : 0}}, s) != cudaSuccess)
         return SWIGLU_ERR_CUDA;
     }
@@ -676,13 +675,14 @@ swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W
   }
   const bool bf = dtype == SWIGLU_BF16;
   if (dW != nullptr &&
-      host::gemm_dw(host::K_LINEAR_DW, bf, G, X, dW, M, N, K, accumulate, err, ws_bytes, s) != cudaSuccess)
+      host::gemm_dw(host::K_LINEAR_DW, bf, G, X, dW, M, N, K, accumulate, err, ws_bytes, first, s) != cudaSuccess)
     return SWIGLU_ERR_CUDA;
+  first = first && dW == nullptr;
   if (dX != nullptr) {
     const EpiDAct::Params ep{X_pre, dX, K, x_act};
-    const cudaError_t c = x_act == SWIGLU_ACT_NONE ? host::gemm_dx(host::K_LINEAR_DX, bf, G, W, dX, M, N, K, err, ws_bytes, s)
-                          : bf ? linear_dx<true>(G, W, ep, M, N, K, err, ws_bytes, s)
-                               : linear_dx<false>(G, W, ep, M, N, K, err, ws_bytes, s);
+    const cudaError_t c = x_act == SWIGLU_ACT_NONE ? host::gemm_dx(host::K_LINEAR_DX, bf, G, W, dX, M, N, K, err, ws_bytes, first, s)
+                          : bf ? linear_dx<true>(G, W, ep, M, N, K, err, ws_bytes, first, s)
+                               : linear_dx<false>(G, W, ep, M, N, K, err, ws_bytes, first, s);
     if (c != cudaSuccess) return SWIGLU_ERR_CUDA;
   }
   return SWIGLU_OK;

@@ -22,6 +22,7 @@ struct DactArgs {
   int64_t M;
   int N;
   int act;
+  int* err;         // cleared here
   RowCheck chk;
 };
 
@@ -34,6 +35,7 @@ __global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
   __shared__ float acc[DA_WARPS][32][N + 1];
   pdl_wait();  // launched early: nothing is touched before the kernel before has ended
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = (blockIdx.x * 32 + lane) * N;
   const int64_t r0 = a.M * blockIdx.y / gridDim.y, r1 = a.M * (blockIdx.y + 1) / gridDim.y;

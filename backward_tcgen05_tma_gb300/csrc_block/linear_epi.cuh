@@ -92,100 +92,85 @@ struct EpiLinear {
   }
 };
 
-// The same for the kernel on SM pairs, which is where many rows go: tiles leave by
-// TMA.  A lane writes its row of a 32 x 64 chunk into the warp's Z and Y boxes
-// (128-byte swizzle: no bank conflicts) and one lane stores both; they are written
-// again when the stores have read them, a chunk's arithmetic later.  The tensor
-// maps clip at M rows and N columns.  The plain form turns every 32 x 32 chunk
-// round through shared memory to store whole sectors, and is bound by those
-// instructions and their latencies: 16384 x 2816 x 1024 with gelu and Z took 117
-// us with it, 107 with boxes of 32 columns in two slots.
-struct EpiLinearTma {
-  static constexpr bool TMA_OUT = true;
-  using Params = EpiLinear::Params;  // (y and z by the tensor maps tmG, tmU)
+// 32 bytes, a whole sector, to or from a lane's own row
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// The same where rows start on 32 bytes (N a multiple of 16, buffers aligned so):
+// a lane stores its own row's sectors whole, straight from its registers.  The
+// plain form turns every chunk round through shared memory to that end, and
+// stores by TMA wait behind the ring's loads in that unit.
+struct EpiLinearSectors {
+  using Params = EpiLinear::Params;
   template <int BN, bool BF16>
   static __device__ __forceinline__ void run(const Params& p, const TcShape& s, uint32_t tacc, int m0, int nt,
-                                             int row, int half, uint8_t* slots, const CUtensorMap* tmY,
-                                             const CUtensorMap* tmZ) {
-    static_assert(GU_SLOTS * GU_SLOT_BYTES >= 2 * 32 * 128, "a Z box and a Y box");
+                                             int row, int half, uint8_t*) {
     using P = Pack<BF16>;
-    const int lane = row & 31;
-    const int mw = m0 + (row & ~31), m = mw + lane;
-    const int n0 = nt * BN + half * (BN / 2);
-    const uint32_t zbox = smem_u32(slots), ybox = zbox + 4096;
-    constexpr int CH = BN / 128;
-    // 16-byte unit q of row r at q ^ (r mod 8)
-    auto put = [&](uint32_t box, int q, const uint32_t* w) {
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((q ^ (lane & 7)) << 4)),
-                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                   : "memory");
+    const int m = m0 + row, n0 = nt * BN;
+    constexpr int CH = BN / 64;
+    auto at = [&](const void* base, int nc) {
+      return static_cast<uint8_t*>(const_cast<void*>(base)) + ((int64_t)m * p.ld + nc) * 2;
     };
-    auto load = [&](uint4 (&v)[8], const void* base, int64_t at, int nc, bool in) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (at + nc) * 2);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        v[q] = in && nc + q * 8 + 8 <= s.N && SWIGLU_CHECK_PTR(s.dbg, src + q, 16, s.err) ? src[q]
-                                                                                         : make_uint4(0u, 0u, 0u, 0u);
-    };
-    if (mw >= s.M) return;
-    uint4 bq[8];
-    load(bq, p.bias, 0, n0, p.bias != nullptr);
 #pragma unroll 1
-    for (int c = 0; c < CH; ++c) {
-      const int nc = n0 + c * 64;
+    for (int c = half * CH; c < (half + 1) * CH; ++c) {
+      const int nc = n0 + c * 32;
       if (nc >= s.N) return;
-      float v[64];
-      {
-        uint32_t r0[32], r1[32];
-        tmem_ld_32x32b_x32(tacc + (half * CH + c) * 64, r0);
-        tmem_ld_32x32b_x32(tacc + (half * CH + c) * 64 + 32, r1);
-        tmem_ld_wait();
+      const bool in0 = m < s.M, in1 = m < s.M && nc + 32 <= s.N;  // the row's two sectors
+      uint32_t rr[16], w[16];
+      uint4 bq[4];
+      const uint4* bias = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.bias) + (int64_t)nc * 2);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 b = P::unpack((&bq[i >> 2].x)[i & 3]);
-          const uint32_t a0 = i < 16 ? r0[2 * i & 31] : r1[2 * i & 31], a1 = i < 16 ? r0[(2 * i & 31) + 1] : r1[(2 * i & 31) + 1];
-          add2(F2(__uint_as_float(a0), __uint_as_float(a1)), F2(b.x, b.y)).get(v[2 * i], v[2 * i + 1]);
-        }
+      for (int q = 0; q < 4; ++q)
+        bq[q] = p.bias != nullptr && nc + q * 8 + 8 <= s.N && SWIGLU_CHECK_PTR(s.dbg, bias + q, 16, s.err)
+                    ? bias[q]
+                    : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) rr[i] = 0;
+      if (p.res != nullptr) {
+        if (in0 && SWIGLU_CHECK_PTR(s.dbg, at(p.res, nc), 32, s.err)) ld_sector(at(p.res, nc), rr);
+        if (in1 && SWIGLU_CHECK_PTR(s.dbg, at(p.res, nc + 16), 32, s.err)) ld_sector(at(p.res, nc + 16), rr + 8);
       }
-      if (c + 1 < CH) load(bq, p.bias, 0, nc + 64, p.bias != nullptr);
-      if (lane == 0) bulk_wait_group_read<0>();  // the boxes are free
-      __syncwarp();
+      auto store = [&](void* base) {
+        if (in0 && SWIGLU_CHECK_PTR(s.dbg, at(base, nc), 32, s.err)) st_sector(at(base, nc), w);
+        if (in1 && SWIGLU_CHECK_PTR(s.dbg, at(base, nc + 16), 32, s.err)) st_sector(at(base, nc + 16), w + 8);
+      };
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tacc + c * 32, r);
+      tmem_ld_wait();
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 b = P::unpack((&bq[i >> 2].x)[i & 3]);
+        add2(F2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), F2(b.x, b.y)).get(v[2 * i], v[2 * i + 1]);
+      }
       if (p.z != nullptr) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = P::two(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
-          put(zbox, q, w);
-        }
+        for (int i = 0; i < 16; ++i) w[i] = P::two(v[2 * i], v[2 * i + 1]);
+        store(p.z);
       }
       act_switch(p.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) act_value2<decltype(a)::value>(v[i], v[i + 1]);
+        for (int i = 0; i < 32; i += 2) act_value2<decltype(a)::value>(v[i], v[i + 1]);
       });
       if (p.res != nullptr) {
-        uint4 rr[8];
-        load(rr, p.res, (int64_t)m * p.ld, nc, m < s.M);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 b = P::unpack((&rr[i >> 2].x)[i & 3]);
+        for (int i = 0; i < 16; ++i) {
+          const float2 b = P::unpack(rr[i]);
           add2(F2(v[2 * i], v[2 * i + 1]), F2(b.x, b.y)).get(v[2 * i], v[2 * i + 1]);
         }
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = P::two(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
-        put(ybox, q, w);
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        if (p.z != nullptr) tma_store_2d(tmZ, zbox, nc, mw);
-        tma_store_2d(tmY, ybox, nc, mw);
-        bulk_commit_group();
-      }
+      for (int i = 0; i < 16; ++i) w[i] = P::two(v[2 * i], v[2 * i + 1]);
+      store(p.y);
     }
   }
 };

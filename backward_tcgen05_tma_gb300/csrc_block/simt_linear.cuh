@@ -30,6 +30,7 @@ struct SlArgs {
   int m_tiles, n_tiles;
   int per;           // k of a part, a multiple of SL_BK
   float* part;       // [parts][M][N], or null: one part, the epilogue at once
+  int* clear;        // the error word, cleared by the first kernel of a call, or null
   SimtCheck chk;
 };
 
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(SL_THREADS, 2) simt_linear_kernel(const SlArgs
   using TB = SlTile<SL_BN, B_KC>;
   __shared__ __align__(16) float As[2][SL_BK * TA::LD];
   __shared__ __align__(16) float Bs[2][SL_BK * TB::LD];
+  if (a.clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.clear = 0;
   const int per_group = 16 * a.n_tiles, grp = blockIdx.x / per_group, left = blockIdx.x - grp * per_group;
   const int gh = min(16, a.m_tiles - grp * 16);
   const int m0 = (grp * 16 + left % gh) * BM, n0 = left / gh * SL_BN;

@@ -43,11 +43,12 @@ int pair_units();
 
 // The plain GEMMs of a backward pass over M tokens, bf16 or fp16: dW [N, K] =
 // G^T X, or with `accumulate` dW + that product; dX [M, K] = G W.  G [M, N], X
-// [M, K] and W [N, K] are contiguous; err: the workspace, cleared by the caller.
+// [M, K] and W [N, K] are contiguous; err: the workspace, whose error word the
+// `first` kernel of a call clears and whose counters are zero between kernels.
 cudaError_t gemm_dw(int id, bool bf16, const void* G, const void* X, void* dW, int64_t M, int64_t N,
-                    int64_t K, int accumulate, int* err, size_t ws_bytes, cudaStream_t st);
+                    int64_t K, int accumulate, int* err, size_t ws_bytes, bool first, cudaStream_t st);
 cudaError_t gemm_dx(int id, bool bf16, const void* G, const void* W, void* dX, int64_t M, int64_t N,
-                    int64_t K, int* err, size_t ws_bytes, cudaStream_t st);
+                    int64_t K, int* err, size_t ws_bytes, bool first, cudaStream_t st);
 
 // Tensor map of a 16-bit array [n2][n1][n0] (n0 contiguous) with boxes of
 // b2 x b1 x b0 elements, 128-byte swizzle; elements outside read as 0.
