@@ -732,13 +732,14 @@ def activation_code(name: str) -> int:
     return ACTIVATIONS[name]
 
 
-def _block_call(f, where, ws, device, *args):
-    """One call on ``device`` (made current where it is not) and its current
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _ready(where, f, args, ws, dev):
+    """One call on device ``dev`` (made current where it is not) and its current
     stream; ``ws`` None: a call without a workspace."""
-    dev = device.index
-    n = 0 if ws is None else ws.numel()
-    w = 0 if ws is None else ws.data_ptr()
-    if dev == torch.cuda.current_device():
+    n, w = (0, 0) if ws is None else (ws.numel(), ws.data_ptr())
+    if dev == _current_device():
         code = f(*args, w, n, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -750,31 +751,49 @@ def _block_call(f, where, ws, device, *args):
             _device_check(ws, where)
 
 
-def _same(where, X, shapes):
-    """Each (name, tensor or None, shape): X's dtype and device, contiguous."""
-    dev, dt = X.get_device(), X.dtype
+def _is(t, shape, dtype, dev) -> bool:
+    return t is None or (t.shape == shape and t.dtype is dtype and t.is_contiguous()
+                         and t.get_device() == dev)
+
+
+def _refuse(where, X, shapes):
+    """Names the one of (name, tensor or None, shape) that is not what it has to be."""
     for name, t, shape in shapes:
-        if t is None:
-            continue
-        if t.shape != shape or t.dtype != dt or t.get_device() != dev or not t.is_contiguous():
+        if not _is(t, shape, X.dtype, X.get_device()):
             raise ValueError("%s: %s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s"
-                             % (where, name, dt, tuple(shape), X.device, t.dtype, tuple(t.shape),
+                             % (where, name, X.dtype, tuple(shape), X.device, t.dtype, tuple(t.shape),
                                 t.device))
 
 
 def _rows(where, X):
-    if X.dim() != 2 or not X.is_cuda or not X.is_contiguous():
+    if X.dim() != 2 or X.get_device() < 0 or not X.is_contiguous():
         raise ValueError("%s: expected contiguous CUDA rows [M, D], got %s" % (where, tuple(X.shape)))
     return X.shape
 
 
-def _sized_ws(ws, size, device, where):
+def _made(out, name, shape, dtype, dev):
+    """The caller's output tensor, checked, or a new one."""
+    t = out.get(name) if out else None
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not _is(t, shape, dtype, dev):
+        raise ValueError("out[%r] must be a contiguous %s tensor of shape %s on cuda:%d"
+                         % (name, dtype, tuple(shape), dev))
+    return t
+
+
+def _sized_ws(ws, where, f, args, dev):
     """The caller's workspace (its size is checked by the call) or a new one."""
     if ws is None:
-        return torch.zeros(int(size()), dtype=torch.uint8, device=device)
-    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError("%s: ws must be a contiguous uint8 tensor on %s" % (where, device))
+        with torch.cuda.device(dev):
+            return torch.zeros(int(f(*args)), dtype=torch.uint8, device=dev)
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("%s: ws must be a contiguous uint8 tensor on cuda:%d" % (where, dev))
     return ws
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def layer_norm_workspace(M: int, D: int, dtype: torch.dtype, device) -> torch.Tensor:
@@ -798,18 +817,20 @@ def swiglu_mlp_layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, resi
     (Y, S, mean, rstd).  S is X itself or the rounded sum; mean and rstd (fp32
     [M], for the backward pass) are None without ``stats``."""
     where = "swiglu_mlp_layer_norm_fwd"
-    M, D = _rows(where, X)
-    _same(where, X, (("weight", weight, (D,)), ("bias", bias, (D,)), ("residual", residual, (M, D))))
-    dev = X.device
-    Y = _out(out, "Y", (M, D), X.dtype, dev)
-    S = None if residual is None else _out(out, "S", (M, D), X.dtype, dev)
-    mean = _out(out, "mean", (M,), torch.float32, dev) if stats else None
-    rstd = _out(out, "rstd", (M,), torch.float32, dev) if stats else None
-    ptr = lambda t: 0 if t is None else t.data_ptr()
+    M, D = rows = _rows(where, X)
+    dt, dev = X.dtype, X.get_device()
+    if not (_is(weight, (D,), dt, dev) and _is(bias, (D,), dt, dev) and _is(residual, rows, dt, dev)):
+        _refuse(where, X, (("weight", weight, (D,)), ("bias", bias, (D,)), ("residual", residual, rows)))
+    Y = _made(out, "Y", rows, dt, dev)
+    S = None if residual is None else _made(out, "S", rows, dt, dev)
+    mean = rstd = None
+    if stats:
+        mean = _made(out, "mean", (M,), torch.float32, dev)
+        rstd = _made(out, "rstd", (M,), torch.float32, dev)
     ws = torch.zeros(256, dtype=torch.uint8, device=dev) if _use_debug else None
-    _block_call((_lib or lib()).swiglu_mlp_layer_norm_fwd, where, ws, dev, X.data_ptr(), ptr(residual),
-                ptr(weight), ptr(bias), ptr(S), Y.data_ptr(), ptr(mean), ptr(rstd), M, D, eps,
-                dtype_code(X.dtype))
+    _ready(where, (_lib or lib()).swiglu_mlp_layer_norm_fwd,
+           (X.data_ptr(), _at(residual), _at(weight), _at(bias), _at(S), Y.data_ptr(), _at(mean), _at(rstd),
+            M, D, eps, dtype_code(dt)), ws, dev)
     return Y, X if S is None else S, mean, rstd
 
 
@@ -821,24 +842,28 @@ def swiglu_mlp_layer_norm_bwd(dY, S, weight, mean, rstd, dS=None, need_dweight: 
     residual stream's), added into dX.  dX is the residual's gradient too.
     ``accumulate``: add into the dweight and dbias given in ``out``."""
     where = "swiglu_mlp_layer_norm_bwd"
-    M, D = _rows(where, S)
-    _same(where, S, (("dY", dY, (M, D)), ("weight", weight, (D,)), ("dS", dS, (M, D))))
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.shape != (M,) or t.dtype != torch.float32 or t.device != S.device or not t.is_contiguous():
-            raise ValueError("%s: %s must be a contiguous fp32 tensor of shape (%d,)" % (where, name, M))
-    dev, want = S.device, {"dweight": need_dweight, "dbias": need_dbias}
-    if accumulate and not all((out or {}).get(k) is not None for k, v in want.items() if v):
+    M, D = rows = _rows(where, S)
+    dt, dev = S.dtype, S.get_device()
+    if not (_is(dY, rows, dt, dev) and _is(weight, (D,), dt, dev) and _is(dS, rows, dt, dev)):
+        _refuse(where, S, (("dY", dY, rows), ("weight", weight, (D,)), ("dS", dS, rows)))
+    if not (_is(mean, (M,), torch.float32, dev) and _is(rstd, (M,), torch.float32, dev)):
+        raise ValueError("%s: mean and rstd must be contiguous fp32 tensors of shape (%d,)" % (where, M))
+    if accumulate and ((need_dweight and _none(out, "dweight")) or (need_dbias and _none(out, "dbias"))):
         raise ValueError("accumulate needs the held dweight and dbias in out")
-    dX = _out(out, "dX", (M, D), S.dtype, dev)
-    dw, db = (_out(out, k, (D,), S.dtype, dev) if v else None for k, v in want.items())
+    dX = _made(out, "dX", rows, dt, dev)
+    dw = _made(out, "dweight", (D,), dt, dev) if need_dweight else None
+    db = _made(out, "dbias", (D,), dt, dev) if need_dbias else None
     L = _lib or lib()
-    dt = dtype_code(S.dtype)
-    ws = _sized_ws(ws, lambda: L.swiglu_mlp_layer_norm_workspace_bytes(M, D, dt), dev, where)
-    ptr = lambda t: 0 if t is None else t.data_ptr()
-    _block_call(L.swiglu_mlp_layer_norm_bwd, where, ws, dev, dY.data_ptr(), S.data_ptr(), ptr(weight),
-                mean.data_ptr(), rstd.data_ptr(), ptr(dS), dX.data_ptr(), ptr(dw), ptr(db), M, D,
-                int(accumulate), dt)
+    code = dtype_code(dt)
+    ws = _sized_ws(ws, where, L.swiglu_mlp_layer_norm_workspace_bytes, (M, D, code), dev)
+    _ready(where, L.swiglu_mlp_layer_norm_bwd,
+           (dY.data_ptr(), S.data_ptr(), _at(weight), mean.data_ptr(), rstd.data_ptr(), _at(dS),
+            dX.data_ptr(), _at(dw), _at(db), M, D, int(accumulate), code), ws, dev)
     return dX, dw, db
+
+
+def _none(out, name) -> bool:
+    return not out or out.get(name) is None
 
 
 def swiglu_mlp_linear_fwd(X, W, bias=None, activation: str = "none", residual=None,
@@ -849,17 +874,17 @@ def swiglu_mlp_linear_fwd(X, W, bias=None, activation: str = "none", residual=No
     where = "swiglu_mlp_linear_fwd"
     M, K = _rows(where, X)
     act = activation_code(activation)
-    N = W.shape[0]
-    _same(where, X, (("W", W, (N, K)), ("bias", bias, (N,)), ("residual", residual, (M, N))))
-    dev = X.device
-    Y = _out(out, "Y", (M, N), X.dtype, dev)
-    Z = _out(out, "Z", (M, N), X.dtype, dev) if keep else None
+    N, dt, dev = W.shape[0], X.dtype, X.get_device()
+    if not (_is(W, (N, K), dt, dev) and _is(bias, (N,), dt, dev) and _is(residual, (M, N), dt, dev)):
+        _refuse(where, X, (("W", W, (N, K)), ("bias", bias, (N,)), ("residual", residual, (M, N))))
+    Y = _made(out, "Y", (M, N), dt, dev)
+    Z = _made(out, "Z", (M, N), dt, dev) if keep else None
     L = _lib or lib()
-    dt = dtype_code(X.dtype)
-    ws = _sized_ws(ws, lambda: L.swiglu_mlp_linear_workspace_bytes(M, N, K, dt, SWIGLU_OP_FWD), dev, where)
-    ptr = lambda t: 0 if t is None else t.data_ptr()
-    _block_call(L.swiglu_mlp_linear_fwd, where, ws, dev, X.data_ptr(), W.data_ptr(), ptr(bias),
-                ptr(residual), ptr(Z), Y.data_ptr(), M, N, K, act, dt)
+    code = dtype_code(dt)
+    ws = _sized_ws(ws, where, L.swiglu_mlp_linear_workspace_bytes, (M, N, K, code, SWIGLU_OP_FWD), dev)
+    _ready(where, L.swiglu_mlp_linear_fwd,
+           (X.data_ptr(), W.data_ptr(), _at(bias), _at(residual), _at(Z), Y.data_ptr(), M, N, K, act, code),
+           ws, dev)
     return Y, Z
 
 
@@ -874,26 +899,26 @@ def swiglu_mlp_linear_bwd(dY, X, W, Z=None, activation: str = "none", X_pre=None
     the pre-activation is left in out["dZ"] where that is given.
     ``accumulate``: add into the dW and dbias given in ``out``."""
     where = "swiglu_mlp_linear_bwd"
-    M, N = _rows(where, dY)
+    M, N = rows = _rows(where, dY)
     act, x_act = activation_code(activation), activation_code(x_activation)
-    K = W.shape[1]
-    _same(where, dY, (("X", X, (M, K)), ("W", W, (N, K)), ("Z", Z, (M, N)), ("X_pre", X_pre, (M, K))))
+    K, dt, dev = W.shape[1], dY.dtype, dY.get_device()
+    if not (_is(X, (M, K), dt, dev) and _is(W, (N, K), dt, dev) and _is(Z, rows, dt, dev)
+            and _is(X_pre, (M, K), dt, dev)):
+        _refuse(where, dY, (("X", X, (M, K)), ("W", W, (N, K)), ("Z", Z, rows), ("X_pre", X_pre, (M, K))))
     if (act and Z is None) or (x_act and need_dX and X_pre is None):
         raise ValueError("%s: activation needs Z, x_activation needs X_pre" % where)
-    if accumulate and any(v and (out or {}).get(k) is None for k, v in (("dW", need_dW), ("dbias", need_dbias))):
+    if accumulate and ((need_dW and _none(out, "dW")) or (need_dbias and _none(out, "dbias"))):
         raise ValueError("accumulate needs the held dW and dbias in out")
-    dev, dtype = dY.device, dY.dtype
-    dZ = _out(out, "dZ", (M, N), dtype, dev) if act else None
-    dX = _out(out, "dX", (M, K), dtype, dev) if need_dX else None
-    dW = _out(out, "dW", (N, K), dtype, dev) if need_dW else None
-    db = _out(out, "dbias", (N,), dtype, dev) if need_dbias else None
+    dZ = _made(out, "dZ", rows, dt, dev) if act else None
+    dX = _made(out, "dX", (M, K), dt, dev) if need_dX else None
+    dW = _made(out, "dW", (N, K), dt, dev) if need_dW else None
+    db = _made(out, "dbias", (N,), dt, dev) if need_dbias else None
     L = _lib or lib()
-    dt = dtype_code(dtype)
-    ws = _sized_ws(ws, lambda: L.swiglu_mlp_linear_workspace_bytes(M, N, K, dt, SWIGLU_OP_BWD), dev, where)
-    ptr = lambda t: 0 if t is None else t.data_ptr()
-    _block_call(L.swiglu_mlp_linear_bwd, where, ws, dev, dY.data_ptr(), X.data_ptr(), W.data_ptr(),
-                ptr(Z), act, ptr(X_pre), x_act, ptr(dZ), ptr(dX), ptr(dW), ptr(db), M, N, K,
-                int(accumulate), dt)
+    code = dtype_code(dt)
+    ws = _sized_ws(ws, where, L.swiglu_mlp_linear_workspace_bytes, (M, N, K, code, SWIGLU_OP_BWD), dev)
+    _ready(where, L.swiglu_mlp_linear_bwd,
+           (dY.data_ptr(), X.data_ptr(), W.data_ptr(), _at(Z), act, _at(X_pre), x_act, _at(dZ), _at(dX),
+            _at(dW), _at(db), M, N, K, int(accumulate), code), ws, dev)
     return dX, dW, db
 
 

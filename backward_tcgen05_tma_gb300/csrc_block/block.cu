@@ -68,6 +68,20 @@ RowCheck row_check(void* ws, std::initializer_list<Win> wins) {
   return c;
 }
 
+// The dynamic shared memory of a kernel, raised once per device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+
 // A launch that may start while the kernel before it on the stream ends; the
 // kernels wait for it before they touch anything.
 template <class... P, class... A>
@@ -149,7 +163,7 @@ cudaError_t ln_backward(LnBwdArgs a, int grid, cudaStream_t st) {
   // the ring, and then the groups' sums in its place
   constexpr int groups = LNB_THREADS / TPR, n = Vec<T>::N;
   const int smem = std::max(a.stages * stage, groups * 2 * (a.D + 4 * n) * 4);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LNB_SMEM);
+  const cudaError_t e = allow_smem<kern>(LNB_SMEM);
   if (e != cudaSuccess) return e;
   return launch(host::K_DLN, kern, dim3((unsigned)grid), LNB_THREADS, (size_t)smem, st, a);
 }
@@ -247,32 +261,34 @@ FewPlan few_plan(int64_t M, int64_t N, int64_t K) {
 // about four blocks on each SM.
 int dact_parts(int64_t M, int64_t N, swiglu_dtype dt) {
   const int64_t strips = (N * (int64_t)bytes_of(dt) + 511) / 512;
-  const int64_t most = (M + DA_WARPS * DA_BATCH - 1) / (DA_WARPS * DA_BATCH);
+  const int64_t most = (M + 2 * DA_WARPS - 1) / (2 * DA_WARPS);
   const int64_t want = (4 * (int64_t)(host::sms() > 0 ? host::sms() : TC_SK_MAX_SMS) + strips - 1) / strips;
   return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
-// fp32 products: tile rows, and parts of the contraction.  Two blocks fit an SM;
-// with fewer tiles than that the contraction is split so that every SM has its
-// two (parts of 64 k at least), whose sums pass through the workspace.
+// fp32 products: which tiles are split over the contraction (parts of 64 k at
+// least), so that two blocks an SM are busy to the end.
 struct SlPlan {
-  int tm, m_tiles, n_tiles, parts, per;
+  int tm, m_tiles, n_tiles, whole, parts, per;
+  int split() const { return m_tiles * n_tiles - whole; }
 };
 SlPlan sl_plan(int64_t M, int64_t N, int64_t K) {
   SlPlan p;
   p.tm = M <= 32 ? 2 : 8;
   p.m_tiles = (int)((M + 16 * p.tm - 1) / (16 * p.tm));
   p.n_tiles = (int)((N + SL_BN - 1) / SL_BN);
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, room = 2 * (int64_t)nsm();
-  int64_t parts = std::max<int64_t>(1, std::min(room / std::max<int64_t>(tiles, 1), (K + 63) / 64));
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, room = 2 * (int64_t)nsm(), rest = tiles % room;
+  const int64_t parts = rest > 0 ? std::min(room / rest, (K + 63) / 64) : 1;
+  p.whole = (int)(parts > 1 ? tiles - rest : tiles);
   p.per = (int)(((K + parts - 1) / parts + SL_BK - 1) / SL_BK * SL_BK);
   p.parts = (int)((K + p.per - 1) / p.per);
+  if (p.parts == 1) p.whole = (int)tiles;
   return p;
 }
 size_t sl_bytes(int64_t M, int64_t N, int64_t K) {
   if (host::sms() < 1) return (size_t)2 * TC_SK_MAX_SMS * 128 * SL_BN * 4;
   const SlPlan p = sl_plan(M, N, K);
-  return p.parts > 1 ? (size_t)p.parts * M * N * 4 : 0;
+  return (size_t)p.split() * p.parts * 16 * p.tm * SL_BN * 4;
 }
 
 size_t linear_bwd_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dt) {
@@ -361,7 +377,7 @@ StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
 template <bool BF16, int NT>
 cudaError_t linear_stream(const StreamPlan& p, LfArgs a, cudaStream_t st) {
   constexpr auto kern = linear_few_kernel<BF16, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LF_SMEM);
+  cudaError_t e = allow_smem<kern>(LF_SMEM);
   if (e != cudaSuccess) return e;
   a.blocks = p.blocks;
   a.halves = p.halves;
@@ -472,18 +488,21 @@ cudaError_t simt_product(int id, const float* A, int64_t lda, const float* B, in
                          int64_t K, const Epi& epi, void* ws, bool first, std::initializer_list<Win> wins,
                          cudaStream_t st) {
   const SlPlan p = sl_plan(M, N, K);
-  SlArgs a = {A, B, lda, ldb, (int)M, (int)N, (int)K, p.m_tiles, p.n_tiles, p.per, nullptr, first ? static_cast<int*>(ws) : nullptr, {}};
-  if (p.parts > 1) a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED);
+  const int split = p.split();
+  SlArgs a = {A, B, lda, ldb, (int)M, (int)N, (int)K, p.m_tiles, p.n_tiles, p.whole, p.parts, p.per,
+              reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED), first ? static_cast<int*>(ws) : nullptr, {}};
 #ifdef SWIGLU_DEBUG
-  // the partial sums take the output's place in the first kernel, and follow it in the second
+  // where all tiles are split, the partial sums take the output's place in the first kernel
   Win with[DBG_WINS];
   const int nw = (int)(std::copy(wins.begin(), wins.end(), with) - with);
-  with[nw] = Win{a.part, p.parts > 1 ? (size_t)p.parts * M * N * 4 : 0};
-  if (p.parts > 1) std::swap(with[0], with[nw]);
+  with[nw] = Win{a.part, (size_t)split * p.parts * 16 * p.tm * SL_BN * 4};
+  if (p.whole == 0) std::swap(with[0], with[nw]);
   a.chk.err = static_cast<int*>(ws);
   a.chk.win = host::windows(with, nw + 1);
+#else
+  (void)wins;
 #endif
-  const dim3 grid((unsigned)(p.m_tiles * p.n_tiles), (unsigned)p.parts);
+  const dim3 grid((unsigned)(p.whole + split * p.parts));
   {
     host::Prof prof(id, st);
     if (p.tm == 2)
@@ -493,16 +512,17 @@ cudaError_t simt_product(int id, const float* A, int64_t lda, const float* B, in
     host::count_launch();
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.parts == 1) return e;
-  const int64_t blocks = (M * N / 4 + 255) / 256;
-  SimtCheck chk = a.chk;
+  if (e != cudaSuccess || split == 0) return e;
 #ifdef SWIGLU_DEBUG
-  std::swap(with[0], with[nw]);
-  chk.win = host::windows(with, nw + 1);
+  if (p.whole == 0) std::swap(with[0], with[nw]);
+  a.chk.win = host::windows(with, nw + 1);
 #endif
   host::Prof prof(id, st);
-  simt_sum_kernel<Epi><<<(unsigned)std::min<int64_t>(blocks, 8 * (int64_t)nsm()), 256, 0, st>>>(
-      a.part, p.parts, (int)M, (int)N, epi, chk);
+  const dim3 sums((unsigned)split, (unsigned)(16 * p.tm * SL_BN / 4 / 256));
+  if (p.tm == 2)
+    simt_sum_kernel<2, Epi><<<sums, 256, 0, st>>>(a, epi);
+  else
+    simt_sum_kernel<8, Epi><<<sums, 256, 0, st>>>(a, epi);
   host::count_launch();
   return cudaGetLastError();
 }
@@ -647,7 +667,8 @@ swiglu_status swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W
     a.chk = row_check(ws, {{has ? dZ : ws, has ? mn : ws_bytes}, {ws, ws_bytes}, {dY, mn}, {Z, has ? mn : 0}});
     const dim3 grid((unsigned)((N * e + 511) / 512), (unsigned)parts);
     cudaError_t c = by_type(dtype, [&](auto t) {
-      return launch(host::K_DACT, dact_kernel<decltype(t)>, grid, DA_THREADS, 0, s, a);
+      return launch(host::K_DACT, has ? dact_kernel<decltype(t), true> : dact_kernel<decltype(t), false>, grid,
+                    DA_THREADS, 0, s, a);
     });
     if (c == cudaSuccess && dbias != nullptr)
       c = column_sums(part, parts, (int)N, dbias, nullptr, (int)N, accumulate, dtype, ws, ws_bytes, s);

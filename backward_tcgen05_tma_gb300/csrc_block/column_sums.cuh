@@ -16,8 +16,8 @@ namespace swiglu {
 
 struct DactArgs {
   const void* dy;   // [M, N]
-  const void* z;    // [M, N], or null: no activation
-  void* dz;         // [M, N] where z is given
+  const void* z;    // [M, N], with an activation
+  void* dz;         // [M, N], with one
   float* part;      // [gridDim.y][N], or null: no sums
   int64_t M;
   int N;
@@ -26,12 +26,12 @@ struct DactArgs {
   RowCheck chk;
 };
 
-constexpr int DA_THREADS = 256, DA_WARPS = DA_THREADS / 32, DA_BATCH = 2;
+constexpr int DA_THREADS = 256, DA_WARPS = DA_THREADS / 32;
 
-template <class T>
-__global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
+template <class T, bool ACT>
+__global__ void __launch_bounds__(DA_THREADS, 4) dact_kernel(const DactArgs a) {
   using V = Vec<T>;
-  constexpr int N = V::N;
+  constexpr int N = V::N, DA_BATCH = ACT ? 2 : 4;  // rows of a warp at a time
   __shared__ float acc[DA_WARPS][32][N + 1];
   pdl_wait();  // launched early: nothing is touched before the kernel before has ended
   pdl_launch_dependents();
@@ -49,11 +49,12 @@ __global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
 #pragma unroll
       for (int b = 0; b < DA_BATCH; ++b) {
         const int64_t row = r + b * DA_WARPS, o = row * a.N + col;
-        wy[b] = wz[b] = make_uint4(0u, 0u, 0u, 0u);
+        wy[b] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (ACT) wz[b] = wy[b];
         if (row < r1) {
           const T* py = static_cast<const T*>(a.dy) + o;
           if (row_ok(a.chk, py, 16)) wy[b] = ld_stream(py);
-          if (a.z != nullptr) {
+          if constexpr (ACT) {
             const T* pz = static_cast<const T*>(a.z) + o;
             if (row_ok(a.chk, pz, 16)) wz[b] = ld_stream(pz);
           }
@@ -66,16 +67,17 @@ __global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
 #pragma unroll
       for (int b = 0; b < DA_BATCH; ++b) {
         cy[b] = wy[b];
-        cz[b] = wz[b];
+        if constexpr (ACT) cz[b] = wz[b];
       }
       load(r + DA_WARPS * DA_BATCH);
 #pragma unroll
       for (int b = 0; b < DA_BATCH; ++b) {
         const int64_t row = r + b * DA_WARPS;
         if (row >= r1) break;
-        float y[N], z[N];
+        float y[N];
         V::unpack(cy[b], y);
-        if (a.z != nullptr) {
+        if constexpr (ACT) {
+          float z[N];
           V::unpack(cz[b], z);
           act_switch(a.act, [&](auto t) {
 #pragma unroll

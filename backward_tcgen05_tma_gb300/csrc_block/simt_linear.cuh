@@ -7,9 +7,11 @@
 // Blocks of 256 threads compute 16 TM x 128 tiles, TM x 8 a thread (TM = 8; 2 for
 // up to 32 rows), over k in steps of 16 through two shared-memory buffers that
 // hold both operands with k outermost.  Two columns share one fma.rn.f32x2, each
-// half rounded as an fma of its own, which halves the instructions to issue.  Where
-// the tiles are fewer than two for each SM, the contraction is split and a second
-// kernel adds the parts in order and applies the epilogue.
+// half rounded as an fma of its own, which halves the instructions to issue.  Two
+// blocks fit an SM.  The tiles of a last round that would leave half of those
+// places empty or more are split over the contraction, and a second kernel adds
+// the parts in order and applies the epilogue.  1999 x 2824 x 1032 (368 tiles of
+// 128 x 128, 64 of them in 4 parts): 221 us, 53 TFLOP/s; 324 with all tiles whole.
 //
 // An operand comes with k contiguous (KC: rows of it are turned on the way to
 // shared memory) or with its own index contiguous.
@@ -28,8 +30,10 @@ struct SlArgs {
   int64_t lda, ldb;  // elements between rows of k (KC), or between k
   int M, N, K;
   int m_tiles, n_tiles;
+  int whole;         // tiles [0, whole) are taken whole, the others in parts
+  int parts;
   int per;           // k of a part, a multiple of SL_BK
-  float* part;       // [parts][M][N], or null: one part, the epilogue at once
+  float* part;       // [(tiles - whole) * parts][tile]
   int* clear;        // the error word, cleared by the first kernel of a call, or null
   SimtCheck chk;
 };
@@ -152,6 +156,13 @@ struct SlTile {
 
 // Tiles go down columns of up to 16 tile rows, so that the blocks that run at one
 // time share few columns of B.
+__device__ __forceinline__ void sl_tile(const SlArgs& a, int tile, int bm, int& m0, int& n0) {
+  const int per_group = 16 * a.n_tiles, grp = tile / per_group, left = tile - grp * per_group;
+  const int gh = min(16, a.m_tiles - grp * 16);
+  m0 = (grp * 16 + left % gh) * bm;
+  n0 = left / gh * SL_BN;
+}
+
 template <int TM, bool A_KC, bool B_KC, class Epi>
 __global__ void __launch_bounds__(SL_THREADS, 2) simt_linear_kernel(const SlArgs a, const Epi epi) {
   constexpr int BM = 16 * TM;
@@ -160,10 +171,10 @@ __global__ void __launch_bounds__(SL_THREADS, 2) simt_linear_kernel(const SlArgs
   __shared__ __align__(16) float As[2][SL_BK * TA::LD];
   __shared__ __align__(16) float Bs[2][SL_BK * TB::LD];
   if (a.clear != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.clear = 0;
-  const int per_group = 16 * a.n_tiles, grp = blockIdx.x / per_group, left = blockIdx.x - grp * per_group;
-  const int gh = min(16, a.m_tiles - grp * 16);
-  const int m0 = (grp * 16 + left % gh) * BM, n0 = left / gh * SL_BN;
-  const int k0 = blockIdx.y * a.per, k1 = min(a.K, k0 + a.per);
+  const int split = (int)blockIdx.x - a.whole;  // >= 0: a part of a split tile
+  int m0, n0;
+  sl_tile(a, split < 0 ? (int)blockIdx.x : a.whole + split / a.parts, BM, m0, n0);
+  const int k0 = split < 0 ? 0 : split % a.parts * a.per, k1 = split < 0 ? a.K : min(a.K, k0 + a.per);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   constexpr int AV = TM < 4 ? TM : 4;  // rows of a thread that follow one another
   uint64_t acc[TM][4];
@@ -227,39 +238,39 @@ __global__ void __launch_bounds__(SL_THREADS, 2) simt_linear_kernel(const SlArgs
   }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = m0 + (i / AV) * 16 * AV + ty * AV + i % AV;
+    const int mt = (i / AV) * 16 * AV + ty * AV + i % AV, m = m0 + mt;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int n = n0 + j * 64 + tx * 4;
-      if (m >= a.M || n >= a.N) continue;
       float v[4];
       asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(acc[i][2 * j]));
       asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2]), "=f"(v[3]) : "l"(acc[i][2 * j + 1]));
-      if (a.part != nullptr)
-        sl_store4(a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n, v, a.chk);
-      else
+      if (split >= 0)
+        sl_store4(a.part + (int64_t)split * (BM * SL_BN) + mt * SL_BN + (n - n0), v, a.chk);
+      else if (m < a.M && n < a.N)
         epi.apply(m, n, v, a.chk);
     }
   }
 }
 
-template <class Epi>
-__global__ void __launch_bounds__(256) simt_sum_kernel(const float* part, int parts, int M, int N, const Epi epi,
-                                                       const SimtCheck chk) {
-  const int64_t quads = (int64_t)M * N / 4;
-  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < quads; q += (int64_t)gridDim.x * 256) {
-    const int m = (int)(q / (N / 4)), n = (int)(q - (int64_t)m * (N / 4)) * 4;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+template <int TM, class Epi>
+__global__ void __launch_bounds__(256) simt_sum_kernel(const SlArgs a, const Epi epi) {
+  constexpr int BM = 16 * TM, QUADS = BM * SL_BN / 4;
+  const int t = blockIdx.x;
+  int m0, n0;
+  sl_tile(a, a.whole + t, BM, m0, n0);
+  const int q = blockIdx.y * 256 + threadIdx.x, m = m0 + q / (SL_BN / 4), n = n0 + q % (SL_BN / 4) * 4;
+  if (q >= QUADS || m >= a.M || n >= a.N) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float4 w = sl_load4(part + (int64_t)p * M * N + q * 4, chk);
-      v[0] += w.x;
-      v[1] += w.y;
-      v[2] += w.z;
-      v[3] += w.w;
-    }
-    epi.apply(m, n, v, chk);
+  for (int p = 0; p < a.parts; ++p) {
+    const float4 w = sl_load4(a.part + ((int64_t)t * a.parts + p) * (BM * SL_BN) + q * 4, a.chk);
+    v[0] += w.x;
+    v[1] += w.y;
+    v[2] += w.z;
+    v[3] += w.w;
   }
+  epi.apply(m, n, v, a.chk);
 }
 
 }  // namespace swiglu
