@@ -782,11 +782,16 @@ def _made(out, name, shape, dtype, dev):
     return t
 
 
+_WS_ZERO = 1280  # bytes of a workspace that have to be zero before its first use here
+
+
 def _sized_ws(ws, where, f, args, dev):
     """The caller's workspace (its size is checked by the call) or a new one."""
     if ws is None:
         with torch.cuda.device(dev):
-            return torch.zeros(int(f(*args)), dtype=torch.uint8, device=dev)
+            ws = torch.empty(int(f(*args)), dtype=torch.uint8, device=dev)
+            ws[:_WS_ZERO].zero_()
+        return ws
     if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("%s: ws must be a contiguous uint8 tensor on cuda:%d" % (where, dev))
     return ws

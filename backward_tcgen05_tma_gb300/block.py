@@ -261,8 +261,10 @@ class MLPBlock(torch.nn.Module):
 
     ``mlp`` is an ``MLP`` (the sum is in its second product's epilogue), a
     ``module.SwiGLUMLP``, or for inference a ``serving.W4SwiGLUMLP`` or
-    ``serving.MoESwiGLU``.  ``delta`` is what the sublayer before (an attention)
-    adds to the stream: it is added in the norm's kernel."""
+    ``serving.MoESwiGLU``.  ``delta`` is what the sublayer before (an attention,
+    or another of these) adds to the stream: it is added in the norm's kernel.
+    With ``join=False`` the sum behind is left to the next one in the same way:
+    (s, mlp(norm(s))) is returned."""
 
     def __init__(self, mlp, hidden_size: int | None = None, eps: float = 1e-5, bias: bool = True,
                  dtype=torch.bfloat16, device=None):
@@ -271,11 +273,13 @@ class MLPBlock(torch.nn.Module):
         self.norm = LayerNorm(D, eps, bias=bias, dtype=dtype, device=device)
         self.mlp = mlp
 
-    def forward(self, x, delta=None):
+    def forward(self, x, delta=None, join: bool = True):
         if delta is None:
             y, s = self.norm(x), x
         else:
             y, s = self.norm(delta, x)
+        if not join:
+            return s, self.mlp(y)
         if isinstance(self.mlp, MLP):
             return self.mlp(y, s)
         return s + self.mlp(y)

@@ -599,7 +599,7 @@ size_t swiglu_mlp_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, swiglu
   if (check_linear(M, N, K, 0, dtype) != SWIGLU_OK || (op != SWIGLU_OP_FWD && op != SWIGLU_OP_BWD)) return 0;
   if (op == SWIGLU_OP_BWD) return linear_bwd_bytes(M, N, K, dtype);
   if (dtype == SWIGLU_F32_IEEE) return FIXED + sl_bytes(M, N, K);
-  if (few_tokens(M, dtype)) return few_plan(M, N, K).bytes;
+  if (few_tokens(M, dtype)) return stream_plan(M, N, K).fits ? FIXED : few_plan(M, N, K).bytes;
   return FIXED + gemm_part_bytes(M, N, K, false);
 }
 

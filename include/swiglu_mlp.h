@@ -445,11 +445,11 @@ swiglu_status swiglu_mlp_moe_fwd_nograd(const void* X, const void* Wr, const voi
  * `accumulate` (0 or 1): 1 adds to the gradients of weights and biases that are
  * there, with one rounding of the fp32 sum.
  *
- * Workspaces follow the workspace rules (zero-filled before first use and
- * after a timeout; calls that share one must not overlap).  One that is large
- * enough serves the calls of this section in turn, whatever their kinds and
- * sizes; after calls of other sections its first 1280 bytes (header and
- * counters) have to be zero again.
+ * Workspaces follow the workspace rules (calls that share one must not overlap),
+ * but only their first 1280 bytes (header and counters) have to be zero before
+ * first use and after a timeout.  One that is large enough serves the calls of
+ * this section in turn, whatever their kinds and sizes; after calls of other
+ * sections those bytes have to be zero again.
  *
  * Infinities and NaN give what the formulas give, in their own rows (and in
  * the sums over rows); the activations' derivatives take their limits at
