@@ -29,7 +29,7 @@ struct DactArgs {
 constexpr int DA_THREADS = 256, DA_WARPS = DA_THREADS / 32;
 
 template <class T, bool ACT>
-__global__ void __launch_bounds__(DA_THREADS, 4) dact_kernel(const DactArgs a) {
+__global__ void __launch_bounds__(DA_THREADS) dact_kernel(const DactArgs a) {
   using V = Vec<T>;
   constexpr int N = V::N, DA_BATCH = ACT ? 2 : 4;  // rows of a warp at a time
   __shared__ float acc[DA_WARPS][32][N + 1];
