@@ -5,8 +5,12 @@
 //   dZ = rnd(dY act'(Z)),   db = sum over rows of dY act'(Z) (not of the rounded dZ)
 //
 // Bound by memory.  A warp reads 512 contiguous bytes of a row; a block's 8
-// warps take the rows of its part in turn and its sums meet in shared memory;
-// the parts' sums are added by a second kernel in the order of the parts.
+// warps take the rows of its part in turn, the next ones' loads under way, and its
+// sums meet in shared memory; the parts' sums are added by a second kernel in the
+// order of the parts.  Measured: 16384 x 2816 fp16 with gelu 52 us (5.3 TB/s; 78
+// before activations went in pairs and rows were read ahead), 32768 x 2048 bf16
+// without 26 us (5.2 TB/s).  No more registers than it needs: where they filled
+// the SM, the products behind it could not start early (20 us of 205).
 #pragma once
 
 #include "act.cuh"

@@ -16,15 +16,21 @@
 // small against their sum of sizes.
 //
 // Both are bound by memory: every input is read once and every output written
-// once.  A row is held by TPR threads, VPT vectors of 16 bytes each.
+// once.  A row is held by TPR threads, VPT vectors of 16 bytes each.  Measured,
+// with the residual: 65536 x 4096 bf16 309 us forward (6.9 TB/s) and 330 us
+// backward (6.5 TB/s); 16384 x 1024 fp16 backward without one 27 us (3.7 TB/s: 7
+// rows a warp, of which the first has to arrive and the sums to be added up).
 //
 // Backward is persistent: a block's groups of TPR threads (a warp up to 1024
 // 16-bit elements: what bounds short rows is the latency of a row's two sums, so
-// many rows are in progress) take rows in turn and keep the gradients of w and b of their columns in registers, so that the
-// reduction over rows costs one partial row pair per block.  Its rows arrive
-// through a ring in shared memory that each thread fills for itself (cp.async):
-// no thread waits for another's copies.  Partial sums are added in the order of
-// the groups, then of the blocks: the result does not depend on timing.
+// many rows are in progress) take rows in turn and keep the gradients of w and b
+// of their columns in registers, so that the reduction over rows costs one
+// partial row pair per block.  Its rows arrive through a ring in shared memory
+// that each thread fills for itself (cp.async): no thread waits for another's
+// copies.  (With two vectors a thread, half as many rows in progress, and the
+// groups' sums added one group after another, these two cases took 390 and 36
+// us.)  Partial sums are added in the order of the groups, then of the blocks: the
+// result does not depend on timing.
 #pragma once
 
 #include "vec16.cuh"

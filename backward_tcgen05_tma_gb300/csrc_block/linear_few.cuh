@@ -18,6 +18,10 @@
 // items.  (A third one meant code for three orders of them, which the compiler
 // folded into moves of registers and waits for what they hold.)
 //
+// Measured, back to back: 2816 x 1024 one token 5.0 us (tcgen05 form: 11.2), 2056 x
+// 5640 thirteen 7.5 (14.3; 3.1 TB/s), 11008 x 4096 one 20.5 (26.4; 4.4 TB/s).  At
+// 64 tokens the products' instructions and their latencies bound it.
+//
 // Each warp's receive buffers are two: what a source sends for a use of one of
 // them it sends after it was itself sent to, in between, by a warp that had done
 // with the use before last (ownership goes round the parts evenly).

@@ -11,7 +11,8 @@
 // blocks fit an SM.  The tiles of a last round that would leave half of those
 // places empty or more are split over the contraction, and a second kernel adds
 // the parts in order and applies the epilogue.  1999 x 2824 x 1032 (368 tiles of
-// 128 x 128, 64 of them in 4 parts): 221 us, 53 TFLOP/s; 324 with all tiles whole.
+// 128 x 128, 64 of them in 4 parts): 277 us, 42 TFLOP/s, the FMA pipe busy two
+// thirds of the time; 324 with all tiles whole, 577 with tiles of 64 x 64.
 //
 // An operand comes with k contiguous (KC: rows of it are turned on the way to
 // shared memory) or with its own index contiguous.
