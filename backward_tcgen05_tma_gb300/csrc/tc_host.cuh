@@ -273,7 +273,9 @@ inline TcShape linear_plan(int64_t M, int64_t N, int64_t K, int64_t n_per_tile, 
   }
   int64_t best = kb, units = tiles;
   for (int64_t s = 2; (s - 1) * tiles < all; ++s) {
-    const int64_t u = s * tiles < all ? s * tiles : all, cost = kb * tiles / u + 18 + 8 * s;
+    // (parts that are no whole share of a tile give it one more reader's sums to read)
+    const bool even = s * tiles <= all;
+    const int64_t u = even ? s * tiles : all, cost = kb * tiles / u + 18 + 8 * (even ? s : s + 1);
     if (cost < best) {
       best = cost;
       units = u;
