@@ -267,9 +267,14 @@ class MLPBlock(torch.nn.Module):
     (s, mlp(norm(s))) is returned."""
 
     def __init__(self, mlp, hidden_size: int | None = None, eps: float = 1e-5, bias: bool = True,
-                 dtype=torch.bfloat16, device=None):
+                 dtype=None, device=None):
         super().__init__()
         D = int(mlp.hidden_size if hidden_size is None else hidden_size)
+        like = next(mlp.parameters(), None)  # the norm's type and place, unless given
+        if like is not None:
+            dtype = like.dtype if dtype is None else dtype
+            device = like.device if device is None else device
+        dtype = torch.bfloat16 if dtype is None else dtype
         self.norm = LayerNorm(D, eps, bias=bias, dtype=dtype, device=device)
         self.mlp = mlp
 

@@ -149,7 +149,8 @@ def test_modules_load_other_blocks_state():
         m = block.MLP(64, 96, dtype=torch.float32)
         m.load_state_dict(state)
         assert torch.equal(m.up_weight, lins[0].weight) and torch.equal(m.down_bias, lins[1].bias)
-        b = block.MLPBlock(block.MLP(64, 96, dtype=torch.float32), dtype=torch.float32)
+        b = block.MLPBlock(block.MLP(64, 96, dtype=torch.float32))
+        assert b.norm.weight.dtype == torch.float32
         b.load_state_dict({"norm.weight": ref.weight, "norm.bias": ref.bias,
                            **{"mlp." + k: v for k, v in state.items()}})
         assert torch.equal(b.mlp.down_weight, lins[1].weight)
