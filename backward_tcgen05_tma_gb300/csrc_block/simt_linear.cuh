@@ -8,11 +8,11 @@
 // up to 32 rows), over k in steps of 16 through two shared-memory buffers that
 // hold both operands with k outermost.  Two columns share one fma.rn.f32x2, each
 // half rounded as an fma of its own, which halves the instructions to issue.  Two
-// blocks fit an SM.  The tiles of a last round that would leave half of those
-// places empty or more are split over the contraction, and a second kernel adds
-// the parts in order and applies the epilogue.  1999 x 2824 x 1032 (368 tiles of
-// 128 x 128, 64 of them in 4 parts): 277 us, 42 TFLOP/s, the FMA pipe busy two
-// thirds of the time; 324 with all tiles whole, 577 with tiles of 64 x 64.
+// blocks fit an SM.  The tiles of a last round that would leave many of those
+// places empty are split over the contraction, and a second kernel adds the parts
+// in order and applies the epilogue.  1999 x 2824 x 1032 (368 tiles of 128 x 128,
+// 64 of them split): 263 us, 44 TFLOP/s, 60% of the FMA pipe; 324 with all tiles
+// whole, 577 with tiles of 64 x 64.
 //
 // An operand comes with k contiguous (KC: rows of it are turned on the way to
 // shared memory) or with its own index contiguous.
@@ -133,8 +133,15 @@ struct SlTile {
       const int r = r0 + (KC ? q / (SL_BK / 4) : q % (ROWS / 4) * 4);
       const int k = k0 + (KC ? q % (SL_BK / 4) * 4 : q / (ROWS / 4));
       const float* at = p + (KC ? (int64_t)r * ld + k : (int64_t)k * ld + r);
-      const bool in = q < QUADS && r < rows && k < k1;
-      v[i] = in ? sl_load4(at, chk) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      bool in = q < QUADS && r < rows && k < k1;
+      in = in && SWIGLU_CHECK_PTR(chk.win, at, 16, chk.err);
+      // predicated and in its place: a k-tile's arithmetic ahead of its use
+      v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
+          "@p ld.global.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+          : "+f"(v[i].x), "+f"(v[i].y), "+f"(v[i].z), "+f"(v[i].w)
+          : "l"(at), "r"((int)in));
     }
   }
   __device__ __forceinline__ void put(float* s) const {
@@ -252,6 +259,63 @@ __global__ void __launch_bounds__(SL_THREADS, 2) simt_linear_kernel(const SlArgs
         epi.apply(m, n, v, a.chk);
     }
   }
+}
+
+// Up to 8 rows of X (ROWS >= M of them, R rows of W a block): the weights' bytes are
+// the bound.  A block's 8 warps split k; lanes read 16 bytes of each row, coalesced,
+// X from the caches; sums meet over the lanes, then over the warps in order.
+// 4096 x 4096, one row, weights in the L2: 52 us in tiles of 32 rows, 6.6 so.
+template <int ROWS, class Epi>
+__global__ void __launch_bounds__(SL_THREADS) simt_rows_kernel(const SlArgs a, const Epi epi) {
+  constexpr int R = ROWS == 8 ? 4 : 8, WARPS = SL_THREADS / 32;
+  static_assert(R % 4 == 0, "the epilogue takes four columns");
+  __shared__ float sums[WARPS][ROWS][R];
+  if (a.clear != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.clear = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * R;
+  const int quads = a.K / 4, q0 = (int)((int64_t)quads * warp / WARPS), q1 = (int)((int64_t)quads * (warp + 1) / WARPS);
+  float acc[ROWS][R];
+#pragma unroll
+  for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[m][r] = 0.0f;
+#pragma unroll 2
+  for (int q = q0 + lane; q < q1; q += 32) {
+    float4 w[R], x[ROWS];
+#pragma unroll
+    for (int r = 0; r < R; ++r)  // (rows past N repeat the last)
+      w[r] = sl_load4(a.B + (int64_t)min(n0 + r, a.N - 1) * a.ldb + q * 4, a.chk);
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) x[m] = sl_load4(a.A + (int64_t)min(m, a.M - 1) * a.lda + q * 4, a.chk);
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v = acc[m][r];
+        v = fmaf(x[m].x, w[r].x, v);
+        v = fmaf(x[m].y, w[r].y, v);
+        v = fmaf(x[m].z, w[r].z, v);
+        acc[m][r] = fmaf(x[m].w, w[r].w, v);
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v = acc[m][r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) sums[warp][m][r] = v;
+    }
+  __syncthreads();
+  const int m = threadIdx.x / (R / 4), c = threadIdx.x % (R / 4) * 4;
+  if (m >= ROWS || m >= a.M || n0 + c >= a.N) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += sums[w][m][c + i];
+  epi.apply(m, n0 + c, v, a.chk);
 }
 
 template <int TM, class Epi>

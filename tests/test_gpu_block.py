@@ -322,6 +322,14 @@ def test_linear_few_tokens_both_forms(dtn, M, N, K):
     within(Y, act64("silu", z) + R.double(), U[dtn], slack, 1.2 * root + z.abs() + R.double().abs())
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 4, 4), (2, 12, 20), (4, 1004, 132), (5, 44, 20004), (8, 2060, 516), (9, 44, 5004),
+                                   (32, 132, 9004), (2500, 1500, 2052), (1500, 2500, 36)])
+def test_linear_in_fp32(M, N, K):
+    # up to 8 rows, sizes that are odd multiples of 4, and last rounds in many parts
+    test_linear_forward("f32", M, N, K)
+    test_linear_backward("f32", M, N, K)
+
+
 def test_activation_slopes_are_those_of_differences():
     z = torch.linspace(-6, 6, 997, dtype=torch.float64)
     for act in ACTS:
