@@ -48,7 +48,7 @@ struct NgArgs {
   int sk_tiles;     // tiles [0, sk_tiles) are shared stream-K; the rest are whole,
                     //   (tiles - sk_tiles) / gridDim.x per CTA
   int seg_max;      // partial slots per CTA (>= stream-K segments of any CTA)
-  float* part;      // [gridDim.x * seg_max][128][NT] fp32 partial tiles
+  float* part;      // [gridDim.x * seg_max][128][NT] fp32 partial tiles (ng_part_at)
   int* counters;    // [tiles] arrival counters, zero at launch
   int* zero_ptr;    // block 0 zeroes zero_ptr[0 .. zero_count): the other
   int zero_count;   //   kernel's counters (after the dependency wait)
@@ -235,7 +235,14 @@ __device__ __forceinline__ void ng_store_whole(const NgArgs& a, int tile, uint32
   }
 }
 
-// The accumulator as an fp32 partial tile [128][NT] at ``dst`` (the stores
+// A partial tile is laid out [NT / 4][128 rows][4]: the lanes of a warp, one row
+// each, move 512 consecutive bytes with each float4.
+template <int NT>
+__device__ __forceinline__ int ng_part_at(int row, int n) {
+  return (n >> 2) * 512 + row * 4;
+}
+
+// The accumulator as an fp32 partial tile at ``dst`` (the stores
 // skipped when ``ok`` is false: a debug check failed).  Callers publish it
 // with one release after a barrier over the 128 threads.
 template <int NT>
@@ -243,7 +250,6 @@ __device__ __forceinline__ void ng_store_partial(float* dst, uint32_t tacc, uint
                                                  bool ok = true) {
   const int row = (threadIdx.x & 96) + (threadIdx.x & 31);
   tc_fence_after();
-  float* drow = dst + (size_t)row * NT;
   const uint32_t taddr = tacc + ((uint32_t)(row & 96) << 16);
 #pragma unroll
   for (int c = 0; c < NT; c += 16) {
@@ -253,7 +259,7 @@ __device__ __forceinline__ void ng_store_partial(float* dst, uint32_t tacc, uint
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (ok)
-        reinterpret_cast<float4*>(drow + c)[q] =
+        *reinterpret_cast<float4*>(dst + ng_part_at<NT>(row, c + 4 * q)) =
             make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
                         __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
   }
@@ -286,9 +292,9 @@ __device__ __forceinline__ void ng_reduce_store(const NgArgs& a, int tile, int n
           const bool pok = SWIGLU_CHECK_PTR(a.dbg, pb, 128 * NT * 4, a.err);
 #pragma unroll
           for (int k = 0; k < NT / 8; ++k) {
-            vg[q][k] = pok ? __ldcg(reinterpret_cast<const float4*>(pb + jr * NT + h * (NT / 2)) + k)
+            vg[q][k] = pok ? __ldcg(reinterpret_cast<const float4*>(pb + ng_part_at<NT>(jr, h * (NT / 2) + 4 * k)))
                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            vu[q][k] = pok ? __ldcg(reinterpret_cast<const float4*>(pb + (64 + jr) * NT + h * (NT / 2)) + k)
+            vu[q][k] = pok ? __ldcg(reinterpret_cast<const float4*>(pb + ng_part_at<NT>(64 + jr, h * (NT / 2) + 4 * k)))
                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
         }
@@ -324,10 +330,9 @@ __device__ __forceinline__ void ng_reduce_store(const NgArgs& a, int tile, int n
         if (i0 + q < n) {
           const float* pt = part_of(i0 + q);
           const bool pok = SWIGLU_CHECK_PTR(a.dbg, pt, 128 * NT * 4, a.err);
-          const float* pb = pt + e * NT;
 #pragma unroll
           for (int k = 0; k < NT / 4; ++k)
-            v[q][k] = pok ? __ldcg(reinterpret_cast<const float4*>(pb) + k)
+            v[q][k] = pok ? __ldcg(reinterpret_cast<const float4*>(pt + ng_part_at<NT>(e, 4 * k)))
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
