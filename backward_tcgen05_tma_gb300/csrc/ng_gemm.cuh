@@ -62,10 +62,6 @@ struct NgArgs {
   float scale = 1.0f;  // gate/up: gate multiplier (SiLU(scale g) u); down: Y = scale y
   const uint8_t* wpack = nullptr;  // PACKED: this GEMM's boxes, box (tile, kb) at
                                    //   (tile * kb_tile + kb) * 16 KB
-  const void* bias = nullptr;      // outputs with an epilogue of their own (linear_epi.cuh):
-  const void* res = nullptr;       //   bias [rows], residual and pre-activation [M, ld_out],
-  void* z = nullptr;               //   activation
-  int act = 0;
 #ifdef SWIGLU_DEBUG
   DbgWin dbg;       // buffers the kernel may touch by plain accesses: out, workspace
 #endif
@@ -83,18 +79,6 @@ __device__ __forceinline__ void ng_put(const NgArgs& a, int m, int col, float v)
     if (SWIGLU_CHECK_PTR(a.dbg, o, 2, a.err)) *o = __float2half_rn(v);
   }
 }
-
-// The plain output of a feature d of the not gated form: out[n, d] = rnd(scale v[n]).
-struct NgPlain {
-  static constexpr bool WAIT_FIRST = false;  // (a gated pair's second kernel has its own wait)
-  template <int NT, bool BF16>
-  static __device__ __forceinline__ void store(const NgArgs& a, int d, const float (&v)[NT]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n < a.M) ng_put<BF16>(a, n, d, a.scale * v[n]);
-    }
-  }
-};
 
 template <int NT, int RING_KB = 110>
 struct NgSmem {
@@ -195,7 +179,7 @@ __device__ __forceinline__ int epi_bar_and(int v) {
 
 // A whole tile's output straight from TMEM.  gate/up: rows 0..63 hold G and
 // rows 64..127 U of the same 64 hidden units, met through ``ustage``.
-template <int NT, bool GATE_UP, bool BF16, class Out = NgPlain>
+template <int NT, bool GATE_UP, bool BF16>
 __device__ __forceinline__ void ng_store_whole(const NgArgs& a, int tile, uint32_t tacc,
                                                uint32_t acce, float* ustage) {
   const int row = (threadIdx.x & 96) + (threadIdx.x & 31);  // (warp & 3) * 32 + lane
@@ -231,7 +215,12 @@ __device__ __forceinline__ void ng_store_whole(const NgArgs& a, int tile, uint32
     epi_bar_sync();  // ustage is free again
   } else {
     const int d = tile * 128 + row;
-    if (d < a.rows) Out::template store<NT, BF16>(a, d, v);
+    if (d < a.rows) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n < a.M) ng_put<BF16>(a, n, d, a.scale * v[n]);
+      }
+    }
   }
 }
 
@@ -269,7 +258,7 @@ __device__ __forceinline__ void ng_store_partial(float* dst, uint32_t tacc, uint
 
 // Sums the n partial tiles part_of(0), ..., part_of(n-1) in that order and
 // writes the tile's output (gate/up: A = rnd(SiLU(g) * u); down: Y = rnd(y)).
-template <int NT, bool GATE_UP, bool BF16, class Out = NgPlain, class PartOf>
+template <int NT, bool GATE_UP, bool BF16, class PartOf>
 __device__ __forceinline__ void ng_reduce_store(const NgArgs& a, int tile, int n, PartOf part_of) {
   // partials loaded per batch (the down tiles' per-thread share is half the
   // gate/up pair's)
@@ -345,7 +334,12 @@ __device__ __forceinline__ void ng_reduce_store(const NgArgs& a, int tile, int n
           }
         }
     }
-    if (d < a.rows) Out::template store<NT, BF16>(a, d, y);
+    if (d < a.rows) {
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        if (q < a.M) ng_put<BF16>(a, q, d, a.scale * y[q]);
+      }
+    }
   }
 }
 
@@ -353,14 +347,14 @@ __device__ __forceinline__ void ng_reduce_store(const NgArgs& a, int tile, int n
 // TMEM; else this CTA's partial to the workspace, and the tile's last
 // contributor (per-tile arrival counter) sums the partials in CTA order and
 // writes the output.  Returns true when this CTA wrote the tile's output.
-template <int NT, bool GATE_UP, bool BF16, class Out>
+template <int NT, bool GATE_UP, bool BF16>
 __device__ __forceinline__ bool ng_epilogue_segment(const NgArgs& a, int tile, bool whole, int seg,
                                                     uint32_t tacc, uint32_t acce, int64_t total,
                                                     int64_t ctas, float* ustage,
                                                     volatile int* abort_flag,
                                                     volatile int* last_flag) {
   if (whole) {
-    ng_store_whole<NT, GATE_UP, BF16, Out>(a, tile, tacc, acce, ustage);
+    ng_store_whole<NT, GATE_UP, BF16>(a, tile, tacc, acce, ustage);
     return true;
   }
   float* const dst = a.part + ((size_t)blockIdx.x * a.seg_max + seg) * 128 * NT;
@@ -385,7 +379,7 @@ __device__ __forceinline__ bool ng_epilogue_segment(const NgArgs& a, int tile, b
   if (last) {
     __threadfence();
     // partial of CTA c for this tile: its segment index is tile - (first tile of c)
-    ng_reduce_store<NT, GATE_UP, BF16, Out>(a, tile, nparts, [&](int i) -> const float* {
+    ng_reduce_store<NT, GATE_UP, BF16>(a, tile, nparts, [&](int i) -> const float* {
       const int c = c_first + i;
       const int j = tile - (int)(ng_start(c, total, ctas) / a.kb_tile);
       return SWIGLU_CHECK(j >= 0 && j < a.seg_max, a.err)
@@ -399,7 +393,7 @@ __device__ __forceinline__ bool ng_epilogue_segment(const NgArgs& a, int tile, b
 
 constexpr int NG_THREADS = 192;  // producer warp, MMA warp, 4 epilogue warps
 
-template <int NT, bool GATE_UP, bool BF16, bool PACKED = false, class Out = NgPlain>
+template <int NT, bool GATE_UP, bool BF16, bool PACKED = false>
 __global__ void __launch_bounds__(NG_THREADS, 1)
     ng_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const NgArgs a) {
@@ -425,9 +419,6 @@ __global__ void __launch_bounds__(NG_THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if constexpr (Out::WAIT_FIRST) {
-    pdl_wait();  // launched early: nothing is touched before the kernel before has ended
-  }
   if (blockIdx.x == 0 && a.clear_err && threadIdx.x == 0) *a.err = 0;
   if (!a.dependent) {
     if (blockIdx.x == 0 &&
@@ -619,7 +610,7 @@ __global__ void __launch_bounds__(NG_THREADS, 1)
         ok = mbar_wait_bounded(accf_bar(acc), acc_phase, a.wait_limit_ns, abort_flag, a.err) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!epi_bar_and(ok)) break;  // all four epilogue warps leave together
-      ng_epilogue_segment<NT, GATE_UP, BF16, Out>(a, tile, whole, seg, tmem_base + acc * NT,
+      ng_epilogue_segment<NT, GATE_UP, BF16>(a, tile, whole, seg, tmem_base + acc * NT,
                                              acce_bar(acc), total, ctas, ustage, abort_flag,
                                              last_flag);
       if (++acc == 2) {

@@ -405,10 +405,10 @@ inline int ng_max_grid() {
 inline void ng_grid(int tiles, int kb, int& ctas, int& sk_tiles, int& seg_max) {
   ng_split(tiles, kb, ng_max_grid(), ctas, sk_tiles, seg_max);
 }
-template <int NT, bool GATE_UP, bool BF16, bool PACKED = false, class Out = NgPlain>
+template <int NT, bool GATE_UP, bool BF16, bool PACKED = false>
 cudaError_t launch_ng(int kid, const CUtensorMap& tw, const CUtensorMap& tx, NgArgs a,
                       cudaStream_t st) {
-  auto kern = ng_gemm_kernel<NT, GATE_UP, BF16, PACKED, Out>;
+  auto kern = ng_gemm_kernel<NT, GATE_UP, BF16, PACKED>;
   constexpr int smem = NgSmem<NT>::DYN_BYTES;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -426,7 +426,7 @@ cudaError_t launch_ng(int kid, const CUtensorMap& tw, const CUtensorMap& tx, NgA
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   // the down kernel overlaps its prologue and weight prefetch with gate/up's tail
   // (per-kernel event timing would serialise the two, so it is not used then)
-  const bool pdl = (a.dependent || Out::WAIT_FIRST) && !host::profiling();
+  const bool pdl = a.dependent && !host::profiling();
   if (!pdl) a.dependent = 0;
   cfg.attrs = pdl ? attr : nullptr;
   cfg.numAttrs = pdl ? 1 : 0;

@@ -15,6 +15,7 @@
 #include "layer_norm.cuh"
 #include "linear_epi.cuh"
 #include "linear_few.cuh"
+#include "linear_mid.cuh"
 #include "simt_linear.cuh"
 
 using namespace swiglu;
@@ -206,7 +207,17 @@ cudaError_t column_sums(const float* part, int parts, int cols, void* out0, void
 // ---------------------------------------------------------------------------
 // linear
 // ---------------------------------------------------------------------------
-bool few_tokens(int64_t M, swiglu_dtype dt) { return dt != SWIGLU_F32_IEEE && M <= NG_MAX_M; }
+// 16-bit products that linear_mid_kernel takes (fewer tokens: the streaming form where
+// it fits), those of some size only while they have too few tiles of 256 x 256 for the
+// pairs of SMs.  Measured in us, this form first, the GEMM of large tiles after it:
+// 11008 x 4096 128 tokens 22, 35, 512 tokens 38, 48, 768 tokens 57, 48; 4096 x 11008
+// 768 tokens 56, 81; 32768 x 4096 256 tokens 63, 56; 2816 x 1024 128 tokens 7.5, 14.2,
+// 1024 tokens 10.5, 14.2.
+bool mid_tokens(int64_t M, int64_t N, int64_t K) {
+  if (M <= 64) return true;
+  if (host::cta_pairs() == 2) return false;  // pairs asked for, whatever the size
+  return M <= 1024 && ((double)M * N * K < 0x1p35 || (M + 255) / 256 * ((N + 255) / 256) < nsm() / 2);
+}
 
 swiglu_status check_linear(int64_t M, int64_t N, int64_t K, int act, swiglu_dtype dt) {
   swiglu_status st = check_dtype(dt);
@@ -236,25 +247,6 @@ size_t gemm_part_bytes(int64_t Mg, int64_t N, int64_t K, bool may_be_wide) {
                                               TC2_WIDE_BN));
   }
   return best;
-}
-
-struct FewPlan {
-  int NT, tiles, kb, ctas, sk_tiles, seg_max;
-  size_t bytes;
-};
-// Only tiles that blocks share are counted, fewer than there are blocks: the
-// counters take the place of the training GEMMs', and like theirs are zero
-// between calls.
-FewPlan few_plan(int64_t M, int64_t N, int64_t K) {
-  FewPlan p;
-  p.NT = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 48 ? 48 : 64));
-  p.tiles = (int)((N + 127) / 128);
-  p.kb = (int)((K + TC_BK - 1) / TC_BK);
-  ng_grid(p.tiles, p.kb, p.ctas, p.sk_tiles, p.seg_max);
-  size_t slots = (size_t)p.ctas * p.seg_max;
-  if (host::sms() < 1) slots = (size_t)p.tiles + 3 * NG_MAX_CTAS;  // for any GPU
-  p.bytes = FIXED + slots * 128 * p.NT * 4;
-  return p;
 }
 
 // Parts of the rows whose column sums are taken apart, in the pass over dY:
@@ -313,14 +305,6 @@ size_t linear_bwd_bytes(int64_t M, int64_t N, int64_t K, swiglu_dtype dt) {
   return FIXED + n;
 }
 
-template <int NT, bool BF16>
-cudaError_t linear_few(const FewPlan& p, const void* X, const void* W, NgArgs a, int64_t K, cudaStream_t st) {
-  CUtensorMap tw, tx;
-  if (!map_kmajor(&tw, BF16, W, K, a.rows, K, 128) || !map_kmajor(&tx, BF16, X, K, a.M, K, ng_x_rows(NT, a.M)))
-    return cudaErrorInvalidValue;
-  return launch_ng<NT, false, BF16, false, NgLinear>(host::K_LINEAR_FEW, tw, tx, a, st);
-}
-
 // Clusters of `split` blocks of a kernel that fit the device at once, kept per
 // device and size.
 template <auto KERNEL>
@@ -354,19 +338,17 @@ struct StreamPlan {
   int nt, blocks, halves, xstride, recv_off, smem;
   bool fits;
 };
-// Clusters of 4 blocks, whose warps in pairs split the contraction 8 ways, as
-// they reach every SM (38 clusters; of 8 blocks 15 fit, 120 SMs); of 8 where a
-// quarter of the token rows does not fit a block.
-// Large products of many tokens are left to the tcgen05 kernel, which streams
-// tokens with every tile but whose products cost it nothing.  Measured in us, this
-// form first, tokens 8 / 16 / 32 / 48 / 64:
-//   11008 x 4096   20.6, 27.0   21.8, 26.1   24.3, 31.1   34.3, 34.2   45.3, 39.6
-//   4096 x 11008   22.2, 23.7   23.5, 24.2   33.2, 27.6*  45.1, 31.8*  (* 8 blocks)
-//   2048 x 5632     8.6, 14.8    8.9, 15.0   10.2, 19.1   16.0, 23.0   18.3, 28.6*
-//   2816 x 1024     5.5, 12.3    5.8, 12.5    6.4, 16.4    7.9, 19.9    8.0, 24.7
+// Up to 16 tokens.  Clusters of 4 blocks, whose warps in pairs split the contraction 8
+// ways, as they reach every SM (38 clusters; of 8 blocks 15 fit, 120 SMs); of 8 where a
+// quarter of the token rows does not fit a block, and linear_mid.cuh's form where an
+// eighth does not.  Measured in us, this form first, tokens 8 / 16 / 32:
+//   11008 x 4096   20.0, 23.0   20.8, 20.5   23.6, 19.7
+//   4096 x 4096    10.4, 11.0   10.8, 10.8   12.1, 10.3
+//   2816 x 1024     5.6, 5.9     5.7, 5.9     6.4, 5.9
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
   StreamPlan p = {};
-  p.nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
+  if (M > LF_MAX_M) return p;
+  p.nt = M <= 8 ? 1 : 2;
   const int64_t nk = (K + 31) / 32;
   int parts = LF_MAX_PARTS;
   while (parts > nk) parts /= 2;
@@ -375,7 +357,7 @@ StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t per = (nk + p.blocks - 1) / p.blocks;
     // rows an odd number of 64 bytes apart: 8 lanes' 16-byte reads of two rows meet no bank twice
     const int64_t xs = (per | 1) * 64, bytes = M * xs + (int64_t)LF_WARPS * 2 * lf_recv(p.nt, parts);
-    if (bytes > LF_SMEM || (double)M * N * K >= (p.blocks <= 4 ? 0x1p31 : 0x1p30)) continue;
+    if (bytes > LF_SMEM) continue;
     p.fits = true;
     p.xstride = (int)xs;
     p.recv_off = (int)(M * xs);
@@ -422,12 +404,103 @@ cudaError_t linear_stream(const StreamPlan& p, LfArgs a, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// How linear_mid_kernel takes a product: weight rows of a tile, blocks of a cluster
+// and the ring of a block (two blocks an SM, or one with a larger ring), by the
+// least of a time's estimate in us.
+struct MidPlan {
+  int bn, split, stages, ring, smem;
+};
+MidPlan mid_plan_of(int mt, int64_t M, int64_t N, int64_t K) {
+  MidPlan best = {};
+  double least = 1e300;
+  const int64_t kb = (K + TC_BK - 1) / TC_BK, m_tiles = (M + mt - 1) / mt;
+  const double hbm = (double)(N * K + M * K + M * N) * 2 / 6.4e6;
+  for (int two = 1; two >= 0; --two)
+    for (int split = 1; split <= 4 && split <= kb; split *= 2)
+      for (int bn = 16 * split; bn <= 256 && (bn < N + 16 || bn == 16 * split); bn += 16) {
+        const int stages = std::min<int>(LM_MAX_STAGES, (two ? 108 : 200) * 1024 / ((mt + bn) * 128));
+        const int each = (bn / 16 + split - 1) / split;
+        const int ring = std::max(lm_ring(mt, bn, stages), split > 1 ? split * each * 8192 : 0);
+        const int smem = ring + LM_BARS + 1024;
+        if (stages < 3 || smem > (two ? 113 : 227) * 1024) continue;
+        // clusters of 4 do not reach every SM
+        const double sms = (split == 4 ? 0.85 : 1.0) * nsm();
+        const double blocks = (double)(m_tiles * ((N + bn - 1) / bn) * split);
+        const double steps = (double)((kb + split - 1) / split), kbytes = (mt + bn) * 0.125;
+        // a block takes a step of k in 0.28 us or more, an SM 140 KB a us
+        const double rounds = std::ceil(blocks / ((two ? 2 : 1) * sms));
+        const double chain = rounds * steps * std::max(0.28, kbytes / (two ? 75 : 115));
+        const double sm = std::ceil(blocks / sms) * steps * kbytes / 140;
+        double t = std::max(hbm, std::max(chain, sm)) + (rounds - 1) * (two ? 4 : 5) + 0.25 * each;
+        if (split > 1) t += 1.5 + (double)mt * bn * (two ? 8 : 4) / 6e4;  // the parts' way through DSMEM
+        if (t < least) {
+          least = t;
+          best = {bn, split, stages, ring, smem};
+        }
+      }
+  return best;
+}
+
+// The same for sizes that this thread asked for lately: 7 us of a call's host time.
+MidPlan mid_plan(int mt, int64_t M, int64_t N, int64_t K) {
+  struct Known {
+    int64_t M, N, K;
+    int mt, sms;
+    MidPlan plan;
+  };
+  static thread_local Known known[32] = {};
+  Known& k = known[(uint64_t)(M * 7 + N * 31 + K * 13) / 8 % 32];
+  if (k.M != M || k.N != N || k.K != K || k.mt != mt || k.sms != nsm()) k = {M, N, K, mt, nsm(), mid_plan_of(mt, M, N, K)};
+  return k.plan;
+}
+
+template <bool BF16, int MT>
+cudaError_t linear_mid(const void* X, const void* W, LmArgs a, int64_t K, cudaStream_t st) {
+  constexpr auto kern = linear_mid_kernel<BF16, MT>;
+  cudaError_t e = allow_smem<kern>(227 * 1024);
+  if (e != cudaSuccess) return e;
+  const MidPlan p = mid_plan(MT, a.M, a.N, K);
+  a.kb = (int)((K + TC_BK - 1) / TC_BK);
+  a.m_tiles = (a.M + MT - 1) / MT;
+  a.split = p.split;
+  a.bn = p.bn;
+  a.stages = p.stages;
+  a.ring = p.ring;
+  a.x_rows = a.m_tiles > 1 ? MT : std::min((a.M + 7) / 8 * 8, MT);
+  a.inject = host::take_stall() ? 1 : 0;
+  CUtensorMap tx, tw;
+  if (!map_kmajor(&tx, BF16, X, K, a.M, K, a.x_rows) || !map_kmajor(&tw, BF16, W, K, a.N, K, p.bn))
+    return cudaErrorInvalidValue;
+  host::Prof prof(host::K_LINEAR_FEW, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.m_tiles * ((a.N + p.bn - 1) / p.bn) * p.split));
+  cfg.blockDim = dim3(LM_THREADS);
+  cfg.dynamicSmemBytes = (size_t)p.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  // per-kernel event timing would serialise the launches, so no overlap then
+  if (!host::profiling()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (p.split > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n++].val.clusterDim = {(unsigned)p.split, 1, 1};
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  e = cudaLaunchKernelEx(&cfg, kern, tx, tw, a);
+  host::count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <bool BF16>
 cudaError_t linear_forward(const void* X, const void* W, const EpiLinear::Params& ep, int64_t M, int64_t N,
                            int64_t K, int* err, size_t ws_bytes, cudaStream_t st) {
   const Win y{ep.y, (size_t)(M * N * 2)}, z{ep.z, ep.z ? (size_t)(M * N * 2) : 0},
       res{ep.res, ep.res ? (size_t)(M * N * 2) : 0}, bias{ep.bias, ep.bias ? (size_t)N * 2 : 0}, w{err, ws_bytes};
-  const StreamPlan sp = M <= NG_MAX_M ? stream_plan(M, N, K) : StreamPlan{};
+  const StreamPlan sp = stream_plan(M, N, K);
   if (sp.fits) {
     LfArgs a = {};
     a.X = static_cast<const uint8_t*>(X);
@@ -443,31 +516,21 @@ cudaError_t linear_forward(const void* X, const void* W, const EpiLinear::Params
     a.wait_limit_ns = host::wait_limit_ns();
     a.err = err;
     set_windows(a, {y, w, z, res, bias, {X, (size_t)(M * K * 2)}, {W, (size_t)(N * K * 2)}});
-    switch (sp.nt) {
-      case 1: return linear_stream<BF16, 1>(sp, a, st);
-      case 2: return linear_stream<BF16, 2>(sp, a, st);
-      case 4: return linear_stream<BF16, 4>(sp, a, st);
-      default: return linear_stream<BF16, 8>(sp, a, st);
-    }
+    return sp.nt == 1 ? linear_stream<BF16, 1>(sp, a, st) : linear_stream<BF16, 2>(sp, a, st);
   }
-  if (M <= NG_MAX_M) {
-    const FewPlan p = few_plan(M, N, K);
-    NgArgs a{(int)M, (int)N, p.kb, p.tiles, 0, 0, nullptr, nullptr, nullptr, 0, 1, 0, 0, ep.y, N,
-             host::wait_limit_ns(), err};
-    a.counters = reinterpret_cast<int*>(reinterpret_cast<char*>(err) + WS_HEADER);
-    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(err) + FIXED);
-    a.zero_ptr = a.counters;
-    a.bias = ep.bias;
-    a.res = ep.res;
-    a.z = ep.z;
+  if (mid_tokens(M, N, K)) {
+    LmArgs a = {};
+    a.M = (int)M;
+    a.N = (int)N;
+    a.bias = static_cast<const uint8_t*>(ep.bias);
+    a.res = static_cast<const uint8_t*>(ep.res);
+    a.z = static_cast<uint8_t*>(ep.z);
+    a.y = static_cast<uint8_t*>(ep.y);
     a.act = ep.act;
+    a.wait_limit_ns = host::wait_limit_ns();
+    a.err = err;
     set_windows(a, {y, w, z, res, bias});
-    switch (p.NT) {
-      case 16: return linear_few<16, BF16>(p, X, W, a, K, st);
-      case 32: return linear_few<32, BF16>(p, X, W, a, K, st);
-      case 48: return linear_few<48, BF16>(p, X, W, a, K, st);
-      default: return linear_few<64, BF16>(p, X, W, a, K, st);
-    }
+    return M <= 64 ? linear_mid<BF16, 64>(X, W, a, K, st) : linear_mid<BF16, 128>(X, W, a, K, st);
   }
   const bool pairs = use_pairs(M, N, TC_BN, K);
   CUtensorMap tx, tw;
@@ -629,7 +692,7 @@ size_t swiglu_mlp_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, swiglu
   if (check_linear(M, N, K, 0, dtype) != SWIGLU_OK || (op != SWIGLU_OP_FWD && op != SWIGLU_OP_BWD)) return 0;
   if (op == SWIGLU_OP_BWD) return linear_bwd_bytes(M, N, K, dtype);
   if (dtype == SWIGLU_F32_IEEE) return FIXED + (M <= 8 ? 0 : sl_bytes(M, N, K));
-  if (few_tokens(M, dtype)) return stream_plan(M, N, K).fits ? FIXED : few_plan(M, N, K).bytes;
+  if (mid_tokens(M, N, K)) return FIXED;
   return FIXED + gemm_part_bytes(M, N, K, false);
 }
 

@@ -1,5 +1,5 @@
 // linear_epi.cuh -- the epilogues of the linear operators for the tensor-core
-// kernels (tc_gemm.cuh, tc2_gemm.cuh) and the few-token one (ng_gemm.cuh).
+// kernels (tc_gemm.cuh, tc2_gemm.cuh).
 //
 //   forward   z = acc + bias[n],  Z = rnd(z) where it is kept,  Y = rnd(act(z) + R)
 //   backward  dX = rnd(acc act'(Xpre)), the gradient of what X = act(Xpre) was made from
@@ -7,7 +7,6 @@
 // Bias, activation and residual meet in fp32 and are rounded once.
 #pragma once
 
-#include "../csrc/ng_gemm.cuh"
 #include "../csrc/tc2_gemm.cuh"
 #include "act.cuh"
 
@@ -220,56 +219,6 @@ struct EpiDAct {
         }
       });
       warp_store_tile(buf, w, lane, checked_rows(s, chunk_rows(s, p.out, p.ld, mw, nc), ok), ok);
-    }
-  }
-};
-
-// Few tokens: one thread has output feature d of all tokens.
-struct NgLinear {
-  static constexpr bool WAIT_FIRST = true;
-  template <bool BF16>
-  static __device__ __forceinline__ float get(const NgArgs& a, const void* base, int64_t at) {
-    using T = typename Pack<BF16>::T;
-    const T* p = static_cast<const T*>(base) + at;
-    if (!SWIGLU_CHECK_PTR(a.dbg, p, 2, a.err)) return 0.0f;
-    if constexpr (BF16)
-      return __bfloat162float(*p);
-    else
-      return __half2float(*p);
-  }
-  template <int NT, bool BF16>
-  static __device__ __forceinline__ void store(const NgArgs& a, int d, const float (&v)[NT]) {
-    const float b = a.bias != nullptr ? get<BF16>(a, a.bias, d) : 0.0f;
-    constexpr int G = 16;  // tokens at a time: their residuals are loaded together
-#pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += G) {
-      if (n0 >= a.M) break;
-      float y[G], r[G];
-      if (a.res != nullptr) {
-#pragma unroll
-        for (int i = 0; i < G; ++i)
-          r[i] = n0 + i < a.M ? get<BF16>(a, a.res, (int64_t)(n0 + i) * a.ld_out + d) : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < G; ++i) y[i] = v[n0 + i] + b;
-      if (a.z != nullptr) {
-        NgArgs z = a;
-        z.out = a.z;
-#pragma unroll
-        for (int i = 0; i < G; ++i)
-          if (n0 + i < a.M) ng_put<BF16>(z, n0 + i, d, y[i]);
-      }
-      act_switch(a.act, [&](auto t) {
-#pragma unroll
-        for (int i = 0; i < G; i += 2) act_value2<decltype(t)::value>(y[i], y[i + 1]);
-      });
-      if (a.res != nullptr) {
-#pragma unroll
-        for (int i = 0; i < G; ++i) y[i] += r[i];
-      }
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        if (n0 + i < a.M) ng_put<BF16>(a, n0 + i, d, y[i]);
     }
   }
 };

@@ -1,4 +1,4 @@
-// linear_few.cuh -- Y [M, N] = act(X W^T + bias) + residual for up to 64 tokens
+// linear_few.cuh -- Y [M, N] = act(X W^T + bias) + residual for up to 16 tokens
 // and 16-bit weights, bound by streaming W from HBM.
 //
 // mma.sync with W's rows as its M (16 rows a warp at a time) and the tokens as
@@ -18,9 +18,9 @@
 // items.  (A third one meant code for three orders of them, which the compiler
 // folded into moves of registers and waits for what they hold.)
 //
-// Measured, back to back: 2816 x 1024 one token 5.0 us (tcgen05 form: 11.2), 2056 x
-// 5640 thirteen 7.5 (14.3; 3.1 TB/s), 11008 x 4096 one 20.5 (26.4; 4.4 TB/s).  At
-// 64 tokens the products' instructions and their latencies bound it.
+// Measured, back to back: 2816 x 1024 one token 5.0 us, 2056 x 5640 thirteen 7.5
+// (3.1 TB/s), 11008 x 4096 one 20.5 (4.4 TB/s).  At more tokens the products'
+// instructions and their latencies bound it.
 //
 // Each warp's receive buffers are two: what a source sends for a use of one of
 // them it sends after it was itself sent to, in between, by a warp that had done
@@ -34,6 +34,7 @@ namespace swiglu {
 
 constexpr int LF_THREADS = 256, LF_WARPS = LF_THREADS / 32;
 constexpr int LF_BLOCKS = 4;      // 32-k blocks of a chunk
+constexpr int LF_MAX_M = 16;
 constexpr int LF_MAX_PARTS = 8;
 constexpr int LF_SMEM = 226 * 1024;
 

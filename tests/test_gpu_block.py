@@ -322,6 +322,16 @@ def test_linear_few_tokens_both_forms(dtn, M, N, K):
     within(Y, act64("silu", z) + R.double(), U[dtn], slack, 1.2 * root + z.abs() + R.double().abs())
 
 
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(17, 8, 8), (24, 40, 72), (33, 264, 520), (64, 2816, 1024), (63, 1032, 2056), (65, 24, 64),
+                                   (128, 4104, 264), (129, 16, 5640), (200, 1032, 2824), (520, 5640, 136), (1000, 2056, 264),
+                                   (1024, 8, 8), (1025, 272, 136), (2500, 1040, 264)])
+def test_linear_some_tokens(dtn, M, N, K):
+    # whole tiles and tiles of two and four blocks, boxes of fewer tokens than a tile,
+    # one block of k, columns and tokens that end inside a tile; then the larger form
+    test_linear_forward(dtn, M, N, K)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 4, 4), (2, 12, 20), (4, 1004, 132), (5, 44, 20004), (8, 2060, 516), (9, 44, 5004),
                                    (32, 132, 9004), (2500, 1500, 2052), (1500, 2500, 36)])
 def test_linear_in_fp32(M, N, K):
@@ -676,7 +686,7 @@ def test_debug_build_checks_every_access(dtn):
     assert all(torch.equal(a, b) for a, b in zip(release, debug))
 
 
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [8, 40, 300, 2000])
 def test_a_wait_that_runs_out_is_reported(M):
     g = gen(M)
     X, W = normal(g, M, 1032, dtype=torch.bfloat16), normal(g, 264, 1032, dtype=torch.bfloat16)
