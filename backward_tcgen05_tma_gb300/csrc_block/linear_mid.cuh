@@ -139,16 +139,23 @@ __global__ void __launch_bounds__(LM_THREADS, 2)
     for (int i = lane; i < 2 * LM_MAX_STAGES + 2; i += 32) mbar_init(bar0 + 8u * i, 1);
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), columns);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   pdl_wait();  // launched early: nothing is touched before the kernel before has ended
-  pdl_launch_dependents();
+  // TMEM is asked for only now: that kernel, beside this one on the SM, may not have
+  // asked for its own yet, and would wait for a block that waits for it.  The next
+  // kernel is let in behind it for the same reason.
+  uint32_t tmem = 0;
+  if (warp != 0) {
+    if (warp == 1) {
+      tmem_alloc(smem_u32(tmem_slot), columns);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 1, 160;" ::: "memory");
+    tc_fence_after();
+    tmem = *tmem_slot;
+    pdl_launch_dependents();
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
 
   const int rank = a.split > 1 ? (int)cluster_ctarank() : 0, tile = (int)blockIdx.x / a.split;

@@ -497,8 +497,9 @@ size_t swiglu_mlp_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, swiglu
 /* z = X W^T + bias in fp32;  Y = rnd(act(z) + residual);  Z = rnd(z).
  * X [M, K], W [N, K], bias [N] or NULL, residual [M, N] or NULL, Z [M, N] or
  * NULL (kept for the backward pass of an activation), Y [M, N].  Y may be the
- * residual's buffer.  One kernel: bf16 and fp16 up to 64 tokens stream the
- * weights over all SMs, beyond that tcgen05 tiles; fp32 IEEE products. */
+ * residual's buffer.  One kernel: bf16 and fp16 up to 16 tokens stream the
+ * weights over all SMs, beyond that tcgen05 tiles; fp32 IEEE products, whose
+ * last tiles' parts a second kernel adds. */
 swiglu_status swiglu_mlp_linear_fwd(const void* X, const void* W, const void* bias, const void* residual,
                                     void* Z, void* Y, int64_t M, int64_t N, int64_t K,
                                     swiglu_activation act, swiglu_dtype dtype, void* ws, size_t ws_bytes,
