@@ -16,6 +16,7 @@
 #include "simt_gemm.cuh"
 #include "tc2_gemm.cuh"
 #include "tc_gemm.cuh"
+#include "tc_plan.h"
 
 namespace swiglu {
 
@@ -132,28 +133,6 @@ inline bool map_mnmajor(CUtensorMap* tm, bool bf16, const void* base, int64_t MN
 // shared-tile counters, then the fp32 partial tiles.
 constexpr size_t TC_SK_COUNTER_BYTES = 1024;  // up to 256 shared tiles
 constexpr int TC_SK_MAX_SMS = 256;
-
-struct TcPlan {
-  int grid, sk_tiles, seg_max;
-};
-
-// Whole tiles round-robin, unless the last round would leave more than 3% of
-// the SMs' time idle: then the (tiles mod SMs) tiles of that round (all of
-// them when there are fewer tiles than SMs) are shared stream-K style.  A
-// CTA's shared range is at most one tile long, so it meets at most two tiles.
-inline TcPlan tc_plan(int64_t tiles, int64_t kb, int nsm) {
-  TcPlan p{(int)(tiles < nsm ? tiles : nsm), 0, 1};
-  const int64_t waves = (tiles + nsm - 1) / nsm;
-  const double fill = (double)tiles / ((double)waves * nsm);
-  if (fill >= 0.97 || kb < 8) return p;
-  p.sk_tiles = (int)(tiles >= nsm ? tiles % nsm : tiles);
-  const int64_t total = (int64_t)p.sk_tiles * kb;
-  p.grid = nsm;
-  if (tiles < nsm && total < nsm) p.grid = (int)total;
-  const int64_t range = (total + p.grid - 1) / p.grid;
-  p.seg_max = (int)((range + kb - 1) / kb) + 1;
-  return p;
-}
 
 // Workspace bytes left for stream-K partial tiles after the header and the
 // tile counters.

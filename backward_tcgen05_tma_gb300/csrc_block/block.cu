@@ -17,6 +17,7 @@
 #include "linear_few.cuh"
 #include "linear_mid.cuh"
 #include "simt_linear.cuh"
+#include "simt_plan.h"
 
 using namespace swiglu;
 
@@ -258,39 +259,9 @@ int dact_parts(int64_t M, int64_t N, swiglu_dtype dt) {
   return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
-// fp32 products: which tiles are split over the contraction (parts of 64 k at
-// least), so that two blocks an SM are busy to the end.
-struct SlPlan {
-  int tm, m_tiles, n_tiles, whole, parts, per;
-  int split() const { return m_tiles * n_tiles - whole; }
-};
-SlPlan sl_plan(int64_t M, int64_t N, int64_t K) {
-  SlPlan p;
-  p.tm = M <= 32 ? 2 : 8;
-  p.m_tiles = (int)((M + 16 * p.tm - 1) / (16 * p.tm));
-  p.n_tiles = (int)((N + SL_BN - 1) / SL_BN);
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, room = 2 * (int64_t)nsm(), rest = tiles % room;
-  // Rounds of the places that the last tiles' parts take, a whole tile's being 1, and
-  // the parts' way through memory (128 KB at 6 TB/s against 0.16 us a k of a tile).
-  // 2816 x 1024 over 4096: 176 tiles for 304 places, 731 us whole, 436 in 5 parts.
-  int64_t parts = 1;
-  double best = 1.0;
-  for (int64_t n = 2; rest > 0 && n <= std::min(4 * room / rest, (K + 63) / 64); ++n) {
-    const double cost = (double)((rest * n + room - 1) / room) / n + (double)rest * n / (7.6 * K);
-    if (cost < best) {
-      best = cost;
-      parts = n;
-    }
-  }
-  p.whole = (int)(parts > 1 ? tiles - rest : tiles);
-  p.per = (int)(((K + parts - 1) / parts + SL_BK - 1) / SL_BK * SL_BK);
-  p.parts = (int)((K + p.per - 1) / p.per);
-  if (p.parts == 1) p.whole = (int)tiles;
-  return p;
-}
 size_t sl_bytes(int64_t M, int64_t N, int64_t K) {
   if (host::sms() < 1) return (size_t)8 * TC_SK_MAX_SMS * 128 * SL_BN * 4;
-  const SlPlan p = sl_plan(M, N, K);
+  const SlPlan p = sl_plan(M, N, K, nsm());
   return (size_t)p.split() * p.parts * 16 * p.tm * SL_BN * 4;
 }
 
@@ -577,7 +548,7 @@ template <bool A_KC, bool B_KC, class Epi>
 cudaError_t simt_product(int id, const float* A, int64_t lda, const float* B, int64_t ldb, int64_t M, int64_t N,
                          int64_t K, const Epi& epi, void* ws, bool first, std::initializer_list<Win> wins,
                          cudaStream_t st) {
-  const SlPlan p = sl_plan(M, N, K);
+  const SlPlan p = sl_plan(M, N, K, nsm());
   const int split = p.split();
   SlArgs a = {A, B, lda, ldb, (int)M, (int)N, (int)K, p.m_tiles, p.n_tiles, p.whole, p.parts, p.per,
               reinterpret_cast<float*>(static_cast<char*>(ws) + FIXED), first ? static_cast<int*>(ws) : nullptr, {}};

@@ -20,10 +20,11 @@
 
 #include "../csrc/simt_gemm.cuh"
 #include "act.cuh"
+#include "simt_plan.h"
 
 namespace swiglu {
 
-constexpr int SL_THREADS = 256, SL_BN = 128, SL_BK = 16;
+constexpr int SL_THREADS = 256;
 
 struct SlArgs {
   const float* A;

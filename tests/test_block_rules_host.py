@@ -1,0 +1,50 @@
+"""Rules of the layer norm and the linear layers that need no GPU to be checked:
+launch plans at every size, what the build rebuilds, the order of waits and
+accesses in the kernels' sources, the modules' defaults."""
+import os
+import subprocess
+
+from backward_tcgen05_tma_gb300 import build
+
+PLANS = r"""
+#include <algorithm>
+#include <cstdio>
+#include "tc_plan.h"
+#include "simt_plan.h"
+using namespace swiglu;
+#define HOLD(what) if (!(what)) { printf("%s: line %d at %lld %lld %lld\n", #what, __LINE__, (long long)a, (long long)b, (long long)c); return 1; }
+int main() {
+  const int64_t sizes[] = {0, 1, 2, 4, 7, 8, 9, 16, 44, 75, 76, 77, 151, 152, 153, 300, 2047, 16384, 1 << 20};
+  // tiles, blocks of k, SMs
+  for (int64_t a : sizes) for (int64_t b : sizes) for (int c : {1, 75, 76, 148, 152, 256}) {
+    const TcPlan p = tc_plan(a, b, c);
+    HOLD(p.grid >= std::min<int64_t>(a, 1) && p.grid <= c);
+    HOLD(p.sk_tiles >= 0 && p.sk_tiles < c && p.sk_tiles <= a && p.seg_max >= 1);
+    HOLD(a > 0 || (p.grid == 0 && p.sk_tiles == 0));
+    HOLD(p.sk_tiles == 0 || p.grid * (int64_t)(p.seg_max - 1) * b >= (int64_t)p.sk_tiles * b);
+  }
+  // rows, columns, k of an fp32 product
+  const int64_t more[] = {0, 1, 4, 8, 9, 12, 31, 32, 33, 64, 132, 1000, 2048, 9004, 120000};
+  for (int64_t a : more) for (int64_t b : more) for (int64_t c : more) {
+    const SlPlan p = sl_plan(a, b, c, 152);
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    HOLD((int64_t)p.m_tiles * 16 * p.tm >= a && (int64_t)p.n_tiles * SL_BN >= b);
+    HOLD(p.parts >= 1 && p.per >= SL_BK && p.per % SL_BK == 0 && (int64_t)p.parts * p.per >= c);
+    HOLD(p.whole >= 0 && p.whole <= tiles && (p.parts > 1 || p.whole == tiles));
+    HOLD(p.parts == 1 || (int64_t)(p.parts - 1) * p.per < c);  // no part is empty
+  }
+  return 0;
+}
+"""
+
+
+def test_plans_hold_at_every_size(tmp_path):
+    # an empty batch among them: the sizes of its backward pass's workspace come
+    # from the same plans (a division by zero ends the process on some machines)
+    (tmp_path / "plans.cpp").write_text(PLANS)
+    exe = str(tmp_path / "plans")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=integer-divide-by-zero",
+                    "-fno-sanitize-recover=all", "-I", build.CSRC, "-I", build.CSRC_BLOCK, "-o", exe,
+                    str(tmp_path / "plans.cpp")], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -1,0 +1,42 @@
+"""Layer norm and linear layers where a call's form, rather than its formula, can
+go wrong.  Tolerances as in test_gpu_block.py, whose restatements are used."""
+import pytest
+import torch
+
+from backward_tcgen05_tma_gb300 import api, block, build
+from test_gpu_block import DT, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    api.lib()
+
+
+@pytest.mark.parametrize("dtn", list(DT))
+@pytest.mark.parametrize("N,K", [(2816, 1024), (1024, 2816), (520, 12000), (8, 2048)])
+def test_an_empty_batch_of_wide_layers(dtn, N, K):
+    # sizes whose plans share tiles: there is none to share here
+    dt, g = DT[dtn], gen(N)
+    for op in (api.SWIGLU_OP_FWD, api.SWIGLU_OP_BWD):
+        assert api.linear_workspace(0, N, K, dt, op, "cuda").numel() >= 1280
+    X, dY, W = (torch.empty(0, K, dtype=dt, device="cuda"), torch.empty(0, N, dtype=dt, device="cuda"),
+                normal(g, N, K, dtype=dt))
+    b = normal(g, N, dtype=dt)
+    assert api.swiglu_mlp_linear_fwd(X, W, b, "gelu")[0].shape == (0, N)
+    dX, dW, db = api.swiglu_mlp_linear_bwd(dY, X, W, dY, "gelu", X_pre=X, x_activation="silu")
+    assert dX.shape == (0, K) and dW.shape == (N, K) and not dW.any() and not db.any()
+    held = {"dW": W.clone(), "dbias": b.clone()}
+    api.swiglu_mlp_linear_bwd(dY, X, W, out=held, accumulate=True)
+    assert torch.equal(held["dW"], W) and torch.equal(held["dbias"], b)
+    x = torch.empty(2, 0, K, dtype=dt, device="cuda", requires_grad=True)
+    m = block.MLPBlock(block.MLP(K, N, dtype=dt, device="cuda"))
+    m(x).sum().backward()
+    assert x.grad.shape == x.shape and all(not p.grad.any() for p in m.parameters())
+    w = W.clone().requires_grad_()
+    block.linear(x, w, None, "relu").sum().backward()
+    assert not w.grad.any()
