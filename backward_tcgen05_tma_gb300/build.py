@@ -3,8 +3,8 @@ sources with -DSWIGLU_DEBUG: device index checks) in place with nvcc for
 sm_103a (GB300).  The two compile in parallel."""
 from __future__ import annotations
 
-import glob
 import os
+import re
 import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,12 +16,12 @@ SO = os.path.join(HERE, "libswiglu_mlp.so")
 SO_DEBUG = os.path.join(HERE, "libswiglu_mlp_debug.so")
 BUILD = os.path.join(HERE, "_build")  # objects, kept for the next build
 
-# translation units and the directories their headers come from
-SOURCES = {
-    os.path.join(CSRC, "swiglu_mlp.cu"): [CSRC, os.path.join(CSRC_SERVING, "host_shared.h")],
-    os.path.join(CSRC_SERVING, "serving.cu"): [CSRC_SERVING, os.path.join(CSRC, "sm103_ptx.cuh")],
-    os.path.join(CSRC_BLOCK, "block.cu"): [CSRC_BLOCK, CSRC, os.path.join(CSRC_SERVING, "host_shared.h")],
-}
+# translation units
+SOURCES = [
+    os.path.join(CSRC, "swiglu_mlp.cu"),
+    os.path.join(CSRC_SERVING, "serving.cu"),
+    os.path.join(CSRC_BLOCK, "block.cu"),
+]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
@@ -35,12 +35,20 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def _includes(path: str, found: set[str]) -> set[str]:
+    """path and the files that its quoted includes lead to (each is looked for
+    beside the file that names it)."""
+    path = os.path.normpath(path)
+    if path not in found and os.path.exists(path):
+        found.add(path)
+        with open(path) as f:
+            for name in re.findall(r'^[ \t]*#[ \t]*include[ \t]+"([^"]+)"', f.read(), re.M):
+                _includes(os.path.join(os.path.dirname(path), name), found)
+    return found
+
+
 def _deps(src: str) -> list[str]:
-    deps = [src, os.path.join(ROOT, "include", "swiglu_mlp.h"), os.path.abspath(__file__)]
-    for d in SOURCES[src]:
-        deps += [d] if os.path.isfile(d) else \
-            glob.glob(os.path.join(d, "*.cuh")) + glob.glob(os.path.join(d, "*.h"))
-    return deps
+    return sorted(_includes(src, set())) + [os.path.abspath(__file__)]
 
 
 def _stale(target: str, deps: list[str]) -> bool:

@@ -48,3 +48,16 @@ def test_plans_hold_at_every_size(tmp_path):
                     str(tmp_path / "plans.cpp")], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_an_object_is_rebuilt_for_every_file_that_it_includes(tmp_path):
+    # as the compiler lists them; an older object would stay in the library unseen
+    for src in build.SOURCES:
+        out = str(tmp_path / "deps")
+        subprocess.run([build._nvcc(), *build.NVCC_FLAGS, "-MM", src, "-o", out], check=True)
+        with open(out) as f:
+            named = f.read().split(":", 1)[1].replace("\\\n", " ").split()
+        named = {os.path.normpath(os.path.join(build.ROOT, n)) for n in named}
+        ours = {n for n in named if n.startswith(build.ROOT + os.sep)}
+        known = {os.path.normpath(d) for d in build._deps(src)}
+        assert len(ours) > 3 and ours <= known, sorted(ours - known)
