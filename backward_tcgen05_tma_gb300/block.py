@@ -270,10 +270,10 @@ class MLPBlock(torch.nn.Module):
                  dtype=None, device=None):
         super().__init__()
         D = int(mlp.hidden_size if hidden_size is None else hidden_size)
-        like = next(mlp.parameters(), None)  # the norm's type and place, unless given
-        if like is not None:
-            dtype = like.dtype if dtype is None else dtype
-            device = like.device if device is None else device
+        # the norm's type and place, unless given: 4-bit weights are no parameters, their module says
+        like = next(mlp.parameters(), mlp)
+        dtype = getattr(like, "dtype", None) if dtype is None else dtype
+        device = getattr(like, "device", None) if device is None else device
         dtype = torch.bfloat16 if dtype is None else dtype
         self.norm = LayerNorm(D, eps, bias=bias, dtype=dtype, device=device)
         self.mlp = mlp

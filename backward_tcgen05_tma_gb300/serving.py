@@ -83,6 +83,20 @@ class W4SwiGLUMLP(torch.nn.Module):
         self.down_w4 = PackedW4(api.swiglu_mlp_w4_pack(*down, group=group))
 
     @property
+    def hidden_size(self) -> int:
+        return self.gate_up.K
+
+    @property
+    def dtype(self):
+        """The activations' type, None while no weights have been set or loaded."""
+        f = self.gate_up_w4._format
+        return None if f is None else getattr(torch, f["dtype"])
+
+    @property
+    def device(self):
+        return self.gate_up_w4.packed.device
+
+    @property
     def gate_up(self) -> api.W4Weights:
         return self.gate_up_w4.weights
 
@@ -132,6 +146,7 @@ class MoESwiGLU(torch.nn.Module):
                  device=None):
         super().__init__()
         D, H, E = int(hidden_size), int(intermediate_size), int(num_experts)
+        self.hidden_size = D
         self.top_k, self.norm_topk, self.route_scale = int(top_k), bool(norm_topk), float(route_scale)
         new = lambda *s: torch.nn.Parameter(torch.empty(*s, dtype=dtype, device=device),
                                             requires_grad=False)

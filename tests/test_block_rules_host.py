@@ -4,7 +4,11 @@ accesses in the kernels' sources, the modules' defaults."""
 import os
 import subprocess
 
-from backward_tcgen05_tma_gb300 import build
+import pytest
+import torch
+
+from backward_tcgen05_tma_gb300 import api, block, build
+from backward_tcgen05_tma_gb300.serving import MoESwiGLU, PackedW4, W4SwiGLUMLP
 
 PLANS = r"""
 #include <algorithm>
@@ -61,3 +65,25 @@ def test_an_object_is_rebuilt_for_every_file_that_it_includes(tmp_path):
         ours = {n for n in named if n.startswith(build.ROOT + os.sep)}
         known = {os.path.normpath(d) for d in build._deps(src)}
         assert len(ours) > 3 and ours <= known, sorted(ours - known)
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_a_sublayers_norm_takes_after_4_bit_weights(device):
+    # their packed bytes are a buffer, so there is no parameter to go by
+    packed = lambda n, k, pair: PackedW4(api.W4Weights(torch.zeros(64, dtype=torch.uint8, device=device), n, k, 64,
+                                                       False, pair, torch.float16, None))
+    w4 = W4SwiGLUMLP()
+    w4.gate_up_w4, w4.down_w4 = packed(32, 72, True), packed(72, 16, False)
+    norm = block.MLPBlock(w4).norm
+    assert norm.weight.dtype is torch.float16 and norm.weight.device.type == device and norm.hidden_size == 72
+    norm = block.MLPBlock(w4, hidden_size=72, dtype=torch.bfloat16, device="cpu").norm
+    assert norm.weight.dtype is torch.bfloat16 and norm.weight.device.type == "cpu"
+    moe = MoESwiGLU(72, 16, 4, 2, dtype=torch.float16, device=device)
+    moe._experts_w4(packed(32, 72, True), packed(72, 16, False))
+    norm = block.MLPBlock(moe).norm
+    assert norm.weight.dtype is torch.float16 and norm.weight.device.type == device and norm.hidden_size == 72
+    # empty until a state is loaded: the place is known, the sizes are not
+    empty = block.MLPBlock(W4SwiGLUMLP(device=device), hidden_size=72)
+    assert empty.norm.weight.device.type == device
+    with pytest.raises(RuntimeError):
+        block.MLPBlock(W4SwiGLUMLP())

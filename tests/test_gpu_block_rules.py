@@ -4,6 +4,8 @@ import pytest
 import torch
 
 from backward_tcgen05_tma_gb300 import api, block, build
+from backward_tcgen05_tma_gb300.module import SwiGLUMLP
+from backward_tcgen05_tma_gb300.serving import MoESwiGLU, W4SwiGLUMLP
 from test_gpu_block import DT, gen, normal
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +42,16 @@ def test_an_empty_batch_of_wide_layers(dtn, N, K):
     w = W.clone().requires_grad_()
     block.linear(x, w, None, "relu").sum().backward()
     assert not w.grad.any()
+
+
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+def test_sublayers_of_serving_modules_go_by_their_weights(dtn):
+    # without a word on type, place or size
+    dt, D = DT[dtn], 256
+    torch.manual_seed(1)
+    with torch.no_grad():
+        x = normal(gen(1), 5, D, dtype=dt)
+        for mlp in (W4SwiGLUMLP(SwiGLUMLP(D, 704, dtype=dt, device="cuda"), group=64),
+                    MoESwiGLU(D, 128, 8, 2, dtype=dt, device="cuda")):
+            m = block.MLPBlock(mlp)
+            assert torch.equal(m(x), x + mlp(block.layer_norm(x)))
