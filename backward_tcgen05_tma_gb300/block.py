@@ -6,7 +6,7 @@ and the pre-norm sublayer x + mlp(norm(x)) of any of this package's MLPs.
 The tensors are CUDA tensors of one dtype (bf16, fp16, or fp32 for the IEEE
 mode); every computation runs in the library's kernels.  Nothing that a
 backward pass needs is overwritten, so a graph may be kept and run again;
-double differentiation is refused.  A captured training step takes its
+double differentiation and forward-mode derivatives are refused.  A captured training step takes its
 gradients with ``torch.autograd.grad``, or through leaves that no graph from
 outside the capture holds.
 """
@@ -17,6 +17,7 @@ import math
 import torch
 
 from . import api
+from .module import refuse_tangents
 
 
 def _rows(x, D):
@@ -82,6 +83,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None):
     D = x.shape[-1] if x.dim() else 0
     _last(x, D, "layer_norm")
     _alike(x, residual, x.shape, "residual")
+    refuse_tangents("layer_norm", x, weight, bias, residual)
     if _recording(x, weight, bias, residual):
         return LayerNormFunction.apply(x, weight, bias, float(eps), residual)
     r = None if residual is None else _rows(residual, D)
@@ -124,6 +126,7 @@ def linear(x, weight, bias=None, activation: str = "none", residual=None):
     api.activation_code(activation)
     _last(x, K, "linear")
     _alike(x, residual, (*x.shape[:-1], N), "residual")
+    refuse_tangents("linear", x, weight, bias, residual)
     if _recording(x, weight, bias, residual):
         return LinearFunction.apply(x, weight, bias, activation, residual)
     R = None if residual is None else _rows(residual, N)
@@ -170,6 +173,7 @@ def mlp(x, w1, b1, w2, b2, activation: str = "gelu", residual=None):
     api.activation_code(activation)
     _last(x, w1.shape[1], "mlp")
     _alike(x, residual, (*x.shape[:-1], w2.shape[0]), "residual")
+    refuse_tangents("mlp", x, w1, b1, w2, b2, residual)
     if _recording(x, w1, b1, w2, b2, residual):
         return MLPFunction.apply(x, w1, b1, w2, b2, activation, residual)
     return linear(linear(x, w1, b1, activation), w2, b2, "none", residual)

@@ -18,8 +18,17 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import api
+
+
+def refuse_tangents(what, *tensors):
+    """No forward-mode derivatives: a dual tensor that does not require a gradient
+    would pass the autograd function by, and its tangent would be gone unseen."""
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError("%s has no forward-mode derivative" % what)
 
 
 class SwiGLUMLPFunction(torch.autograd.Function):
@@ -57,6 +66,7 @@ class SwiGLUMLPFunction(torch.autograd.Function):
 def swiglu_mlp(X, Wgu, Wd, gate_mul: float = 1.0, down_mul: float = 1.0):
     """Functional form: autograd-aware when any input requires grad, otherwise
     the no-grad path (A and Y only, no G/U saved)."""
+    refuse_tangents("swiglu_mlp", X, Wgu, Wd)
     if torch.is_grad_enabled() and (X.requires_grad or Wgu.requires_grad or Wd.requires_grad):
         return SwiGLUMLPFunction.apply(X, Wgu, Wd, float(gate_mul), float(down_mul))
     D = X.shape[-1]
@@ -170,6 +180,7 @@ class SwiGLUMLP(torch.nn.Module):
                 x.requires_grad or self.gate_up_weight.requires_grad or
                 self.down_weight.requires_grad)):
             D = x.shape[-1]
+            refuse_tangents("SwiGLUMLP", x, self.gate_up_weight, self.down_weight)
             X = x.reshape(-1, D).contiguous()
             if 0 < X.shape[0] <= PACKED_MAX_TOKENS:
                 Y, _ = api.swiglu_mlp_fwd_nograd_packed(X, packed, self.intermediate_size,

@@ -12,6 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import api
+from .module import refuse_tangents
 
 MAX_TOKENS = 64  # of one call of the few-token operators
 
@@ -19,6 +20,7 @@ MAX_TOKENS = 64  # of one call of the few-token operators
 def _no_grad_only(x, what):
     if torch.is_grad_enabled() and x.requires_grad:
         raise RuntimeError("%s has no backward pass: call it under torch.no_grad()" % what)
+    refuse_tangents(what, x)
 
 
 class PackedW4(torch.nn.Module):

@@ -7,7 +7,7 @@ import subprocess
 import pytest
 import torch
 
-from backward_tcgen05_tma_gb300 import api, block, build
+from backward_tcgen05_tma_gb300 import api, block, build, module
 from backward_tcgen05_tma_gb300.serving import MoESwiGLU, PackedW4, W4SwiGLUMLP
 
 PLANS = r"""
@@ -87,3 +87,27 @@ def test_a_sublayers_norm_takes_after_4_bit_weights(device):
     assert empty.norm.weight.device.type == device
     with pytest.raises(RuntimeError):
         block.MLPBlock(W4SwiGLUMLP())
+
+
+def test_forward_mode_is_refused_by_every_layer():
+    # a dual tensor that does not require a gradient, with and without recording;
+    # (CPU tensors: what is not refused for its tangent is a ValueError)
+    x, w, v = torch.zeros(4, 64), torch.zeros(64, 64), torch.zeros(64)
+    pair, down = torch.zeros(192, 64), torch.zeros(64, 96)
+    w4 = W4SwiGLUMLP(device="cpu")
+    moe, mlp = MoESwiGLU(64, 96, 4, 2), module.SwiGLUMLP(64, 96, dtype=torch.float32)
+    mlp._packed = (x, mlp._weights_state())
+    fs = [lambda d: block.layer_norm(d(x)), lambda d: block.layer_norm(x, d(v)), lambda d: block.layer_norm(x, v, d(v)),
+          lambda d: block.layer_norm(x, residual=d(x)), lambda d: block.linear(d(x), w), lambda d: block.linear(x, d(w)),
+          lambda d: block.linear(x, w, d(v)), lambda d: block.linear(x, w, residual=d(x)),
+          lambda d: block.mlp(d(x), w, v, w, v), lambda d: block.mlp(x, w, v, d(w), v),
+          lambda d: block.mlp(x, w, v, w, v, residual=d(x)), lambda d: module.swiglu_mlp(d(x), pair, down),
+          lambda d: module.swiglu_mlp(x, pair, d(down)), lambda d: mlp(d(x)), lambda d: w4(d(x)), lambda d: moe(d(x))]
+    ad = torch.autograd.forward_ad
+    for f in fs:
+        for recording in (True, False):
+            with ad.dual_level(), torch.set_grad_enabled(recording):
+                with pytest.raises(RuntimeError, match="forward-mode"):
+                    f(lambda t: ad.make_dual(t, torch.ones_like(t)))
+    with ad.dual_level(), pytest.raises(ValueError):  # a level without tangents is nothing to refuse
+        block.linear(x, w)
