@@ -8,11 +8,16 @@
 //
 // Two forms of each.  PRECISE (fp32 storage) calls CUDA's functions.  The other
 // one (16-bit storage) takes e^x and 1/x from the special-function unit, a few
-// fp32 ulp, and Phi from Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26: erfc(w) = (a1 t + ... + a5 t^5) e^(-w^2), t = 1/(1 + p w),
-// whose error in erf is at most 1.5e-7, below 2^-13 of half a step of either
-// 16-bit type around 1.  With w = |z| / sqrt 2 its exponential is e^(-z^2/2),
-// which is also what Phi' needs, so the derivative costs two products more.
+// fp32 ulp, and Phi from its tail on either side,
+//   Phi(-w) = e^(-w^2/2) (c1 t + ... + c6 t^6),  t = 1 / (1 + 0.412 w),
+// the sum being the polynomial in t of the least largest error against
+// e^(w^2/2) erfc(w / sqrt 2) / 2 under these bounds (a linear programme over 3000
+// points; fp32 evaluation by itself costs about 2e-7): 8e-8 absolutely and 8e-6 of
+// the value up to w = 6, where the tail is below any fp16 step, and 8e-4 of the
+// value beyond, a fifth of half a bf16 step.  The value z Phi(z) is a product, so
+// that what is left of Phi far left stays exact to so many digits; 1 - Phi(-w)
+// takes its place right of 0 only.  The exponential is also what Phi' needs, so the
+// derivative costs two products more.
 // Values go in pairs through fma.rn.f32x2 and the like, as the epilogues that
 // apply them are bound by the instructions they issue; for the same reason gelu
 // and gelu_tanh let exponentials below 2^-126 become 0 (the forms that keep them
@@ -68,18 +73,22 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 
 constexpr float ACT_TANH_K = 1.5957691216057308f;  // 2 sqrt(2/pi)
 
-// e = e^(-z^2 / 2) and h = 1/2 - Phi(-|z|), for both
-__device__ __forceinline__ void phi2(F2 z, float z0, float z1, F2& e, F2& h) {
-  float a0, a1;
+// e = e^(-z^2 / 2) and p0, p1 = Phi(z), for both
+__device__ __forceinline__ void phi2(F2 z, float z0, float z1, F2& e, float& p0, float& p1) {
+  float a0, a1, q0, q1, r0, r1;
   mul2(mul2(z, z), F2(-0.72134752044448170f)).get(a0, a1);
   e = F2(ex2_ftz(a0), ex2_ftz(a1));
-  constexpr float P = 0.3275911f * 0.70710678118654752f;
-  const F2 t(rcp_ftz(fmaf(fabsf(z0), P, 1.0f)), rcp_ftz(fmaf(fabsf(z1), P, 1.0f)));
-  F2 p = fma2(t, F2(-0.5f * 1.061405429f), F2(0.5f * 1.453152027f));
-  p = fma2(t, p, F2(-0.5f * 1.421413741f));
-  p = fma2(t, p, F2(0.5f * 0.284496736f));
-  p = fma2(t, p, F2(-0.5f * 0.254829592f));
-  h = fma2(mul2(p, t), e, F2(0.5f));
+  const F2 t(rcp_ftz(fmaf(fabsf(z0), 0.412f, 1.0f)), rcp_ftz(fmaf(fabsf(z1), 0.412f, 1.0f)));
+  // minus the sum
+  F2 p = fma2(t, F2(-0.057465021f), F2(0.24332555f));
+  p = fma2(t, p, F2(-0.29056361f));
+  p = fma2(t, p, F2(-0.050197825f));
+  p = fma2(t, p, F2(-0.18221125f));
+  p = mul2(fma2(t, p, F2(-0.16288793f)), t);
+  mul2(p, e).get(q0, q1);
+  fma2(p, e, F2(1.0f)).get(r0, r1);
+  p0 = z0 > 0.0f ? r0 : -q0;
+  p1 = z1 > 0.0f ? r1 : -q1;
 }
 // sigma(2 sqrt(2/pi) (z + 0.044715 z^3)); far left 1 / (1 + infinity)
 __device__ __forceinline__ F2 sigma_tanh2(F2 z, F2 zz) {
@@ -97,13 +106,10 @@ __device__ __forceinline__ void act_value2(float& a, float& b) {
     b = b < 0.0f ? 0.0f : b;
   } else if constexpr (A == ACT_GELU) {
     const F2 z(a, b);
-    F2 e(0.0f), h(0.0f);
-    phi2(z, a, b, e, h);
-    float h0, h1, y0, y1;
-    h.get(h0, h1);
-    mul2(z, F2(0.5f)).get(y0, y1);
-    a = fmaf(fabsf(a), h0, y0);  // z Phi(z) = z / 2 + |z| h
-    b = fmaf(fabsf(b), h1, y1);
+    F2 e(0.0f);
+    float p0, p1;
+    phi2(z, a, b, e, p0, p1);
+    mul2(z, F2(p0, p1)).get(a, b);
   } else if constexpr (A == ACT_GELU_TANH) {
     const F2 z(a, b);
     mul2(z, sigma_tanh2(z, mul2(z, z))).get(a, b);
@@ -121,12 +127,10 @@ __device__ __forceinline__ void act_slope2(float& a, float& b) {
     b = b <= 0.0f ? 0.0f : 1.0f;
   } else if constexpr (A == ACT_GELU) {
     const F2 z(a, b);
-    F2 e(0.0f), h(0.0f);
-    phi2(z, a, b, e, h);
-    float h0, h1, f0, f1;
-    h.get(h0, h1);
+    F2 e(0.0f);
+    float p0, p1, f0, f1;
+    phi2(z, a, b, e, p0, p1);
     mul2(mul2(z, e), F2(0.3989422804014327f)).get(f0, f1);
-    const float p0 = 0.5f + copysignf(h0, a), p1 = 0.5f + copysignf(h1, b);  // Phi(z)
     a = p0 + (fabsf(a) < 128.0f ? f0 : 0.0f);
     b = p1 + (fabsf(b) < 128.0f ? f1 : 0.0f);
   } else if constexpr (A == ACT_GELU_TANH) {
