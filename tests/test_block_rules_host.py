@@ -2,6 +2,7 @@
 launch plans at every size, what the build rebuilds, the order of waits and
 accesses in the kernels' sources, the modules' defaults."""
 import os
+import re
 import subprocess
 
 import pytest
@@ -111,3 +112,76 @@ def test_forward_mode_is_refused_by_every_layer():
                     f(lambda t: ad.make_dual(t, torch.ones_like(t)))
     with ad.dual_level(), pytest.raises(ValueError):  # a level without tangents is nothing to refuse
         block.linear(x, w)
+
+
+# kernels that are launched before the one in front of them has ended: file, kernel,
+# its arguments' structures, what waits
+EARLY = [("csrc_block/layer_norm.cuh", "ln_fwd_kernel", ["LnFwdArgs"], "pdl_wait();"),
+         ("csrc_block/layer_norm.cuh", "ln_bwd_kernel", ["LnBwdArgs"], "pdl_wait();"),
+         ("csrc_block/column_sums.cuh", "dact_kernel", ["DactArgs"], "pdl_wait();"),
+         ("csrc_block/column_sums.cuh", "column_sum_kernel", ["ColumnSumArgs"], "pdl_wait();"),
+         ("csrc_block/linear_few.cuh", "linear_few_kernel", ["LfArgs"], "pdl_wait();"),
+         ("csrc_block/linear_mid.cuh", "linear_mid_kernel", ["LmArgs"], "pdl_wait();"),
+         ("csrc/tc_gemm.cuh", "tc_gemm_kernel", ["TcShape"], "tc_begin(s);"),
+         ("csrc/tc2_gemm.cuh", "tc2_gemm_kernel", ["TcShape"], "tc_begin(s);")]
+ACCESS = (r"\btma_load|\btma_store|\bcp16\(|\bld_stream\(|\bld\.global|\bst\.global|cp\.async|\bprefetch\.global|__ldcg|"
+          r"__ldg|\batomic|\bred\.")
+
+
+def without_comments(name):
+    with open(os.path.join(build.HERE, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def pointers_of(text, struct):
+    body = text[text.index("struct %s {" % struct):]
+    return re.findall(r"\*\s*(\w+)\s*;", body[:body.index("\n};")])
+
+
+def before_the_wait(text, kernel, wait):
+    """A kernel's body up to its wait."""
+    at = re.search(r"__global__[^;{]*\b%s\(" % kernel, text).end()
+    at = text.index(") {", at)
+    return text[at:text.index(wait, at)]
+
+
+def accesses(head, pointers):
+    """What a kernel's head does with global memory, but for descriptors."""
+    found = re.findall(ACCESS, head) + re.findall(r"\b(?:a|s|ep)\.(?:%s)\b" % "|".join(pointers), head)
+    return found + re.findall(r"\bep\.\w+", head)
+
+
+@pytest.mark.parametrize("name,kernel,structs,wait", EARLY, ids=[e[1] for e in EARLY])
+def test_early_kernels_touch_nothing_before_their_wait(name, kernel, structs, wait):
+    text = without_comments(name)
+    defined = text + without_comments("csrc/tc_gemm.cuh")
+    pointers = [p for s in structs for p in pointers_of(defined, s)]
+    assert len(pointers) >= 3
+    head = before_the_wait(text, kernel, wait)
+    assert accesses(head, pointers) == []
+    # the same check sees a read that is planted there
+    for planted in ("const float x = a.%s[0];" % pointers[0], "tma_load_2d(s, &tmX, full(0), 0, 0);",
+                    "x = *s.%s;" % pointers[-1], 'asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p));'):
+        assert accesses(head + planted, pointers) != []
+    # the wait is every thread's: at the body's own level
+    assert head.count("{") - head.count("}") == 1
+
+
+def test_what_waits_waits_first():
+    # tc_begin waits where the launch was early; TMEM that a kernel beside it may
+    # still ask for is not asked for before the wait
+    text = without_comments("csrc/tc_gemm.cuh")
+    body = text[text.index("void tc_begin("):]
+    body = body[:body.index("\n}\n")]
+    assert re.search(r"if \(s\.early\) \{\s*pdl_wait\(\);\s*pdl_launch_dependents\(\);", body)
+    assert body.index("pdl_wait") < body.index("*s.err")
+    mid = without_comments("csrc_block/linear_mid.cuh")
+    assert "tmem_alloc" not in before_the_wait(mid, "linear_mid_kernel", "pdl_wait();")
+    assert mid.index("tmem_alloc(") < mid.index("pdl_launch_dependents();")
+    # and every launch of this part that is early is of one of the kernels above
+    host = without_comments("csrc_block/block.cu")
+    started = set(re.findall(r"\b(\w+_kernel)\b", host))
+    plain = {"simt_rows_kernel", "simt_linear_kernel", "simt_sum_kernel"}
+    assert started - plain == {e[1] for e in EARLY if e[0].startswith("csrc_block")}
+    for name in plain:
+        assert re.findall(r"%s<[^;]*?>(<<<|\()" % name, host) and not re.search(r"auto kern = %s" % name, host)
