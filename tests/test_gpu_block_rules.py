@@ -8,7 +8,9 @@ import torch
 from backward_tcgen05_tma_gb300 import api, block, build
 from backward_tcgen05_tma_gb300.module import SwiGLUMLP
 from backward_tcgen05_tma_gb300.serving import MoESwiGLU, W4SwiGLUMLP
-from test_gpu_block import DT, TINY, U, dact64, gen, normal, within
+from conftest import device_status
+import test_gpu_block as base
+from test_gpu_block import DT, TINY, U, act_slack, dact64, gen, normal, within
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +90,133 @@ def test_gelu_keeps_its_digits_far_left(dtn, M):
     dZ = torch.empty(M, N, dtype=dt, device="cuda")
     api.swiglu_mlp_linear_bwd(torch.ones_like(dZ), X, W, Z, "gelu", need_dX=False, need_dW=False, out={"dZ": dZ})
     within(dZ[M - 1], dact64("gelu", z), U[dtn], 1.0, rel * (phi + bell) + least)
+
+
+@pytest.fixture
+def large_forms():
+    """set(pairs, wide): the kernels that large sizes take, on small ones."""
+    old = api.swiglu_mlp_set_cta_pairs(1), api.swiglu_mlp_set_wide_tiles(1)
+
+    def choose(pairs, wide):
+        api.swiglu_mlp_set_cta_pairs(pairs)
+        api.swiglu_mlp_set_wide_tiles(wide)
+    yield choose
+    choose(*old)
+
+
+# N a multiple of 16: outputs leave by whole sectors; rows and columns that end inside a tile
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(65, 16, 328), (257, 272, 1032), (300, 1040, 264), (513, 2816, 1024), (2500, 528, 136)])
+@pytest.mark.parametrize("wide", [0, 2])
+def test_linear_on_sm_pairs_in_sectors_and_wide_tiles(large_forms, dtn, M, N, K, wide):
+    large_forms(2, wide)
+    if not wide:
+        base.test_linear_forward(dtn, M, N, K)
+    base.test_linear_backward(dtn, M, N, K)
+    # dW and the bias gradient added to what is there
+    g, dt = gen(M), DT[dtn]
+    dY, X, W = normal(g, M, N, std=0.5, dtype=dt), normal(g, M, K, dtype=dt), normal(g, N, K, std=0.1, dtype=dt)
+    hW, hb = normal(g, N, K, dtype=dt), normal(g, N, dtype=dt)
+    out = {"dW": hW.clone(), "dbias": hb.clone()}
+    for _ in range(2):  # (twice the same, on what the first one left)
+        out["dW"].copy_(hW)
+        out["dbias"].copy_(hb)
+        api.swiglu_mlp_linear_bwd(dY, X, W, out=out, accumulate=True)
+        y = dY.double()
+        within(out["dW"], hW.double() + y.T @ X.double(), U[dtn], act_slack(M),
+               (y.square().T @ X.double().square()).sqrt() + hW.double().abs())
+        within(out["dbias"], hb.double() + y.sum(0), U[dtn], act_slack(M), y.square().sum(0).sqrt() + hb.double().abs())
+
+
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+@pytest.mark.parametrize("pairs", [0, 2])
+@pytest.mark.parametrize("M,N,K", [(9, 48, 264), (70, 272, 328), (300, 1040, 264), (2100, 528, 136)])
+def test_buffers_that_start_inside_a_sector(large_forms, dtn, pairs, M, N, K):
+    # 16-byte aligned, as asked for: not by whole sectors, the same arithmetic
+    large_forms(pairs, 1)
+    g, dt = gen(N), DT[dtn]
+    X, W, b = normal(g, M, K, dtype=dt), normal(g, N, K, std=K ** -0.5, dtype=dt), normal(g, N, dtype=dt)
+
+    def inside(t=None):
+        v = torch.empty(M * N + 8, dtype=dt, device="cuda")[8:].view(M, N)
+        assert v.data_ptr() % 32 == 16
+        return v if t is None else v.copy_(t)
+    R = normal(g, M, N, dtype=dt)
+    for act, keep in (("none", False), ("gelu", True)):
+        ref = api.swiglu_mlp_linear_fwd(X, W, b, act, R, keep=keep)
+        for r, y, z in ((inside(R), None, None), (R, inside(), None), (R, None, inside()), (inside(R), inside(), inside())):
+            got = api.swiglu_mlp_linear_fwd(X, W, b, act, r, keep=keep, out={"Y": y, "Z": z})
+            assert torch.equal(got[0], ref[0]) and (not keep or torch.equal(got[1], ref[1]))
+
+
+def chain(dt, M, wait, ws, seed):
+    """Calls whose inputs are the outputs of those before them, each an early launch
+    on the one before: all outputs that later calls read."""
+    D, N, g = 264, 528, gen(seed)
+    x, r = normal(g, M, D, dtype=dt), normal(g, M, D, dtype=dt)
+    W1, b1, W2 = (normal(g, *s, std=0.06, dtype=dt) for s in ((N, D), (N,), (D, N)))
+    w, b = normal(g, D, std=0.1, mean=1, dtype=dt), normal(g, D, dtype=dt)
+    kept = []
+    for _ in range(4):
+        y, s, mean, rstd = wait(api.swiglu_mlp_layer_norm_fwd(x, w, b, residual=r))
+        a, z = wait(api.swiglu_mlp_linear_fwd(y, W1, b1, "gelu", keep=True, ws=ws))
+        r, _ = wait(api.swiglu_mlp_linear_fwd(a, W2, b, "none", s, ws=ws))
+        da, dw2, db2 = wait(api.swiglu_mlp_linear_bwd(r, a, W2, X_pre=z, x_activation="gelu", ws=ws))
+        dy, dw1, db1 = wait(api.swiglu_mlp_linear_bwd(da, y, W1, z, "silu", ws=ws))
+        x, dw, db = wait(api.swiglu_mlp_layer_norm_bwd(dy, s, w, mean, rstd, dS=r, ws=ws))
+        # the gradients are the next weights, brought to their size by a norm
+        W1 = wait(api.swiglu_mlp_layer_norm_fwd(dw1, dw, db, stats=False))[0]
+        W2 = wait(api.swiglu_mlp_layer_norm_fwd(dw2, db1, stats=False))[0]
+        W1, W2 = (wait(api.swiglu_mlp_layer_norm_fwd(v, stats=False))[0].mul_(0.06) for v in (W1, W2))
+        b = wait(api.swiglu_mlp_layer_norm_fwd(db2.view(1, D), stats=False))[0].view(D)
+        kept += [y, s, mean, rstd, a, z, r, da, dw2, db2, dy, dw1, db1, x, dw, db, W1, W2, b]
+        x, r = (wait(api.swiglu_mlp_layer_norm_fwd(v, stats=False))[0] for v in (x, r))
+    return kept
+
+
+def bits(t):
+    """As whole numbers, so that what is no number compares too."""
+    return t.view(torch.int32 if t.dtype is torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("dtn", list(DT))
+@pytest.mark.parametrize("M", [1, 5, 40, 200, 1500])
+def test_calls_in_a_row_read_what_the_one_before_wrote(large_forms, dtn, M):
+    # (fp16: the weights' gradients of later rounds exceed 65504, in 64 bits in the same
+    # places, and their norms are then no numbers)
+    dt = DT[dtn]
+    ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+
+    def slowly(out):
+        torch.cuda.synchronize()
+        return out
+    for pairs, wide in ((1, 1), (2, 2)) if dtn != "f32" and M > 64 else ((1, 1),):
+        large_forms(pairs, wide)
+        ref = chain(dt, M, slowly, ws, M)
+        assert dtn == "f16" or all(bool(t.isfinite().all()) for t in ref)
+        for _ in range(10):
+            got = chain(dt, M, lambda out: out, ws, M)
+            assert all(torch.equal(bits(p), bits(q)) for p, q in zip(got, ref))
+
+
+@pytest.mark.parametrize("dtn", ["bf16", "f16"])
+def test_debug_build_checks_the_large_forms(large_forms, dtn):
+    # accesses by sectors, on pairs and on single SMs, and 512-column tiles
+    M, N, K, g, dt = 1100, 272, 1032, gen(1), DT[dtn]
+    X, W, b, R = (normal(g, *s, std=0.3, dtype=dt) for s in ((M, K), (N, K), (N,), (M, N)))
+    for pairs in (0, 2):
+        large_forms(pairs, 2)
+        ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+        run = lambda: (*api.swiglu_mlp_linear_fwd(X, W, b, "gelu", R, keep=True, ws=ws),
+                       *api.swiglu_mlp_linear_bwd(R, X, W, R, "gelu", X_pre=X, x_activation="silu", ws=ws))
+        release = run()
+        prev = api.use_debug_library(True)
+        try:
+            large_forms(pairs, 2)  # (the debug library keeps its own)
+            debug = run()  # (raises on a failed check)
+            api.lib().swiglu_mlp_debug_narrow_once(1)
+            assert device_status(lambda: api.swiglu_mlp_linear_fwd(X, W, b, "gelu", R, ws=ws), ws) == 7
+            large_forms(1, 1)
+        finally:
+            api.use_debug_library(prev)
+        assert all(torch.equal(p, q) for p, q in zip(release, debug))
