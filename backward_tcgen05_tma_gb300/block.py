@@ -24,6 +24,13 @@ def _rows(x, D):
     return x.reshape(-1, D).contiguous()
 
 
+def _output(x, X, N):
+    """An output [..., N] for x's batch and its rows [M, N].  The output is no view:
+    autograd refuses changes in place of a custom function's views."""
+    Y = x.new_empty(*x.shape[:-1], N)
+    return Y, Y.view(X.shape[0], N)
+
+
 def _grad_rows(g, like):
     """A gradient as contiguous rows of the forward's type (it may come expanded)."""
     return g.reshape(like.shape).to(like.dtype).contiguous()
@@ -49,17 +56,18 @@ class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, residual):
         D = x.shape[-1]
+        X, out = _rows(x, D), {}
         r = None if residual is None else _rows(residual, D)
-        Y, S, mean, rstd = api.swiglu_mlp_layer_norm_fwd(_rows(x, D), weight, bias, eps, residual=r)
+        Y, out["Y"] = _output(x, X, D)
+        S = X
+        if residual is not None:
+            S, out["S"] = _output(x, X, D)
+        _, _, mean, rstd = api.swiglu_mlp_layer_norm_fwd(X, weight, bias, eps, residual=r, out=out)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(S, weight, mean, rstd)
         ctx.shape = x.shape
         ctx.has_residual = residual is not None
-        Y = Y.reshape(x.shape)
-        if residual is None:
-            return Y
-        S = S.reshape(x.shape)
-        return Y, S
+        return Y if residual is None else (Y, S)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -100,11 +108,12 @@ class LinearFunction(torch.autograd.Function):
         N, K = weight.shape
         X = _rows(x, K)
         R = None if residual is None else _rows(residual, N)
-        Y, Z = api.swiglu_mlp_linear_fwd(X, weight, bias, activation, R, keep=activation != "none")
+        Y, rows = _output(x, X, N)
+        _, Z = api.swiglu_mlp_linear_fwd(X, weight, bias, activation, R, keep=activation != "none", out={"Y": rows})
         ctx.save_for_backward(X, weight, Z)
         ctx.activation = activation
         ctx.shape = x.shape
-        return Y.reshape(*x.shape[:-1], N)
+        return Y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -143,11 +152,12 @@ class MLPFunction(torch.autograd.Function):
         X = _rows(x, w1.shape[1])
         R = None if residual is None else _rows(residual, w2.shape[0])
         A, Z = api.swiglu_mlp_linear_fwd(X, w1, b1, activation, keep=activation != "none")
-        Y, _ = api.swiglu_mlp_linear_fwd(A, w2, b2, "none", R)
+        Y, rows = _output(x, X, w2.shape[0])
+        api.swiglu_mlp_linear_fwd(A, w2, b2, "none", R, out={"Y": rows})
         ctx.save_for_backward(X, w1, Z, A, w2)
         ctx.activation = activation
         ctx.shape = x.shape
-        return Y.reshape(*x.shape[:-1], w2.shape[0])
+        return Y
 
     @staticmethod
     @torch.autograd.function.once_differentiable

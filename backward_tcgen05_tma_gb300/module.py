@@ -40,12 +40,14 @@ class SwiGLUMLPFunction(torch.autograd.Function):
         D = X.shape[-1]
         lead = X.shape[:-1]
         X2 = X.reshape(-1, D).contiguous()
-        Y, saved = api.swiglu_mlp_fwd(X2, Wgu, Wd, gate_mul=gate_mul, down_mul=down_mul)
+        Y = X.new_empty(*lead, D)  # no view: a caller may change it in place
+        _, saved = api.swiglu_mlp_fwd(X2, Wgu, Wd, {"Y": Y.view(X2.shape)},
+                                      gate_mul=gate_mul, down_mul=down_mul)
         ctx.save_for_backward(X2, Wgu, Wd, saved)
         ctx.lead = lead
         ctx.muls = (gate_mul, down_mul)
         ctx.consumed = False
-        return Y.reshape(*lead, D)
+        return Y
 
     @staticmethod
     @torch.autograd.function.once_differentiable

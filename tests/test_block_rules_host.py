@@ -185,3 +185,31 @@ def test_what_waits_waits_first():
     assert started - plain == {e[1] for e in EARLY if e[0].startswith("csrc_block")}
     for name in plain:
         assert re.findall(r"%s<[^;]*?>(<<<|\()" % name, host) and not re.search(r"auto kern = %s" % name, host)
+
+
+def test_outputs_may_be_changed_in_place(monkeypatch):
+    # as nn.Linear's may: the outputs that autograd hands out are no views.  The
+    # calls are restated on the host, as there is no GPU here.
+    def put(out, name, value):
+        t = out[name] if out and out.get(name) is not None else torch.empty_like(value)
+        return t.copy_(value)
+
+    def norm_fwd(X, weight, bias, eps, residual=None, out=None, stats=True):
+        S = X if residual is None else put(out, "S", X + residual)
+        mean, rstd = S.mean(1), S.var(1, correction=0).add(eps).rsqrt()
+        return put(out, "Y", (S - mean[:, None]) * rstd[:, None]), S, mean, rstd
+
+    def linear_fwd(X, W, bias=None, activation="none", residual=None, keep=False, out=None, ws=None):
+        return put(out, "Y", X @ W.T), X @ W.T if keep else None
+    monkeypatch.setattr(api, "swiglu_mlp_layer_norm_fwd", norm_fwd)
+    monkeypatch.setattr(api, "swiglu_mlp_linear_fwd", linear_fwd)
+    monkeypatch.setattr(api, "swiglu_mlp_fwd", lambda X, *a, **k: (put(a[2] if len(a) > 2 else None, "Y", X), X))
+    w, pair, down = torch.randn(64, 64), torch.randn(192, 64), torch.randn(64, 96)
+    for shape in ((4, 64), (2, 3, 64), (64,), (2, 0, 64)):
+        x = torch.randn(shape, requires_grad=True)
+        for y in (block.layer_norm(x), *block.layer_norm(x, residual=x), block.linear(x, w, None, "relu"),
+                  block.mlp(x, w, None, w, None), module.swiglu_mlp(x, pair, down)):
+            ref = y.detach().clone()
+            assert y.shape == shape and y.requires_grad
+            y += 1
+            assert torch.equal(y, ref + 1)

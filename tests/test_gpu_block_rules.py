@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from backward_tcgen05_tma_gb300 import api, block, build
+from backward_tcgen05_tma_gb300 import api, block, build, module
 from backward_tcgen05_tma_gb300.module import SwiGLUMLP
 from backward_tcgen05_tma_gb300.serving import MoESwiGLU, W4SwiGLUMLP
 from conftest import device_status
@@ -220,3 +220,24 @@ def test_debug_build_checks_the_large_forms(large_forms, dtn):
         finally:
             api.use_debug_library(prev)
         assert all(torch.equal(p, q) for p, q in zip(release, debug))
+
+
+@pytest.mark.parametrize("dtn", list(DT))
+def test_outputs_changed_in_place_have_their_gradients(dtn):
+    dt, g = DT[dtn], gen(6)
+    w, x = normal(g, 64, 64, std=0.2, dtype=dt).requires_grad_(), normal(g, 3, 5, 64, dtype=dt).requires_grad_()
+    layers = [lambda v: block.layer_norm(v), lambda v: block.layer_norm(v, residual=v)[0],
+              lambda v: block.linear(v, w, None, "gelu"), lambda v: block.mlp(v, w, None, w, None)]
+    if dtn != "f32":
+        pair, down = normal(g, 192, 64, std=0.2, dtype=dt), normal(g, 64, 96, std=0.2, dtype=dt)
+        layers.append(lambda v: module.swiglu_mlp(v, pair, down))
+    for f in layers:
+        y = f(x)
+        y *= 2
+        got = torch.autograd.grad(y.sum(), x)[0]
+        assert torch.equal(got, torch.autograd.grad((f(x) * 2).sum(), x)[0])
+    # the sum is what backward reads: changing it is noticed
+    y, s = block.layer_norm(x, residual=x)
+    s += 1
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y.sum(), x)
