@@ -17,11 +17,7 @@ import math
 import torch
 
 from . import api
-from .module import refuse_tangents
-
-
-def _rows(x, D):
-    return x.reshape(-1, D).contiguous()
+from .module import refuse_tangents, rows_of as _rows
 
 
 def _output(x, X, N):
@@ -31,9 +27,9 @@ def _output(x, X, N):
     return Y, Y.view(X.shape[0], N)
 
 
-def _grad_rows(g, like):
-    """A gradient as contiguous rows of the forward's type (it may come expanded)."""
-    return g.reshape(like.shape).to(like.dtype).contiguous()
+def _grad_rows(g, D, dtype):
+    """A gradient as rows of the forward's type (it may come expanded)."""
+    return _rows(g.to(dtype), D)
 
 
 def _last(x, D, what):
@@ -76,10 +72,10 @@ class LayerNormFunction(torch.autograd.Function):
         _, need_w, need_b, _, need_r = ctx.needs_input_grad
         if dY is None:  # the sum alone was used
             return dS, None, None, None, dS if ctx.has_residual else None
-        S = S.reshape(-1, S.shape[-1])
+        D = S.shape[-1]
         dX, dw, db = api.swiglu_mlp_layer_norm_bwd(
-            _grad_rows(dY, S), S, weight, mean, rstd, dS=None if dS is None else _grad_rows(dS, S),
-            need_dweight=need_w, need_dbias=need_b)
+            _grad_rows(dY, D, S.dtype), S.reshape(-1, D), weight, mean, rstd,
+            dS=None if dS is None else _grad_rows(dS, D, S.dtype), need_dweight=need_w, need_dbias=need_b)
         dX = dX.reshape(ctx.shape)
         return dX, dw, db, None, dX if need_r else None
 
@@ -122,7 +118,7 @@ class LinearFunction(torch.autograd.Function):
         need_x, need_w, need_b, _, need_r = ctx.needs_input_grad
         dX = dW = db = None
         if need_x or need_w or need_b:
-            g = dY.reshape(X.shape[0], weight.shape[0]).to(X.dtype).contiguous()
+            g = _grad_rows(dY, weight.shape[0], X.dtype)
             dX, dW, db = api.swiglu_mlp_linear_bwd(g, X, weight, Z, ctx.activation, need_dX=need_x,
                                                    need_dW=need_w, need_dbias=need_b)
         return (None if dX is None else dX.reshape(ctx.shape), dW, db, None, dY if need_r else None)
@@ -167,7 +163,7 @@ class MLPFunction(torch.autograd.Function):
         first = need_x or need_w1 or need_b1
         dX = dW1 = db1 = dW2 = db2 = None
         if first or need_w2 or need_b2:
-            g = dY.reshape(X.shape[0], w2.shape[0]).to(X.dtype).contiguous()
+            g = _grad_rows(dY, w2.shape[0], X.dtype)
             dZ, dW2, db2 = api.swiglu_mlp_linear_bwd(g, A, w2, X_pre=Z, x_activation=ctx.activation,
                                                      need_dX=first, need_dW=need_w2,
                                                      need_dbias=need_b2)

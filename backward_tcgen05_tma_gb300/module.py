@@ -31,6 +31,13 @@ def refuse_tangents(what, *tensors):
         raise RuntimeError("%s has no forward-mode derivative" % what)
 
 
+def rows_of(x, D):
+    """x's rows [M, D] as the calls take them: contiguous, on 16 bytes.  (A slice, or
+    the gradient of one, can be contiguous and start anywhere.)"""
+    r = x.reshape(-1, D).contiguous()
+    return r.clone() if r.data_ptr() % 16 else r
+
+
 class SwiGLUMLPFunction(torch.autograd.Function):
     """Y = md (SiLU(mg X Wg^T) * (X Wu^T)) Wd^T with Wgu = [Wg; Wu] ([2H, D]);
     the gate/down multipliers mg, md are 1 for the standard MLP."""
@@ -39,7 +46,7 @@ class SwiGLUMLPFunction(torch.autograd.Function):
     def forward(ctx, X, Wgu, Wd, gate_mul=1.0, down_mul=1.0):
         D = X.shape[-1]
         lead = X.shape[:-1]
-        X2 = X.reshape(-1, D).contiguous()
+        X2 = rows_of(X, D)
         Y = X.new_empty(*lead, D)  # no view: a caller may change it in place
         _, saved = api.swiglu_mlp_fwd(X2, Wgu, Wd, {"Y": Y.view(X2.shape)},
                                       gate_mul=gate_mul, down_mul=down_mul)
@@ -59,7 +66,7 @@ class SwiGLUMLPFunction(torch.autograd.Function):
         ctx.consumed = True
         X2, Wgu, Wd, saved = ctx.saved_tensors
         D = X2.shape[1]
-        dY2 = dY.reshape(-1, D).to(X2.dtype).contiguous()
+        dY2 = rows_of(dY.to(X2.dtype), D)
         dX, dWgu, dWd = api.swiglu_mlp_bwd(dY2, X2, Wgu, Wd, saved, gate_mul=ctx.muls[0],
                                            down_mul=ctx.muls[1])
         return dX.reshape(*ctx.lead, D), dWgu, dWd, None, None
@@ -72,8 +79,7 @@ def swiglu_mlp(X, Wgu, Wd, gate_mul: float = 1.0, down_mul: float = 1.0):
     if torch.is_grad_enabled() and (X.requires_grad or Wgu.requires_grad or Wd.requires_grad):
         return SwiGLUMLPFunction.apply(X, Wgu, Wd, float(gate_mul), float(down_mul))
     D = X.shape[-1]
-    Y, _ = api.swiglu_mlp_fwd_nograd(X.reshape(-1, D).contiguous(), Wgu, Wd, gate_mul=gate_mul,
-                                     down_mul=down_mul)
+    Y, _ = api.swiglu_mlp_fwd_nograd(rows_of(X, D), Wgu, Wd, gate_mul=gate_mul, down_mul=down_mul)
     return Y.reshape(*X.shape[:-1], D)
 
 
@@ -183,7 +189,7 @@ class SwiGLUMLP(torch.nn.Module):
                 self.down_weight.requires_grad)):
             D = x.shape[-1]
             refuse_tangents("SwiGLUMLP", x, self.gate_up_weight, self.down_weight)
-            X = x.reshape(-1, D).contiguous()
+            X = rows_of(x, D)
             if 0 < X.shape[0] <= PACKED_MAX_TOKENS:
                 Y, _ = api.swiglu_mlp_fwd_nograd_packed(X, packed, self.intermediate_size,
                                                         gate_mul=self.gate_multiplier,

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import api
-from .module import refuse_tangents
+from .module import refuse_tangents, rows_of
 
 MAX_TOKENS = 64  # of one call of the few-token operators
 
@@ -125,7 +125,7 @@ class W4SwiGLUMLP(torch.nn.Module):
 
     def forward(self, x):
         _no_grad_only(x, "W4SwiGLUMLP")
-        X = x.reshape(-1, x.shape[-1]).contiguous()
+        X = rows_of(x, x.shape[-1])
         muls = dict(gate_mul=self.gate_multiplier, down_mul=self.down_multiplier)
         if X.shape[0] <= MAX_TOKENS:
             Y, _ = api.swiglu_mlp_fwd_nograd_w4(X, self.gate_up, self.down, **muls)
@@ -184,7 +184,7 @@ class MoESwiGLU(torch.nn.Module):
     def forward(self, x):
         _no_grad_only(x, "MoESwiGLU")
         D = x.shape[-1]
-        X = x.reshape(-1, D).contiguous()
+        X = rows_of(x, D)
         if self.gate_up_w4 is not None:
             gu, down = self.gate_up_w4.weights, self.down_w4.weights
         else:

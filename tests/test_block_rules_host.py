@@ -213,3 +213,14 @@ def test_outputs_may_be_changed_in_place(monkeypatch):
             assert y.shape == shape and y.requires_grad
             y += 1
             assert torch.equal(y, ref + 1)
+
+
+def test_rows_start_where_the_calls_can_read_them():
+    # contiguous slices that start inside 16 bytes
+    buf = torch.arange(8 * 64 + 8, dtype=torch.float32).to(torch.bfloat16)
+    x = buf[3:3 + 8 * 64].view(8, 64)
+    assert x.is_contiguous() and x.data_ptr() % 16
+    for rows in (module.rows_of(x, 64), module.rows_of(x.view(2, 4, 64), 64), block._grad_rows(x.view(4, 2, 64), 64, x.dtype)):
+        assert rows.data_ptr() % 16 == 0 and torch.equal(rows, x)
+    y = buf[:8 * 64].view(8, 64)
+    assert module.rows_of(y, 64).data_ptr() == y.data_ptr()  # nothing to move

@@ -241,3 +241,34 @@ def test_outputs_changed_in_place_have_their_gradients(dtn):
     s += 1
     with pytest.raises(RuntimeError):
         torch.autograd.grad(y.sum(), x)
+
+
+@pytest.mark.parametrize("dtn", list(DT))
+def test_layers_take_inputs_and_gradients_that_start_anywhere(dtn):
+    dt, g, M, D = DT[dtn], gen(7), 6, 64
+    w = normal(g, D, D, std=0.2, dtype=dt).requires_grad_()
+    pair, down = normal(g, 192, 64, std=0.2, dtype=dt), normal(g, 64, 96, std=0.2, dtype=dt)
+    a, c = normal(g, 3, dtype=dt), normal(g, 3 + M * D, dtype=dt)
+    x = normal(g, 3 + M * D, dtype=dt)[3:].view(M, D)  # contiguous, inside 16 bytes
+    assert x.data_ptr() % 16
+    layers = [lambda v: block.layer_norm(v), lambda v: block.layer_norm(v, residual=v)[1], lambda v: block.linear(v, w, None, "gelu"),
+              lambda v: block.linear(v, w, None, "none", v), lambda v: block.mlp(v, w, None, w, None),
+              lambda v: sum(block.layer_norm(v, residual=v)), lambda v: module.swiglu_mlp(v, pair, down)]
+    if dtn != "f32":
+        with torch.no_grad():
+            layers.append(W4SwiGLUMLP(SwiGLUMLP(D, 96, dtype=dt, device="cuda"), group=32))
+            layers.append(MoESwiGLU(D, 64, 4, 2, dtype=dt, device="cuda"))
+    for f in layers:
+        with torch.no_grad():
+            assert torch.equal(f(x), f(x.clone()))
+        if isinstance(f, torch.nn.Module):
+            continue
+        grads = []
+        for v in (x, x.clone()):
+            v = v.detach().requires_grad_()
+            # the gradient of the second part of a row of values starts behind three others
+            joined = torch.cat([a, f(v).flatten()])
+            grads.append(torch.autograd.grad(joined, v, c)[0])
+        v = x.clone().requires_grad_()
+        grads.append(torch.autograd.grad(f(v), v, c[3:].view(M, D).clone())[0])
+        assert torch.equal(grads[0], grads[1]) and torch.equal(grads[1], grads[2])
