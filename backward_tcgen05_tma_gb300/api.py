@@ -765,6 +765,12 @@ def _refuse(where, X, shapes):
                                 t.device))
 
 
+def _needed(where, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError("%s: %s is needed" % (where, name))
+
+
 def _rows(where, X):
     if X.dim() != 2 or X.get_device() < 0 or not X.is_contiguous():
         raise ValueError("%s: expected contiguous CUDA rows [M, D], got %s" % (where, tuple(X.shape)))
@@ -822,6 +828,7 @@ def swiglu_mlp_layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, resi
     (Y, S, mean, rstd).  S is X itself or the rounded sum; mean and rstd (fp32
     [M], for the backward pass) are None without ``stats``."""
     where = "swiglu_mlp_layer_norm_fwd"
+    _needed(where, X=X)
     M, D = rows = _rows(where, X)
     dt, dev = X.dtype, X.get_device()
     if not (_is(weight, (D,), dt, dev) and _is(bias, (D,), dt, dev) and _is(residual, rows, dt, dev)):
@@ -847,6 +854,7 @@ def swiglu_mlp_layer_norm_bwd(dY, S, weight, mean, rstd, dS=None, need_dweight: 
     residual stream's), added into dX.  dX is the residual's gradient too.
     ``accumulate``: add into the dweight and dbias given in ``out``."""
     where = "swiglu_mlp_layer_norm_bwd"
+    _needed(where, dY=dY, S=S, mean=mean, rstd=rstd)
     M, D = rows = _rows(where, S)
     dt, dev = S.dtype, S.get_device()
     if not (_is(dY, rows, dt, dev) and _is(weight, (D,), dt, dev) and _is(dS, rows, dt, dev)):
@@ -877,6 +885,7 @@ def swiglu_mlp_linear_fwd(X, W, bias=None, activation: str = "none", residual=No
     rounded pre-activation, which the backward pass of an activation needs,
     with ``keep``, else None."""
     where = "swiglu_mlp_linear_fwd"
+    _needed(where, X=X, W=W)
     M, K = _rows(where, X)
     act = activation_code(activation)
     N, dt, dev = W.shape[0], X.dtype, X.get_device()
@@ -901,9 +910,11 @@ def swiglu_mlp_linear_bwd(dY, X, W, Z=None, activation: str = "none", X_pre=None
     None in the place of one that is not needed; the residual's gradient is dY.
     Z: the pre-activation that forward kept.  With ``x_activation``, X is that
     activation of X_pre, and dX becomes the gradient of X_pre.  The gradient of
-    the pre-activation is left in out["dZ"] where that is given.
+    the pre-activation is left in out["dZ"] where that is given.  X may be None
+    where dW is not needed.
     ``accumulate``: add into the dW and dbias given in ``out``."""
     where = "swiglu_mlp_linear_bwd"
+    _needed(where, dY=dY, W=W, X=X if need_dW else ())
     M, N = rows = _rows(where, dY)
     act, x_act = activation_code(activation), activation_code(x_activation)
     K, dt, dev = W.shape[1], dY.dtype, dY.get_device()
@@ -922,7 +933,7 @@ def swiglu_mlp_linear_bwd(dY, X, W, Z=None, activation: str = "none", X_pre=None
     code = dtype_code(dt)
     ws = _sized_ws(ws, where, L.swiglu_mlp_linear_workspace_bytes, (M, N, K, code, SWIGLU_OP_BWD), dev)
     _ready(where, L.swiglu_mlp_linear_bwd,
-           (dY.data_ptr(), X.data_ptr(), W.data_ptr(), _at(Z), act, _at(X_pre), x_act, _at(dZ), _at(dX),
+           (dY.data_ptr(), _at(X), W.data_ptr(), _at(Z), act, _at(X_pre), x_act, _at(dZ), _at(dX),
             _at(dW), _at(db), M, N, K, int(accumulate), code), ws, dev)
     return dX, dW, db
 

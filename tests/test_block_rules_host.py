@@ -224,3 +224,17 @@ def test_rows_start_where_the_calls_can_read_them():
         assert rows.data_ptr() % 16 == 0 and torch.equal(rows, x)
     y = buf[:8 * 64].view(8, 64)
     assert module.rows_of(y, 64).data_ptr() == y.data_ptr()  # nothing to move
+
+
+def test_the_binding_names_what_is_missing():
+    x, w, v = torch.zeros(4, 64), torch.zeros(64, 64), torch.zeros(4)
+    for name, call in (("X", lambda: api.swiglu_mlp_layer_norm_fwd(None)), ("X", lambda: api.swiglu_mlp_linear_fwd(None, w)),
+                       ("W", lambda: api.swiglu_mlp_linear_fwd(x, None)),
+                       ("dY", lambda: api.swiglu_mlp_layer_norm_bwd(None, x, None, v, v)),
+                       ("S", lambda: api.swiglu_mlp_layer_norm_bwd(x, None, None, v, v)),
+                       ("mean", lambda: api.swiglu_mlp_layer_norm_bwd(x, x, None, None, v)),
+                       ("rstd", lambda: api.swiglu_mlp_layer_norm_bwd(x, x, None, v, None)),
+                       ("dY", lambda: api.swiglu_mlp_linear_bwd(None, x, w)), ("X", lambda: api.swiglu_mlp_linear_bwd(x, None, w)),
+                       ("W", lambda: api.swiglu_mlp_linear_bwd(x, x, None))):
+        with pytest.raises(ValueError, match=r": %s is needed" % name):
+            call()

@@ -272,3 +272,12 @@ def test_layers_take_inputs_and_gradients_that_start_anywhere(dtn):
         v = x.clone().requires_grad_()
         grads.append(torch.autograd.grad(f(v), v, c[3:].view(M, D).clone())[0])
         assert torch.equal(grads[0], grads[1]) and torch.equal(grads[1], grads[2])
+
+
+@pytest.mark.parametrize("dtn", list(DT))
+def test_input_gradients_without_the_input(dtn):
+    g, dt = gen(8), DT[dtn]
+    dY, X, W, Z = (normal(g, *s, dtype=dt) for s in ((40, 136), (40, 264), (136, 264), (40, 136)))
+    dX, _, db = api.swiglu_mlp_linear_bwd(dY, X, W, Z, "gelu")
+    got = api.swiglu_mlp_linear_bwd(dY, None, W, Z, "gelu", need_dW=False)
+    assert torch.equal(got[0], dX) and got[1] is None and torch.equal(got[2], db)
