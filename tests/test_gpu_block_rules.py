@@ -281,3 +281,90 @@ def test_input_gradients_without_the_input(dtn):
     dX, _, db = api.swiglu_mlp_linear_bwd(dY, X, W, Z, "gelu")
     got = api.swiglu_mlp_linear_bwd(dY, None, W, Z, "gelu", need_dW=False)
     assert torch.equal(got[0], dX) and got[1] is None and torch.equal(got[2], db)
+
+
+def test_relus_slope_where_there_is_no_number():
+    # 1, as its other side gives: the gradient passes
+    for dt in DT.values():
+        for M in (3, 300):
+            z = torch.full((M, 16), float("nan"), dtype=dt, device="cuda")
+            dY, W = normal(gen(1), M, 16, dtype=dt), torch.zeros(16, 8, dtype=dt, device="cuda")
+            pre = torch.full((M, 8), float("nan"), dtype=dt, device="cuda")
+            W[:8] = torch.eye(8)
+            dZ = torch.empty_like(dY)
+            dX, _, _ = api.swiglu_mlp_linear_bwd(dY, None, W, z, "relu", X_pre=pre, x_activation="relu", need_dW=False,
+                                                 out={"dZ": dZ})
+            assert torch.equal(dZ, dY) and torch.equal(dX, dY[:, :8])
+
+
+# ---------------------------------------------------------------------------
+# offsets that pass 32 bits: the last rows are what a call on them alone gives
+# ---------------------------------------------------------------------------
+def large(rows, columns, dt=torch.bfloat16, seed=0):
+    """Rows of 2^20 different values, repeated (quickly made)."""
+    n = 1 << 20
+    v = normal(gen(seed), n, dtype=dt)
+    return v.repeat((rows * columns + n - 1) // n + 1)[: rows * columns].view(rows, columns)
+
+
+TAIL = 40
+
+
+def test_norms_of_more_than_2_to_the_31_elements():
+    M, D = 140_000, 16384
+    x, dy = large(M, D, seed=1), large(M, D, seed=2)
+    w = normal(gen(3), D, dtype=x.dtype)
+    Y, S, mean, rstd = api.swiglu_mlp_layer_norm_fwd(x, w, None, residual=dy)
+    dX, dw, _ = api.swiglu_mlp_layer_norm_bwd(dy, S, w, mean, rstd, dS=x, need_dbias=False)
+    t = slice(M - TAIL, M)
+    y2, s2, m2, r2 = api.swiglu_mlp_layer_norm_fwd(x[t], w, None, residual=dy[t])
+    d2, _, _ = api.swiglu_mlp_layer_norm_bwd(dy[t], s2, w, m2, r2, dS=x[t])
+    for a, b in ((Y[t], y2), (S[t], s2), (mean[t], m2), (rstd[t], r2), (dX[t], d2)):
+        assert torch.equal(a, b)
+    # dw, by parts of the rows
+    ref, size = torch.zeros(D, dtype=torch.float64, device="cuda"), torch.zeros(D, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 4000):
+        h = dy[i:i + 4000].double() * (S[i:i + 4000].double() - mean[i:i + 4000, None]) * rstd[i:i + 4000, None]
+        ref += h.sum(0)
+        size += h.square().sum(0)
+    within(dw, ref, U["bf16"], 4 * math.sqrt(M) * 2.0 ** -24 + 2.0 ** -20, size.sqrt())
+
+
+@pytest.mark.parametrize("dtn", ["bf16", "f32"])
+def test_outputs_of_more_than_2_to_the_31_elements(dtn):
+    M, N, K, dt = 600_000, 4096, 64, DT[dtn]
+    X, W, b = large(M, K, dt), normal(gen(1), N, K, std=0.1, dtype=dt), normal(gen(2), N, dtype=dt)
+    Y, Z = api.swiglu_mlp_linear_fwd(X, W, b, "silu", keep=True)
+    assert Y.numel() > 2 ** 31
+    t = slice(M - 1200, M)  # (as many as take the same kernel)
+    y2, z2 = api.swiglu_mlp_linear_fwd(X[t], W, b, "silu", keep=True)
+    assert torch.equal(Y[t], y2) and torch.equal(Z[t], z2)
+    dZ = torch.empty_like(Y)
+    dX, _, db = api.swiglu_mlp_linear_bwd(Y, X, W, Z, "silu", need_dW=False, out={"dZ": dZ})
+    e2 = torch.empty_like(y2)
+    d2, _, _ = api.swiglu_mlp_linear_bwd(y2, X[t], W, z2, "silu", need_dW=False, out={"dZ": e2})
+    assert torch.equal(dZ[t], e2)
+    u, n = U[dtn], act_slack(N)
+    ref = e2.double() @ W.double()
+    within(dX[t], ref, u, n, (e2.double().square() @ W.double().square()).sqrt())
+    # db: the rows come again and again, so the terms of a column add up and their
+    # roundings do not go like a random walk.  A warp adds every eighth row of a part
+    # one after another (4096 columns: 32 strips of fp32, 19 parts, 3948 rows; 16 strips
+    # of bf16, 38 parts, 1974 rows), each sum rounded by up to 2^-24 of itself, which is
+    # at most the sum of all absolute values; a slope is off by up to 2^-18 of |Y|
+    ref, size = torch.zeros(N, dtype=torch.float64, device="cuda"), torch.zeros(N, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 20_000):
+        v = Y[i:i + 20_000].double() * dact64("silu", Z[i:i + 20_000].double())
+        ref += v.sum(0)
+        size += v.abs().sum(0) + 2.0 ** -18 / (4100 * 2.0 ** -24) * Y[i:i + 20_000].double().abs().sum(0)
+    within(db, ref, u, 4100 * 2.0 ** -24, size)
+
+
+@pytest.mark.parametrize("dtn,M", [("bf16", 1), ("f16", 16), ("bf16", 64), ("bf16", 200), ("f32", 1), ("f32", 8), ("f32", 40)])
+def test_weights_of_more_than_2_to_the_31_elements(dtn, M):
+    N, K, dt = 300_000, 8192, DT[dtn]
+    X, W = normal(gen(M), M, K, dtype=dt), large(N, K, dt)
+    Y, _ = api.swiglu_mlp_linear_fwd(X, W)
+    for t in (slice(0, 64), slice(N - 64, N)):
+        x, w = X.double(), W[t].double()
+        within(Y[:, t], x @ w.T, U[dtn], act_slack(K), (x.square() @ w.square().T).sqrt())
