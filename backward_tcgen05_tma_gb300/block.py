@@ -4,7 +4,10 @@ bias, activation and residual, the MLP without a gate that two of them make,
 and the pre-norm sublayer x + mlp(norm(x)) of any of this package's MLPs.
 
 The tensors are CUDA tensors of one dtype (bf16, fp16, or fp32 for the IEEE
-mode); every computation runs in the library's kernels.  Nothing that a
+mode).  Norms, products, activations and their gradients run in the library's
+kernels, and so do the sums of a residual stream in a norm or in an ``MLP``; the
+one behind another kind of MLP in ``MLPBlock`` is a sum of tensors, unless it is
+left to the next norm (``join=False``).  Nothing that a
 backward pass needs is overwritten, so a graph may be kept and run again;
 double differentiation and forward-mode derivatives are refused.  A captured training step takes its
 gradients with ``torch.autograd.grad``, or through leaves that no graph from

@@ -26,7 +26,7 @@ namespace {
 constexpr int64_t LN_MAX_D = 16384;            // a row fits the registers of a block
 constexpr int64_t MAX_ROWS = 0x7fffffffLL - 256;  // the kernels' 32-bit row and column indexes
 constexpr size_t FIXED = WS_HEADER + TC_SK_COUNTER_BYTES;  // error word and counters of shared tiles
-static_assert(NG_MAX_CTAS * 4 <= TC_SK_COUNTER_BYTES, "the few-token kernel counts fewer shared tiles than blocks");
+static_assert(TC_SK_MAX_SMS * 4 <= TC_SK_COUNTER_BYTES, "fewer tiles are shared than there are SMs to share them");
 
 swiglu_status status_of(cudaError_t e) { return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA; }
 
@@ -312,10 +312,11 @@ struct StreamPlan {
 // Up to 16 tokens.  Clusters of 4 blocks, whose warps in pairs split the contraction 8
 // ways, as they reach every SM (38 clusters; of 8 blocks 15 fit, 120 SMs); of 8 where a
 // quarter of the token rows does not fit a block, and linear_mid.cuh's form where an
-// eighth does not.  Measured in us, this form first, tokens 8 / 16 / 32:
-//   11008 x 4096   20.0, 23.0   20.8, 20.5   23.6, 19.7
-//   4096 x 4096    10.4, 11.0   10.8, 10.8   12.1, 10.3
-//   2816 x 1024     5.6, 5.9     5.7, 5.9     6.4, 5.9
+// eighth does not.  Measured in us, this form first, 8 and 16 tokens:
+//   11008 x 4096   20.0, 23.0   20.8, 20.5
+//   4096 x 4096    10.4, 11.0   10.8, 10.8
+//   2816 x 1024     5.6, 5.9     5.7, 5.9
+// (at 32 tokens 23.6, 19.7 and 12.1, 10.3: it is for 16 at most)
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
   StreamPlan p = {};
   if (M > LF_MAX_M) return p;

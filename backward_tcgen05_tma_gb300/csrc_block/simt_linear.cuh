@@ -11,7 +11,7 @@
 // blocks fit an SM.  The tiles of a last round that would leave many of those
 // places empty are split over the contraction, and a second kernel adds the parts
 // in order and applies the epilogue.  1999 x 2824 x 1032 (368 tiles of 128 x 128,
-// 64 of them split): 263 us, 44 TFLOP/s, 60% of the FMA pipe; 324 with all tiles
+// 64 of them split): 272 us, 43 TFLOP/s, 58% of the FMA pipe; 324 with all tiles
 // whole, 577 with tiles of 64 x 64.
 //
 // An operand comes with k contiguous (KC: rows of it are turned on the way to

@@ -453,15 +453,17 @@ swiglu_status swiglu_mlp_moe_fwd_nograd(const void* X, const void* Wr, const voi
  *
  * Infinities and NaN give what the formulas give, in their own rows (and in
  * the sums over rows); the activations' derivatives take their limits at
- * infinities. */
+ * infinities, and relu's is 1 where there is no number.  Statistics are fp32: a
+ * row whose squared deviations from its mean add up to more than fp32 holds has
+ * an rstd of 0. */
 
 /* S = rnd(X + residual), or X where residual is NULL (then S is NULL too);
  *   mu = mean of S's row,  rstd = (mean of (S - mu)^2 + eps)^-1/2,
  *   Y = rnd((S - mu) rstd weight + bias).
  * weight, bias [D]: NULL for 1 and 0.  mean, rstd: fp32 [M], kept for the
  * backward pass, each NULL if not wanted.  S may be X's or the residual's
- * buffer, and Y may be any of theirs where S is not.  ws: NULL, or a workspace of 256 bytes whose
- * error word the debug build's checks record in.  One kernel. */
+ * buffer, and Y may be any of theirs where S is not.  ws: NULL, or a workspace of
+ * 256 bytes whose error word the debug build's checks record in.  One kernel. */
 swiglu_status swiglu_mlp_layer_norm_fwd(const void* X, const void* residual, const void* weight,
                                         const void* bias, void* S, void* Y, float* mean, float* rstd,
                                         int64_t M, int64_t D, float eps, swiglu_dtype dtype, void* ws,
