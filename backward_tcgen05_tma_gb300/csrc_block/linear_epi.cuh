@@ -109,8 +109,8 @@ __device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
 // plain form turns every chunk round through shared memory to that end, and
 // stores by TMA wait behind the ring's loads in that unit: 16384 x 2816 x 1024 with
 // gelu and Z took 117 us with it (stream-K shares among it), 90 with TMA stores, 80
-// with these and launches that overlap.  Without Z it takes 12 us less, the rate at
-// which Z's bytes go to memory.
+// with these and launches that overlap (81 to 88 on other boxes).  Without Z it takes
+// 12 us less, the rate at which Z's bytes go to memory.
 struct EpiLinearSectors {
   using Params = EpiLinear::Params;
   template <int BN, bool BF16>
